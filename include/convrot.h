@@ -113,7 +113,8 @@ typedef enum convrot_dtype {
     CONVROT_F32 = 0,
     CONVROT_BF16 = 1,
     CONVROT_I8 = 2,
-    CONVROT_I32 = 3
+    CONVROT_I32 = 3,
+    CONVROT_F8E4M3 = 4         /* OCP e4m3: 4 exponent bits, no infinities, max 448 */
 } convrot_dtype;
 
 typedef enum convrot_layout {
@@ -404,6 +405,205 @@ CONVROT_API int convrot_swiglu_bf16(const uint16_t *gu, int64_t M, int64_t F, ui
 /* s[i] = fp32(silu(a[i])) for n bf16 values, the s of every SwiGLU path
  * (test hook: lets a test compare every bf16 pattern at fp32 precision). */
 CONVROT_API int convrot_silu_f32(const uint16_t *a, int64_t n, float *s, void *stream);
+
+/* ------------------------------------------------------------------ */
+/* FP8 block-scaled linear                                             */
+/* ------------------------------------------------------------------ */
+
+/* The projection from 8-bit floating-point weights, without a rotation: e4m3
+ * codes with one F32 scale for each 128 x 128 block of W and, computed per
+ * call, for each 128 inputs of a token:
+ *   amax = max |x| over the 128 inputs;  s_x = max(amax / 448, 2^-126) (fp32,
+ *   correctly rounded division), 0 when amax is 0;  POW2: the smallest power of
+ *   two not below it;  q = e4m3(x * (1 / s_x)) (fp32 quotient and product, then
+ *   round to nearest even).
+ *   y[m, n] = sum over k-blocks b of (sum_{k in b} qx qw) * (s_x[m, b] * s_w[n / 128, b])
+ *   (+ bias[n]); bf16 outputs round to nearest even.
+ * Sums: F32 outputs are summed in fp32 throughout.  BF16 outputs use the FP8
+ * matrix instructions, which cut each product to a multiple of 2^-13 of the
+ * largest of its 8 neighbours' products before adding them (2e-6 of the sum of
+ * magnitudes on Gaussian inputs) and add the rest in fp32.
+ * The order of the sums depends on the shape, so a row slice of a call can
+ * differ from the full call in the last bits of the fp32 sums; calls of the
+ * same shape repeat bit for bit.  A NaN or an infinity among a token's inputs
+ * makes that token's outputs NaN (of a POW2 weight too) and no other's.
+ * Shapes as for the INT8 linear: K % 128 == 0, N % 16 == 0 (the last block of
+ * rows may be partial), K <= 65536, Mp * K and N * K < 2^31. */
+
+/* Scale kinds, in convrot_fp8_weights.scales: any F32 values, or powers of two
+ * (and zeros).  A POW2 weight's forward rounds the activations' scales up to
+ * powers of two as well, and both are applied by the matrix instruction. */
+#define CONVROT_FP8_SCALE_F32 0
+#define CONVROT_FP8_SCALE_POW2 1
+#define CONVROT_FP8_MAGIC 0x38465243u /* "CRF8" little-endian */
+#define CONVROT_FP8_VERSION 1u
+
+/* Prepared weights: a host struct holding caller-owned device pointers, like
+ * convrot_weights. */
+typedef struct convrot_fp8_weights {
+    uint32_t magic;            /* CONVROT_FP8_MAGIC once prepared */
+    uint32_t version;          /* CONVROT_FP8_VERSION */
+    int64_t N;                 /* output channels */
+    int64_t K;                 /* input channels */
+    int32_t scales;            /* CONVROT_FP8_SCALE_F32 or _POW2 (set by the caller) */
+    int32_t reserved;          /* 0 */
+    uint8_t *codes;            /* device, K-tiled e4m3 codes of W [N, K] */
+    float *scale;              /* device, [ceil(N / 128), K / 128] row-major */
+} convrot_fp8_weights;
+
+/* Bytes of the codes and of the scales of an [N, K] weight (0 for invalid
+ * shapes), and of the workspaces of the two calls below (0 is a valid answer:
+ * the prepare call needs one only for input-major float weights, the forward
+ * none for M <= 16, where one kernel quantises and multiplies). */
+CONVROT_API size_t convrot_fp8_packed_bytes(int64_t N, int64_t K);
+CONVROT_API size_t convrot_fp8_scale_bytes(int64_t N, int64_t K);
+CONVROT_API size_t convrot_fp8_prepare_workspace_bytes(int64_t N, int64_t K, int w_dtype,
+                                                       int layout);
+CONVROT_API size_t convrot_fp8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N);
+
+/* Prepare a weight: W F32 or BF16 (quantised here, scale and codes as for the
+ * activations with the amax of the 128 x 128 block), or CONVROT_F8E4M3 codes
+ * with src_scale, device F32 [ceil(N / 128), K / 128] row-major (imported
+ * unchanged; with POW2 they must be powers of two or 0, which is not checked
+ * here).  Layout per `layout`, [N, K] or [K, N]; src_scale keeps its order
+ * either way.  out->codes, out->scale: caller allocations; out->scales selects
+ * the kind.  Errors as for convrot_linear_prepare_weights. */
+CONVROT_API int convrot_fp8_prepare_weights(const void *W, int w_dtype, int layout,
+                                            const float *src_scale, int64_t N, int64_t K,
+                                            convrot_fp8_weights *out, void *ws,
+                                            size_t ws_bytes, void *stream);
+
+/* Y [M, N] = the product above for bf16 X [M, K]; bias F32 [N] or NULL,
+ * y_dtype CONVROT_BF16 or CONVROT_F32. */
+CONVROT_API int convrot_fp8_linear_forward(const void *X, int64_t M,
+                                           const convrot_fp8_weights *W, const float *bias,
+                                           void *Y, int y_dtype, void *ws, size_t ws_bytes,
+                                           void *stream);
+
+/* Its two stages, as test hooks: q K-tiled e4m3 codes (Mp x K bytes; padding
+ * rows are left as they were) and s F32 [K / 128, Mp] (k-block major, Mp = M
+ * rounded up to 16; padding columns are left as they were) of bf16 X [M, K];
+ * and the product of such codes and scales with W. */
+CONVROT_API int convrot_fp8_quantize(const void *X, int64_t M, int64_t K, int scales, uint8_t *q,
+                                     float *s, void *stream);
+CONVROT_API int convrot_fp8_gemm_dequant(const uint8_t *q, const float *s, int64_t M,
+                                         const convrot_fp8_weights *W, const float *bias, void *Y,
+                                         int y_dtype, void *stream);
+
+/* ------------------------------------------------------------------ */
+/* norms and rotary positions of queries and keys                      */
+/* ------------------------------------------------------------------ */
+
+/* What stands between the QKV projection and attention: an RMS norm of each
+ * head's query and key and a rotation by the token's position, which has up to
+ * four axes (time, height, width, ...).
+ *   Pair p = 0 .. R/2 - 1 of the rotary_dim R rotated channels turns by
+ *   positions[token, axis[p]] * freq[p] radians: (a, b) -> (a cos - b sin,
+ *   b cos + a sin).  INTERLEAVED: a, b = channels 2p, 2p + 1; HALF: channels p,
+ *   p + R/2.  Channels R .. head_dim - 1 pass unchanged.
+ *   Angles are formed and reduced in fp64, the rest is fp32, rounded once to
+ *   the tensors' type. */
+#define CONVROT_ROPE_INTERLEAVED 0
+#define CONVROT_ROPE_HALF 1
+#define CONVROT_ROPE_MAX_AXES 4
+#define CONVROT_ROPE_MAGIC 0x504f5243u /* "CROP" little-endian */
+#define CONVROT_ROPE_VERSION 1u
+
+typedef struct convrot_rope {
+    uint32_t magic;            /* CONVROT_ROPE_MAGIC once prepared */
+    uint32_t version;          /* CONVROT_ROPE_VERSION */
+    int32_t axes;              /* position axes, 1 .. CONVROT_ROPE_MAX_AXES */
+    int32_t head_dim;          /* D: a multiple of 8, at most 512 */
+    int32_t rotary_dim;        /* R <= D, even (HALF: a multiple of 8) */
+    int32_t pairing;           /* CONVROT_ROPE_INTERLEAVED or CONVROT_ROPE_HALF */
+    double *freq;              /* device, [R / 2] radians per position unit */
+    int32_t *axis;             /* device, [R / 2] axis of each pair */
+} convrot_rope;
+
+/* Fill a plan's tables (out->freq, out->axis: caller allocations of 4 R and
+ * 2 R bytes).  Axis a owns dims[a] / 2 consecutive pairs (dims: host array,
+ * each even and positive; R is their sum).  spectrum 0: each axis runs through
+ * all frequencies, theta^(-2 j / dims[a]) for its pair j; spectrum 1: the pairs
+ * share one, theta^(-2 p / R).  A caller with other frequencies or another
+ * assignment of axes overwrites the tables (an axis outside [0, axes) is read
+ * as the nearest one inside). */
+#define CONVROT_ROPE_SPECTRUM_AXIS 0
+#define CONVROT_ROPE_SPECTRUM_WHOLE 1
+CONVROT_API int convrot_rope_prepare(const int32_t *dims, int axes, int head_dim, double theta,
+                                     int pairing, int spectrum, convrot_rope *out, void *stream);
+
+/* A view of per-head rows: element (batch b, token t, head h, channel d) at
+ * data + b * batch_stride + t * token_stride + h * head_stride + d elements.
+ * data and every stride are multiples of 16 bytes (EALIGN; the stride of an
+ * extent of 1 is not looked at).  An output may be its input (same data and
+ * strides); it may not overlap one otherwise, nor itself. */
+typedef struct convrot_heads {
+    void *data;
+    int32_t heads;
+    int32_t reserved;          /* 0 */
+    int64_t batch_stride, token_stride, head_stride;
+} convrot_heads;
+
+/* Positions of the tokens: device, [B, T, axes] with batches pos_batch_stride
+ * elements apart (0: one [T, axes] array for every batch), pos_dtype
+ * CONVROT_I32 or CONVROT_F32 (fractional positions). */
+
+/* q_out = R q and k_out = R k; k and k_out may both be NULL.  dtype (of q, k
+ * and their outputs): CONVROT_BF16 or CONVROT_F32.  CONVROT_ROPE_INVERSE turns
+ * by the negative angles: the backward pass, on the outputs' gradients. */
+#define CONVROT_ROPE_INVERSE 1u
+CONVROT_API int convrot_rope_forward(int64_t B, int64_t T, int dtype, const convrot_heads *q,
+                                     const convrot_heads *q_out, const convrot_heads *k,
+                                     const convrot_heads *k_out, const convrot_rope *rope,
+                                     const void *positions, int pos_dtype,
+                                     int64_t pos_batch_stride, uint32_t flags, void *stream);
+
+/* q_out = R (q * rsqrt(mean(q^2) + eps) * w_q), k_out likewise with w_k: the
+ * norm over a head's head_dim channels, w_q and w_k F32 [head_dim], shared by
+ * the heads, or NULL (ones).  eps > 0, finite. */
+CONVROT_API int convrot_qk_norm_rope_forward(int64_t B, int64_t T, int dtype,
+                                             const convrot_heads *q, const convrot_heads *q_out,
+                                             const float *w_q, const convrot_heads *k,
+                                             const convrot_heads *k_out, const float *w_k,
+                                             float eps, const convrot_rope *rope,
+                                             const void *positions, int pos_dtype,
+                                             int64_t pos_batch_stride, void *stream);
+
+/* Its backward pass.  g_q, g_k: the gradients of the outputs; q, k: the
+ * forward's inputs; dq, dk: the gradients of q and k (each may be its g or its
+ * input in place); dw_q, dw_k: F32 [head_dim], sums over every batch, token and
+ * head, written (not added to), in an order that does not change from call to
+ * call.  k's five arguments may all be NULL.  ws: device workspace of
+ * convrot_qk_norm_rope_workspace_bytes(B, T, heads of q, heads of k, D) bytes
+ * (the partial sums of dw). */
+CONVROT_API size_t convrot_qk_norm_rope_workspace_bytes(int64_t B, int64_t T, int heads_q,
+                                                        int heads_k, int head_dim);
+CONVROT_API int convrot_qk_norm_rope_backward(
+    int64_t B, int64_t T, int dtype, const convrot_heads *g_q, const convrot_heads *q,
+    const convrot_heads *dq, const float *w_q, float *dw_q, const convrot_heads *g_k,
+    const convrot_heads *k, const convrot_heads *dk, const float *w_k, float *dw_k, float eps,
+    const convrot_rope *rope, const void *positions, int pos_dtype, int64_t pos_batch_stride,
+    void *ws, size_t ws_bytes, void *stream);
+
+/* The QKV projection of an attention layer: Y [B T, N] = linear(X; W) + bias
+ * with N = (heads_q + 2 heads_kv) head_dim columns, queries, keys, then values,
+ * and then the norms and the rotation above in place on the query and key
+ * columns (of the outputs as rounded to y_dtype).  ws as for
+ * convrot_linear_forward or convrot_fp8_linear_forward with M = B T.  ELAYOUT
+ * if W->N does not fit the heads. */
+CONVROT_API int convrot_qkv_forward(const void *X, int64_t B, int64_t T, const convrot_weights *W,
+                                    const float *bias, int heads_q, int heads_kv,
+                                    const float *w_q, const float *w_k, float eps,
+                                    const convrot_rope *rope, const void *positions,
+                                    int pos_dtype, int64_t pos_batch_stride, void *Y, int y_dtype,
+                                    void *ws, size_t ws_bytes, void *stream);
+CONVROT_API int convrot_fp8_qkv_forward(const void *X, int64_t B, int64_t T,
+                                        const convrot_fp8_weights *W, const float *bias,
+                                        int heads_q, int heads_kv, const float *w_q,
+                                        const float *w_k, float eps, const convrot_rope *rope,
+                                        const void *positions, int pos_dtype,
+                                        int64_t pos_batch_stride, void *Y, int y_dtype, void *ws,
+                                        size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------ */
 /* comparison variant (not the W8A8 path)                              */

@@ -16,7 +16,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libconvrot.so")
 
 OK, EINVAL, EALIGN, EWORKSPACE, ELAYOUT, EUNSUPPORTED, EHIP = 0, -1, -2, -3, -4, -5, -6
-F32, BF16, I8, I32 = 0, 1, 2, 3
+F32, BF16, I8, I32, F8E4M3 = 0, 1, 2, 3, 4
 OUT_MAJOR, IN_MAJOR = 0, 1
 WEIGHTS_MAGIC = 0x38545243
 WEIGHTS_VERSION = 2
@@ -25,6 +25,13 @@ ROTATIONS = {"sylvester": 0, "regular": ROT_REGULAR}
 FLAG_GELU = 1
 FLAG_SWIGLU = 2
 SWIGLU_PAIRS = 0x200         # weight flag: interleaved SwiGLU gate/up rows
+FP8_MAGIC, FP8_VERSION = 0x38465243, 1
+FP8_SCALES = {"f32": 0, "pow2": 1}
+ROPE_MAGIC, ROPE_VERSION = 0x504F5243, 1
+ROPE_PAIRINGS = {"interleaved": 0, "half": 1}
+ROPE_SPECTRA = {"axis": 0, "whole": 1}
+ROPE_MAX_AXES = 4
+ROPE_INVERSE = 1
 
 _c_i64 = ctypes.c_int64
 _c_int = ctypes.c_int
@@ -46,6 +53,48 @@ class convrot_weights(ctypes.Structure):
 
 
 _W = ctypes.POINTER(convrot_weights)
+
+
+class convrot_fp8_weights(ctypes.Structure):
+    _fields_ = [
+        ("magic", ctypes.c_uint32),
+        ("version", ctypes.c_uint32),
+        ("N", ctypes.c_int64),
+        ("K", ctypes.c_int64),
+        ("scales", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("codes", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+    ]
+
+
+class convrot_rope(ctypes.Structure):
+    _fields_ = [
+        ("magic", ctypes.c_uint32),
+        ("version", ctypes.c_uint32),
+        ("axes", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32),
+        ("pairing", ctypes.c_int32),
+        ("freq", ctypes.c_void_p),
+        ("axis", ctypes.c_void_p),
+    ]
+
+
+class convrot_heads(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("heads", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("batch_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+    ]
+
+
+_FW = ctypes.POINTER(convrot_fp8_weights)
+_RP = ctypes.POINTER(convrot_rope)
+_H = ctypes.POINTER(convrot_heads)
 
 _SIGNATURES = {
     "convrot_status_string": (ctypes.c_char_p, [_c_int]),
@@ -90,6 +139,36 @@ _SIGNATURES = {
         _c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_p, _c_p, _c_p,
                  ctypes.c_size_t, _c_p]),
     "convrot_gelu_bf16": (_c_int, [_c_p, _c_i64, _c_p, _c_p]),
+    "convrot_fp8_packed_bytes": (_c_sz, [_c_i64, _c_i64]),
+    "convrot_fp8_scale_bytes": (_c_sz, [_c_i64, _c_i64]),
+    "convrot_fp8_prepare_workspace_bytes": (_c_sz, [_c_i64, _c_i64, _c_int, _c_int]),
+    "convrot_fp8_linear_workspace_bytes": (_c_sz, [_c_i64, _c_i64, _c_i64]),
+    "convrot_fp8_prepare_weights": (
+        _c_int, [_c_p, _c_int, _c_int, _c_p, _c_i64, _c_i64, _FW, _c_p, _c_sz, _c_p]),
+    "convrot_fp8_linear_forward": (
+        _c_int, [_c_p, _c_i64, _FW, _c_p, _c_p, _c_int, _c_p, _c_sz, _c_p]),
+    "convrot_fp8_quantize": (_c_int, [_c_p, _c_i64, _c_i64, _c_int, _c_p, _c_p, _c_p]),
+    "convrot_fp8_gemm_dequant": (
+        _c_int, [_c_p, _c_p, _c_i64, _FW, _c_p, _c_p, _c_int, _c_p]),
+    "convrot_rope_prepare": (
+        _c_int, [ctypes.POINTER(ctypes.c_int32), _c_int, _c_int, ctypes.c_double, _c_int, _c_int,
+                 _RP, _c_p]),
+    "convrot_rope_forward": (
+        _c_int, [_c_i64, _c_i64, _c_int, _H, _H, _H, _H, _RP, _c_p, _c_int, _c_i64,
+                 ctypes.c_uint32, _c_p]),
+    "convrot_qk_norm_rope_forward": (
+        _c_int, [_c_i64, _c_i64, _c_int, _H, _H, _c_p, _H, _H, _c_p, ctypes.c_float, _RP, _c_p,
+                 _c_int, _c_i64, _c_p]),
+    "convrot_qk_norm_rope_workspace_bytes": (_c_sz, [_c_i64, _c_i64, _c_int, _c_int, _c_int]),
+    "convrot_qk_norm_rope_backward": (
+        _c_int, [_c_i64, _c_i64, _c_int, _H, _H, _H, _c_p, _c_p, _H, _H, _H, _c_p, _c_p,
+                 ctypes.c_float, _RP, _c_p, _c_int, _c_i64, _c_p, _c_sz, _c_p]),
+    "convrot_qkv_forward": (
+        _c_int, [_c_p, _c_i64, _c_i64, _W, _c_p, _c_int, _c_int, _c_p, _c_p, ctypes.c_float, _RP,
+                 _c_p, _c_int, _c_i64, _c_p, _c_int, _c_p, _c_sz, _c_p]),
+    "convrot_fp8_qkv_forward": (
+        _c_int, [_c_p, _c_i64, _c_i64, _FW, _c_p, _c_int, _c_int, _c_p, _c_p, ctypes.c_float, _RP,
+                 _c_p, _c_int, _c_i64, _c_p, _c_int, _c_p, _c_sz, _c_p]),
     "convrot_probe_mfma_i8": (_c_int, [_c_i64, _c_p, _c_p, ctypes.POINTER(ctypes.c_int64),
                                        _c_p]),
     "convrot_probe_stream": (_c_int, [_c_p, _c_p, _c_i64, _c_int, _c_p]),
@@ -143,8 +222,30 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _launch(device, fn: str, stream, *args, scratch=()):
+    """Call the library with `device` current, on `stream` (default: that
+    device's current stream).  scratch: tensors allocated here for the call; on
+    a caller's stream the allocator must not hand them out again before that
+    stream has passed the call."""
+    if stream is None:
+        s = torch.cuda.current_stream(device)
+    else:
+        s = stream
+        for t in scratch:
+            if t is not None:
+                t.record_stream(stream)
+    fun = getattr(library(), fn)
+    if device.index == torch.cuda.current_device():
+        rc = fun(*args, ctypes.c_void_p(s.cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            rc = fun(*args, ctypes.c_void_p(s.cuda_stream))
+    _check(fn, rc)
+
+
 def _dtype_tag(dt: torch.dtype) -> int:
-    return {torch.float32: F32, torch.bfloat16: BF16, torch.int8: I8, torch.int32: I32}[dt]
+    return {torch.float32: F32, torch.bfloat16: BF16, torch.int8: I8, torch.int32: I32,
+            torch.float8_e4m3fn: F8E4M3}[dt]
 
 
 def _torch_dtype(tag: int) -> torch.dtype:
@@ -585,6 +686,343 @@ def lowrank_bf16_forward(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, bias
     return out
 
 
+# --------------------------------------------- FP8 block-scaled linear ----
+
+class FP8Weights:
+    """A prepared FP8 weight: the C descriptor plus the tensors it points into."""
+
+    def __init__(self, desc: convrot_fp8_weights, codes: torch.Tensor, scale: torch.Tensor):
+        self.desc = desc
+        self.codes = codes
+        self.scale = scale
+
+    @property
+    def N(self):
+        return self.desc.N
+
+    @property
+    def K(self):
+        return self.desc.K
+
+    def ref(self):
+        return ctypes.byref(self.desc)
+
+
+def _fp8_weights(W, name: str):
+    if not isinstance(W, FP8Weights):
+        raise ValueError(f"{name} must be FP8Weights from convrot_fp8_prepare_weights")
+    return W.codes.device
+
+
+def convrot_fp8_packed_bytes(N: int, K: int) -> int:
+    return library().convrot_fp8_packed_bytes(N, K)
+
+
+def convrot_fp8_linear_workspace_bytes(M: int, K: int, N: int) -> int:
+    return library().convrot_fp8_linear_workspace_bytes(M, K, N)
+
+
+def convrot_fp8_prepare_weights(W: torch.Tensor, layout: int = OUT_MAJOR,
+                                src_scale: torch.Tensor | None = None, scales: str = "f32",
+                                stream=None) -> FP8Weights:
+    """Quantise and pack a weight (``[N, K]`` or ``[K, N]`` per layout) to e4m3
+    with one scale per 128 x 128 block, float32 or (scales='pow2') a power of
+    two; or import float8_e4m3fn codes with src_scale [ceil(N/128), K/128]."""
+    lib = library()
+    if not isinstance(W, torch.Tensor) or W.dim() != 2:
+        raise ValueError("W must be a 2-D tensor")
+    if layout not in (OUT_MAJOR, IN_MAJOR):
+        raise ValueError("layout must be OUT_MAJOR or IN_MAJOR")
+    N, K = W.shape if layout == OUT_MAJOR else W.shape[::-1]
+    if W.dtype not in (torch.float32, torch.bfloat16, torch.float8_e4m3fn):
+        raise ValueError(f"W must be float32, bfloat16 or float8_e4m3fn codes, got {W.dtype}")
+    if (W.dtype == torch.float8_e4m3fn) != (src_scale is not None):
+        raise ValueError("src_scale is required for float8_e4m3fn codes and only for them")
+    _opt(src_scale, "src_scale", torch.float32, (-(-N // 128), K // 128))
+    if scales not in FP8_SCALES:
+        raise ValueError(f"scales must be one of {sorted(FP8_SCALES)}")
+    W = W.contiguous()
+    _on_device(W.device, W=W, src_scale=src_scale)
+    if src_scale is not None and scales == "pow2":
+        # load time: the one check that reads the tensor's values
+        bits = src_scale.view(torch.int32)
+        if bool((((bits & 0x7FFFFF) != 0) | (bits < 0)).any()):
+            raise ValueError("src_scale of a pow2 weight must hold powers of two or zeros")
+    nbytes = lib.convrot_fp8_packed_bytes(N, K)
+    if nbytes == 0:
+        raise ConvRotError("convrot_fp8_prepare_weights", EUNSUPPORTED)
+    tag = _dtype_tag(W.dtype)
+    codes = torch.empty(nbytes, dtype=torch.uint8, device=W.device)
+    scale = torch.empty((-(-N // 128), K // 128), dtype=torch.float32, device=W.device)
+    desc = convrot_fp8_weights()
+    desc.codes, desc.scale, desc.scales = codes.data_ptr(), scale.data_ptr(), FP8_SCALES[scales]
+    wsb = lib.convrot_fp8_prepare_workspace_bytes(N, K, tag, layout)
+    ws = _workspace(wsb, W.device, None)
+    _launch(W.device, "convrot_fp8_prepare_weights", stream, _ptr(W), tag, layout,
+            _ptr(src_scale), N, K, ctypes.byref(desc), _ptr(ws), wsb, scratch=(codes, scale, ws))
+    fw = FP8Weights(desc, codes, scale)
+    fw._ws = ws  # keep alive until the stream has consumed it
+    return fw
+
+
+def convrot_fp8_linear_forward(X: torch.Tensor, W: FP8Weights, bias=None,
+                               out_dtype: torch.dtype = torch.bfloat16, out=None,
+                               workspace=None, stream=None) -> torch.Tensor:
+    """Y [M, N] = X . W^T (+ bias) with X quantised to e4m3 per 128 inputs."""
+    lib = library()
+    dev = _fp8_weights(W, "W")
+    M = _rows(X, "X", W.K)
+    _opt(bias, "bias", torch.float32, (W.N,))
+    _output(out, M, W.N, (torch.bfloat16, torch.float32))
+    wsb = lib.convrot_fp8_linear_workspace_bytes(M, W.K, W.N)
+    _check_workspace(wsb, workspace)
+    _on_device(dev, X=X, bias=bias, out=out, workspace=workspace)
+    if out is None:
+        out = torch.empty((M, W.N), dtype=out_dtype, device=dev)
+    ws = _workspace(wsb, dev, workspace)
+    _launch(dev, "convrot_fp8_linear_forward", stream, _ptr(X), M, W.ref(), _ptr(bias),
+            _ptr(out), _dtype_tag(out.dtype), _ptr(ws), ws.numel() if ws is not None else 0,
+            scratch=(out, ws))
+    return out
+
+
+# ----------------------------------- norms and rotary positions of Q and K ----
+
+class RopePlan:
+    """A rotary plan: the C descriptor plus its tables.  freq (float64, radians
+    per position unit) and axis (int32), one entry per pair, may be overwritten
+    by a caller with other frequencies or another assignment of axes."""
+
+    def __init__(self, desc: convrot_rope, freq: torch.Tensor, axis: torch.Tensor):
+        self.desc = desc
+        self.freq = freq
+        self.axis = axis
+
+    @property
+    def axes(self):
+        return self.desc.axes
+
+    @property
+    def head_dim(self):
+        return self.desc.head_dim
+
+    def ref(self):
+        return ctypes.byref(self.desc)
+
+
+def convrot_rope_prepare(dims, head_dim: int, theta: float = 10000.0,
+                         pairing: str = "interleaved", spectrum: str = "axis", device="cuda",
+                         stream=None) -> RopePlan:
+    """A plan whose axis a turns dims[a] channels of every head (1 to 4 axes,
+    each even; together at most head_dim): pairs 'interleaved' (2p, 2p + 1) or
+    'half' (p, p + R/2), every axis running through all frequencies
+    (spectrum='axis') or the pairs sharing one spectrum ('whole')."""
+    dims = [int(d) for d in dims]
+    if not 1 <= len(dims) <= ROPE_MAX_AXES or any(d <= 0 or d % 2 for d in dims):
+        raise ValueError(f"dims must be 1 to {ROPE_MAX_AXES} positive even numbers, got {dims}")
+    if sum(dims) > head_dim:
+        raise ValueError(f"dims {dims} exceed head_dim {head_dim}")
+    if pairing not in ROPE_PAIRINGS:
+        raise ValueError(f"pairing must be one of {sorted(ROPE_PAIRINGS)}")
+    if spectrum not in ROPE_SPECTRA:
+        raise ValueError(f"spectrum must be one of {sorted(ROPE_SPECTRA)}")
+    device = torch.device(device)
+    if device.type != "cuda":
+        raise ValueError(f"device must be a GPU, got {device}")
+    half = sum(dims) // 2
+    freq = torch.empty(half, dtype=torch.float64, device=device)
+    axis = torch.empty(half, dtype=torch.int32, device=device)
+    desc = convrot_rope()
+    desc.freq, desc.axis = freq.data_ptr(), axis.data_ptr()
+    _launch(freq.device, "convrot_rope_prepare", stream, (ctypes.c_int32 * len(dims))(*dims),
+            len(dims), head_dim, theta, ROPE_PAIRINGS[pairing], ROPE_SPECTRA[spectrum],
+            ctypes.byref(desc), scratch=(freq, axis))
+    return RopePlan(desc, freq, axis)
+
+
+def _heads(t, name: str, dtype, B: int, T: int, H: int, D: int):
+    """A [B, T, H, D] (or, with B == 1, [T, H, D]) tensor of per-head rows; any
+    strides with contiguous channels."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise ValueError(f"{name} must be a {dtype} tensor")
+    shape = (B, T, H, D)
+    if tuple(t.shape) not in ((shape, shape[1:]) if B == 1 else (shape,)):
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name} must have contiguous channels")
+    return t
+
+
+def _view(t):
+    """The C view of a checked heads tensor (None passes)."""
+    if t is None:
+        return None
+    st = t.stride()
+    return ctypes.byref(convrot_heads(t.data_ptr(), t.shape[-2], 0,
+                                      st[0] if t.dim() == 4 else 0, st[-3], st[-2]))
+
+
+def _heads_pair(q, k, rope, positions):
+    """The checks shared by the rope and norm calls: (B, T, position stride)."""
+    if not isinstance(rope, RopePlan):
+        raise ValueError("rope must be a RopePlan from convrot_rope_prepare")
+    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
+        raise ValueError("q must be a tensor [B, T, heads, D] or [T, heads, D]")
+    if q.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"q must be float32 or bfloat16, got {q.dtype}")
+    B, T = (q.shape[0], q.shape[1]) if q.dim() == 4 else (1, q.shape[0])
+    D = rope.head_dim
+    _heads(q, "q", q.dtype, B, T, q.shape[-2], D)
+    if k is not None:
+        if not isinstance(k, torch.Tensor) or k.dim() != q.dim():
+            raise ValueError("k must have as many dimensions as q")
+        _heads(k, "k", q.dtype, B, T, k.shape[-2], D)
+    return (B, T, _positions(positions, B, T, rope.axes))
+
+
+def _positions(positions, B, T, axes):
+    if not isinstance(positions, torch.Tensor) \
+            or positions.dtype not in (torch.int32, torch.float32):
+        raise ValueError("positions must be an int32 or float32 tensor")
+    shape = tuple(positions.shape)
+    if axes == 1 and shape in ((T,), (B, T)):
+        shape += (1,)
+    if shape not in ((T, axes), (B, T, axes)):
+        raise ValueError(f"positions must have shape {(T, axes)} or {(B, T, axes)}, got "
+                         f"{tuple(positions.shape)}")
+    if not positions.is_contiguous():
+        raise ValueError("positions must be contiguous")
+    return T * axes if len(shape) == 3 else 0
+
+
+def _heads_out(out, name, like):
+    """A caller's output, checked, or a new contiguous one."""
+    if like is None:
+        if out is not None:
+            raise ValueError(f"{name} given without its input")
+        return None
+    if out is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    if out.dim() != like.dim():
+        raise ValueError(f"{name} must have as many dimensions as its input")
+    B, T = (like.shape[0], like.shape[1]) if like.dim() == 4 else (1, like.shape[0])
+    return _heads(out, name, like.dtype, B, T, like.shape[-2], like.shape[-1])
+
+
+def convrot_rope_forward(q: torch.Tensor, k, rope: RopePlan, positions: torch.Tensor,
+                         inverse: bool = False, out_q=None, out_k=None, stream=None):
+    """(q_out, k_out): q and k [B, T, heads, D] turned by the tokens' positions
+    [T, axes] or [B, T, axes] (int32 or float32); k may be None.  Out of place
+    unless out_q is q.  inverse: by the negative angles, the backward pass."""
+    B, T, psb = _heads_pair(q, k, rope, positions)
+    _on_device(rope.freq.device, q=q, k=k, positions=positions, out_q=out_q, out_k=out_k)
+    out_q, out_k = _heads_out(out_q, "out_q", q), _heads_out(out_k, "out_k", k)
+    _launch(q.device, "convrot_rope_forward", stream, B, T, _dtype_tag(q.dtype), _view(q),
+            _view(out_q), _view(k), _view(out_k), rope.ref(), _ptr(positions),
+            _dtype_tag(positions.dtype), psb, ROPE_INVERSE if inverse else 0,
+            scratch=(out_q, out_k))
+    return out_q, out_k
+
+
+def convrot_qk_norm_rope_forward(q: torch.Tensor, k, w_q, w_k, rope: RopePlan,
+                                 positions: torch.Tensor, eps: float = 1e-6, out_q=None,
+                                 out_k=None, stream=None):
+    """convrot_rope_forward of q * rsqrt(mean(q^2) + eps) * w_q over each head's
+    channels and of k likewise; w_q, w_k float32 [D] or None."""
+    B, T, psb = _heads_pair(q, k, rope, positions)
+    _opt(w_q, "w_q", torch.float32, (rope.head_dim,))
+    _opt(w_k, "w_k", torch.float32, (rope.head_dim,))
+    _on_device(rope.freq.device, q=q, k=k, w_q=w_q, w_k=w_k, positions=positions, out_q=out_q,
+               out_k=out_k)
+    out_q, out_k = _heads_out(out_q, "out_q", q), _heads_out(out_k, "out_k", k)
+    _launch(q.device, "convrot_qk_norm_rope_forward", stream, B, T, _dtype_tag(q.dtype),
+            _view(q), _view(out_q), _ptr(w_q), _view(k), _view(out_k), _ptr(w_k), eps, rope.ref(),
+            _ptr(positions), _dtype_tag(positions.dtype), psb, scratch=(out_q, out_k))
+    return out_q, out_k
+
+
+def convrot_qk_norm_rope_workspace_bytes(B, T, heads_q, heads_k, head_dim) -> int:
+    return library().convrot_qk_norm_rope_workspace_bytes(B, T, heads_q, heads_k, head_dim)
+
+
+def convrot_qk_norm_rope_backward(g_q: torch.Tensor, g_k, q: torch.Tensor, k, w_q, w_k,
+                                  rope: RopePlan, positions: torch.Tensor, eps: float = 1e-6,
+                                  dq=None, dk=None, dw_q=None, dw_k=None, workspace=None,
+                                  stream=None):
+    """(dq, dk, dw_q, dw_k) of convrot_qk_norm_rope_forward(q, k, ...) from the
+    gradients g_q and g_k of its outputs."""
+    lib = library()
+    B, T, psb = _heads_pair(q, k, rope, positions)
+    D = rope.head_dim
+    for g, x, n in ((g_q, q, "g_q"), (g_k, k, "g_k")):
+        if (g is None) != (x is None):
+            raise ValueError(f"{n} must be given with its input and only then")
+        if g is not None:
+            if not isinstance(g, torch.Tensor) or g.dim() != x.dim():
+                raise ValueError(f"{n} must have as many dimensions as its input")
+            _heads(g, n, x.dtype, B, T, x.shape[-2], D)
+    if k is None and dw_k is not None:
+        raise ValueError("dw_k given without k")
+    for t, n in ((w_q, "w_q"), (w_k, "w_k"), (dw_q, "dw_q"), (dw_k, "dw_k")):
+        _opt(t, n, torch.float32, (D,))
+    wsb = lib.convrot_qk_norm_rope_workspace_bytes(B, T, q.shape[-2],
+                                                   0 if k is None else k.shape[-2], D)
+    _check_workspace(wsb, workspace)
+    dev = rope.freq.device
+    _on_device(dev, g_q=g_q, g_k=g_k, q=q, k=k, w_q=w_q, w_k=w_k, positions=positions, dq=dq,
+               dk=dk, dw_q=dw_q, dw_k=dw_k, workspace=workspace)
+    dq, dk = _heads_out(dq, "dq", q), _heads_out(dk, "dk", k)
+    if dw_q is None:
+        dw_q = torch.empty(D, dtype=torch.float32, device=dev)
+    if dw_k is None and k is not None:
+        dw_k = torch.empty(D, dtype=torch.float32, device=dev)
+    ws = _workspace(wsb, dev, workspace)
+    _launch(dev, "convrot_qk_norm_rope_backward", stream, B, T, _dtype_tag(q.dtype), _view(g_q),
+            _view(q), _view(dq), _ptr(w_q), _ptr(dw_q), _view(g_k), _view(k), _view(dk),
+            _ptr(w_k), _ptr(dw_k), eps, rope.ref(), _ptr(positions),
+            _dtype_tag(positions.dtype), psb, _ptr(ws), ws.numel() if ws is not None else 0,
+            scratch=(dq, dk, dw_q, dw_k, ws))
+    return dq, dk, dw_q, dw_k
+
+
+def convrot_qkv_forward(X: torch.Tensor, W, heads_q: int, heads_kv: int, w_q, w_k,
+                        rope: RopePlan, positions: torch.Tensor, bias=None, eps: float = 1e-6,
+                        out_dtype: torch.dtype = torch.bfloat16, out=None, workspace=None,
+                        stream=None) -> torch.Tensor:
+    """The QKV projection of X [M, K] or [B, T, K] with the norms and rotation
+    of its queries and keys: [.., (heads_q + 2 heads_kv) D], queries, keys, then
+    values.  W: PreparedWeights or FP8Weights."""
+    lib = library()
+    fp8 = isinstance(W, FP8Weights)
+    dev = _fp8_weights(W, "W") if fp8 else _weights(W, "W")
+    if not isinstance(rope, RopePlan):
+        raise ValueError("rope must be a RopePlan from convrot_rope_prepare")
+    if not isinstance(X, torch.Tensor) or X.dim() not in (2, 3):
+        raise ValueError(f"X must be a tensor [M, {W.K}] or [B, T, {W.K}]")
+    _need(X, "X", torch.bfloat16, (*X.shape[:-1], W.K))
+    B, T = (X.shape[0], X.shape[1]) if X.dim() == 3 else (1, X.shape[0])
+    psb = _positions(positions, B, T, rope.axes)
+    _opt(bias, "bias", torch.float32, (W.N,))
+    _opt(w_q, "w_q", torch.float32, (rope.head_dim,))
+    _opt(w_k, "w_k", torch.float32, (rope.head_dim,))
+    _opt(out, "out", (torch.bfloat16, torch.float32), (*X.shape[:-1], W.N))
+    M = B * T
+    wsb = (lib.convrot_fp8_linear_workspace_bytes(M, W.K, W.N) if fp8 else
+           lib.convrot_linear_workspace_bytes(M, W.K, W.N, W.block))
+    _check_workspace(wsb, workspace)
+    _on_device(dev, X=X, bias=bias, w_q=w_q, w_k=w_k, freq=rope.freq, positions=positions,
+               out=out, workspace=workspace)
+    if out is None:
+        out = torch.empty((*X.shape[:-1], W.N), dtype=out_dtype, device=dev)
+    ws = _workspace(wsb, dev, workspace)
+    name = "convrot_fp8_qkv_forward" if fp8 else "convrot_qkv_forward"
+    _launch(dev, name, stream, _ptr(X), B, T, W.ref(), _ptr(bias), heads_q, heads_kv, _ptr(w_q),
+            _ptr(w_k), eps, rope.ref(), _ptr(positions), _dtype_tag(positions.dtype), psb,
+            _ptr(out), _dtype_tag(out.dtype), _ptr(ws), ws.numel() if ws is not None else 0,
+            scratch=(out, ws))
+    return out
+
+
 # ------------------------------------------------------------- hooks ----
 
 def padded_rows(M: int) -> int:
@@ -706,6 +1144,44 @@ def convrot_gelu_bf16(u: torch.Tensor, out=None, stream=None) -> torch.Tensor:
         out = torch.empty_like(u)
     _check("convrot_gelu_bf16", lib.convrot_gelu_bf16(_ptr(u), u.numel(), _ptr(out),
                                                       _stream(stream)))
+    return out
+
+
+def convrot_fp8_quantize(X: torch.Tensor, scales: str = "f32", q=None, s=None, stream=None):
+    """(q, s): the K-tiled e4m3 codes (Mp, K) uint8 of the bf16 rows X and their
+    scales [K/128, Mp] float32."""
+    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+        raise ValueError("X must be a 2-D tensor [M, K]")
+    M, K = X.shape
+    _need(X, "X", torch.bfloat16, (M, K))
+    if scales not in FP8_SCALES:
+        raise ValueError(f"scales must be one of {sorted(FP8_SCALES)}")
+    Mp = padded_rows(M)
+    _opt(q, "q", torch.uint8, (Mp, K))
+    _opt(s, "s", torch.float32, (K // 128, Mp))
+    _on_device(X.device, X=X, q=q, s=s)
+    if q is None:
+        q = torch.empty((Mp, K), dtype=torch.uint8, device=X.device)
+    if s is None:
+        s = torch.empty((K // 128, Mp), dtype=torch.float32, device=X.device)
+    _launch(X.device, "convrot_fp8_quantize", stream, _ptr(X), M, K, FP8_SCALES[scales], _ptr(q),
+            _ptr(s), scratch=(q, s))
+    return q, s
+
+
+def convrot_fp8_gemm_dequant(q: torch.Tensor, s: torch.Tensor, M: int, W: FP8Weights, bias=None,
+                             out_dtype: torch.dtype = torch.bfloat16, out=None, stream=None):
+    """Y [M, N] from the codes and scales of M rows (convrot_fp8_quantize)."""
+    dev = _fp8_weights(W, "W")
+    _need(q, "q", torch.uint8, (padded_rows(M), W.K))
+    _need(s, "s", torch.float32, (W.K // 128, padded_rows(M)))
+    _opt(bias, "bias", torch.float32, (W.N,))
+    _output(out, M, W.N, (torch.bfloat16, torch.float32))
+    _on_device(dev, q=q, s=s, bias=bias, out=out)
+    if out is None:
+        out = torch.empty((M, W.N), dtype=out_dtype, device=dev)
+    _launch(dev, "convrot_fp8_gemm_dequant", stream, _ptr(q), _ptr(s), M, W.ref(), _ptr(bias),
+            _ptr(out), _dtype_tag(out.dtype), scratch=(out,))
     return out
 
 

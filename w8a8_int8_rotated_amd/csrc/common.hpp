@@ -27,6 +27,16 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
     return f32_to_bf16_bits(lo) | (f32_to_bf16_bits(hi) << 16);
 }
 
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// Two fp32 -> packed bf16 with v_cvt_pk_bf16_f32 (round to nearest even).
+__device__ __forceinline__ uint32_t cvt_pk_bf16(float lo, float hi)
+{
+    const bf16x2 p = __builtin_convertvector((f32x2){lo, hi}, bf16x2);
+    return __builtin_bit_cast(uint32_t, p);
+}
+
 } // namespace convrot
 
 // ------------------------------------------------------ kernel launchers ----
@@ -143,6 +153,59 @@ hipError_t launch_gemm_i8(const int8_t *qx, const int8_t *qw, const float *sx,
 // K * elem_bytes % 4 == 0.
 hipError_t launch_swiglu_interleave(const void *src, void *dst, int64_t F, int64_t K,
                                     int elem_bytes, hipStream_t stream);
+
+// ---------------------------------------------- FP8 block-scaled linear ----
+// e4m3 codes, K-tiled like the INT8 ones; activation scales fp32
+// [K/128][padded_rows(M)], weight scales fp32 [ceil(N/128)][K/128].
+// launch_fp8_block_weights quantises output-major float weights per 128 x 128
+// block; launch_fp8_quantize bf16 rows per 128 inputs.  pow2: scales rounded up
+// to powers of two.
+hipError_t launch_fp8_block_weights(const void *W, InType in, int64_t N, int64_t K, bool pow2,
+                                    uint8_t *codes, float *scale, hipStream_t stream);
+hipError_t launch_fp8_quantize(const void *X, int64_t M, int64_t K, bool pow2, uint8_t *q,
+                               float *s, hipStream_t stream);
+// Rows that need no quantise pass: launch_fp8_skinny reads bf16 X itself.
+bool fp8_fuses_quantize(int64_t M);
+hipError_t launch_fp8_skinny(const void *X, int64_t M, const uint8_t *qw, const float *sw,
+                             bool pow2, const float *bias, void *Y, bool f32_out, int64_t N,
+                             int64_t K, hipStream_t stream);
+hipError_t launch_fp8_gemm(const uint8_t *qx, const float *sx, const uint8_t *qw,
+                           const float *sw, bool pow2, const float *bias, void *Y, bool f32_out,
+                           int64_t M, int64_t N, int64_t K, hipStream_t stream);
+
+// ------------------------------------------ norms and rotary positions ----
+// Per-head rows: element (b, t, h, d) at p + b sb + t st + h sh + d.
+struct HeadRows {
+    void *p;
+    int64_t sb, st, sh;
+};
+
+// One launch over the queries (side 0) and keys (side 1, heads[1] may be 0).
+struct NormRope {
+    HeadRows x[2], out[2], g[2];   // inputs, outputs, (backward) output gradients
+    const float *w[2];             // norm weights [D] or null
+    float *dw[2];                  // (backward) [D]
+    int heads[2];
+    int B, T, D, R;
+    float eps;
+    const double *freq;            // [R/2] radians per position unit
+    const int32_t *axis;           // [R/2]
+    const void *pos;               // [B][T][axes], batches pos_sb elements apart
+    int64_t pos_sb;
+    int axes;
+    bool pos_f32, half, inverse, f32;
+    float *partial;                // (backward) workspace of norm_rope_partial_rows rows
+};
+enum class NormRopeMode { ROPE = 0, NORM = 1, BACKWARD = 2 };
+hipError_t launch_norm_rope(NormRopeMode mode, const NormRope &a, hipStream_t stream);
+// Rows of 2 D floats of partial weight gradients a backward launch writes.
+int64_t norm_rope_partial_rows(int64_t tokens);
+// freq and axis of a plan: axis a owns dims[a] / 2 pairs (by value: up to 4).
+struct RopeDims {
+    int d[4];
+};
+hipError_t launch_rope_tables(RopeDims dims, int axes, double theta, bool whole, double *freq,
+                              int32_t *axis, hipStream_t stream);
 
 // Measurement probes (probes.hip): INT8 MFMA rounds on changing operands, one
 // workgroup per CU (probe_mfma_i8_ops: the INT8 operations of one launch),

@@ -181,7 +181,7 @@ const char *convrot_status_string(int status)
 
 int convrot_last_hip_error(void) { return g_last_hip_error; }
 
-int convrot_version(void) { return 100; }
+int convrot_version(void) { return 200; }
 
 size_t convrot_weights_packed_bytes(int64_t N, int64_t K, int block)
 {
@@ -612,6 +612,504 @@ int convrot_linear_forward_noalloc(const void *X, int64_t M, const convrot_weigh
         rc = linear_forward_impl(X, M, W, bias, Y, y_dtype, ws, CONVROT_NOALLOC_SCRATCH_BYTES,
                                  stream);
     log_call("convrot_linear_forward_noalloc", M, W ? W->N : 0, W ? W->K : 0, rc);
+    return rc;
+}
+
+// ---------------------------------------------------------------------------
+// FP8 block-scaled linear.
+// ---------------------------------------------------------------------------
+
+static size_t fp8_scales_count(int64_t N, int64_t K)
+{
+    return (size_t)((N + 127) / 128) * (size_t)(K / 128);
+}
+// activation scales [K / 128, Mp]
+static size_t fp8_row_scales_bytes(int64_t M, int64_t K)
+{
+    return round_up((size_t)convrot::padded_rows(M) * (size_t)(K / 128) * 4u, kAlign);
+}
+
+static bool valid_fp8_scales(int kind)
+{
+    return kind == CONVROT_FP8_SCALE_F32 || kind == CONVROT_FP8_SCALE_POW2;
+}
+
+static int check_fp8_weights(const convrot_fp8_weights *W)
+{
+    if (!W) return CONVROT_EINVAL;
+    if (W->magic != CONVROT_FP8_MAGIC || W->version != CONVROT_FP8_VERSION ||
+        !valid_fp8_scales(W->scales) || W->reserved != 0)
+        return CONVROT_ELAYOUT;
+    if (!W->codes || !W->scale) return CONVROT_EINVAL;
+    if (!aligned16(W->codes) || !aligned16(W->scale)) return CONVROT_EALIGN;
+    const int rc = check_linear_shape(W->N, W->K, 128);
+    return rc == CONVROT_EINVAL ? CONVROT_ELAYOUT : rc;
+}
+
+size_t convrot_fp8_packed_bytes(int64_t N, int64_t K)
+{
+    return check_linear_shape(N, K, 128) == CONVROT_OK ? (size_t)N * (size_t)K : 0;
+}
+
+size_t convrot_fp8_scale_bytes(int64_t N, int64_t K)
+{
+    return check_linear_shape(N, K, 128) == CONVROT_OK ? fp8_scales_count(N, K) * 4u : 0;
+}
+
+size_t convrot_fp8_prepare_workspace_bytes(int64_t N, int64_t K, int w_dtype, int layout)
+{
+    return convrot_prepare_workspace_bytes(N, K, 128, w_dtype, layout);
+}
+
+size_t convrot_fp8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N)
+{
+    if (check_linear_shape(N, K, 128) != CONVROT_OK || check_rows(M, K) != CONVROT_OK ||
+        convrot::fp8_fuses_quantize(M))
+        return 0;
+    return codes_bytes(M, K) + fp8_row_scales_bytes(M, K);
+}
+
+static int fp8_prepare_impl(const void *W, int w_dtype, int layout, const float *src_scale,
+                            int64_t N, int64_t K, convrot_fp8_weights *out, void *ws,
+                            size_t ws_bytes, void *stream)
+{
+    if (!W || !out || !out->codes || !out->scale) return CONVROT_EINVAL;
+    int rc = check_linear_shape(N, K, 128);
+    if (rc != CONVROT_OK) return rc;
+    if (layout != CONVROT_OUT_MAJOR && layout != CONVROT_IN_MAJOR) return CONVROT_EINVAL;
+    if (w_dtype != CONVROT_F32 && w_dtype != CONVROT_BF16 && w_dtype != CONVROT_F8E4M3)
+        return CONVROT_EUNSUPPORTED;
+    const bool import = w_dtype == CONVROT_F8E4M3;
+    if (import != (src_scale != nullptr) || !valid_fp8_scales(out->scales)) return CONVROT_EINVAL;
+    if (!aligned16(W) || !aligned16(out->codes) || !aligned16(out->scale) ||
+        (src_scale && !aligned16(src_scale)))
+        return CONVROT_EALIGN;
+    const size_t need = convrot_fp8_prepare_workspace_bytes(N, K, w_dtype, layout);
+    if (need > 0 && (!ws || ws_bytes < need)) return CONVROT_EWORKSPACE;
+    if (ws && !aligned16(ws)) return CONVROT_EALIGN;
+
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    hipError_t e = hipSuccess;
+    if (import) {
+        e = convrot::launch_tile_codes(static_cast<const int8_t *>(W), layout == CONVROT_IN_MAJOR,
+                                       reinterpret_cast<int8_t *>(out->codes), N, K, s);
+        if (e == hipSuccess)
+            e = hipMemcpyAsync(out->scale, src_scale, fp8_scales_count(N, K) * 4u,
+                               hipMemcpyDeviceToDevice, s);
+    } else {
+        const void *rows = W;
+        if (layout == CONVROT_IN_MAJOR) {
+            e = convrot::launch_transpose(W, ws, K, N, w_dtype == CONVROT_F32 ? 4 : 2, s);
+            rows = ws;
+        }
+        if (e == hipSuccess)
+            e = convrot::launch_fp8_block_weights(
+                rows, w_dtype == CONVROT_F32 ? convrot::InType::F32 : convrot::InType::BF16, N, K,
+                out->scales == CONVROT_FP8_SCALE_POW2, out->codes, out->scale, s);
+    }
+    rc = hip_status(e);
+    if (rc != CONVROT_OK) return rc;
+    out->magic = CONVROT_FP8_MAGIC;
+    out->version = CONVROT_FP8_VERSION;
+    out->N = N;
+    out->K = K;
+    out->reserved = 0;
+    return CONVROT_OK;
+}
+
+int convrot_fp8_prepare_weights(const void *W, int w_dtype, int layout, const float *src_scale,
+                                int64_t N, int64_t K, convrot_fp8_weights *out, void *ws,
+                                size_t ws_bytes, void *stream)
+{
+    const int rc = fp8_prepare_impl(W, w_dtype, layout, src_scale, N, K, out, ws, ws_bytes,
+                                    stream);
+    log_call("convrot_fp8_prepare_weights", 0, N, K, rc);
+    return rc;
+}
+
+// The checks of a forward, shared with the QKV path (which makes them before
+// it launches anything).
+static int fp8_forward_check(const void *X, int64_t M, const convrot_fp8_weights *W,
+                             const float *bias, const void *Y, int y_dtype, const void *ws,
+                             size_t ws_bytes)
+{
+    int rc = check_fp8_weights(W);
+    if (rc != CONVROT_OK) return rc;
+    if ((rc = check_rows(M, W->K)) != CONVROT_OK) return rc;
+    if ((rc = check_out_dtype(y_dtype)) != CONVROT_OK) return rc;
+    if (M == 0) return CONVROT_OK;
+    if (!X || !Y) return CONVROT_EINVAL;
+    if (!aligned16(X) || !aligned16(Y) || (bias && !aligned16(bias)) || (ws && !aligned16(ws)))
+        return CONVROT_EALIGN;
+    const size_t need = convrot_fp8_linear_workspace_bytes(M, W->K, W->N);
+    return need > 0 && (!ws || ws_bytes < need) ? CONVROT_EWORKSPACE : CONVROT_OK;
+}
+
+static int fp8_forward_impl(const void *X, int64_t M, const convrot_fp8_weights *W,
+                            const float *bias, void *Y, int y_dtype, void *ws, size_t ws_bytes,
+                            void *stream)
+{
+    const int rc = fp8_forward_check(X, M, W, bias, Y, y_dtype, ws, ws_bytes);
+    if (rc != CONVROT_OK || M == 0) return rc;
+    const bool pow2 = W->scales == CONVROT_FP8_SCALE_POW2, f32 = y_dtype == CONVROT_F32;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (convrot::fp8_fuses_quantize(M))
+        return hip_status(convrot::launch_fp8_skinny(X, M, W->codes, W->scale, pow2, bias, Y, f32,
+                                                     W->N, W->K, s));
+    Carve c(ws);
+    uint8_t *q = static_cast<uint8_t *>(c.take(codes_bytes(M, W->K)));
+    float *sx = static_cast<float *>(c.take(fp8_row_scales_bytes(M, W->K)));
+    hipError_t e = convrot::launch_fp8_quantize(X, M, W->K, pow2, q, sx, s);
+    if (e == hipSuccess)
+        e = convrot::launch_fp8_gemm(q, sx, W->codes, W->scale, pow2, bias, Y, f32, M, W->N, W->K,
+                                     s);
+    return hip_status(e);
+}
+
+int convrot_fp8_linear_forward(const void *X, int64_t M, const convrot_fp8_weights *W,
+                               const float *bias, void *Y, int y_dtype, void *ws,
+                               size_t ws_bytes, void *stream)
+{
+    const int rc = fp8_forward_impl(X, M, W, bias, Y, y_dtype, ws, ws_bytes, stream);
+    log_call("convrot_fp8_linear_forward", M, W ? W->N : 0, W ? W->K : 0, rc);
+    return rc;
+}
+
+int convrot_fp8_quantize(const void *X, int64_t M, int64_t K, int scales, uint8_t *q, float *s,
+                         void *stream)
+{
+    if (M < 0 || K <= 0 || K % 128 != 0 || !valid_fp8_scales(scales)) return CONVROT_EINVAL;
+    if (K > kMaxK || check_rows(M, K) != CONVROT_OK) return CONVROT_EUNSUPPORTED;
+    if (M == 0) return CONVROT_OK;
+    if (!X || !q || !s) return CONVROT_EINVAL;
+    if (!aligned16(X) || !aligned16(q) || !aligned16(s)) return CONVROT_EALIGN;
+    return hip_status(convrot::launch_fp8_quantize(X, M, K, scales == CONVROT_FP8_SCALE_POW2, q,
+                                                   s, static_cast<hipStream_t>(stream)));
+}
+
+int convrot_fp8_gemm_dequant(const uint8_t *q, const float *s, int64_t M,
+                             const convrot_fp8_weights *W, const float *bias, void *Y,
+                             int y_dtype, void *stream)
+{
+    int rc = check_fp8_weights(W);
+    if (rc != CONVROT_OK) return rc;
+    if ((rc = check_rows(M, W->K)) != CONVROT_OK) return rc;
+    if ((rc = check_out_dtype(y_dtype)) != CONVROT_OK) return rc;
+    if (M == 0) return CONVROT_OK;
+    if (!q || !s || !Y) return CONVROT_EINVAL;
+    if (!aligned16(q) || !aligned16(s) || !aligned16(Y) || (bias && !aligned16(bias)))
+        return CONVROT_EALIGN;
+    return hip_status(convrot::launch_fp8_gemm(q, s, W->codes, W->scale,
+                                               W->scales == CONVROT_FP8_SCALE_POW2, bias, Y,
+                                               y_dtype == CONVROT_F32, M, W->N, W->K,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// Norms and rotary positions of queries and keys.
+// ---------------------------------------------------------------------------
+
+static int check_rope_shape(int axes, int head_dim, int rotary_dim, int pairing)
+{
+    if (axes < 1 || head_dim <= 0 || rotary_dim <= 0 || rotary_dim % 2 != 0 ||
+        rotary_dim > head_dim ||
+        (pairing != CONVROT_ROPE_INTERLEAVED && pairing != CONVROT_ROPE_HALF))
+        return CONVROT_EINVAL;
+    if (axes > CONVROT_ROPE_MAX_AXES || head_dim % 8 != 0 || head_dim > 512 ||
+        (pairing == CONVROT_ROPE_HALF && rotary_dim % 8 != 0))
+        return CONVROT_EUNSUPPORTED;
+    return CONVROT_OK;
+}
+
+static int check_rope(const convrot_rope *r)
+{
+    if (!r) return CONVROT_EINVAL;
+    if (r->magic != CONVROT_ROPE_MAGIC || r->version != CONVROT_ROPE_VERSION)
+        return CONVROT_ELAYOUT;
+    if (!r->freq || !r->axis) return CONVROT_EINVAL;
+    if (!aligned16(r->freq) || !aligned16(r->axis)) return CONVROT_EALIGN;
+    return check_rope_shape(r->axes, r->head_dim, r->rotary_dim, r->pairing) == CONVROT_OK
+               ? CONVROT_OK : CONVROT_ELAYOUT;
+}
+
+int convrot_rope_prepare(const int32_t *dims, int axes, int head_dim, double theta, int pairing,
+                         int spectrum, convrot_rope *out, void *stream)
+{
+    if (!dims || !out || !out->freq || !out->axis || axes < 1) return CONVROT_EINVAL;
+    if (axes > CONVROT_ROPE_MAX_AXES) return CONVROT_EUNSUPPORTED;
+    convrot::RopeDims d = {};
+    int64_t R = 0;
+    for (int a = 0; a < axes; ++a) {
+        if (dims[a] <= 0 || dims[a] % 2 != 0) return CONVROT_EINVAL;
+        d.d[a] = dims[a];
+        R += dims[a];
+    }
+    if (R > head_dim || !(theta > 0.0) || !std::isfinite(theta) ||
+        (spectrum != CONVROT_ROPE_SPECTRUM_AXIS && spectrum != CONVROT_ROPE_SPECTRUM_WHOLE))
+        return CONVROT_EINVAL;
+    int rc = check_rope_shape(axes, head_dim, (int)R, pairing);
+    if (rc != CONVROT_OK) return rc;
+    if (!aligned16(out->freq) || !aligned16(out->axis)) return CONVROT_EALIGN;
+    rc = hip_status(convrot::launch_rope_tables(d, axes, theta,
+                                                spectrum == CONVROT_ROPE_SPECTRUM_WHOLE, out->freq,
+                                                out->axis, static_cast<hipStream_t>(stream)));
+    if (rc != CONVROT_OK) return rc;
+    out->magic = CONVROT_ROPE_MAGIC;
+    out->version = CONVROT_ROPE_VERSION;
+    out->axes = axes;
+    out->head_dim = head_dim;
+    out->rotary_dim = (int32_t)R;
+    out->pairing = pairing;
+    return CONVROT_OK;
+}
+
+// A view of per-head rows (elements of es bytes) as the kernels take it.
+static int head_rows(const convrot_heads *v, int heads, int64_t B, int64_t T, int es,
+                     convrot::HeadRows *out)
+{
+    if (!v || v->heads != heads || v->reserved != 0) return CONVROT_EINVAL;
+    if (B * T > 0 && !v->data) return CONVROT_EINVAL;
+    const int64_t ext[3] = {B, T, heads};
+    int64_t st[3] = {v->batch_stride, v->token_stride, v->head_stride};
+    for (int i = 0; i < 3; ++i) {
+        if (ext[i] <= 1) st[i] = 0;
+        if ((st[i] * es) % 16 != 0) return CONVROT_EALIGN;
+        if (st[i] < 0) return CONVROT_EINVAL;
+    }
+    if (!aligned16(v->data)) return CONVROT_EALIGN;
+    *out = {v->data, st[0], st[1], st[2]};
+    return CONVROT_OK;
+}
+
+// The arguments the three calls share, checked and gathered.
+static int norm_rope_args(int64_t B, int64_t T, int dtype, const convrot_rope *rope,
+                          const void *positions, int pos_dtype, int64_t pos_batch_stride,
+                          convrot::NormRope *a)
+{
+    if (B < 0 || T < 0) return CONVROT_EINVAL;
+    int rc = check_rope(rope);
+    if (rc != CONVROT_OK) return rc;
+    if (dtype != CONVROT_F32 && dtype != CONVROT_BF16) return CONVROT_EUNSUPPORTED;
+    if (pos_dtype != CONVROT_I32 && pos_dtype != CONVROT_F32) return CONVROT_EUNSUPPORTED;
+    if (B >= kI32Bound || T >= kI32Bound || B * T >= kI32Bound - 8192)
+        return CONVROT_EUNSUPPORTED;
+    if (pos_batch_stride < 0) return CONVROT_EINVAL;
+    if (B * T > 0) {
+        if (!positions) return CONVROT_EINVAL;
+        if (!aligned16(positions)) return CONVROT_EALIGN;
+    }
+    a->B = (int)B;
+    a->T = (int)T;
+    a->D = rope->head_dim;
+    a->R = rope->rotary_dim;
+    a->freq = rope->freq;
+    a->axis = rope->axis;
+    a->axes = rope->axes;
+    a->half = rope->pairing == CONVROT_ROPE_HALF;
+    a->pos = positions;
+    a->pos_sb = pos_batch_stride;
+    a->pos_f32 = pos_dtype == CONVROT_F32;
+    a->f32 = dtype == CONVROT_F32;
+    return CONVROT_OK;
+}
+
+// One side (0 queries, 1 keys): its input and output views.
+static int norm_rope_side(convrot::NormRope *a, int side, const convrot_heads *x,
+                          const convrot_heads *y)
+{
+    if (!x || !y || x->heads < 1) return CONVROT_EINVAL;
+    if (x->heads > 65536) return CONVROT_EUNSUPPORTED;
+    const int es = a->f32 ? 4 : 2;
+    a->heads[side] = x->heads;
+    int rc = head_rows(x, x->heads, a->B, a->T, es, &a->x[side]);
+    if (rc == CONVROT_OK) rc = head_rows(y, x->heads, a->B, a->T, es, &a->out[side]);
+    return rc;
+}
+
+// B * T for the call log (0 where the product would not fit).
+static int64_t token_count(int64_t B, int64_t T)
+{
+    return B > 0 && T > 0 && B < kI32Bound && T < kI32Bound ? B * T : 0;
+}
+
+static int check_eps(float eps) { return eps > 0.0f && std::isfinite(eps) ? CONVROT_OK : CONVROT_EINVAL; }
+
+static int rope_forward_impl(int64_t B, int64_t T, int dtype, const convrot_heads *q,
+                             const convrot_heads *q_out, const convrot_heads *k,
+                             const convrot_heads *k_out, const convrot_rope *rope,
+                             const void *positions, int pos_dtype, int64_t pos_batch_stride,
+                             uint32_t flags, void *stream)
+{
+    convrot::NormRope a = {};
+    int rc = norm_rope_args(B, T, dtype, rope, positions, pos_dtype, pos_batch_stride, &a);
+    if (rc != CONVROT_OK) return rc;
+    if ((flags & ~CONVROT_ROPE_INVERSE) != 0) return CONVROT_EUNSUPPORTED;
+    if ((rc = norm_rope_side(&a, 0, q, q_out)) != CONVROT_OK) return rc;
+    if ((k || k_out) && (rc = norm_rope_side(&a, 1, k, k_out)) != CONVROT_OK) return rc;
+    a.inverse = (flags & CONVROT_ROPE_INVERSE) != 0;
+    return hip_status(convrot::launch_norm_rope(convrot::NormRopeMode::ROPE, a,
+                                                static_cast<hipStream_t>(stream)));
+}
+
+int convrot_rope_forward(int64_t B, int64_t T, int dtype, const convrot_heads *q,
+                         const convrot_heads *q_out, const convrot_heads *k,
+                         const convrot_heads *k_out, const convrot_rope *rope,
+                         const void *positions, int pos_dtype, int64_t pos_batch_stride,
+                         uint32_t flags, void *stream)
+{
+    const int rc = rope_forward_impl(B, T, dtype, q, q_out, k, k_out, rope, positions, pos_dtype,
+                                     pos_batch_stride, flags, stream);
+    log_call("convrot_rope_forward", token_count(B, T), q ? q->heads : 0, rope ? rope->head_dim : 0, rc);
+    return rc;
+}
+
+static int qk_norm_rope_check(int64_t B, int64_t T, int dtype, const convrot_heads *q,
+                              const convrot_heads *q_out, const float *w_q,
+                              const convrot_heads *k, const convrot_heads *k_out,
+                              const float *w_k, float eps, const convrot_rope *rope,
+                              const void *positions, int pos_dtype, int64_t pos_batch_stride,
+                              convrot::NormRope *a)
+{
+    int rc = norm_rope_args(B, T, dtype, rope, positions, pos_dtype, pos_batch_stride, a);
+    if (rc != CONVROT_OK) return rc;
+    if ((rc = check_eps(eps)) != CONVROT_OK) return rc;
+    if ((rc = norm_rope_side(a, 0, q, q_out)) != CONVROT_OK) return rc;
+    if ((k || k_out || w_k) && (rc = norm_rope_side(a, 1, k, k_out)) != CONVROT_OK) return rc;
+    if ((w_q && !aligned16(w_q)) || (w_k && !aligned16(w_k))) return CONVROT_EALIGN;
+    a->w[0] = w_q;
+    a->w[1] = w_k;
+    a->eps = eps;
+    return CONVROT_OK;
+}
+
+int convrot_qk_norm_rope_forward(int64_t B, int64_t T, int dtype, const convrot_heads *q,
+                                 const convrot_heads *q_out, const float *w_q,
+                                 const convrot_heads *k, const convrot_heads *k_out,
+                                 const float *w_k, float eps, const convrot_rope *rope,
+                                 const void *positions, int pos_dtype, int64_t pos_batch_stride,
+                                 void *stream)
+{
+    convrot::NormRope a = {};
+    int rc = qk_norm_rope_check(B, T, dtype, q, q_out, w_q, k, k_out, w_k, eps, rope, positions,
+                                pos_dtype, pos_batch_stride, &a);
+    if (rc == CONVROT_OK)
+        rc = hip_status(convrot::launch_norm_rope(convrot::NormRopeMode::NORM, a,
+                                                  static_cast<hipStream_t>(stream)));
+    log_call("convrot_qk_norm_rope_forward", token_count(B, T), q ? q->heads : 0, rope ? rope->head_dim : 0,
+             rc);
+    return rc;
+}
+
+size_t convrot_qk_norm_rope_workspace_bytes(int64_t B, int64_t T, int heads_q, int heads_k,
+                                            int head_dim)
+{
+    if (B < 0 || T < 0 || B >= kI32Bound || T >= kI32Bound || B * T >= kI32Bound - 8192 ||
+        heads_q < 1 || heads_q > 65536 || heads_k < 0 || heads_k > 65536 || head_dim <= 0 ||
+        head_dim % 8 != 0 || head_dim > 512)
+        return 0;
+    return round_up((size_t)convrot::norm_rope_partial_rows(B * T) * 2u * (size_t)head_dim * 4u,
+                    kAlign);
+}
+
+int convrot_qk_norm_rope_backward(int64_t B, int64_t T, int dtype, const convrot_heads *g_q,
+                                  const convrot_heads *q, const convrot_heads *dq,
+                                  const float *w_q, float *dw_q, const convrot_heads *g_k,
+                                  const convrot_heads *k, const convrot_heads *dk,
+                                  const float *w_k, float *dw_k, float eps,
+                                  const convrot_rope *rope, const void *positions, int pos_dtype,
+                                  int64_t pos_batch_stride, void *ws, size_t ws_bytes,
+                                  void *stream)
+{
+    convrot::NormRope a = {};
+    auto run = [&]() -> int {
+        int rc = qk_norm_rope_check(B, T, dtype, q, dq, w_q, k, dk, w_k, eps, rope, positions,
+                                    pos_dtype, pos_batch_stride, &a);
+        if (rc != CONVROT_OK) return rc;
+        const bool keys = a.heads[1] > 0;
+        if (!dw_q || !g_q || keys != (g_k != nullptr) || keys != (dw_k != nullptr))
+            return CONVROT_EINVAL;
+        const int es = a.f32 ? 4 : 2;
+        if ((rc = head_rows(g_q, a.heads[0], B, T, es, &a.g[0])) != CONVROT_OK) return rc;
+        if (keys && (rc = head_rows(g_k, a.heads[1], B, T, es, &a.g[1])) != CONVROT_OK) return rc;
+        if (!aligned16(dw_q) || (dw_k && !aligned16(dw_k)) || (ws && !aligned16(ws)))
+            return CONVROT_EALIGN;
+        const size_t need =
+            convrot_qk_norm_rope_workspace_bytes(B, T, a.heads[0], a.heads[1], a.D);
+        if (need > 0 && (!ws || ws_bytes < need)) return CONVROT_EWORKSPACE;
+        a.dw[0] = dw_q;
+        a.dw[1] = dw_k;
+        a.partial = static_cast<float *>(ws);
+        a.inverse = true;
+        return hip_status(convrot::launch_norm_rope(convrot::NormRopeMode::BACKWARD, a,
+                                                    static_cast<hipStream_t>(stream)));
+    };
+    const int rc = run();
+    log_call("convrot_qk_norm_rope_backward", token_count(B, T), q ? q->heads : 0, rope ? rope->head_dim : 0,
+             rc);
+    return rc;
+}
+
+// The QKV path: the linear, then the norms and the rotation in place on the
+// query and key columns of its output rows.  Everything is checked before the
+// linear is launched.
+static int qkv_norm_rope_args(int64_t B, int64_t T, int64_t N, int heads_q, int heads_kv,
+                              const float *w_q, const float *w_k, float eps,
+                              const convrot_rope *rope, const void *positions, int pos_dtype,
+                              int64_t pos_batch_stride, void *Y, int y_dtype,
+                              convrot::NormRope *a)
+{
+    if (heads_q < 1 || heads_kv < 1) return CONVROT_EINVAL;
+    int rc = check_rope(rope);
+    if (rc != CONVROT_OK) return rc;
+    const int64_t D = rope->head_dim;
+    if (N != ((int64_t)heads_q + 2 * (int64_t)heads_kv) * D) return CONVROT_ELAYOUT;
+    const size_t es = y_dtype == CONVROT_F32 ? 4u : 2u;
+    const convrot_heads q = {Y, heads_q, 0, T * N, N, D};
+    const convrot_heads k = {Y ? static_cast<char *>(Y) + (size_t)(heads_q * D) * es : nullptr,
+                             heads_kv, 0, T * N, N, D};
+    return qk_norm_rope_check(B, T, y_dtype, &q, &q, w_q, &k, &k, w_k, eps, rope, positions,
+                              pos_dtype, pos_batch_stride, a);
+}
+
+int convrot_qkv_forward(const void *X, int64_t B, int64_t T, const convrot_weights *W,
+                        const float *bias, int heads_q, int heads_kv, const float *w_q,
+                        const float *w_k, float eps, const convrot_rope *rope,
+                        const void *positions, int pos_dtype, int64_t pos_batch_stride, void *Y,
+                        int y_dtype, void *ws, size_t ws_bytes, void *stream)
+{
+    convrot::NormRope a = {};
+    int rc = check_weights(W);
+    if (rc == CONVROT_OK) rc = check_out_dtype(y_dtype);
+    if (rc == CONVROT_OK)
+        rc = qkv_norm_rope_args(B, T, W->N, heads_q, heads_kv, w_q, w_k, eps, rope, positions,
+                                pos_dtype, pos_batch_stride, Y, y_dtype, &a);
+    if (rc == CONVROT_OK)
+        rc = linear_forward_impl(X, B * T, W, bias, Y, y_dtype, ws, ws_bytes, stream);
+    if (rc == CONVROT_OK)
+        rc = hip_status(convrot::launch_norm_rope(convrot::NormRopeMode::NORM, a,
+                                                  static_cast<hipStream_t>(stream)));
+    log_call("convrot_qkv_forward", token_count(B, T), W ? W->N : 0, W ? W->K : 0, rc);
+    return rc;
+}
+
+int convrot_fp8_qkv_forward(const void *X, int64_t B, int64_t T, const convrot_fp8_weights *W,
+                            const float *bias, int heads_q, int heads_kv, const float *w_q,
+                            const float *w_k, float eps, const convrot_rope *rope,
+                            const void *positions, int pos_dtype, int64_t pos_batch_stride,
+                            void *Y, int y_dtype, void *ws, size_t ws_bytes, void *stream)
+{
+    convrot::NormRope a = {};
+    int rc = check_fp8_weights(W);
+    if (rc == CONVROT_OK) rc = check_out_dtype(y_dtype);
+    if (rc == CONVROT_OK)
+        rc = qkv_norm_rope_args(B, T, W->N, heads_q, heads_kv, w_q, w_k, eps, rope, positions,
+                                pos_dtype, pos_batch_stride, Y, y_dtype, &a);
+    if (rc == CONVROT_OK)
+        rc = fp8_forward_impl(X, B * T, W, bias, Y, y_dtype, ws, ws_bytes, stream);
+    if (rc == CONVROT_OK)
+        rc = hip_status(convrot::launch_norm_rope(convrot::NormRopeMode::NORM, a,
+                                                  static_cast<hipStream_t>(stream)));
+    log_call("convrot_fp8_qkv_forward", token_count(B, T), W ? W->N : 0, W ? W->K : 0, rc);
     return rc;
 }
 

@@ -134,16 +134,6 @@ __device__ __forceinline__ void interleave()
     interleave_all<MFMAS, VMEMS, DSREADS>(std::make_integer_sequence<int, MFMAS>{});
 }
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-
-// Two fp32 -> packed bf16 with v_cvt_pk_bf16_f32 (round to nearest even).
-__device__ __forceinline__ uint32_t cvt_pk_bf16(float lo, float hi)
-{
-    const bf16x2 p = __builtin_convertvector((f32x2){lo, hi}, bf16x2);
-    return __builtin_bit_cast(uint32_t, p);
-}
-
 
 // Dequantise and store a wave's 128 x 128 block.  FULL: the tile lies inside
 // [M, N], so no per-lane bounds checks are needed.
