@@ -1,0 +1,406 @@
+// FP8 (e4m3) x FP8 GEMM on gfx950 matrix cores with a scale per 128 inputs:
+//   Y[m, n] = sum_b (sum_{k in b} qx[m, k] qw[n, k]) (sx[b, m] sw[n / 128, b])
+//             (+ bias[n])
+// Both code matrices are K-tiled (common.hpp); a k-block of 128 inputs is two
+// consecutive 1 KiB tiles of each 16-row block.
+//
+// fp8_gemm_kernel (any scales).  The scale changes with every k-block, so each
+// block's sum is formed from zero by one v_mfma_f32_16x16x128_f8f6f4 and joined
+// by four fp32 fused multiply-adds per lane: 16 VALU cycles for 32 matrix
+// cycles, on the same SIMD.  A VALU instruction cannot name an accumulator
+// register, so the 128 sums of a lane have to sit in ordinary registers: 8 waves (two
+// per SIMD, 256 registers each) own 128 x 64 of a 256 (n) x 256 (m) tile, and one
+// wave's matrix instructions run under the other's additions.  The sums of row
+// tile i are joined while row tile i + 1 multiplies.
+//
+// Copies go straight to LDS (buffer_load ... lds), one k-block (64 KiB) per stage,
+// two stages.  A wave walks a stage's 8 weight tiles with one operand in
+// registers and the next on its way; before the last one every wave has read
+// the stage, and a barrier there frees it for the k-block after next.  The copies of
+// a k-block so have one whole k-block (2048 matrix cycles) to land.  The stream
+// of k-blocks runs on across the tiles of a persistent workgroup.  With an odd
+// number of k-blocks a tile takes one more, of zeros.
+//
+// F32 outputs (F32 = true) convert the codes to bf16 and use
+// v_mfma_f32_16x16x32_bf16 (see fp8.hip on the precision of the FP8 sums): half the
+// matrix rate, the conversions of the activations kept for a k-block.
+#include "common.hpp"
+#include "gemm_common.hpp"
+
+#include <algorithm>
+
+namespace convrot {
+namespace {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+
+constexpr int kKB = 128;        // inputs per k-block
+constexpr int kGroup = 4;       // tile-rows per L2 group
+
+// One tile's operands: rows past the end are out of range and read as zero.
+struct Src {
+    const uint8_t *w, *x;
+    const float *s;
+    int wn, xn, sn;             // bytes in range
+};
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *p, int n)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, n, kRsrcWord3);
+}
+
+__device__ __forceinline__ v8i frag(const uint8_t *__restrict__ tile)
+{
+    const v4i lo = *reinterpret_cast<const v4i *>(tile);
+    const v4i hi = *reinterpret_cast<const v4i *>(tile + 1024);
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// 8 e4m3 codes as bf16, exactly.
+__device__ __forceinline__ v8bf bf16_of_codes(int lo, int hi)
+{
+    const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+    const v2bf b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+    const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+    const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+    return (v8bf){a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+// An operand tile as the matrix instructions take it.
+template <bool F32> struct Operand;
+template <> struct Operand<false> {
+    v8i q;
+    __device__ __forceinline__ void set(const v8i &v) { q = v; }
+};
+template <> struct Operand<true> {
+    v8bf h[4];
+    __device__ __forceinline__ void set(const v8i &v)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = bf16_of_codes(v[2 * i], v[2 * i + 1]);
+    }
+};
+
+__device__ __forceinline__ v4f product(const Operand<false> &a, const Operand<false> &b)
+{
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.q, b.q, (v4f)(0.0f), 0, 0, 0, 0, 0,
+                                                            0);
+}
+__device__ __forceinline__ v4f product(const Operand<true> &a, const Operand<true> &b)
+{
+    v4f p = (v4f)(0.0f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.h[i], b.h[i], p, 0, 0, 0);
+    return p;
+}
+
+// Registers that live from one k-block to the next.
+template <int NI, int NJ, bool F32>
+struct State {
+    v4f acc[NI][NJ];
+    v4f t[NJ];                  // products of the row tile not joined yet
+    float ft[NJ];               // ... and their scales
+    float f[NJ];                // scales of the current k-block
+    v8i a;                      // first row tile of the current k-block
+    Operand<F32> b[NJ];         // its column tiles
+};
+
+// Row tile i of a k-block against the column tiles in registers, while the
+// products of the row tile before it are joined.
+template <int NI, int NJ, bool F32>
+__device__ __forceinline__ void row_tile(State<NI, NJ, F32> &st, const v8i &q, int i)
+{
+    Operand<F32> a;
+    a.set(q);
+    v4f t[NJ];
+    v4f(&prev)[NJ] = st.acc[i == 0 ? NI - 1 : i - 1];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+        t[j] = product(a, st.b[j]);
+        const float f = i == 0 ? st.ft[j] : st.f[j];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) prev[j][e] = __builtin_fmaf(st.t[j][e], f, prev[j][e]);
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) st.t[j] = t[j];
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// The row tiles of one k-block but the last, from stage cw; on return the
+// wave has read all of the stage (st.a: the last row tile).
+template <int NI, int NJ, bool F32>
+__device__ __forceinline__ void k_block_head(State<NI, NJ, F32> &st,
+                                             const uint8_t *__restrict__ cw, int off_w)
+{
+#pragma unroll
+    for (int i = 0; i + 1 < NI; ++i) {
+        const v8i q = st.a;
+        st.a = frag(cw + off_w + (i + 1) * 2048);
+        row_tile(st, q, i);
+    }
+    wait_lds_reads();
+}
+
+// The last row tile, then the first operands of the next k-block, from the
+// stage (nw, nx, ns), which has landed.
+template <int NI, int NJ, bool F32>
+__device__ __forceinline__ void k_block_tail(State<NI, NJ, F32> &st,
+                                             const uint8_t *__restrict__ nw,
+                                             const uint8_t *__restrict__ nx,
+                                             const float *__restrict__ ns, int off_w, int off_x,
+                                             int off_s, float sw_next)
+{
+    const v8i q = st.a;
+    row_tile(st, q, NI - 1);
+    // (not earlier: the column tiles are still being multiplied)
+    st.a = frag(nw + off_w);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+        st.b[j].set(frag(nx + off_x + j * 2048));
+        st.ft[j] = st.f[j];
+        st.f[j] = ns[off_s + 16 * j] * sw_next;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// This wave's copies of k-block kb of a tile into a stage (zeros if `none`).
+template <int CW, int CX>
+__device__ __forceinline__ void copy_block(const Src &s, int kb, bool none, int Mp,
+                                           const uint32_t *vw, const uint32_t *vx, int odd,
+                                           uint32_t vs, int wave, int sgrp, uint8_t *dw,
+                                           uint8_t *dx, float *ds)
+{
+    const __amdgpu_buffer_rsrc_t rw = rsrc(s.w, none ? 0 : s.wn), rx = rsrc(s.x, none ? 0 : s.xn),
+                                 rs = rsrc(s.s + (int64_t)kb * Mp, none ? 0 : s.sn);
+#pragma unroll
+    for (int j = 0; j < CW; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rw, (__attribute__((address_space(3))) void *)(dw + (wave * CW + j) * 1024), 16,
+            vw[j >> 1], kb * 2048 + (j & 1) * 1024, 0, 0);
+#pragma unroll
+    for (int j = 0; j < CX; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rx, (__attribute__((address_space(3))) void *)(dx + (wave * CX + j) * 1024), 16,
+            vx[j >> 1], kb * 2048 + (j & 1) * 1024 + odd, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rs, (__attribute__((address_space(3))) void *)(ds + sgrp * 64), 4, vs, 0, 0, 0);
+}
+
+template <int NI, int NJ, bool F32, bool HAS_BIAS>
+__global__ __launch_bounds__(512, 2) void fp8_gemm_kernel(
+    const uint8_t *__restrict__ qx, const float *__restrict__ sx, const uint8_t *__restrict__ qw,
+    const float *__restrict__ sw, const float *__restrict__ bias, void *__restrict__ Y, int M,
+    int N, int K, int tiles_m, int tiles_n, int tiles_per_xcd, int wgs_per_xcd)
+{
+    constexpr int TN = 32 * NI, TM = 64 * NJ;
+    constexpr int CW = TN / 64, CX = TM / 64, C = CW + CX + 1;   // copies per wave and k-block
+    __shared__ __attribute__((aligned(1024))) uint8_t sw0[TN * kKB], sw1[TN * kKB];
+    __shared__ __attribute__((aligned(1024))) uint8_t sx0[TM * kKB], sx1[TM * kKB];
+    __shared__ __attribute__((aligned(1024))) float ss0[256], ss1[256];
+    __shared__ __attribute__((aligned(16))) float sbias[TN];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wave & 1, wm = wave >> 1;
+    const int r = lane & 15, g = lane >> 4;
+    const int nkb = K / kKB, nkp = (nkb + 1) & ~1;
+    const int Mp = (int)padded_rows(M);
+    const int tiles = tiles_m * tiles_n;
+    const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+
+    // i-th tile of this workgroup (XCD-contiguous ranges, grouped along m)
+    auto tile_at = [&](int i, int &m0, int &n0) -> bool {
+        const int tl = slot + i * wgs_per_xcd;
+        const int t = xcd * tiles_per_xcd + tl;
+        if (tl >= tiles_per_xcd || t >= tiles) return false;
+        const int width = kGroup * tiles_n;
+        const int first_m = (t / width) * kGroup;
+        const int gsz = min(tiles_m - first_m, kGroup);
+        m0 = (first_m + (t % width) % gsz) * TM;
+        n0 = ((t % width) / gsz) * TN;
+        return true;
+    };
+    auto src_of = [&](int m0, int n0) {
+        return Src{qw + (int64_t)n0 * K, qx + (int64_t)m0 * K, sx + m0, (N - n0) * K,
+                   (Mp - m0) * K, (Mp - m0) * 4};
+    };
+    // the scales of this wave's weight rows: one row of the scale matrix
+    auto sw_row = [&](int n0) {
+        return sw + (int64_t)(min(n0 + wn * 16 * NI, N - 1) >> 7) * nkb;
+    };
+
+    int m0, n0;
+    if (!tile_at(0, m0, n0)) return;
+    int nm0 = m0, nn0 = n0;
+    bool more = tile_at(1, nm0, nn0);
+    Src cur = src_of(m0, n0), nxt = src_of(nm0, nn0);
+    const float *swc = sw_row(n0), *swn = sw_row(nn0);
+
+    // copy c of a stage moves 1 KiB: tile c & 1 of row block c >> 1.  The row's
+    // offset is in the lane's offset (the one that is checked against the range),
+    // the k-block's in the scalar one
+    constexpr int VW = (CW + 1) / 2, VX = (CX + 1) / 2;
+    uint32_t vw[VW], vx[VX];
+#pragma unroll
+    for (int j = 0; j < VW; ++j) vw[j] = ((wave * CW) / 2 + j) * 16 * K + lane * 16;
+#pragma unroll
+    for (int j = 0; j < VX; ++j) vx[j] = ((wave * CX) / 2 + j) * 16 * K + lane * 16;
+    const int odd = CX == 1 ? (wave & 1) * 1024 : 0;
+    // TM scales, 64 per wave; the other waves repeat them
+    const int sgrp = wave & (CX - 1);
+    const uint32_t vs = sgrp * 256 + lane * 4;
+
+    // k-block k of the stream (from nkp on: of the next tile) into a stage;
+    // zeros beyond a tile's k-blocks and after the last tile
+    auto copy = [&](int k, uint8_t *dw, uint8_t *dx, float *ds) {
+        const bool next = k >= nkp;
+        const int kb = next ? k - nkp : k;
+        const bool none = kb >= nkb || (next && !more);
+        copy_block<CW, CX>(next ? nxt : cur, none ? 0 : kb, none, Mp, vw, vx, odd, vs, wave,
+                           sgrp, dw, dx, ds);
+    };
+
+    const int in_tile = r * 64 + ((g ^ swz(r)) << 4);
+    const int off_w = wn * NI * 2048 + in_tile, off_x = wm * NJ * 2048 + in_tile;
+    const int off_s = wm * NJ * 16 + r;
+
+    float b_reg = 0.0f;
+    auto load_bias = [&](int n0_) {
+        if constexpr (HAS_BIAS) b_reg = bias[min(n0_ + (tid & (TN - 1)), N - 1)];
+    };
+    load_bias(n0);
+
+    State<NI, NJ, F32> st;
+    copy(0, sw0, sx0, ss0);
+    copy(1, sw1, sx1, ss1);
+    wait_vmcnt<C>();
+    block_barrier();
+    st.a = frag(sw0 + off_w);
+    {
+        const float s0 = swc[0];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            st.b[j].set(frag(sx0 + off_x + j * 2048));
+            st.f[j] = ss0[off_s + 16 * j] * s0;
+        }
+    }
+
+    for (int it = 0;; ++it) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) st.acc[i][j] = (v4f)(0.0f);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            st.t[j] = (v4f)(0.0f);
+            st.ft[j] = 0.0f;
+        }
+        // two k-blocks per round, so that every access names its stage
+        for (int k = 0; k < nkp; k += 2) {
+            k_block_head(st, sw0, off_w);
+            wait_vmcnt<0>();       // k-block k + 1 has landed, ...
+            block_barrier();       // ... and this stage is free
+            copy(k + 2, sw0, sx0, ss0);
+            k_block_tail(st, sw1, sx1, ss1, off_w, off_x, off_s, swc[min(k + 1, nkb - 1)]);
+            k_block_head(st, sw1, off_w);
+            wait_vmcnt<0>();
+            block_barrier();
+            copy(k + 3, sw1, sx1, ss1);
+            k_block_tail(st, sw0, sx0, ss0, off_w, off_x, off_s,
+                         *(k + 2 < nkp ? swc + k + 2 : swn));
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                st.acc[NI - 1][j][e] = __builtin_fmaf(st.t[j][e], st.ft[j], st.acc[NI - 1][j][e]);
+
+        if constexpr (HAS_BIAS) {
+            sbias[tid & (TN - 1)] = b_reg;
+            wait_lds_reads();
+            block_barrier();
+        }
+        // lane (r, g) holds outputs 16 i + 4 g + 0..3 of token r of its tiles
+        const bool full = m0 + TM <= M && n0 + TN <= N;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const int m = m0 + (wm * NJ + j) * 16 + r;
+#pragma unroll
+            for (int i = 0; i < NI; i += 2) {
+                const int nl = wn * 16 * NI + 16 * i;
+                v4f v0 = st.acc[i][j], v1 = st.acc[i + 1][j];
+                if constexpr (HAS_BIAS) {
+                    v0 += *reinterpret_cast<const v4f *>(&sbias[nl + 4 * g]);
+                    v1 += *reinterpret_cast<const v4f *>(&sbias[nl + 16 + 4 * g]);
+                }
+                if constexpr (F32) {
+                    float *const o = static_cast<float *>(Y) + (int64_t)m * N + n0 + nl + 4 * g;
+                    if (full || (m < M && n0 + nl < N)) *reinterpret_cast<v4f *>(o) = v0;
+                    if (full || (m < M && n0 + nl + 16 < N)) *reinterpret_cast<v4f *>(o + 16) = v1;
+                } else {
+                    // neighbouring lane rows trade halves: even g then hold 8
+                    // consecutive outputs of tile i, odd g of tile i + 1
+                    const auto s0 = __builtin_amdgcn_permlane16_swap(
+                        cvt_pk_bf16(v0[0], v0[1]), cvt_pk_bf16(v1[0], v1[1]), false, false);
+                    const auto s1 = __builtin_amdgcn_permlane16_swap(
+                        cvt_pk_bf16(v0[2], v0[3]), cvt_pk_bf16(v1[2], v1[3]), false, false);
+                    const int n = n0 + nl + (g & 1) * 16 + (g >> 1) * 8;
+                    if (full || (m < M && n < N))
+                        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(Y) + (int64_t)m * N + n) =
+                            make_uint4(s0[0], s1[0], s0[1], s1[1]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        if (!more) break;
+        m0 = nm0;
+        n0 = nn0;
+        cur = nxt;
+        swc = swn;
+        load_bias(n0);
+        more = tile_at(it + 2, nm0, nn0);
+        nxt = src_of(nm0, nn0);
+        swn = sw_row(nn0);
+        // sbias is rewritten only after the next tile's barriers
+    }
+    // no copy may still be writing LDS when the workgroup ends
+    wait_vmcnt<0>();
+}
+
+template <int NI, int NJ, bool F32>
+hipError_t launch_tile(const uint8_t *qx, const float *sx, const uint8_t *qw, const float *sw,
+                       const float *bias, void *Y, int64_t M, int64_t N, int64_t K,
+                       hipStream_t stream)
+{
+    constexpr int TN = 32 * NI, TM = 64 * NJ;
+    const int tiles_m = (int)((M + TM - 1) / TM), tiles_n = (int)((N + TN - 1) / TN);
+    const int per_xcd = (tiles_m * tiles_n + 7) / 8;
+    const int wgs = std::max(1, std::min(device_cu_count() / 8, per_xcd));
+    const dim3 grid(8 * wgs), block(512);
+    if (bias)
+        hipLaunchKernelGGL((fp8_gemm_kernel<NI, NJ, F32, true>), grid, block, 0, stream, qx, sx,
+                           qw, sw, bias, Y, (int)M, (int)N, (int)K, tiles_m, tiles_n, per_xcd,
+                           wgs);
+    else
+        hipLaunchKernelGGL((fp8_gemm_kernel<NI, NJ, F32, false>), grid, block, 0, stream, qx, sx,
+                           qw, sw, bias, Y, (int)M, (int)N, (int)K, tiles_m, tiles_n, per_xcd,
+                           wgs);
+    return hipGetLastError();
+}
+
+} // namespace
+
+hipError_t launch_fp8_gemm_tiled(const uint8_t *qx, const float *sx, const uint8_t *qw,
+                                 const float *sw, const float *bias, void *Y, bool f32_out,
+                                 int64_t M, int64_t N, int64_t K, hipStream_t stream)
+{
+    return f32_out ? launch_tile<4, 4, true>(qx, sx, qw, sw, bias, Y, M, N, K, stream)
+                   : launch_tile<8, 4, false>(qx, sx, qw, sw, bias, Y, M, N, K, stream);
+}
+
+} // namespace convrot
