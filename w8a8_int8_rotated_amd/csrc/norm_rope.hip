@@ -9,13 +9,18 @@
 // Each row is read and written once, so the bound is memory: 4 bytes per bf16
 // element forward, 6 backward.
 //
-// A workgroup takes one token at a time: its threads evaluate the token's R/2
-// cosines and sines once, into LDS, and its waves share out the token's heads
-// (84 heads of 128 channels use 64 sincos).  A lane holds 16 channels of a head,
-// two runs of 8: adjacent ones when pairs are interleaved, 8 channels and their
-// 8 partners for the half-split pairs, so that a rotation never leaves the
-// lane.  A head is LPH lanes (a power of two), a wave 64 / LPH heads, and the
-// norm's sum runs over the LPH lanes with DPP.
+// A lane holds 16 channels of a head, two runs of 8: adjacent ones when pairs
+// are interleaved, 8 channels and their 8 partners for the half-split pairs, so
+// that a rotation never leaves the lane.  A head is LPH lanes (a power of two), a
+// wave 64 / LPH heads ("unit"), and the norm's sum runs over the LPH lanes with DPP.
+//
+// A wave takes units of the queries or of the keys of one token (all of them
+// when tokens are many).  It evaluates the token's R/2 cosines and sines once,
+// one pair per lane, and hands them round through its own piece of LDS, so waves
+// never wait for each other; the first rows are on their way meanwhile and each
+// unit's rows are requested before the unit before is finished.  (One workgroup
+// per token, sharing one table behind a barrier, left the loads of a token in
+// line behind its table: 595 us for 84 heads of 38656 tokens.)
 //
 // Angles: positions times frequencies in fp64, reduced to revolutions in
 // [-1/2, 1/2] there (an fp32 angle at position 10^6 is off by 0.06 radians),
@@ -79,34 +84,52 @@ __device__ __forceinline__ LaneMap lane_map(int c, int D, int R)
     return m;
 }
 
-// A run of n (0, 4 or 8) channels at p; zeros beyond n.  Half-split pairs with
-// R/2 an odd multiple of 4 (kHalf4) start runs 8 bytes off, so bf16 runs move as two
-// 8-byte halves there.
+// A run of n (0, 4 or 8) channels as it was loaded; zeros beyond n.  Half-split
+// pairs with R/2 an odd multiple of 4 (kHalf4) start runs 8 bytes off, so bf16 runs
+// move as two 8-byte halves there.
+template <bool F32> struct Raw {
+    uint4 u[F32 ? 2 : 1];
+};
+
 template <bool F32, int PAIR>
-__device__ __forceinline__ void load_run(const void *base, int64_t off, int n, float (&v)[8])
+__device__ __forceinline__ Raw<F32> load_raw(const void *base, int64_t off, int n)
 {
+    Raw<F32> r;
+    r.u[0] = make_uint4(0, 0, 0, 0);
     if constexpr (F32) {
-        const float *p = static_cast<const float *>(base) + off;
-        const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float4 a = n > 0 ? *reinterpret_cast<const float4 *>(p) : z;
-        const float4 b = n > 4 ? *reinterpret_cast<const float4 *>(p + 4) : z;
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        r.u[1] = r.u[0];
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(base) + off);
+        if (n > 0) r.u[0] = p[0];
+        if (n > 4) r.u[1] = p[1];
     } else {
         const uint16_t *p = static_cast<const uint16_t *>(base) + off;
-        uint4 u = make_uint4(0, 0, 0, 0);
         if constexpr (PAIR == kHalf4) {
             if (n > 0) {
                 const uint2 a = *reinterpret_cast<const uint2 *>(p);
-                u.x = a.x; u.y = a.y;
+                r.u[0].x = a.x; r.u[0].y = a.y;
             }
             if (n > 4) {
                 const uint2 b = *reinterpret_cast<const uint2 *>(p + 4);
-                u.z = b.x; u.w = b.y;
+                r.u[0].z = b.x; r.u[0].w = b.y;
             }
         } else {
-            if (n > 0) u = *reinterpret_cast<const uint4 *>(p);
+            if (n > 0) r.u[0] = *reinterpret_cast<const uint4 *>(p);
         }
+    }
+    return r;
+}
+
+template <bool F32>
+__device__ __forceinline__ void widen(const Raw<F32> &r, float (&v)[8])
+{
+    const uint4 &u = r.u[0];
+    if constexpr (F32) {
+        const uint4 &w = r.u[1];
+        v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y);
+        v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
+        v[4] = __uint_as_float(w.x); v[5] = __uint_as_float(w.y);
+        v[6] = __uint_as_float(w.z); v[7] = __uint_as_float(w.w);
+    } else {
         v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x); v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
         v[4] = bf16_lo(u.z); v[5] = bf16_hi(u.z); v[6] = bf16_lo(u.w); v[7] = bf16_hi(u.w);
     }
@@ -148,81 +171,115 @@ __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float
     }
 }
 
-// cos and sin of the token's pairs into tab; entries from R/2 up to npad are
-// never used in a rotation but are read.
+// cos and sin of the token's pairs into this wave's table; entries from R/2 up
+// to npad are never used in a rotation but are read.
 __device__ __forceinline__ void fill_table(const NormRope &a, int64_t pos_at, float2 *tab,
-                                           int npad)
+                                           int npad, int lane)
 {
     const int half = a.R >> 1;
-    for (int p = threadIdx.x; p < npad; p += blockDim.x) {
+    double pos[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t at = pos_at + min(i, a.axes - 1);
+        pos[i] = a.pos_f32 ? (double)static_cast<const float *>(a.pos)[at]
+                           : (double)static_cast<const int32_t *>(a.pos)[at];
+    }
+    for (int p = lane; p < npad; p += 64) {
         float s = 0.0f, c = 1.0f;
         if (p < half) {
             const int ax = min(max(a.axis[p], 0), a.axes - 1);
-            const double pos = a.pos_f32
-                                   ? (double)static_cast<const float *>(a.pos)[pos_at + ax]
-                                   : (double)static_cast<const int32_t *>(a.pos)[pos_at + ax];
-            double rev = pos * a.freq[p] * 0.15915494309189535;
+            const double x = ax == 0 ? pos[0] : ax == 1 ? pos[1] : ax == 2 ? pos[2] : pos[3];
+            double rev = x * a.freq[p] * 0.15915494309189535;
             rev -= rint(rev);
             sincospif((float)(2.0 * rev), &s, &c);
             if (a.inverse) s = -s;
         }
         tab[p] = make_float2(c, s);
     }
+    // the table is written and read by this wave only: LDS serves it in order,
+    // the compiler must keep that order
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
-// Token loop of a workgroup of W waves; wave w takes units w, w + W, ..., a
-// unit being up to 64 / LPH heads of the queries or of the keys.  The table is
-// double-buffered, so one barrier per token separates its writers from its
-// readers (a wave can be at most one token ahead of another).
+// A launch's shape: W = wq + wk waves per token, wave w < wq on the queries'
+// units w, w + wq, ..., the others on the keys'; `slots` tokens at a time.
+struct Shape {
+    int lg, wq, wk, slots;
+};
+
 template <bool F32, NormRopeMode MODE, int PAIR>
-__global__ void norm_rope_kernel(NormRope a, int lg)
+__global__ __launch_bounds__(256) void norm_rope_kernel(NormRope a, Shape sh)
 {
     constexpr bool NORM = MODE != NormRopeMode::ROPE;
     constexpr bool BWD = MODE == NormRopeMode::BACKWARD;
     extern __shared__ __attribute__((aligned(16))) float lds[];
-    const int lph = 1 << lg, hpw = 64 >> lg, npad = 8 * lph;
-    float2 *const tab = reinterpret_cast<float2 *>(lds);
+    const int lg = sh.lg, lph = 1 << lg, hpw = 64 >> lg, npad = 8 * lph;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int waves = blockDim.x >> 6;
+    float2 *const tab = reinterpret_cast<float2 *>(lds) + wave * npad;
     const LaneMap m = lane_map<PAIR>(lane & (lph - 1), a.D, a.R);
     const int hg = lane >> lg;
-    const int units0 = (a.heads[0] + hpw - 1) >> (6 - lg);
-    const int units = units0 + ((a.heads[1] + hpw - 1) >> (6 - lg));
-    const int tokens = a.B * a.T;
+    const uint32_t tokens = (uint32_t)(a.B * a.T);
     const float invD = 1.0f / (float)a.D;
 
-    float dw[2][2][8] = {};   // backward: [side][run] sums of g' x r
-    int buf = 0;
-    for (int tok = blockIdx.x; tok < tokens; tok += gridDim.x, buf ^= 1) {
-        const int b = tok / a.T, t = tok - b * a.T;
-        float2 *const tb = tab + buf * npad;
-        fill_table(a, b * a.pos_sb + (int64_t)t * a.axes, tb, npad);
-        __syncthreads();
+    const int W = sh.wq + sh.wk;
+    const int gw = blockIdx.x * 4 + wave;
+    const int slot = gw / W, w = gw - slot * W;
+    const int side = w >= sh.wq ? 1 : 0;
+    const int first = side ? w - sh.wq : w, step = side ? sh.wk : sh.wq;
+    const int heads = side ? a.heads[1] : a.heads[0];
+    const HeadRows xr = side ? a.x[1] : a.x[0], yr = side ? a.out[1] : a.out[0];
+    const HeadRows gr = side ? a.g[1] : a.g[0];
+    const float *const wp = side ? a.w[1] : a.w[0];
+    const int units = (heads + hpw - 1) >> (6 - lg);
+
+    float wa[8], wb[8];
+    if constexpr (NORM) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) wa[i] = wb[i] = 1.0f;
+        if (wp) {
+            widen<true>(load_raw<true, PAIR>(wp, m.off[0], m.n[0]), wa);
+            widen<true>(load_raw<true, PAIR>(wp, m.off[1], m.n[1]), wb);
+        }
+    }
+    float dwa[8] = {}, dwb[8] = {};      // backward: sums of g' x r
+
+    for (uint32_t tok = slot < sh.slots ? slot : tokens; tok < tokens; tok += sh.slots) {
+        const int b = (int)(tok / (uint32_t)a.T), t = (int)tok - b * a.T;
+        const int64_t x0 = b * xr.sb + t * xr.st, y0 = b * yr.sb + t * yr.st;
+        const int64_t g0 = b * gr.sb + t * gr.st;
+        Raw<F32> xa, xb, ga, gb;
+        auto load = [&](int u, Raw<F32> &pa, Raw<F32> &pb, const HeadRows &v, int64_t at) {
+            const int head = u * hpw + hg;
+            const bool live = head < heads;
+            at += head * v.sh;
+            pa = load_raw<F32, PAIR>(v.p, at + m.off[0], live ? m.n[0] : 0);
+            pb = load_raw<F32, PAIR>(v.p, at + m.off[1], live ? m.n[1] : 0);
+        };
+        load(first, xa, xb, xr, x0);
+        if constexpr (BWD) load(first, ga, gb, gr, g0);
+        fill_table(a, b * a.pos_sb + (int64_t)t * a.axes, tab, npad, lane);
         float cs[8], sn[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float2 v = tb[m.p0 + i];
+            const float2 v = tab[m.p0 + i];
             cs[i] = v.x;
             sn[i] = v.y;
         }
-        for (int u = wave; u < units; u += waves) {
-            const int side = u >= units0 ? 1 : 0;
-            const int head = (u - (side ? units0 : 0)) * hpw + hg;
-            const bool live = head < a.heads[side];
-            const HeadRows &xr = a.x[side], &yr = a.out[side];
-            const int na = live ? m.n[0] : 0, nb = live ? m.n[1] : 0;
-            float va[8], vb[8], w[2][8];
-            const int64_t xo = b * xr.sb + t * xr.st + head * xr.sh;
-            load_run<F32, PAIR>(xr.p, xo + m.off[0], na, va);
-            load_run<F32, PAIR>(xr.p, xo + m.off[1], nb, vb);
-            if constexpr (NORM) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[0][i] = w[1][i] = 1.0f;
-                if (a.w[side]) {
-                    load_run<true, PAIR>(a.w[side], m.off[0], m.n[0], w[0]);
-                    load_run<true, PAIR>(a.w[side], m.off[1], m.n[1], w[1]);
-                }
+        for (int u = first; u < units; u += step) {
+            const int head = u * hpw + hg;
+            const bool live = head < heads;
+            float va[8], vb[8], da[8], db[8];
+            widen(xa, va);
+            widen(xb, vb);
+            if constexpr (BWD) {
+                widen(ga, da);
+                widen(gb, db);
+            }
+            if (u + step < units) {
+                load(u + step, xa, xb, xr, x0);
+                if constexpr (BWD) load(u + step, ga, gb, gr, g0);
             }
             float r = 1.0f;
             if constexpr (NORM) {
@@ -236,64 +293,57 @@ __global__ void norm_rope_kernel(NormRope a, int lg)
                 if constexpr (NORM) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        va[i] = va[i] * r * w[0][i];
-                        vb[i] = vb[i] * r * w[1][i];
+                        va[i] = va[i] * r * wa[i];
+                        vb[i] = vb[i] * r * wb[i];
                     }
                 }
                 rotate<PAIR>(va, vb, cs, sn, m.nrot);
             } else {
-                const HeadRows &gr = a.g[side];
-                const int64_t go = b * gr.sb + t * gr.st + head * gr.sh;
-                float ga[8], gb[8];
-                load_run<F32, PAIR>(gr.p, go + m.off[0], na, ga);
-                load_run<F32, PAIR>(gr.p, go + m.off[1], nb, gb);
-                rotate<PAIR>(ga, gb, cs, sn, m.nrot);
+                rotate<PAIR>(da, db, cs, sn, m.nrot);
                 float dot = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     va[i] *= r;
                     vb[i] *= r;
-                    if (side) {
-                        dw[1][0][i] = __builtin_fmaf(ga[i], va[i], dw[1][0][i]);
-                        dw[1][1][i] = __builtin_fmaf(gb[i], vb[i], dw[1][1][i]);
-                    } else {
-                        dw[0][0][i] = __builtin_fmaf(ga[i], va[i], dw[0][0][i]);
-                        dw[0][1][i] = __builtin_fmaf(gb[i], vb[i], dw[0][1][i]);
-                    }
-                    ga[i] *= w[0][i];
-                    gb[i] *= w[1][i];
-                    dot = __builtin_fmaf(ga[i], va[i], __builtin_fmaf(gb[i], vb[i], dot));
+                    dwa[i] = __builtin_fmaf(da[i], va[i], dwa[i]);
+                    dwb[i] = __builtin_fmaf(db[i], vb[i], dwb[i]);
+                    da[i] *= wa[i];
+                    db[i] *= wb[i];
+                    dot = __builtin_fmaf(da[i], va[i], __builtin_fmaf(db[i], vb[i], dot));
                 }
                 const float mean = group_sum(dot, lg) * invD;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    va[i] = r * __builtin_fmaf(-va[i], mean, ga[i]);
-                    vb[i] = r * __builtin_fmaf(-vb[i], mean, gb[i]);
+                    va[i] = r * __builtin_fmaf(-va[i], mean, da[i]);
+                    vb[i] = r * __builtin_fmaf(-vb[i], mean, db[i]);
                 }
             }
-            const int64_t yo = b * yr.sb + t * yr.st + head * yr.sh;
-            store_run<F32, PAIR>(yr.p, yo + m.off[0], na, va);
-            store_run<F32, PAIR>(yr.p, yo + m.off[1], nb, vb);
+            const int64_t at = y0 + head * yr.sh;
+            store_run<F32, PAIR>(yr.p, at + m.off[0], live ? m.n[0] : 0, va);
+            store_run<F32, PAIR>(yr.p, at + m.off[1], live ? m.n[1] : 0, vb);
         }
     }
     if constexpr (BWD) {
         // the workgroup's sums: over a wave's head groups, then over its waves
+        // of either side (a wave without a token adds zeros)
         __syncthreads();
         float *const red = lds;   // [wave][side][D]
+        for (int i = lane; i < a.D; i += 64) red[(wave * 2 + (side ^ 1)) * a.D + i] = 0.0f;
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int run = 0; run < 2; ++run)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float v = dw[s][run][i];
-                    for (int k = lph; k < 64; k <<= 1) v += __shfl_xor(v, k, 64);
-                    if (hg == 0 && i < m.n[run]) red[(wave * 2 + s) * a.D + m.off[run] + i] = v;
-                }
+        for (int i = 0; i < 8; ++i) {
+            float va = dwa[i], vb = dwb[i];
+            for (int k = lph; k < 64; k <<= 1) {
+                va += __shfl_xor(va, k, 64);
+                vb += __shfl_xor(vb, k, 64);
+            }
+            float *const dst = red + (wave * 2 + side) * a.D;
+            if (hg == 0 && i < m.n[0]) dst[m.off[0] + i] = va;
+            if (hg == 0 && i < m.n[1]) dst[m.off[1] + i] = vb;
+        }
         __syncthreads();
-        for (int i = threadIdx.x; i < 2 * a.D; i += blockDim.x) {
+        for (int i = threadIdx.x; i < 2 * a.D; i += 256) {
             float v = 0.0f;
-            for (int k = 0; k < waves; ++k) v += red[k * 2 * a.D + i];
+            for (int k = 0; k < 4; ++k) v += red[k * 2 * a.D + i];
             a.partial[(int64_t)blockIdx.x * 2 * a.D + i] = v;
         }
     }
@@ -331,66 +381,81 @@ __global__ __launch_bounds__(256) void rope_tables_kernel(RopeDims dims, int axe
 }
 
 template <bool F32, NormRopeMode MODE>
-void launch_pairing(const NormRope &a, int lg, unsigned grid, unsigned threads, size_t lds,
+void launch_pairing(const NormRope &a, const Shape &sh, unsigned grid, size_t lds,
                     hipStream_t stream)
 {
     if (!a.half)
-        hipLaunchKernelGGL((norm_rope_kernel<F32, MODE, kInterleaved>), dim3(grid), dim3(threads),
-                           lds, stream, a, lg);
+        hipLaunchKernelGGL((norm_rope_kernel<F32, MODE, kInterleaved>), dim3(grid), dim3(256), lds,
+                           stream, a, sh);
     else if (a.R % 16 == 0)
-        hipLaunchKernelGGL((norm_rope_kernel<F32, MODE, kHalf8>), dim3(grid), dim3(threads), lds,
-                           stream, a, lg);
+        hipLaunchKernelGGL((norm_rope_kernel<F32, MODE, kHalf8>), dim3(grid), dim3(256), lds,
+                           stream, a, sh);
     else
-        hipLaunchKernelGGL((norm_rope_kernel<F32, MODE, kHalf4>), dim3(grid), dim3(threads), lds,
-                           stream, a, lg);
+        hipLaunchKernelGGL((norm_rope_kernel<F32, MODE, kHalf4>), dim3(grid), dim3(256), lds,
+                           stream, a, sh);
 }
 
 } // namespace
 
-int64_t norm_rope_partial_rows(int64_t tokens) { return std::min<int64_t>(tokens, 1024); }
+// Waves of a launch when tokens are few (each then takes fewer units), and at
+// most of a backward launch, whose workgroups each write a row of partial sums.
+constexpr int64_t kWaves = 8192, kBackwardWaves = 4096;
+constexpr int kMaxSideWaves = 32;
+constexpr int64_t kMaxSlots = 1 << 22;
+
+int64_t norm_rope_partial_rows(int64_t tokens)
+{
+    return std::min<int64_t>((tokens * 2 * kMaxSideWaves + 3) / 4, kBackwardWaves / 4);
+}
 
 hipError_t launch_norm_rope(NormRopeMode mode, const NormRope &a, hipStream_t stream)
 {
     const int64_t tokens = (int64_t)a.B * a.T;
     const bool bwd = mode == NormRopeMode::BACKWARD;
-    const int64_t grid = bwd ? norm_rope_partial_rows(tokens) : std::min<int64_t>(tokens, 8192);
-    // the sum of the partial rows (none without tokens: zeros)
-    auto weight_grads = [&] {
-        hipLaunchKernelGGL(weight_grad_kernel, dim3(2 * a.D / 16), dim3(256), 0, stream, a.partial,
-                           (int)grid, a.D, a.dw[0], a.heads[1] ? a.dw[1] : nullptr);
-    };
-    if (tokens == 0) {
-        if (bwd) weight_grads();
-        return bwd ? hipGetLastError() : hipSuccess;
-    }
     // lanes of a head: 16 channels each, half-split pairs and the channels
     // that pass unchanged in lanes of their own
     const int half = a.R / 2;
     const int lanes = a.half ? (half + 7) / 8 + (a.D - a.R + 15) / 16 : (a.D + 15) / 16;
-    int lg = 0;
-    while ((1 << lg) < lanes) ++lg;
-    const int hpw = 64 >> lg;
-    const int units = (a.heads[0] + hpw - 1) / hpw + (a.heads[1] + hpw - 1) / hpw;
-    const int waves = std::min(units, bwd && a.D > 256 ? 8 : 16);
-    size_t lds = (size_t)2 * 8 * (1 << lg) * sizeof(float2);
-    if (bwd) lds = std::max(lds, (size_t)waves * 2 * a.D * sizeof(float));
-    const unsigned threads = 64 * waves;
-    switch (mode) {
-    case NormRopeMode::ROPE:
-        a.f32 ? launch_pairing<true, NormRopeMode::ROPE>(a, lg, grid, threads, lds, stream)
-              : launch_pairing<false, NormRopeMode::ROPE>(a, lg, grid, threads, lds, stream);
-        break;
-    case NormRopeMode::NORM:
-        a.f32 ? launch_pairing<true, NormRopeMode::NORM>(a, lg, grid, threads, lds, stream)
-              : launch_pairing<false, NormRopeMode::NORM>(a, lg, grid, threads, lds, stream);
-        break;
-    case NormRopeMode::BACKWARD:
-        a.f32 ? launch_pairing<true, NormRopeMode::BACKWARD>(a, lg, grid, threads, lds, stream)
-              : launch_pairing<false, NormRopeMode::BACKWARD>(a, lg, grid, threads, lds, stream);
-        weight_grads();
-        break;
+    Shape sh = {};
+    while ((1 << sh.lg) < lanes) ++sh.lg;
+    const int hpw = 64 >> sh.lg;
+    int64_t grid = 0;
+    if (tokens > 0) {
+        const int units0 = (a.heads[0] + hpw - 1) / hpw, units1 = (a.heads[1] + hpw - 1) / hpw;
+        // waves per side: its share of kWaves, at least one unit each
+        auto waves = [&](int units) {
+            const int64_t w = (kWaves * units / (units0 + units1) + tokens - 1) / tokens;
+            return (int)std::max<int64_t>(std::min<int64_t>({w, units, kMaxSideWaves}),
+                                          units > 0 ? 1 : 0);
+        };
+        sh.wq = waves(units0);
+        sh.wk = waves(units1);
+        const int W = sh.wq + sh.wk;
+        sh.slots = (int)(bwd ? std::min<int64_t>(tokens, kBackwardWaves / W)
+                              : std::min<int64_t>(tokens, kMaxSlots));
+        grid = ((int64_t)sh.slots * W + 3) / 4;
+        size_t lds = (size_t)4 * 8 * (1 << sh.lg) * sizeof(float2);
+        if (bwd) lds = std::max(lds, (size_t)4 * 2 * a.D * sizeof(float));
+        switch (mode) {
+        case NormRopeMode::ROPE:
+            a.f32 ? launch_pairing<true, NormRopeMode::ROPE>(a, sh, grid, lds, stream)
+                  : launch_pairing<false, NormRopeMode::ROPE>(a, sh, grid, lds, stream);
+            break;
+        case NormRopeMode::NORM:
+            a.f32 ? launch_pairing<true, NormRopeMode::NORM>(a, sh, grid, lds, stream)
+                  : launch_pairing<false, NormRopeMode::NORM>(a, sh, grid, lds, stream);
+            break;
+        case NormRopeMode::BACKWARD:
+            a.f32 ? launch_pairing<true, NormRopeMode::BACKWARD>(a, sh, grid, lds, stream)
+                  : launch_pairing<false, NormRopeMode::BACKWARD>(a, sh, grid, lds, stream);
+            break;
+        }
     }
-    return hipGetLastError();
+    // the sum of the partial rows (none without tokens: zeros)
+    if (bwd)
+        hipLaunchKernelGGL(weight_grad_kernel, dim3(2 * a.D / 16), dim3(256), 0, stream, a.partial,
+                           (int)grid, a.D, a.dw[0], a.heads[1] ? a.dw[1] : nullptr);
+    return bwd || tokens > 0 ? hipGetLastError() : hipSuccess;
 }
 
 hipError_t launch_rope_tables(RopeDims dims, int axes, double theta, bool whole, double *freq,
