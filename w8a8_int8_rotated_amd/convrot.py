@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -94,7 +95,7 @@ class convrot_heads(ctypes.Structure):
 
 _FW = ctypes.POINTER(convrot_fp8_weights)
 _RP = ctypes.POINTER(convrot_rope)
-_H = ctypes.POINTER(convrot_heads)
+_H = ctypes.c_void_p         # const convrot_heads * (byref, or packed bytes)
 
 _SIGNATURES = {
     "convrot_status_string": (ctypes.c_char_p, [_c_int]),
@@ -243,9 +244,12 @@ def _launch(device, fn: str, stream, *args, scratch=()):
     _check(fn, rc)
 
 
+_DTYPE_TAGS = {torch.float32: F32, torch.bfloat16: BF16, torch.int8: I8, torch.int32: I32,
+               torch.float8_e4m3fn: F8E4M3}
+
+
 def _dtype_tag(dt: torch.dtype) -> int:
-    return {torch.float32: F32, torch.bfloat16: BF16, torch.int8: I8, torch.int32: I32,
-            torch.float8_e4m3fn: F8E4M3}[dt]
+    return _DTYPE_TAGS[dt]
 
 
 def _torch_dtype(tag: int) -> torch.dtype:
@@ -840,44 +844,44 @@ def convrot_rope_prepare(dims, head_dim: int, theta: float = 10000.0,
     return RopePlan(desc, freq, axis)
 
 
-def _heads(t, name: str, dtype, B: int, T: int, H: int, D: int):
-    """A [B, T, H, D] (or, with B == 1, [T, H, D]) tensor of per-head rows; any
+# convrot_heads, laid out by struct: several times cheaper to fill per call than
+# a ctypes structure (a bytes object passes as the pointer)
+_HEADS = struct.Struct("Piiqqq")
+assert _HEADS.size == ctypes.sizeof(convrot_heads)
+
+
+def _heads(t, name: str, dtype, lead, H, D: int) -> bytes:
+    """The C view of a tensor of per-head rows [*lead, H, D] (H None: any); any
     strides with contiguous channels."""
     if not isinstance(t, torch.Tensor) or t.dtype != dtype:
         raise ValueError(f"{name} must be a {dtype} tensor")
-    shape = (B, T, H, D)
-    if tuple(t.shape) not in ((shape, shape[1:]) if B == 1 else (shape,)):
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.stride(-1) != 1:
-        raise ValueError(f"{name} must have contiguous channels")
-    return t
-
-
-def _view(t):
-    """The C view of a checked heads tensor (None passes)."""
-    if t is None:
-        return None
+    shape = t.shape
+    if len(shape) != len(lead) + 2:
+        raise ValueError(f"{name} must have as many dimensions as q")
+    if shape[:-2] != lead or shape[-1] != D or (H is not None and shape[-2] != H):
+        want = (*lead, "heads" if H is None else H, D)
+        raise ValueError(f"{name} must have shape {want}, got {tuple(shape)}")
     st = t.stride()
-    return ctypes.byref(convrot_heads(t.data_ptr(), t.shape[-2], 0,
-                                      st[0] if t.dim() == 4 else 0, st[-3], st[-2]))
+    if st[-1] != 1:
+        raise ValueError(f"{name} must have contiguous channels")
+    return _HEADS.pack(t.data_ptr(), shape[-2], 0, st[0] if len(st) == 4 else 0, st[-3], st[-2])
 
 
 def _heads_pair(q, k, rope, positions):
-    """The checks shared by the rope and norm calls: (B, T, position stride)."""
+    """The checks shared by the rope and norm calls: (B, T, position stride),
+    the leading shape and the views of q and k (None without k)."""
     if not isinstance(rope, RopePlan):
         raise ValueError("rope must be a RopePlan from convrot_rope_prepare")
     if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
         raise ValueError("q must be a tensor [B, T, heads, D] or [T, heads, D]")
     if q.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"q must be float32 or bfloat16, got {q.dtype}")
-    B, T = (q.shape[0], q.shape[1]) if q.dim() == 4 else (1, q.shape[0])
-    D = rope.head_dim
-    _heads(q, "q", q.dtype, B, T, q.shape[-2], D)
-    if k is not None:
-        if not isinstance(k, torch.Tensor) or k.dim() != q.dim():
-            raise ValueError("k must have as many dimensions as q")
-        _heads(k, "k", q.dtype, B, T, k.shape[-2], D)
-    return (B, T, _positions(positions, B, T, rope.axes))
+    lead = q.shape[:-2]
+    B, T = lead if len(lead) == 2 else (1, lead[0])
+    D = rope.desc.head_dim
+    vq = _heads(q, "q", q.dtype, lead, None, D)
+    vk = None if k is None else _heads(k, "k", q.dtype, lead, None, D)
+    return B, T, _positions(positions, B, T, rope.desc.axes), lead, vq, vk
 
 
 def _positions(positions, B, T, axes):
@@ -895,18 +899,16 @@ def _positions(positions, B, T, axes):
     return T * axes if len(shape) == 3 else 0
 
 
-def _heads_out(out, name, like):
-    """A caller's output, checked, or a new contiguous one."""
+def _heads_out(out, name, like, lead):
+    """A caller's output, checked, or a new contiguous one, and its view."""
     if like is None:
         if out is not None:
             raise ValueError(f"{name} given without its input")
-        return None
+        return None, None
     if out is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    if out.dim() != like.dim():
-        raise ValueError(f"{name} must have as many dimensions as its input")
-    B, T = (like.shape[0], like.shape[1]) if like.dim() == 4 else (1, like.shape[0])
-    return _heads(out, name, like.dtype, B, T, like.shape[-2], like.shape[-1])
+        out = torch.empty_like(like, memory_format=torch.contiguous_format)
+    H, D = like.shape[-2:]
+    return out, _heads(out, name, like.dtype, lead, H, D)
 
 
 def convrot_rope_forward(q: torch.Tensor, k, rope: RopePlan, positions: torch.Tensor,
@@ -914,13 +916,14 @@ def convrot_rope_forward(q: torch.Tensor, k, rope: RopePlan, positions: torch.Te
     """(q_out, k_out): q and k [B, T, heads, D] turned by the tokens' positions
     [T, axes] or [B, T, axes] (int32 or float32); k may be None.  Out of place
     unless out_q is q.  inverse: by the negative angles, the backward pass."""
-    B, T, psb = _heads_pair(q, k, rope, positions)
-    _on_device(rope.freq.device, q=q, k=k, positions=positions, out_q=out_q, out_k=out_k)
-    out_q, out_k = _heads_out(out_q, "out_q", q), _heads_out(out_k, "out_k", k)
-    _launch(q.device, "convrot_rope_forward", stream, B, T, _dtype_tag(q.dtype), _view(q),
-            _view(out_q), _view(k), _view(out_k), rope.ref(), _ptr(positions),
-            _dtype_tag(positions.dtype), psb, ROPE_INVERSE if inverse else 0,
-            scratch=(out_q, out_k))
+    B, T, psb, lead, vq, vk = _heads_pair(q, k, rope, positions)
+    dev = rope.freq.device
+    _on_device(dev, q=q, k=k, positions=positions, out_q=out_q, out_k=out_k)
+    out_q, oq = _heads_out(out_q, "out_q", q, lead)
+    out_k, ok = _heads_out(out_k, "out_k", k, lead)
+    _launch(dev, "convrot_rope_forward", stream, B, T, _dtype_tag(q.dtype), vq, oq, vk, ok,
+            rope.ref(), _ptr(positions), _dtype_tag(positions.dtype), psb,
+            ROPE_INVERSE if inverse else 0, scratch=(out_q, out_k))
     return out_q, out_k
 
 
@@ -929,15 +932,18 @@ def convrot_qk_norm_rope_forward(q: torch.Tensor, k, w_q, w_k, rope: RopePlan,
                                  out_k=None, stream=None):
     """convrot_rope_forward of q * rsqrt(mean(q^2) + eps) * w_q over each head's
     channels and of k likewise; w_q, w_k float32 [D] or None."""
-    B, T, psb = _heads_pair(q, k, rope, positions)
+    B, T, psb, lead, vq, vk = _heads_pair(q, k, rope, positions)
     _opt(w_q, "w_q", torch.float32, (rope.head_dim,))
     _opt(w_k, "w_k", torch.float32, (rope.head_dim,))
-    _on_device(rope.freq.device, q=q, k=k, w_q=w_q, w_k=w_k, positions=positions, out_q=out_q,
-               out_k=out_k)
-    out_q, out_k = _heads_out(out_q, "out_q", q), _heads_out(out_k, "out_k", k)
-    _launch(q.device, "convrot_qk_norm_rope_forward", stream, B, T, _dtype_tag(q.dtype),
-            _view(q), _view(out_q), _ptr(w_q), _view(k), _view(out_k), _ptr(w_k), eps, rope.ref(),
-            _ptr(positions), _dtype_tag(positions.dtype), psb, scratch=(out_q, out_k))
+    if k is None and w_k is not None:
+        raise ValueError("w_k given without k")
+    dev = rope.freq.device
+    _on_device(dev, q=q, k=k, w_q=w_q, w_k=w_k, positions=positions, out_q=out_q, out_k=out_k)
+    out_q, oq = _heads_out(out_q, "out_q", q, lead)
+    out_k, ok = _heads_out(out_k, "out_k", k, lead)
+    _launch(dev, "convrot_qk_norm_rope_forward", stream, B, T, _dtype_tag(q.dtype), vq, oq,
+            _ptr(w_q), vk, ok, _ptr(w_k), eps, rope.ref(), _ptr(positions),
+            _dtype_tag(positions.dtype), psb, scratch=(out_q, out_k))
     return out_q, out_k
 
 
@@ -952,15 +958,15 @@ def convrot_qk_norm_rope_backward(g_q: torch.Tensor, g_k, q: torch.Tensor, k, w_
     """(dq, dk, dw_q, dw_k) of convrot_qk_norm_rope_forward(q, k, ...) from the
     gradients g_q and g_k of its outputs."""
     lib = library()
-    B, T, psb = _heads_pair(q, k, rope, positions)
+    B, T, psb, lead, vq, vk = _heads_pair(q, k, rope, positions)
     D = rope.head_dim
+    views = []
     for g, x, n in ((g_q, q, "g_q"), (g_k, k, "g_k")):
         if (g is None) != (x is None):
             raise ValueError(f"{n} must be given with its input and only then")
-        if g is not None:
-            if not isinstance(g, torch.Tensor) or g.dim() != x.dim():
-                raise ValueError(f"{n} must have as many dimensions as its input")
-            _heads(g, n, x.dtype, B, T, x.shape[-2], D)
+        views.append(None if g is None else _heads(g, n, x.dtype, lead, x.shape[-2], D))
+    if k is None and w_k is not None:
+        raise ValueError("w_k given without k")
     if k is None and dw_k is not None:
         raise ValueError("dw_k given without k")
     for t, n in ((w_q, "w_q"), (w_k, "w_k"), (dw_q, "dw_q"), (dw_k, "dw_k")):
@@ -971,15 +977,15 @@ def convrot_qk_norm_rope_backward(g_q: torch.Tensor, g_k, q: torch.Tensor, k, w_
     dev = rope.freq.device
     _on_device(dev, g_q=g_q, g_k=g_k, q=q, k=k, w_q=w_q, w_k=w_k, positions=positions, dq=dq,
                dk=dk, dw_q=dw_q, dw_k=dw_k, workspace=workspace)
-    dq, dk = _heads_out(dq, "dq", q), _heads_out(dk, "dk", k)
+    dq, vdq = _heads_out(dq, "dq", q, lead)
+    dk, vdk = _heads_out(dk, "dk", k, lead)
     if dw_q is None:
         dw_q = torch.empty(D, dtype=torch.float32, device=dev)
     if dw_k is None and k is not None:
         dw_k = torch.empty(D, dtype=torch.float32, device=dev)
     ws = _workspace(wsb, dev, workspace)
-    _launch(dev, "convrot_qk_norm_rope_backward", stream, B, T, _dtype_tag(q.dtype), _view(g_q),
-            _view(q), _view(dq), _ptr(w_q), _ptr(dw_q), _view(g_k), _view(k), _view(dk),
-            _ptr(w_k), _ptr(dw_k), eps, rope.ref(), _ptr(positions),
+    _launch(dev, "convrot_qk_norm_rope_backward", stream, B, T, _dtype_tag(q.dtype), views[0],
+            vq, vdq, _ptr(w_q), _ptr(dw_q), views[1], vk, vdk, _ptr(w_k), _ptr(dw_k), eps, rope.ref(), _ptr(positions),
             _dtype_tag(positions.dtype), psb, _ptr(ws), ws.numel() if ws is not None else 0,
             scratch=(dq, dk, dw_q, dw_k, ws))
     return dq, dk, dw_q, dw_k
