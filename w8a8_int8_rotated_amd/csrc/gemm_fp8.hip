@@ -28,6 +28,7 @@
 #include "gemm_common.hpp"
 
 #include <algorithm>
+#include <climits>
 
 namespace convrot {
 namespace {
@@ -40,6 +41,19 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 constexpr int kKB = 128;        // inputs per k-block
 constexpr int kGroup = 4;       // tile-rows per L2 group
+
+// The slot of chunk c of row r in an LDS tile is c ^ lds_swz(r).  A 16 x 16 operand
+// read takes lane (r, g) to chunk g of row r; LDS serves ds_read_b128 in four
+// turns, the first of lanes 0-3, 12-15, 20-23 and 24-27, the second of the other
+// lanes below 32.  With (r >> 2) & 3, as in memory, two lanes of a turn share their
+// banks (half of all LDS cycles were conflicts, SQ_LDS_BANK_CONFLICT); with 0, 2,
+// 3, 1 for the four row quads none do.  A copy's lane fetches the chunk that
+// belongs in its place, from the same contiguous 1 KiB.
+__device__ __forceinline__ int lds_swz(int r)
+{
+    const int q = (r >> 2) & 3;
+    return ((q << 1) & 3) ^ ((q >> 1) * 3);
+}
 
 // One tile's operands: rows past the end are out of range and read as zero.
 struct Src {
@@ -104,79 +118,95 @@ template <int NI, int NJ, bool F32>
 struct State {
     v4f acc[NI][NJ];
     v4f t[NJ];                  // products of the row tile not joined yet
-    float ft[NJ];               // ... and their scales
-    float f[NJ];                // scales of the current k-block
-    v8i a;                      // first row tile of the current k-block
-    Operand<F32> b[NJ];         // its column tiles
+    float f[NJ];                // ... and their scales
+    float sx[NJ], sw;           // the scales of the k-block that begins
+    v8i a, b[NJ];               // its first row tile and its column tiles
 };
 
 // Row tile i of a k-block against the column tiles in registers, while the
-// products of the row tile before it are joined.
+// products of the row tile before it are joined: four additions (16 cycles) beside
+// each matrix instruction.
 template <int NI, int NJ, bool F32>
-__device__ __forceinline__ void row_tile(State<NI, NJ, F32> &st, const v8i &q, int i)
+__device__ __forceinline__ void row_tile(State<NI, NJ, F32> &st, const Operand<F32> &a,
+                                         const Operand<F32> (&b)[NJ], int i)
 {
-    Operand<F32> a;
-    a.set(q);
     v4f t[NJ];
     v4f(&prev)[NJ] = st.acc[i == 0 ? NI - 1 : i - 1];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-        t[j] = product(a, st.b[j]);
-        const float f = i == 0 ? st.ft[j] : st.f[j];
+        t[j] = product(a, b[j]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) prev[j][e] = __builtin_fmaf(st.t[j][e], f, prev[j][e]);
+        for (int e = 0; e < 4; ++e)
+            prev[j][e] = __builtin_fmaf(st.t[j][e], st.f[j], prev[j][e]);
     }
 #pragma unroll
     for (int j = 0; j < NJ; ++j) st.t[j] = t[j];
-    __builtin_amdgcn_sched_barrier(0);
 }
 
-// The row tiles of one k-block but the last, from stage cw; on return the
-// wave has read all of the stage (st.a: the last row tile).
-template <int NI, int NJ, bool F32>
-__device__ __forceinline__ void k_block_head(State<NI, NJ, F32> &st,
-                                             const uint8_t *__restrict__ cw, int off_w)
+// Order of one row tile: the next row tile's LDS reads, then its matrix
+// instructions with the additions (and, in the last row tile, copies) between.
+constexpr int kSgValu = 0x002;
+template <int READS, int MFMAS, int VMEMS>
+__device__ __forceinline__ void order_row_tile()
 {
+    __builtin_amdgcn_sched_group_barrier(kSgDsRead, READS, 0);
 #pragma unroll
-    for (int i = 0; i + 1 < NI; ++i) {
-        const v8i q = st.a;
-        st.a = frag(cw + off_w + (i + 1) * 2048);
-        row_tile(st, q, i);
-    }
-    wait_lds_reads();
-}
-
-// The last row tile, then the first operands of the next k-block, from the
-// stage (nw, nx, ns), which has landed.
-template <int NI, int NJ, bool F32>
-__device__ __forceinline__ void k_block_tail(State<NI, NJ, F32> &st,
-                                             const uint8_t *__restrict__ nw,
-                                             const uint8_t *__restrict__ nx,
-                                             const float *__restrict__ ns, int off_w, int off_x,
-                                             int off_s, float sw_next)
-{
-    const v8i q = st.a;
-    row_tile(st, q, NI - 1);
-    // (not earlier: the column tiles are still being multiplied)
-    st.a = frag(nw + off_w);
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-        st.b[j].set(frag(nx + off_x + j * 2048));
-        st.ft[j] = st.f[j];
-        st.f[j] = ns[off_s + 16 * j] * sw_next;
+    for (int j = 0; j < 4; ++j) {
+        __builtin_amdgcn_sched_group_barrier(kSgMfma, MFMAS, 0);
+        __builtin_amdgcn_sched_group_barrier(kSgValu, 4, 0);
+        if (VMEMS) __builtin_amdgcn_sched_group_barrier(kSgVmemRead, VMEMS, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
 }
+
+// One k-block.  The row tiles but the last come from stage cw; then this wave
+// has read all of the stage and, after the barrier, every wave has, and the next
+// k-block has landed in (nw, nx, ns).  Its first operands are requested ahead of
+// the last row tile, whose column tiles are still in use: two column tiles to
+// registers of their own, the others after it.  COPY refills stage cw.
+#define CONVROT_FP8_K_BLOCK(st, cw, nw, nx, ns, COPY)                                         \
+    do {                                                                                      \
+        Operand<F32> b_[NJ];                                                                  \
+        _Pragma("unroll") for (int j = 0; j < NJ; ++j) b_[j].set(st.b[j]);                    \
+        _Pragma("unroll") for (int i = 0; i + 1 < NI; ++i) {                                  \
+            Operand<F32> a_;                                                                  \
+            a_.set(st.a);                                                                     \
+            st.a = frag(cw + off_w + (i + 1) * 2048);                                         \
+            row_tile(st, a_, b_, i);                                                          \
+            if (i == 0) {                                                                     \
+                _Pragma("unroll") for (int j = 0; j < NJ; ++j) st.f[j] = st.sx[j] * st.sw;    \
+            }                                                                                 \
+            if constexpr (F32) __builtin_amdgcn_sched_barrier(0);                             \
+            else order_row_tile<2, 1, 0>();                                                   \
+        }                                                                                     \
+        Operand<F32> a_;                                                                      \
+        a_.set(st.a);                                                                         \
+        wait_lds_reads();                                                                     \
+        wait_vmcnt<0>();                                                                      \
+        block_barrier();                                                                      \
+        __builtin_amdgcn_sched_barrier(0);                                                    \
+        st.a = frag(nw + off_w);                                                              \
+        const v8i n0_ = frag(nx + off_x), n1_ = frag(nx + off_x + 2048);                      \
+        _Pragma("unroll") for (int j = 0; j < NJ; ++j) st.sx[j] = ns[off_s + 16 * j];         \
+        st.sw = ns[256 + wn_s];                                                               \
+        COPY;                                                                                 \
+        row_tile(st, a_, b_, NI - 1);                                                         \
+        if constexpr (F32) __builtin_amdgcn_sched_barrier(0);                                 \
+        else order_row_tile<6 + NJ + 1, 1, (C + 3) / 4>();                                    \
+        st.b[0] = n0_;                                                                        \
+        st.b[1] = n1_;                                                                        \
+        _Pragma("unroll") for (int j = 2; j < NJ; ++j) st.b[j] = frag(nx + off_x + j * 2048); \
+        __builtin_amdgcn_sched_barrier(0);                                                    \
+    } while (0)
 
 // This wave's copies of k-block kb of a tile into a stage (zeros if `none`).
 template <int CW, int CX>
-__device__ __forceinline__ void copy_block(const Src &s, int kb, bool none, int Mp,
-                                           const uint32_t *vw, const uint32_t *vx, int odd,
+__device__ __forceinline__ void copy_block(const Src &s, int kb, bool none, const uint32_t *vw, const uint32_t *vx, int odd,
                                            uint32_t vs, int wave, int sgrp, uint8_t *dw,
                                            uint8_t *dx, float *ds)
 {
     const __amdgpu_buffer_rsrc_t rw = rsrc(s.w, none ? 0 : s.wn), rx = rsrc(s.x, none ? 0 : s.xn),
-                                 rs = rsrc(s.s + (int64_t)kb * Mp, none ? 0 : s.sn);
+                                 rs = rsrc(s.s, none ? 0 : s.sn);
 #pragma unroll
     for (int j = 0; j < CW; ++j)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -201,7 +231,7 @@ __global__ __launch_bounds__(512, 2) void fp8_gemm_kernel(
     constexpr int CW = TN / 64, CX = TM / 64, C = CW + CX + 1;   // copies per wave and k-block
     __shared__ __attribute__((aligned(1024))) uint8_t sw0[TN * kKB], sw1[TN * kKB];
     __shared__ __attribute__((aligned(1024))) uint8_t sx0[TM * kKB], sx1[TM * kKB];
-    __shared__ __attribute__((aligned(1024))) float ss0[256], ss1[256];
+    __shared__ __attribute__((aligned(1024))) float ss0[320], ss1[320];
     __shared__ __attribute__((aligned(16))) float sbias[TN];
 
     const int tid = threadIdx.x, lane = tid & 63;
@@ -225,49 +255,60 @@ __global__ __launch_bounds__(512, 2) void fp8_gemm_kernel(
         n0 = ((t % width) / gsz) * TN;
         return true;
     };
+    // scales: waves 0-3 copy the tokens' (TM of them, 64 per wave; with fewer
+    // tokens some waves repeat others), waves 4-7 those of the tile's one or two
+    // blocks of 128 weight rows
+    const bool tok = wave < 4;
     auto src_of = [&](int m0, int n0) {
-        return Src{qw + (int64_t)n0 * K, qx + (int64_t)m0 * K, sx + m0, (N - n0) * K,
-                   (Mp - m0) * K, (Mp - m0) * 4};
+        const int row = n0 >> 7, rows = (N + 127) >> 7;
+        return Src{qw + (int64_t)n0 * K, qx + (int64_t)m0 * K,
+                   tok ? sx + m0 : sw + (int64_t)row * nkb, (N - n0) * K, (Mp - m0) * K,
+                   tok ? (Mp - m0) * 4 : row + 1 < rows ? (nkb + 1) * 4 : 4};
     };
-    // the scales of this wave's weight rows: one row of the scale matrix
-    auto sw_row = [&](int n0) {
-        return sw + (int64_t)(min(n0 + wn * 16 * NI, N - 1) >> 7) * nkb;
-    };
+    const int s_step = tok ? Mp : 1;
 
     int m0, n0;
     if (!tile_at(0, m0, n0)) return;
     int nm0 = m0, nn0 = n0;
     bool more = tile_at(1, nm0, nn0);
-    Src cur = src_of(m0, n0), nxt = src_of(nm0, nn0);
-    const float *swc = sw_row(n0), *swn = sw_row(nn0);
+    Src nxt = src_of(nm0, nn0);
 
     // copy c of a stage moves 1 KiB: tile c & 1 of row block c >> 1.  The row's
     // offset is in the lane's offset (the one that is checked against the range),
     // the k-block's in the scalar one
     constexpr int VW = (CW + 1) / 2, VX = (CX + 1) / 2;
     uint32_t vw[VW], vx[VX];
+    const int cr = lane >> 2, cell = cr * 64 + (((lane & 3) ^ swz(cr) ^ lds_swz(cr)) << 4);
 #pragma unroll
-    for (int j = 0; j < VW; ++j) vw[j] = ((wave * CW) / 2 + j) * 16 * K + lane * 16;
+    for (int j = 0; j < VW; ++j) vw[j] = ((wave * CW) / 2 + j) * 16 * K + cell;
 #pragma unroll
-    for (int j = 0; j < VX; ++j) vx[j] = ((wave * CX) / 2 + j) * 16 * K + lane * 16;
+    for (int j = 0; j < VX; ++j) vx[j] = ((wave * CX) / 2 + j) * 16 * K + cell;
     const int odd = CX == 1 ? (wave & 1) * 1024 : 0;
-    // TM scales, 64 per wave; the other waves repeat them
-    const int sgrp = wave & (CX - 1);
-    const uint32_t vs = sgrp * 256 + lane * 4;
+    const int sgrp = tok ? wave & (CX - 1) : 4;
+    const uint32_t vs = tok ? sgrp * 256 + lane * 4 : (lane & 1) * nkb * 4;
 
-    // k-block k of the stream (from nkp on: of the next tile) into a stage;
-    // zeros beyond a tile's k-blocks and after the last tile
-    auto copy = [&](int k, uint8_t *dw, uint8_t *dx, float *ds) {
-        const bool next = k >= nkp;
-        const int kb = next ? k - nkp : k;
-        const bool none = kb >= nkb || (next && !more);
-        copy_block<CW, CX>(next ? nxt : cur, none ? 0 : kb, none, Mp, vw, vx, odd, vs, wave,
-                           sgrp, dw, dx, ds);
+    // The stream of k-blocks: the next one to copy is k-block ikb of `is` (of
+    // nothing, zeros, beyond a tile's k-blocks and after the last tile)
+    Src is = src_of(m0, n0);
+    int ikb = 0;
+    auto copy = [&](uint8_t *dw, uint8_t *dx, float *ds) {
+        const bool none = ikb >= nkb;
+        copy_block<CW, CX>(is, none ? 0 : ikb, none, vw, vx, odd, vs, wave, sgrp, dw, dx, ds);
+        // (selects, not branches: a branch here would split the k-block into
+        // regions the additions get moved across)
+        const bool wrap = ikb + 1 == nkp;
+        is.w = wrap ? nxt.w : is.w;
+        is.x = wrap ? nxt.x : is.x;
+        is.s = wrap ? nxt.s : is.s + (none ? 0 : s_step);
+        is.wn = wrap ? nxt.wn : is.wn;
+        is.xn = wrap ? nxt.xn : is.xn;
+        is.sn = wrap ? nxt.sn : is.sn;
+        ikb = wrap ? (more ? 0 : INT_MAX / 2) : ikb + 1;     // no more: past every k-block
     };
 
-    const int in_tile = r * 64 + ((g ^ swz(r)) << 4);
+    const int in_tile = r * 64 + ((g ^ lds_swz(r)) << 4);
     const int off_w = wn * NI * 2048 + in_tile, off_x = wm * NJ * 2048 + in_tile;
-    const int off_s = wm * NJ * 16 + r;
+    const int off_s = wm * NJ * 16 + r, wn_s = (wn * 16 * NI) >> 7;
 
     float b_reg = 0.0f;
     auto load_bias = [&](int n0_) {
@@ -276,19 +317,17 @@ __global__ __launch_bounds__(512, 2) void fp8_gemm_kernel(
     load_bias(n0);
 
     State<NI, NJ, F32> st;
-    copy(0, sw0, sx0, ss0);
-    copy(1, sw1, sx1, ss1);
+    copy(sw0, sx0, ss0);
+    copy(sw1, sx1, ss1);
     wait_vmcnt<C>();
     block_barrier();
     st.a = frag(sw0 + off_w);
-    {
-        const float s0 = swc[0];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            st.b[j].set(frag(sx0 + off_x + j * 2048));
-            st.f[j] = ss0[off_s + 16 * j] * s0;
-        }
+    for (int j = 0; j < NJ; ++j) {
+        st.b[j] = frag(sx0 + off_x + j * 2048);
+        st.sx[j] = ss0[off_s + 16 * j];
     }
+    st.sw = ss0[256 + wn_s];
 
     for (int it = 0;; ++it) {
 #pragma unroll
@@ -298,27 +337,18 @@ __global__ __launch_bounds__(512, 2) void fp8_gemm_kernel(
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             st.t[j] = (v4f)(0.0f);
-            st.ft[j] = 0.0f;
+            st.f[j] = 0.0f;
         }
         // two k-blocks per round, so that every access names its stage
         for (int k = 0; k < nkp; k += 2) {
-            k_block_head(st, sw0, off_w);
-            wait_vmcnt<0>();       // k-block k + 1 has landed, ...
-            block_barrier();       // ... and this stage is free
-            copy(k + 2, sw0, sx0, ss0);
-            k_block_tail(st, sw1, sx1, ss1, off_w, off_x, off_s, swc[min(k + 1, nkb - 1)]);
-            k_block_head(st, sw1, off_w);
-            wait_vmcnt<0>();
-            block_barrier();
-            copy(k + 3, sw1, sx1, ss1);
-            k_block_tail(st, sw0, sx0, ss0, off_w, off_x, off_s,
-                         *(k + 2 < nkp ? swc + k + 2 : swn));
+            CONVROT_FP8_K_BLOCK(st, sw0, sw1, sx1, ss1, copy(sw0, sx0, ss0));
+            CONVROT_FP8_K_BLOCK(st, sw1, sw0, sx0, ss0, copy(sw1, sx1, ss1));
         }
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                st.acc[NI - 1][j][e] = __builtin_fmaf(st.t[j][e], st.ft[j], st.acc[NI - 1][j][e]);
+                st.acc[NI - 1][j][e] = __builtin_fmaf(st.t[j][e], st.f[j], st.acc[NI - 1][j][e]);
 
         if constexpr (HAS_BIAS) {
             sbias[tid & (TN - 1)] = b_reg;
@@ -360,12 +390,9 @@ __global__ __launch_bounds__(512, 2) void fp8_gemm_kernel(
         if (!more) break;
         m0 = nm0;
         n0 = nn0;
-        cur = nxt;
-        swc = swn;
         load_bias(n0);
         more = tile_at(it + 2, nm0, nn0);
         nxt = src_of(nm0, nn0);
-        swn = sw_row(nn0);
         // sbias is rewritten only after the next tile's barriers
     }
     // no copy may still be writing LDS when the workgroup ends
