@@ -174,8 +174,9 @@ hipError_t launch_fp8_gemm(const uint8_t *qx, const float *sx, const uint8_t *qw
                            int64_t M, int64_t N, int64_t K, hipStream_t stream);
 // The tiled kernels behind launch_fp8_gemm (gemm_fp8.hip).
 hipError_t launch_fp8_gemm_tiled(const uint8_t *qx, const float *sx, const uint8_t *qw,
-                                 const float *sw, const float *bias, void *Y, bool f32_out,
-                                 int64_t M, int64_t N, int64_t K, hipStream_t stream);
+                                 const float *sw, bool pow2, const float *bias, void *Y,
+                                 bool f32_out, int64_t M, int64_t N, int64_t K,
+                                 hipStream_t stream);
 
 // ------------------------------------------ norms and rotary positions ----
 // Per-head rows: element (b, t, h, d) at p + b sb + t st + h sh + d.

@@ -332,7 +332,7 @@ hipError_t launch_fp8_gemm(const uint8_t *qx, const float *sx, const uint8_t *qw
                            int64_t M, int64_t N, int64_t K, hipStream_t stream)
 {
     if (M > 128)
-        return launch_fp8_gemm_tiled(qx, sx, qw, sw, bias, Y, f32_out, M, N, K, stream);
+        return launch_fp8_gemm_tiled(qx, sx, qw, sw, pow2, bias, Y, f32_out, M, N, K, stream);
     return launch_skinny_t<2, 4, false>(qx, sx, qw, sw, pow2, bias, Y, f32_out, M, N, K, 4,
                                         stream);
 }

@@ -84,6 +84,11 @@ __device__ __forceinline__ v8bf bf16_of_codes(int lo, int hi)
     return (v8bf){a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
+// How a kernel multiplies: FP8 products joined by fp32 additions (any scales),
+// FP8 products scaled by the matrix instruction itself (powers of two), or
+// bf16 products (fp32 outputs, any scales).
+enum Math { kAnyScale, kPow2Scale, kBf16 };
+
 // An operand tile as the matrix instructions take it.
 template <bool F32> struct Operand;
 template <> struct Operand<false> {
@@ -114,11 +119,12 @@ __device__ __forceinline__ v4f product(const Operand<true> &a, const Operand<tru
 }
 
 // Registers that live from one k-block to the next.
-template <int NI, int NJ, bool F32>
+template <int NI, int NJ>
 struct State {
     v4f acc[NI][NJ];
     v4f t[NJ];                  // products of the row tile not joined yet
     float f[NJ];                // ... and their scales
+    int ex[NJ], ew;             // kPow2Scale: the k-block's scale exponents
     float sx[NJ], sw;           // the scales of the k-block that begins
     v8i a, b[NJ];               // its first row tile and its column tiles
 };
@@ -126,34 +132,56 @@ struct State {
 // Row tile i of a k-block against the column tiles in registers, while the
 // products of the row tile before it are joined: four additions (16 cycles) beside
 // each matrix instruction.
-template <int NI, int NJ, bool F32>
-__device__ __forceinline__ void row_tile(State<NI, NJ, F32> &st, const Operand<F32> &a,
-                                         const Operand<F32> (&b)[NJ], int i)
+template <Math MATH, int NI, int NJ>
+__device__ __forceinline__ void row_tile(State<NI, NJ> &st, const Operand<MATH == kBf16> &a,
+                                         const Operand<MATH == kBf16> (&b)[NJ], int i)
 {
-    v4f t[NJ];
-    v4f(&prev)[NJ] = st.acc[i == 0 ? NI - 1 : i - 1];
+    if constexpr (MATH == kPow2Scale) {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-        t[j] = product(a, b[j]);
+        for (int j = 0; j < NJ; ++j)
+            st.acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                a.q, b[j].q, st.acc[i][j], 0, 0, 0, st.ew, 0, st.ex[j]);
+    } else {
+        v4f t[NJ];
+        v4f(&prev)[NJ] = st.acc[i == 0 ? NI - 1 : i - 1];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            prev[j][e] = __builtin_fmaf(st.t[j][e], st.f[j], prev[j][e]);
+        for (int j = 0; j < NJ; ++j) {
+            t[j] = product(a, b[j]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                prev[j][e] = __builtin_fmaf(st.t[j][e], st.f[j], prev[j][e]);
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) st.t[j] = t[j];
     }
+}
+
+// The scales of the k-block that begins.  A power of two's exponent field is
+// its e8m0 scale (0 stands for 2^-127, where all codes are 0; 255 for NaN).
+template <Math MATH, int NI, int NJ>
+__device__ __forceinline__ void take_scales(State<NI, NJ> &st)
+{
+    if constexpr (MATH == kPow2Scale) {
+        st.ew = __float_as_uint(st.sw) >> 23;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) st.t[j] = t[j];
+        for (int j = 0; j < NJ; ++j) st.ex[j] = __float_as_uint(st.sx[j]) >> 23;
+    } else {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) st.f[j] = st.sx[j] * st.sw;
+    }
 }
 
 // Order of one row tile: the next row tile's LDS reads, then its matrix
 // instructions with the additions (and, in the last row tile, copies) between.
 constexpr int kSgValu = 0x002;
-template <int READS, int MFMAS, int VMEMS>
+template <Math MATH, int NJ, int READS, int VMEMS>
 __device__ __forceinline__ void order_row_tile()
 {
-    __builtin_amdgcn_sched_group_barrier(kSgDsRead, READS, 0);
+    if constexpr (MATH != kBf16) __builtin_amdgcn_sched_group_barrier(kSgDsRead, READS, 0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        __builtin_amdgcn_sched_group_barrier(kSgMfma, MFMAS, 0);
-        __builtin_amdgcn_sched_group_barrier(kSgValu, 4, 0);
+    for (int j = 0; j < NJ && MATH != kBf16; ++j) {
+        __builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0);
+        if (MATH == kAnyScale) __builtin_amdgcn_sched_group_barrier(kSgValu, 4, 0);
         if (VMEMS) __builtin_amdgcn_sched_group_barrier(kSgVmemRead, VMEMS, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -166,20 +194,18 @@ __device__ __forceinline__ void order_row_tile()
 // registers of their own, the others after it.  COPY refills stage cw.
 #define CONVROT_FP8_K_BLOCK(st, cw, nw, nx, ns, COPY)                                         \
     do {                                                                                      \
-        Operand<F32> b_[NJ];                                                                  \
+        Operand<MATH == kBf16> b_[NJ];                                                                  \
         _Pragma("unroll") for (int j = 0; j < NJ; ++j) b_[j].set(st.b[j]);                    \
         _Pragma("unroll") for (int i = 0; i + 1 < NI; ++i) {                                  \
-            Operand<F32> a_;                                                                  \
+            Operand<MATH == kBf16> a_;                                                                  \
             a_.set(st.a);                                                                     \
             st.a = frag(cw + off_w + (i + 1) * 2048);                                         \
-            row_tile(st, a_, b_, i);                                                          \
-            if (i == 0) {                                                                     \
-                _Pragma("unroll") for (int j = 0; j < NJ; ++j) st.f[j] = st.sx[j] * st.sw;    \
-            }                                                                                 \
-            if constexpr (F32) __builtin_amdgcn_sched_barrier(0);                             \
-            else order_row_tile<2, 1, 0>();                                                   \
+            if (i == 0 && MATH == kPow2Scale) take_scales<MATH>(st);                          \
+            row_tile<MATH>(st, a_, b_, i);                                                    \
+            if (i == 0 && MATH != kPow2Scale) take_scales<MATH>(st);                          \
+            order_row_tile<MATH, NJ, 2, 0>();                                                 \
         }                                                                                     \
-        Operand<F32> a_;                                                                      \
+        Operand<MATH == kBf16> a_;                                                                      \
         a_.set(st.a);                                                                         \
         wait_lds_reads();                                                                     \
         wait_vmcnt<0>();                                                                      \
@@ -190,9 +216,8 @@ __device__ __forceinline__ void order_row_tile()
         _Pragma("unroll") for (int j = 0; j < NJ; ++j) st.sx[j] = ns[off_s + 16 * j];         \
         st.sw = ns[256 + wn_s];                                                               \
         COPY;                                                                                 \
-        row_tile(st, a_, b_, NI - 1);                                                         \
-        if constexpr (F32) __builtin_amdgcn_sched_barrier(0);                                 \
-        else order_row_tile<6 + NJ + 1, 1, (C + 3) / 4>();                                    \
+        row_tile<MATH>(st, a_, b_, NI - 1);                                                   \
+        order_row_tile<MATH, NJ, 6 + NJ + 1, (C + NJ - 1) / NJ>();                            \
         st.b[0] = n0_;                                                                        \
         st.b[1] = n1_;                                                                        \
         _Pragma("unroll") for (int j = 2; j < NJ; ++j) st.b[j] = frag(nx + off_x + j * 2048); \
@@ -221,13 +246,14 @@ __device__ __forceinline__ void copy_block(const Src &s, int kb, bool none, cons
         rs, (__attribute__((address_space(3))) void *)(ds + sgrp * 64), 4, vs, 0, 0, 0);
 }
 
-template <int NI, int NJ, bool F32, bool HAS_BIAS>
+template <int NI, int NJ, Math MATH, bool HAS_BIAS>
 __global__ __launch_bounds__(512, 2) void fp8_gemm_kernel(
     const uint8_t *__restrict__ qx, const float *__restrict__ sx, const uint8_t *__restrict__ qw,
     const float *__restrict__ sw, const float *__restrict__ bias, void *__restrict__ Y, int M,
     int N, int K, int tiles_m, int tiles_n, int tiles_per_xcd, int wgs_per_xcd)
 {
     constexpr int TN = 32 * NI, TM = 64 * NJ;
+    constexpr bool F32 = MATH == kBf16;                          // ... outputs
     constexpr int CW = TN / 64, CX = TM / 64, C = CW + CX + 1;   // copies per wave and k-block
     __shared__ __attribute__((aligned(1024))) uint8_t sw0[TN * kKB], sw1[TN * kKB];
     __shared__ __attribute__((aligned(1024))) uint8_t sx0[TM * kKB], sx1[TM * kKB];
@@ -316,7 +342,7 @@ __global__ __launch_bounds__(512, 2) void fp8_gemm_kernel(
     };
     load_bias(n0);
 
-    State<NI, NJ, F32> st;
+    State<NI, NJ> st;
     copy(sw0, sx0, ss0);
     copy(sw1, sx1, ss1);
     wait_vmcnt<C>();
@@ -345,7 +371,7 @@ __global__ __launch_bounds__(512, 2) void fp8_gemm_kernel(
             CONVROT_FP8_K_BLOCK(st, sw1, sw0, sx0, ss0, copy(sw1, sx1, ss1));
         }
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
+        for (int j = 0; j < NJ && MATH != kPow2Scale; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 st.acc[NI - 1][j][e] = __builtin_fmaf(st.t[j][e], st.f[j], st.acc[NI - 1][j][e]);
@@ -399,7 +425,7 @@ __global__ __launch_bounds__(512, 2) void fp8_gemm_kernel(
     wait_vmcnt<0>();
 }
 
-template <int NI, int NJ, bool F32>
+template <int NI, int NJ, Math MATH>
 hipError_t launch_tile(const uint8_t *qx, const float *sx, const uint8_t *qw, const float *sw,
                        const float *bias, void *Y, int64_t M, int64_t N, int64_t K,
                        hipStream_t stream)
@@ -410,11 +436,11 @@ hipError_t launch_tile(const uint8_t *qx, const float *sx, const uint8_t *qw, co
     const int wgs = std::max(1, std::min(device_cu_count() / 8, per_xcd));
     const dim3 grid(8 * wgs), block(512);
     if (bias)
-        hipLaunchKernelGGL((fp8_gemm_kernel<NI, NJ, F32, true>), grid, block, 0, stream, qx, sx,
+        hipLaunchKernelGGL((fp8_gemm_kernel<NI, NJ, MATH, true>), grid, block, 0, stream, qx, sx,
                            qw, sw, bias, Y, (int)M, (int)N, (int)K, tiles_m, tiles_n, per_xcd,
                            wgs);
     else
-        hipLaunchKernelGGL((fp8_gemm_kernel<NI, NJ, F32, false>), grid, block, 0, stream, qx, sx,
+        hipLaunchKernelGGL((fp8_gemm_kernel<NI, NJ, MATH, false>), grid, block, 0, stream, qx, sx,
                            qw, sw, bias, Y, (int)M, (int)N, (int)K, tiles_m, tiles_n, per_xcd,
                            wgs);
     return hipGetLastError();
@@ -423,11 +449,13 @@ hipError_t launch_tile(const uint8_t *qx, const float *sx, const uint8_t *qw, co
 } // namespace
 
 hipError_t launch_fp8_gemm_tiled(const uint8_t *qx, const float *sx, const uint8_t *qw,
-                                 const float *sw, const float *bias, void *Y, bool f32_out,
-                                 int64_t M, int64_t N, int64_t K, hipStream_t stream)
+                                 const float *sw, bool pow2, const float *bias, void *Y,
+                                 bool f32_out, int64_t M, int64_t N, int64_t K,
+                                 hipStream_t stream)
 {
-    return f32_out ? launch_tile<4, 4, true>(qx, sx, qw, sw, bias, Y, M, N, K, stream)
-                   : launch_tile<8, 4, false>(qx, sx, qw, sw, bias, Y, M, N, K, stream);
+    if (f32_out) return launch_tile<4, 4, kBf16>(qx, sx, qw, sw, bias, Y, M, N, K, stream);
+    return pow2 ? launch_tile<8, 4, kPow2Scale>(qx, sx, qw, sw, bias, Y, M, N, K, stream)
+                : launch_tile<8, 4, kAnyScale>(qx, sx, qw, sw, bias, Y, M, N, K, stream);
 }
 
 } // namespace convrot
