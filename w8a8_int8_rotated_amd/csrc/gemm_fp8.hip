@@ -187,63 +187,86 @@ __device__ __forceinline__ void order_row_tile()
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// One k-block.  The row tiles but the last come from stage cw; then this wave
-// has read all of the stage and, after the barrier, every wave has, and the next
-// k-block has landed in (nw, nx, ns).  Its first operands are requested ahead of
-// the last row tile, whose column tiles are still in use: two column tiles to
-// registers of their own, the others after it.  COPY refills stage cw.
-#define CONVROT_FP8_K_BLOCK(st, cw, nw, nx, ns, COPY)                                         \
+// One k-block, in two halves.  Before the last row tile of a half this wave
+// has read all that the half needs of its stage; then it waits for its copies
+// but the last VM, and the barrier says that every wave has done both:
+//  - at the first half's end the second half's weight rows have landed, and the
+//    first half's and the activations (in registers since the k-block's start)
+//    are free: COPY_A refills them for the k-block after next;
+//  - at the second half's end the next k-block's activations and first half have
+//    landed in (na, nx, ns), and the second half is free (COPY_B).
+// The two halves (ca, cb) are separate LDS objects: a read of one need not wait
+// for copies into the other.
+// Every copy so has one and a half k-blocks to land.  The next k-block's first
+// operands are requested ahead of the last row tile, whose column tiles are still
+// in use: two column tiles to registers of their own, the others after it.
+#define CONVROT_FP8_TURN(VM)                                                                  \
+    wait_lds_reads();                                                                         \
+    wait_vmcnt<VM>();                                                                         \
+    block_barrier();                                                                          \
+    __builtin_amdgcn_sched_barrier(0)
+
+#define CONVROT_FP8_K_BLOCK(st, ca, cb, na, nx, ns, VM, COPY_A, COPY_B)                       \
     do {                                                                                      \
-        Operand<MATH == kBf16> b_[NJ];                                                                  \
+        Operand<MATH == kBf16> b_[NJ];                                                        \
         _Pragma("unroll") for (int j = 0; j < NJ; ++j) b_[j].set(st.b[j]);                    \
         _Pragma("unroll") for (int i = 0; i + 1 < NI; ++i) {                                  \
-            Operand<MATH == kBf16> a_;                                                                  \
+            Operand<MATH == kBf16> a_;                                                        \
             a_.set(st.a);                                                                     \
-            st.a = frag(cw + off_w + (i + 1) * 2048);                                         \
+            if (i + 1 == NI / 2) {                                                            \
+                CONVROT_FP8_TURN(VM);                                                         \
+            }                                                                                 \
+            st.a = frag((i + 1 < NI / 2 ? ca : cb) + off_w + (i + 1) % (NI / 2) * 2048);      \
+            if (i + 1 == NI / 2) COPY_A;                                                      \
             if (i == 0 && MATH == kPow2Scale) take_scales<MATH>(st);                          \
             row_tile<MATH>(st, a_, b_, i);                                                    \
             if (i == 0 && MATH != kPow2Scale) take_scales<MATH>(st);                          \
-            order_row_tile<MATH, NJ, 2, 0>();                                                 \
+            if (i + 1 == NI / 2) order_row_tile<MATH, NJ, 2, (CA + NJ - 1) / NJ>();           \
+            else order_row_tile<MATH, NJ, 2, 0>();                                            \
         }                                                                                     \
-        Operand<MATH == kBf16> a_;                                                                      \
+        Operand<MATH == kBf16> a_;                                                            \
         a_.set(st.a);                                                                         \
-        wait_lds_reads();                                                                     \
-        wait_vmcnt<0>();                                                                      \
-        block_barrier();                                                                      \
-        __builtin_amdgcn_sched_barrier(0);                                                    \
-        st.a = frag(nw + off_w);                                                              \
+        CONVROT_FP8_TURN(VM);                                                                 \
+        st.a = frag(na + off_w);                                                              \
         const v8i n0_ = frag(nx + off_x), n1_ = frag(nx + off_x + 2048);                      \
         _Pragma("unroll") for (int j = 0; j < NJ; ++j) st.sx[j] = ns[off_s + 16 * j];         \
         st.sw = ns[256 + wn_s];                                                               \
-        COPY;                                                                                 \
+        COPY_B;                                                                               \
         row_tile<MATH>(st, a_, b_, NI - 1);                                                   \
-        order_row_tile<MATH, NJ, 6 + NJ + 1, (C + NJ - 1) / NJ>();                            \
+        order_row_tile<MATH, NJ, 6 + NJ + 1, 1>();                                            \
         st.b[0] = n0_;                                                                        \
         st.b[1] = n1_;                                                                        \
         _Pragma("unroll") for (int j = 2; j < NJ; ++j) st.b[j] = frag(nx + off_x + j * 2048); \
         __builtin_amdgcn_sched_barrier(0);                                                    \
     } while (0)
 
-// This wave's copies of k-block kb of a tile into a stage (zeros if `none`).
-template <int CW, int CX>
-__device__ __forceinline__ void copy_block(const Src &s, int kb, bool none, const uint32_t *vw, const uint32_t *vx, int odd,
-                                           uint32_t vs, int wave, int sgrp, uint8_t *dw,
-                                           uint8_t *dx, float *ds)
+// This wave's copies of (half of) the weight rows of a k-block into a stage:
+// CH copies of 1 KiB, of the half whose lane offset is vw.  Zeros if `none`.
+template <int CH>
+__device__ __forceinline__ void copy_weights(const Src &s, int kb, bool none, uint32_t vw,
+                                             uint8_t *dst)
 {
-    const __amdgpu_buffer_rsrc_t rw = rsrc(s.w, none ? 0 : s.wn), rx = rsrc(s.x, none ? 0 : s.xn),
-                                 rs = rsrc(s.s, none ? 0 : s.sn);
+    const __amdgpu_buffer_rsrc_t rw = rsrc(s.w, none ? 0 : s.wn);
 #pragma unroll
-    for (int j = 0; j < CW; ++j)
+    for (int j = 0; j < CH; ++j)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rw, (__attribute__((address_space(3))) void *)(dw + (wave * CW + j) * 1024), 16,
-            vw[j >> 1], kb * 2048 + (j & 1) * 1024, 0, 0);
+            rw, (__attribute__((address_space(3))) void *)(dst + j * 1024), 16, vw,
+            kb * 2048 + j * 1024, 0, 0);
+}
+
+// ... and of its activations and scales.
+template <int CX>
+__device__ __forceinline__ void copy_tokens(const Src &s, int kb, bool none, const uint32_t *vx,
+                                            int odd, uint32_t vs, uint8_t *dst, float *dst_s)
+{
+    const __amdgpu_buffer_rsrc_t rx = rsrc(s.x, none ? 0 : s.xn), rs = rsrc(s.s, none ? 0 : s.sn);
 #pragma unroll
     for (int j = 0; j < CX; ++j)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rx, (__attribute__((address_space(3))) void *)(dx + (wave * CX + j) * 1024), 16,
-            vx[j >> 1], kb * 2048 + (j & 1) * 1024 + odd, 0, 0);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        rs, (__attribute__((address_space(3))) void *)(ds + sgrp * 64), 4, vs, 0, 0, 0);
+            rx, (__attribute__((address_space(3))) void *)(dst + j * 1024), 16, vx[j >> 1],
+            kb * 2048 + (j & 1) * 1024 + odd, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void *)dst_s, 4,
+                                             vs, 0, 0, 0);
 }
 
 template <int NI, int NJ, Math MATH, bool HAS_BIAS>
@@ -254,8 +277,14 @@ __global__ __launch_bounds__(512, 2) void fp8_gemm_kernel(
 {
     constexpr int TN = 32 * NI, TM = 64 * NJ;
     constexpr bool F32 = MATH == kBf16;                          // ... outputs
-    constexpr int CW = TN / 64, CX = TM / 64, C = CW + CX + 1;   // copies per wave and k-block
-    __shared__ __attribute__((aligned(1024))) uint8_t sw0[TN * kKB], sw1[TN * kKB];
+    // copies per wave and k-block: CX of activations and one of scales, twice CH
+    // of weights; CA: those of its first half
+    constexpr int CX = TM / 64, CH = NI / 4, CA = CX + 1 + CH;
+    // copies issued after the ones a turn waits for: half a k-block's of either
+    // kind (a tile's first turn waits for part of the last tile's stores as well)
+    constexpr int VM = CA + CH;
+    __shared__ __attribute__((aligned(1024))) uint8_t wa0[TN * kKB / 2], wb0[TN * kKB / 2],
+        wa1[TN * kKB / 2], wb1[TN * kKB / 2];
     __shared__ __attribute__((aligned(1024))) uint8_t sx0[TM * kKB], sx1[TM * kKB];
     __shared__ __attribute__((aligned(1024))) float ss0[320], ss1[320];
     __shared__ __attribute__((aligned(16))) float sbias[TN];
@@ -299,14 +328,16 @@ __global__ __launch_bounds__(512, 2) void fp8_gemm_kernel(
     bool more = tile_at(1, nm0, nn0);
     Src nxt = src_of(nm0, nn0);
 
-    // copy c of a stage moves 1 KiB: tile c & 1 of row block c >> 1.  The row's
+    // Copy c of a stage moves 1 KiB: tile c & 1 of row block c >> 1.  The row's
     // offset is in the lane's offset (the one that is checked against the range),
-    // the k-block's in the scalar one
-    constexpr int VW = (CW + 1) / 2, VX = (CX + 1) / 2;
-    uint32_t vw[VW], vx[VX];
+    // the k-block's in the scalar one.  Weight halves: row tiles 0 .. NI/2 - 1 of
+    // both waves wn, then the others.
+    constexpr int VX = (CX + 1) / 2;
     const int cr = lane >> 2, cell = cr * 64 + (((lane & 3) ^ swz(cr) ^ lds_swz(cr)) << 4);
-#pragma unroll
-    for (int j = 0; j < VW; ++j) vw[j] = ((wave * CW) / 2 + j) * 16 * K + cell;
+    const int cw = wave * CH, rb = (cw >> 1) / (NI / 2) * NI + (cw >> 1) % (NI / 2);
+    const uint32_t vw0 = rb * 16 * K + (CH == 1 ? (wave & 1) * 1024 : 0) + cell;
+    const uint32_t vw1 = vw0 + NI / 2 * 16 * K;
+    uint32_t vx[VX];
 #pragma unroll
     for (int j = 0; j < VX; ++j) vx[j] = ((wave * CX) / 2 + j) * 16 * K + cell;
     const int odd = CX == 1 ? (wave & 1) * 1024 : 0;
@@ -317,9 +348,15 @@ __global__ __launch_bounds__(512, 2) void fp8_gemm_kernel(
     // nothing, zeros, beyond a tile's k-blocks and after the last tile)
     Src is = src_of(m0, n0);
     int ikb = 0;
-    auto copy = [&](uint8_t *dw, uint8_t *dx, float *ds) {
+    auto copy_a = [&](uint8_t *dw, uint8_t *dx, float *ds) {
         const bool none = ikb >= nkb;
-        copy_block<CW, CX>(is, none ? 0 : ikb, none, vw, vx, odd, vs, wave, sgrp, dw, dx, ds);
+        copy_tokens<CX>(is, none ? 0 : ikb, none, vx, odd, vs, dx + wave * CX * 1024,
+                        ds + sgrp * 64);
+        copy_weights<CH>(is, none ? 0 : ikb, none, vw0, dw + wave * CH * 1024);
+    };
+    auto copy_b = [&](uint8_t *dw) {
+        const bool none = ikb >= nkb;
+        copy_weights<CH>(is, none ? 0 : ikb, none, vw1, dw + wave * CH * 1024);
         // (selects, not branches: a branch here would split the k-block into
         // regions the additions get moved across)
         const bool wrap = ikb + 1 == nkp;
@@ -333,7 +370,7 @@ __global__ __launch_bounds__(512, 2) void fp8_gemm_kernel(
     };
 
     const int in_tile = r * 64 + ((g ^ lds_swz(r)) << 4);
-    const int off_w = wn * NI * 2048 + in_tile, off_x = wm * NJ * 2048 + in_tile;
+    const int off_w = wn * (NI / 2) * 2048 + in_tile, off_x = wm * NJ * 2048 + in_tile;
     const int off_s = wm * NJ * 16 + r, wn_s = (wn * 16 * NI) >> 7;
 
     float b_reg = 0.0f;
@@ -343,11 +380,13 @@ __global__ __launch_bounds__(512, 2) void fp8_gemm_kernel(
     load_bias(n0);
 
     State<NI, NJ> st;
-    copy(sw0, sx0, ss0);
-    copy(sw1, sx1, ss1);
-    wait_vmcnt<C>();
+    copy_a(wa0, sx0, ss0);
+    copy_b(wb0);
+    copy_a(wa1, sx1, ss1);
+    copy_b(wb1);
+    wait_vmcnt<0>();
     block_barrier();
-    st.a = frag(sw0 + off_w);
+    st.a = frag(wa0 + off_w);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
         st.b[j] = frag(sx0 + off_x + j * 2048);
@@ -367,8 +406,8 @@ __global__ __launch_bounds__(512, 2) void fp8_gemm_kernel(
         }
         // two k-blocks per round, so that every access names its stage
         for (int k = 0; k < nkp; k += 2) {
-            CONVROT_FP8_K_BLOCK(st, sw0, sw1, sx1, ss1, copy(sw0, sx0, ss0));
-            CONVROT_FP8_K_BLOCK(st, sw1, sw0, sx0, ss0, copy(sw1, sx1, ss1));
+            CONVROT_FP8_K_BLOCK(st, wa0, wb0, wa1, sx1, ss1, VM, copy_a(wa0, sx0, ss0), copy_b(wb0));
+            CONVROT_FP8_K_BLOCK(st, wa1, wb1, wa0, sx0, ss0, VM, copy_a(wa1, sx1, ss1), copy_b(wb1));
         }
 #pragma unroll
         for (int j = 0; j < NJ && MATH != kPow2Scale; ++j)
