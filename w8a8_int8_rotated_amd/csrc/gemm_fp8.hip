@@ -126,7 +126,7 @@ struct State {
     float f[NJ];                // ... and their scales
     int ex[NJ], ew;             // kPow2Scale: the k-block's scale exponents
     float sx[NJ], sw;           // the scales of the k-block that begins
-    v8i a, b[NJ];               // its first row tile and its column tiles
+    v8i a[2], b[NJ];            // its first two row tiles and its column tiles
 };
 
 // Row tile i of a k-block against the column tiles in registers, while the
@@ -187,8 +187,9 @@ __device__ __forceinline__ void order_row_tile()
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// One k-block, in two halves.  Before the last row tile of a half this wave
-// has read all that the half needs of its stage; then it waits for its copies
+// One k-block, in two halves.  Row tiles are requested two ahead (one ahead
+// leaves a wave that has its SIMD to itself waiting for LDS), so before the last
+// two row tiles of a half this wave has read all that the half needs; then it waits for its copies
 // but the last VM, and the barrier says that every wave has done both:
 //  - at the first half's end the second half's weight rows have landed, and the
 //    first half's and the activations (in registers since the k-block's start)
@@ -197,9 +198,9 @@ __device__ __forceinline__ void order_row_tile()
 //    landed in (na, nx, ns), and the second half is free (COPY_B).
 // The two halves (ca, cb) are separate LDS objects: a read of one need not wait
 // for copies into the other.
-// Every copy so has one and a half k-blocks to land.  The next k-block's first
-// operands are requested ahead of the last row tile, whose column tiles are still
-// in use: two column tiles to registers of their own, the others after it.
+// Every copy so has one and a half k-blocks to land.  The next k-block's column
+// tiles are requested ahead of the last row tile, which still uses the current
+// ones: two to registers of their own, the others after it.
 #define CONVROT_FP8_TURN(VM)                                                                  \
     wait_lds_reads();                                                                         \
     wait_vmcnt<VM>();                                                                         \
@@ -210,30 +211,33 @@ __device__ __forceinline__ void order_row_tile()
     do {                                                                                      \
         Operand<MATH == kBf16> b_[NJ];                                                        \
         _Pragma("unroll") for (int j = 0; j < NJ; ++j) b_[j].set(st.b[j]);                    \
-        _Pragma("unroll") for (int i = 0; i + 1 < NI; ++i) {                                  \
-            Operand<MATH == kBf16> a_;                                                        \
-            a_.set(st.a);                                                                     \
-            if (i + 1 == NI / 2) {                                                            \
+        v8i n0_, n1_;                                                                         \
+        _Pragma("unroll") for (int i = 0; i < NI; ++i) {                                      \
+            if (i == NI / 2 - 2 || i == NI - 2) {                                             \
                 CONVROT_FP8_TURN(VM);                                                         \
             }                                                                                 \
-            st.a = frag((i + 1 < NI / 2 ? ca : cb) + off_w + (i + 1) % (NI / 2) * 2048);      \
-            if (i + 1 == NI / 2) COPY_A;                                                      \
+            Operand<MATH == kBf16> a_;                                                        \
+            a_.set(st.a[0]);                                                                  \
+            st.a[0] = st.a[1];                                                                \
+            st.a[1] = frag((i + 2 >= NI ? na : i + 2 < NI / 2 ? ca : cb) + off_w +            \
+                           (i + 2) % (NI / 2) * 2048);                                        \
+            if (i == NI / 2 - 2) COPY_A;                                                      \
+            if (i == NI - 2) COPY_B;                                                          \
+            if (i == NI - 1) {                                                                \
+                n0_ = frag(nx + off_x);                                                       \
+                n1_ = frag(nx + off_x + 2048);                                                \
+                _Pragma("unroll") for (int j = 0; j < NJ; ++j)                                \
+                    st.sx[j] = ns[off_s + 16 * j];                                            \
+                st.sw = ns[256 + wn_s];                                                       \
+            }                                                                                 \
             if (i == 0 && MATH == kPow2Scale) take_scales<MATH>(st);                          \
             row_tile<MATH>(st, a_, b_, i);                                                    \
             if (i == 0 && MATH != kPow2Scale) take_scales<MATH>(st);                          \
-            if (i + 1 == NI / 2) order_row_tile<MATH, NJ, 2, (CA + NJ - 1) / NJ>();           \
+            if (i == NI - 1) order_row_tile<MATH, NJ, 6 + NJ + 1, 0>();                       \
+            else if (i == NI / 2 - 2) order_row_tile<MATH, NJ, 2, (CA + NJ - 1) / NJ>();      \
+            else if (i == NI - 2) order_row_tile<MATH, NJ, 2, 1>();                           \
             else order_row_tile<MATH, NJ, 2, 0>();                                            \
         }                                                                                     \
-        Operand<MATH == kBf16> a_;                                                            \
-        a_.set(st.a);                                                                         \
-        CONVROT_FP8_TURN(VM);                                                                 \
-        st.a = frag(na + off_w);                                                              \
-        const v8i n0_ = frag(nx + off_x), n1_ = frag(nx + off_x + 2048);                      \
-        _Pragma("unroll") for (int j = 0; j < NJ; ++j) st.sx[j] = ns[off_s + 16 * j];         \
-        st.sw = ns[256 + wn_s];                                                               \
-        COPY_B;                                                                               \
-        row_tile<MATH>(st, a_, b_, NI - 1);                                                   \
-        order_row_tile<MATH, NJ, 6 + NJ + 1, 1>();                                            \
         st.b[0] = n0_;                                                                        \
         st.b[1] = n1_;                                                                        \
         _Pragma("unroll") for (int j = 2; j < NJ; ++j) st.b[j] = frag(nx + off_x + j * 2048); \
@@ -386,7 +390,8 @@ __global__ __launch_bounds__(512, 2) void fp8_gemm_kernel(
     copy_b(wb1);
     wait_vmcnt<0>();
     block_barrier();
-    st.a = frag(wa0 + off_w);
+    st.a[0] = frag(wa0 + off_w);
+    st.a[1] = frag(wa0 + off_w + 2048);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
         st.b[j] = frag(sx0 + off_x + j * 2048);
