@@ -164,19 +164,23 @@ hipError_t launch_fp8_block_weights(const void *W, InType in, int64_t N, int64_t
                                     uint8_t *codes, float *scale, hipStream_t stream);
 hipError_t launch_fp8_quantize(const void *X, int64_t M, int64_t K, bool pow2, uint8_t *q,
                                float *s, hipStream_t stream);
-// Rows that need no quantise pass: launch_fp8_skinny reads bf16 X itself.
+// One product: quantised rows (or, with qx null, bf16 rows X that the kernel for
+// few rows quantises itself: fp8_fuses_quantize) by a prepared weight.
+struct Fp8Gemm {
+    const void *X;
+    const uint8_t *qx;
+    const float *sx;
+    const uint8_t *qw;
+    const float *sw;
+    const float *bias;             // or null
+    void *Y;
+    int64_t M, N, K;
+    bool pow2, f32_out;
+};
 bool fp8_fuses_quantize(int64_t M);
-hipError_t launch_fp8_skinny(const void *X, int64_t M, const uint8_t *qw, const float *sw,
-                             bool pow2, const float *bias, void *Y, bool f32_out, int64_t N,
-                             int64_t K, hipStream_t stream);
-hipError_t launch_fp8_gemm(const uint8_t *qx, const float *sx, const uint8_t *qw,
-                           const float *sw, bool pow2, const float *bias, void *Y, bool f32_out,
-                           int64_t M, int64_t N, int64_t K, hipStream_t stream);
-// The tiled kernels behind launch_fp8_gemm (gemm_fp8.hip).
-hipError_t launch_fp8_gemm_tiled(const uint8_t *qx, const float *sx, const uint8_t *qw,
-                                 const float *sw, bool pow2, const float *bias, void *Y,
-                                 bool f32_out, int64_t M, int64_t N, int64_t K,
-                                 hipStream_t stream);
+hipError_t launch_fp8_gemm(const Fp8Gemm &g, hipStream_t stream);
+// The tiled kernels behind it (gemm_fp8.hip).
+hipError_t launch_fp8_tiles(const Fp8Gemm &g, hipStream_t stream);
 
 // ------------------------------------------ norms and rotary positions ----
 // Per-head rows: element (b, t, h, d) at p + b sb + t st + h sh + d.

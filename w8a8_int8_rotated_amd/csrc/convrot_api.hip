@@ -753,16 +753,18 @@ static int fp8_forward_impl(const void *X, int64_t M, const convrot_fp8_weights 
     if (rc != CONVROT_OK || M == 0) return rc;
     const bool pow2 = W->scales == CONVROT_FP8_SCALE_POW2, f32 = y_dtype == CONVROT_F32;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (convrot::fp8_fuses_quantize(M))
-        return hip_status(convrot::launch_fp8_skinny(X, M, W->codes, W->scale, pow2, bias, Y, f32,
-                                                     W->N, W->K, s));
-    Carve c(ws);
-    uint8_t *q = static_cast<uint8_t *>(c.take(codes_bytes(M, W->K)));
-    float *sx = static_cast<float *>(c.take(fp8_row_scales_bytes(M, W->K)));
-    hipError_t e = convrot::launch_fp8_quantize(X, M, W->K, pow2, q, sx, s);
-    if (e == hipSuccess)
-        e = convrot::launch_fp8_gemm(q, sx, W->codes, W->scale, pow2, bias, Y, f32, M, W->N, W->K,
-                                     s);
+    convrot::Fp8Gemm g = {X, nullptr, nullptr, W->codes, W->scale, bias, Y, M, W->N, W->K, pow2,
+                          f32};
+    hipError_t e = hipSuccess;
+    if (!convrot::fp8_fuses_quantize(M)) {
+        Carve c(ws);
+        uint8_t *q = static_cast<uint8_t *>(c.take(codes_bytes(M, W->K)));
+        float *sx = static_cast<float *>(c.take(fp8_row_scales_bytes(M, W->K)));
+        e = convrot::launch_fp8_quantize(X, M, W->K, pow2, q, sx, s);
+        g.qx = q;
+        g.sx = sx;
+    }
+    if (e == hipSuccess) e = convrot::launch_fp8_gemm(g, s);
     return hip_status(e);
 }
 
@@ -799,10 +801,9 @@ int convrot_fp8_gemm_dequant(const uint8_t *q, const float *s, int64_t M,
     if (!q || !s || !Y) return CONVROT_EINVAL;
     if (!aligned16(q) || !aligned16(s) || !aligned16(Y) || (bias && !aligned16(bias)))
         return CONVROT_EALIGN;
-    return hip_status(convrot::launch_fp8_gemm(q, s, W->codes, W->scale,
-                                               W->scales == CONVROT_FP8_SCALE_POW2, bias, Y,
-                                               y_dtype == CONVROT_F32, M, W->N, W->K,
-                                               static_cast<hipStream_t>(stream)));
+    const convrot::Fp8Gemm g = {nullptr, q, s, W->codes, W->scale, bias, Y, M, W->N, W->K,
+                                W->scales == CONVROT_FP8_SCALE_POW2, y_dtype == CONVROT_F32};
+    return hip_status(convrot::launch_fp8_gemm(g, static_cast<hipStream_t>(stream)));
 }
 
 // ---------------------------------------------------------------------------

@@ -135,25 +135,34 @@ __global__ __launch_bounds__(256) void block_weights_kernel(const T *__restrict_
 
 // Rows: a wave takes 4 rows x one 128-input block per step, 16 lanes x 8 inputs
 // per row, so a step writes two contiguous 256-byte pieces (4 rows of a K-tile).
-// A workgroup is the 16 rows of a row block; blockIdx.y splits the k-blocks.
+// A workgroup is the 16 rows of a row block; blockIdx.y splits the k-blocks, KBS
+// to a workgroup, whose loads all go out first.
+template <int KBS>
 __global__ __launch_bounds__(256) void quantize_kernel(const uint16_t *__restrict__ X, int M,
                                                        int K, bool pow2,
                                                        uint8_t *__restrict__ q,
-                                                       float *__restrict__ s, int kb_per)
+                                                       float *__restrict__ s)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int m = blockIdx.x * 16 + wave * 4 + (lane >> 4), c = (lane & 15) * 8;
-    const int nkb = K / 128, kb0 = blockIdx.y * kb_per, kb1 = min(nkb, kb0 + kb_per);
+    const int nkb = K / 128, kb0 = blockIdx.y * KBS;
     const int64_t Mp = padded_rows(M);
     const bool live = m < M;
-    for (int kb = kb0; kb < kb1; ++kb) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (live) u = *reinterpret_cast<const uint4 *>(X + (int64_t)m * K + kb * 128 + c);
-        const float amax = max16(max8(u));
+    uint4 u[KBS];
+#pragma unroll
+    for (int i = 0; i < KBS; ++i) {
+        u[i] = make_uint4(0, 0, 0, 0);
+        if (live && kb0 + i < nkb)
+            u[i] = *reinterpret_cast<const uint4 *>(X + (int64_t)m * K + (kb0 + i) * 128 + c);
+    }
+#pragma unroll
+    for (int i = 0; i < KBS; ++i) {
+        const int kb = kb0 + i;
+        const float amax = max16(max8(u[i]));
         float sc, inv;
         block_scale(amax, pow2, sc, inv);
-        if (!live) continue;
-        *reinterpret_cast<int2 *>(q + tiled_offset(m, kb * 128 + c, K)) = codes8(u, inv);
+        if (!live || kb >= nkb) continue;
+        *reinterpret_cast<int2 *>(q + tiled_offset(m, kb * 128 + c, K)) = codes8(u[i], inv);
         if ((lane & 15) == 0) s[kb * Mp + m] = sc;
     }
 }
@@ -275,19 +284,20 @@ __global__ __launch_bounds__(1024) void skinny_kernel(const void *__restrict__ X
 }
 
 template <int RT, int MT, bool FUSE>
-hipError_t launch_skinny_t(const void *X, const float *sx, const uint8_t *qw, const float *sw,
-                           bool pow2, const float *bias, void *Y, bool f32_out, int64_t M,
-                           int64_t N, int64_t K, int waves, hipStream_t stream)
+hipError_t launch_skinny(const Fp8Gemm &g, int waves, hipStream_t stream)
 {
-    const dim3 grid((unsigned)((N / 16 + RT - 1) / RT),
-                    (unsigned)(((M + 15) / 16 + MT - 1) / MT));
+    const dim3 grid((unsigned)((g.N / 16 + RT - 1) / RT),
+                    (unsigned)(((g.M + 15) / 16 + MT - 1) / MT));
     const size_t lds = (size_t)waves * RT * MT * 256 * sizeof(float);
-    if (f32_out)
+    const void *const X = FUSE ? g.X : g.qx;
+    if (g.f32_out)
         hipLaunchKernelGGL((skinny_kernel<RT, MT, FUSE, true>), grid, dim3(64 * waves), lds, stream,
-                           X, sx, qw, sw, bias, Y, pow2, (int)M, (int)N, (int)K);
+                           X, g.sx, g.qw, g.sw, g.bias, g.Y, g.pow2, (int)g.M, (int)g.N,
+                           (int)g.K);
     else
         hipLaunchKernelGGL((skinny_kernel<RT, MT, FUSE, false>), grid, dim3(64 * waves), lds,
-                           stream, X, sx, qw, sw, bias, Y, pow2, (int)M, (int)N, (int)K);
+                           stream, X, g.sx, g.qw, g.sw, g.bias, g.Y, g.pow2, (int)g.M, (int)g.N,
+                           (int)g.K);
     return hipGetLastError();
 }
 
@@ -310,31 +320,27 @@ hipError_t launch_fp8_quantize(const void *X, int64_t M, int64_t K, bool pow2, u
                                float *s, hipStream_t stream)
 {
     if (M == 0) return hipSuccess;
-    const int nkb = (int)(K / 128), per = 8;
-    const dim3 grid((unsigned)((M + 15) / 16), (unsigned)((nkb + per - 1) / per));
-    hipLaunchKernelGGL(quantize_kernel, grid, dim3(256), 0, stream,
-                       static_cast<const uint16_t *>(X), (int)M, (int)K, pow2, q, s, per);
+    constexpr int kbs = 4;
+    const dim3 grid((unsigned)((M + 15) / 16), (unsigned)((K / 128 + kbs - 1) / kbs));
+    hipLaunchKernelGGL(quantize_kernel<kbs>, grid, dim3(256), 0, stream,
+                       static_cast<const uint16_t *>(X), (int)M, (int)K, pow2, q, s);
     return hipGetLastError();
 }
 
 bool fp8_fuses_quantize(int64_t M) { return M <= 16; }
 
-hipError_t launch_fp8_skinny(const void *X, int64_t M, const uint8_t *qw, const float *sw,
-                             bool pow2, const float *bias, void *Y, bool f32_out, int64_t N,
-                             int64_t K, hipStream_t stream)
+// Up to 64 rows the weights are read once whatever the kernel, and the tiles'
+// LDS pipeline is slower than loads straight to registers (64 rows at N = K = 5376:
+// 12.3 us against 16.9 us of the best tiles); from 65 rows on the tiles win (128
+// rows: 17.3 us against 17.8 us).  F32 outputs: 128 rows 18.2 us against 34.0 us,
+// 333 rows 33.7 us against 36.8 us, but 105 us against 81 us at N = 16128.
+hipError_t launch_fp8_gemm(const Fp8Gemm &g, hipStream_t stream)
 {
-    return launch_skinny_t<2, 1, true>(X, nullptr, qw, sw, pow2, bias, Y, f32_out, M, N, K, 4,
-                                       stream);
-}
-
-hipError_t launch_fp8_gemm(const uint8_t *qx, const float *sx, const uint8_t *qw,
-                           const float *sw, bool pow2, const float *bias, void *Y, bool f32_out,
-                           int64_t M, int64_t N, int64_t K, hipStream_t stream)
-{
-    if (M > 128)
-        return launch_fp8_gemm_tiled(qx, sx, qw, sw, pow2, bias, Y, f32_out, M, N, K, stream);
-    return launch_skinny_t<2, 4, false>(qx, sx, qw, sw, pow2, bias, Y, f32_out, M, N, K, 4,
-                                        stream);
+    if (!g.qx) return launch_skinny<2, 1, true>(g, 4, stream);
+    if (g.M <= 16) return launch_skinny<2, 1, false>(g, 8, stream);
+    if (g.M <= 32) return launch_skinny<2, 2, false>(g, 8, stream);
+    if (g.M <= 64 || (g.f32_out && g.M <= 256)) return launch_skinny<2, 4, false>(g, 8, stream);
+    return launch_fp8_tiles(g, stream);
 }
 
 } // namespace convrot

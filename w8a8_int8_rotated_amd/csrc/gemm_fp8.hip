@@ -225,7 +225,7 @@ __device__ __forceinline__ void order_row_tile()
             if (i == NI - 2) COPY_B;                                                          \
             if (i == NI - 1) {                                                                \
                 n0_ = frag(nx + off_x);                                                       \
-                n1_ = frag(nx + off_x + 2048);                                                \
+                if constexpr (NJ > 1) n1_ = frag(nx + off_x + 2048);                          \
                 _Pragma("unroll") for (int j = 0; j < NJ; ++j)                                \
                     st.sx[j] = ns[off_s + 16 * j];                                            \
                 st.sw = ns[256 + wn_s];                                                       \
@@ -233,13 +233,13 @@ __device__ __forceinline__ void order_row_tile()
             if (i == 0 && MATH == kPow2Scale) take_scales<MATH>(st);                          \
             row_tile<MATH>(st, a_, b_, i);                                                    \
             if (i == 0 && MATH != kPow2Scale) take_scales<MATH>(st);                          \
-            if (i == NI - 1) order_row_tile<MATH, NJ, 6 + NJ + 1, 0>();                       \
+            if (i == NI - 1) order_row_tile<MATH, NJ, 5 + NJ + 2 * (NJ > 1), 0>();            \
             else if (i == NI / 2 - 2) order_row_tile<MATH, NJ, 2, (CA + NJ - 1) / NJ>();      \
             else if (i == NI - 2) order_row_tile<MATH, NJ, 2, 1>();                           \
             else order_row_tile<MATH, NJ, 2, 0>();                                            \
         }                                                                                     \
         st.b[0] = n0_;                                                                        \
-        st.b[1] = n1_;                                                                        \
+        if constexpr (NJ > 1) st.b[NJ > 1] = n1_;                                             \
         _Pragma("unroll") for (int j = 2; j < NJ; ++j) st.b[j] = frag(nx + off_x + j * 2048); \
         __builtin_amdgcn_sched_barrier(0);                                                    \
     } while (0)
@@ -277,7 +277,7 @@ template <int NI, int NJ, Math MATH, bool HAS_BIAS>
 __global__ __launch_bounds__(512, 2) void fp8_gemm_kernel(
     const uint8_t *__restrict__ qx, const float *__restrict__ sx, const uint8_t *__restrict__ qw,
     const float *__restrict__ sw, const float *__restrict__ bias, void *__restrict__ Y, int M,
-    int N, int K, int tiles_m, int tiles_n, int tiles_per_xcd, int wgs_per_xcd)
+    int N, int K, int m_base, int tiles_m, int tiles_n, int tiles_per_xcd, int wgs_per_xcd)
 {
     constexpr int TN = 32 * NI, TM = 64 * NJ;
     constexpr bool F32 = MATH == kBf16;                          // ... outputs
@@ -310,7 +310,7 @@ __global__ __launch_bounds__(512, 2) void fp8_gemm_kernel(
         const int width = kGroup * tiles_n;
         const int first_m = (t / width) * kGroup;
         const int gsz = min(tiles_m - first_m, kGroup);
-        m0 = (first_m + (t % width) % gsz) * TM;
+        m0 = m_base + (first_m + (t % width) % gsz) * TM;
         n0 = ((t % width) / gsz) * TN;
         return true;
     };
@@ -469,37 +469,93 @@ __global__ __launch_bounds__(512, 2) void fp8_gemm_kernel(
     wait_vmcnt<0>();
 }
 
+// Rows m_base .. m_base + rows - 1 of the product, in 32 NI (n) x 64 NJ (m) tiles.
 template <int NI, int NJ, Math MATH>
-hipError_t launch_tile(const uint8_t *qx, const float *sx, const uint8_t *qw, const float *sw,
-                       const float *bias, void *Y, int64_t M, int64_t N, int64_t K,
-                       hipStream_t stream)
+hipError_t launch_tile(const Fp8Gemm &g, int64_t m_base, int64_t rows, hipStream_t stream)
 {
     constexpr int TN = 32 * NI, TM = 64 * NJ;
-    const int tiles_m = (int)((M + TM - 1) / TM), tiles_n = (int)((N + TN - 1) / TN);
+    const int tiles_m = (int)((rows + TM - 1) / TM), tiles_n = (int)((g.N + TN - 1) / TN);
     const int per_xcd = (tiles_m * tiles_n + 7) / 8;
     const int wgs = std::max(1, std::min(device_cu_count() / 8, per_xcd));
     const dim3 grid(8 * wgs), block(512);
-    if (bias)
-        hipLaunchKernelGGL((fp8_gemm_kernel<NI, NJ, MATH, true>), grid, block, 0, stream, qx, sx,
-                           qw, sw, bias, Y, (int)M, (int)N, (int)K, tiles_m, tiles_n, per_xcd,
-                           wgs);
+    if (g.bias)
+        hipLaunchKernelGGL((fp8_gemm_kernel<NI, NJ, MATH, true>), grid, block, 0, stream, g.qx,
+                           g.sx, g.qw, g.sw, g.bias, g.Y, (int)g.M, (int)g.N, (int)g.K,
+                           (int)m_base, tiles_m, tiles_n, per_xcd, wgs);
     else
-        hipLaunchKernelGGL((fp8_gemm_kernel<NI, NJ, MATH, false>), grid, block, 0, stream, qx, sx,
-                           qw, sw, bias, Y, (int)M, (int)N, (int)K, tiles_m, tiles_n, per_xcd,
-                           wgs);
+        hipLaunchKernelGGL((fp8_gemm_kernel<NI, NJ, MATH, false>), grid, block, 0, stream, g.qx,
+                           g.sx, g.qw, g.sw, g.bias, g.Y, (int)g.M, (int)g.N, (int)g.K,
+                           (int)m_base, tiles_m, tiles_n, per_xcd, wgs);
     return hipGetLastError();
 }
 
+template <Math MATH>
+hipError_t launch_shape(int tn, int tm, const Fp8Gemm &g, int64_t m_base, int64_t rows,
+                        hipStream_t stream)
+{
+    if constexpr (MATH != kBf16) {
+        if (tn == 256)
+            return tm == 256   ? launch_tile<8, 4, MATH>(g, m_base, rows, stream)
+                   : tm == 128 ? launch_tile<8, 2, MATH>(g, m_base, rows, stream)
+                               : launch_tile<8, 1, MATH>(g, m_base, rows, stream);
+    }
+    return tm == 256   ? launch_tile<4, 4, MATH>(g, m_base, rows, stream)
+           : tm == 128 ? launch_tile<4, 2, MATH>(g, m_base, rows, stream)
+                       : launch_tile<4, 1, MATH>(g, m_base, rows, stream);
+}
+
+// Tile shapes and the time of one tile per CU, in units of the largest shape's;
+// measured at K = 5376: bf16 outputs 56 us for 256 x 256 (any scales; M = 256 at
+// N = 5376 leaves one per CU), F32 outputs 70 us for 128 x 256.
+struct TileShape {
+    int tn, tm;
+    double cost;
+};
+constexpr TileShape kFp8Shapes[] = {{256, 256, 1.0}, {256, 128, 0.64}, {128, 256, 0.64},
+                                    {256, 64, 0.46}, {128, 128, 0.42}, {128, 64, 0.32}};
+constexpr TileShape kBf16Shapes[] = {{128, 256, 1.0}, {128, 128, 0.61}, {128, 64, 0.49}};
+constexpr double kSecondLaunch = 0.06;
+
 } // namespace
 
-hipError_t launch_fp8_gemm_tiled(const uint8_t *qx, const float *sx, const uint8_t *qw,
-                                 const float *sw, bool pow2, const float *bias, void *Y,
-                                 bool f32_out, int64_t M, int64_t N, int64_t K,
-                                 hipStream_t stream)
+// The plan with the least estimated time: one shape throughout, or whole rounds
+// of the largest shape and another one for the last rows (M = 4096 at
+// N = K = 5376: 252 tiles of 256 x 256, then 1024 rows in 168 of 256 x 128).
+hipError_t launch_fp8_tiles(const Fp8Gemm &g, hipStream_t stream)
 {
-    if (f32_out) return launch_tile<4, 4, kBf16>(qx, sx, qw, sw, bias, Y, M, N, K, stream);
-    return pow2 ? launch_tile<8, 4, kPow2Scale>(qx, sx, qw, sw, bias, Y, M, N, K, stream)
-                : launch_tile<8, 4, kAnyScale>(qx, sx, qw, sw, bias, Y, M, N, K, stream);
+    const TileShape *const shapes = g.f32_out ? kBf16Shapes : kFp8Shapes;
+    const int n_shapes = g.f32_out ? 3 : 6;
+    const int64_t cus = device_cu_count();
+    auto cost = [&](int i, int64_t rows) {
+        const int64_t tiles = (rows + shapes[i].tm - 1) / shapes[i].tm *
+                              ((g.N + shapes[i].tn - 1) / shapes[i].tn);
+        return (double)((tiles + cus - 1) / cus) * shapes[i].cost;
+    };
+    int best = 0;
+    int64_t m1 = 0;                  // rows of the first launch (shape 0)
+    double best_cost = 1e30;
+    for (int i = 0; i < n_shapes; ++i) {
+        const double c = cost(i, g.M);
+        if (c < best_cost) best = i, best_cost = c;
+    }
+    const int64_t rows0 = (g.M - 1) / shapes[0].tm;      // whole tile-rows before the last
+    for (int64_t a = rows0; a > 0 && a > rows0 - 16; --a)
+        for (int i = 1; i < n_shapes; ++i) {
+            const double c = cost(0, a * shapes[0].tm) + cost(i, g.M - a * shapes[0].tm) +
+                             kSecondLaunch;
+            if (c < best_cost - 0.1) best = i, best_cost = c, m1 = a * shapes[0].tm;
+        }
+    auto launch = [&](int i, int64_t base, int64_t rows) {
+        const int tn = shapes[i].tn, tm = shapes[i].tm;
+        return g.f32_out ? launch_shape<kBf16>(tn, tm, g, base, rows, stream)
+               : g.pow2  ? launch_shape<kPow2Scale>(tn, tm, g, base, rows, stream)
+                         : launch_shape<kAnyScale>(tn, tm, g, base, rows, stream);
+    };
+    if (m1 > 0) {
+        const hipError_t e = launch(0, 0, m1);
+        if (e != hipSuccess) return e;
+    }
+    return launch(best, m1, g.M - m1);
 }
 
 } // namespace convrot
