@@ -177,7 +177,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(const uint16_t *__restric
 // same arithmetic as quantize_kernel.
 // F32: fp32 outputs, summed with the bf16 matrix instructions (see above).
 template <int RT, int MT, bool FUSE, bool F32>
-__global__ __launch_bounds__(1024) void skinny_kernel(const void *__restrict__ X,
+__global__ __launch_bounds__(512) void skinny_kernel(const void *__restrict__ X,
                                                       const float *__restrict__ sx,
                                                       const uint8_t *__restrict__ qw,
                                                       const float *__restrict__ sw,
@@ -336,7 +336,18 @@ bool fp8_fuses_quantize(int64_t M) { return M <= 16; }
 // 333 rows 33.7 us against 36.8 us, but 105 us against 81 us at N = 16128.
 hipError_t launch_fp8_gemm(const Fp8Gemm &g, hipStream_t stream)
 {
-    if (!g.qx) return launch_skinny<2, 1, true>(g, 4, stream);
+    if (!g.qx) {
+        // Row tiles per workgroup, which shares one quantised k-block of the rows
+        // among them: 4 where that still gives one workgroup per CU (8 rows at
+        // N = 32256, K = 5376: 31.6 us, 34.6 us with 2; one row at N = 16128: 17.1 us,
+        // 17.7 us), 1 where 2 would leave most CUs without one (16 rows at
+        // N = 1024, K = 21504: 27.2 us, 30.1 us), else 2 (one row at N = K = 5376:
+        // 7.9 us, with 4 9.2 us, with 1 9.9 us).
+        const int64_t cus = device_cu_count(), blocks = g.N / 16;
+        if (blocks >= 4 * cus - 16) return launch_skinny<4, 1, true>(g, 8, stream);
+        if (2 * blocks <= cus) return launch_skinny<1, 1, true>(g, 8, stream);
+        return launch_skinny<2, 1, true>(g, 8, stream);
+    }
     if (g.M <= 16) return launch_skinny<2, 1, false>(g, 8, stream);
     if (g.M <= 32) return launch_skinny<2, 2, false>(g, 8, stream);
     if (g.M <= 64 || (g.f32_out && g.M <= 256)) return launch_skinny<2, 4, false>(g, 8, stream);

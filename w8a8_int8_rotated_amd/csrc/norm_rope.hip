@@ -9,10 +9,13 @@
 // Each row is read and written once, so the bound is memory: 4 bytes per bf16
 // element forward, 6 backward.
 //
-// A lane holds 16 channels of a head, two runs of 8: adjacent ones when pairs
-// are interleaved, 8 channels and their 8 partners for the half-split pairs, so
-// that a rotation never leaves the lane.  A head is LPH lanes (a power of two), a
-// wave 64 / LPH heads ("unit"), and the norm's sum runs over the LPH lanes with DPP.
+// A lane holds 8 channels of a head, two runs of 4, so that a rotation never
+// leaves the lane: for half-split pairs the second run holds the first's partners.
+// Neighbouring lanes hold neighbouring runs, so loads and stores cover whole cache
+// lines.  A head is LPH lanes (a power of two), a wave 64 / LPH heads ("unit"), and
+// the norm's sum runs over the LPH lanes with DPP.  (16 channels a lane left the
+// backward pass three waves per SIMD, 576 us for 84 heads of 38656 tokens, or
+// spilled registers.)
 //
 // A wave takes units of the queries or of the keys of one token (all of them
 // when tokens are many).  It evaluates the token's R/2 cosines and sines once,
@@ -32,7 +35,7 @@
 namespace convrot {
 namespace {
 
-enum Pairing { kInterleaved = 0, kHalf8 = 1, kHalf4 = 2 };
+enum Pairing { kInterleaved = 0, kHalf = 1 };
 
 // Sum over aligned groups of 1 << lg lanes (lg uniform).
 __device__ __forceinline__ float group_sum(float v, int lg)
@@ -49,71 +52,66 @@ __device__ __forceinline__ float group_sum(float v, int lg)
     return v;
 }
 
-// The channels of one lane: two runs of up to 8, starting at a and b, and its
-// first pair.  n[0], n[1]: channels in each run (0, 4 or 8); nrot: how many of
-// its 8 pairs are rotated.
+// The channels of one lane: two runs of 4, starting at off[0] and off[1], present
+// if on[0], on[1]; the pairs of either run start at p[0], p[1] (2 each when
+// interleaved; half-split, the 4 pairs between the runs), and the first rot[0], rot[1]
+// of them are rotated.
 struct LaneMap {
-    int off[2], n[2], p0, nrot;
+    int off[2], p[2], rot[2];
+    bool on[2];
 };
 
-template <int PAIR>
+template <bool F32, int PAIR>
 __device__ __forceinline__ LaneMap lane_map(int c, int D, int R)
 {
     LaneMap m;
     const int half = R >> 1;
-    m.p0 = 8 * c;
-    m.nrot = min(max(half - 8 * c, 0), 8);
     if (PAIR == kInterleaved) {
-        m.off[0] = 16 * c;
-        m.off[1] = 16 * c + 8;
-        m.n[0] = m.off[0] < D ? 8 : 0;
-        m.n[1] = m.off[1] < D ? 8 : 0;
+        // bf16: one run of 8 (16 bytes); fp32: one run of 4 in either half of the head
+        m.off[0] = F32 ? 4 * c : 8 * c;
+        m.off[1] = F32 ? D / 2 + 4 * c : 8 * c + 4;
+        m.on[0] = m.on[1] = 8 * c < D;
+        m.p[0] = m.off[0] >> 1;
+        m.p[1] = m.on[0] ? m.off[1] >> 1 : m.p[0];
+        m.rot[0] = min(max(half - m.p[0], 0), 2);
+        m.rot[1] = min(max(half - m.p[1], 0), 2);
     } else {
-        const int lanes = (half + 7) >> 3;     // lanes that rotate
-        if (c < lanes) {
-            m.off[0] = 8 * c;
-            m.off[1] = half + 8 * c;
-            m.n[0] = m.n[1] = m.nrot;
-        } else {
-            m.off[0] = R + 16 * (c - lanes);
-            m.off[1] = m.off[0] + 8;
-            m.n[0] = m.off[0] < D ? 8 : 0;
-            m.n[1] = m.off[1] < D ? 8 : 0;
-        }
+        const int lanes = half >> 2;           // lanes that rotate
+        const bool turns = c < lanes;
+        m.off[0] = turns ? 4 * c : R + 8 * (c - lanes);
+        m.off[1] = turns ? half + 4 * c : m.off[0] + 4;
+        m.on[0] = m.on[1] = m.off[0] < D;
+        m.p[0] = m.p[1] = 4 * c;
+        m.rot[0] = m.rot[1] = turns ? 4 : 0;
     }
     return m;
 }
 
-// A run of n (0, 4 or 8) channels as it was loaded; zeros beyond n.  Half-split
-// pairs with R/2 an odd multiple of 4 (kHalf4) start runs 8 bytes off, so bf16 runs
-// move as two 8-byte halves there.
+// A lane's 8 channels as loaded, zeros where it has none.
 template <bool F32> struct Raw {
     uint4 u[F32 ? 2 : 1];
 };
 
 template <bool F32, int PAIR>
-__device__ __forceinline__ Raw<F32> load_raw(const void *base, int64_t off, int n)
+__device__ __forceinline__ Raw<F32> load_raw(const void *base, int64_t at, const LaneMap &m,
+                                             bool live)
 {
     Raw<F32> r;
     r.u[0] = make_uint4(0, 0, 0, 0);
+    if constexpr (F32) r.u[1] = r.u[0];
+    if (!live || !m.on[0]) return r;
     if constexpr (F32) {
-        r.u[1] = r.u[0];
-        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(base) + off);
-        if (n > 0) r.u[0] = p[0];
-        if (n > 4) r.u[1] = p[1];
+        const float *p = static_cast<const float *>(base) + at;
+        r.u[0] = *reinterpret_cast<const uint4 *>(p + m.off[0]);
+        r.u[1] = *reinterpret_cast<const uint4 *>(p + m.off[1]);
     } else {
-        const uint16_t *p = static_cast<const uint16_t *>(base) + off;
-        if constexpr (PAIR == kHalf4) {
-            if (n > 0) {
-                const uint2 a = *reinterpret_cast<const uint2 *>(p);
-                r.u[0].x = a.x; r.u[0].y = a.y;
-            }
-            if (n > 4) {
-                const uint2 b = *reinterpret_cast<const uint2 *>(p + 4);
-                r.u[0].z = b.x; r.u[0].w = b.y;
-            }
+        const uint16_t *p = static_cast<const uint16_t *>(base) + at;
+        if constexpr (PAIR == kInterleaved) {
+            r.u[0] = *reinterpret_cast<const uint4 *>(p + m.off[0]);
         } else {
-            if (n > 0) r.u[0] = *reinterpret_cast<const uint4 *>(p);
+            const uint2 a = *reinterpret_cast<const uint2 *>(p + m.off[0]);
+            const uint2 b = *reinterpret_cast<const uint2 *>(p + m.off[1]);
+            r.u[0] = make_uint4(a.x, a.y, b.x, b.y);
         }
     }
     return r;
@@ -136,38 +134,41 @@ __device__ __forceinline__ void widen(const Raw<F32> &r, float (&v)[8])
 }
 
 template <bool F32, int PAIR>
-__device__ __forceinline__ void store_run(void *base, int64_t off, int n, const float (&v)[8])
+__device__ __forceinline__ void store(void *base, int64_t at, const LaneMap &m, bool live,
+                                      const float (&v)[8])
 {
+    if (!live || !m.on[0]) return;
     if constexpr (F32) {
-        float *p = static_cast<float *>(base) + off;
-        if (n > 0) *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-        if (n > 4) *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        float *p = static_cast<float *>(base) + at;
+        *reinterpret_cast<float4 *>(p + m.off[0]) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4 *>(p + m.off[1]) = make_float4(v[4], v[5], v[6], v[7]);
     } else {
-        uint16_t *p = static_cast<uint16_t *>(base) + off;
-        const uint4 u = make_uint4(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]),
-                                   cvt_pk_bf16(v[4], v[5]), cvt_pk_bf16(v[6], v[7]));
-        if constexpr (PAIR == kHalf4) {
-            if (n > 0) *reinterpret_cast<uint2 *>(p) = make_uint2(u.x, u.y);
-            if (n > 4) *reinterpret_cast<uint2 *>(p + 4) = make_uint2(u.z, u.w);
+        uint16_t *p = static_cast<uint16_t *>(base) + at;
+        const uint2 a = make_uint2(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]));
+        const uint2 b = make_uint2(cvt_pk_bf16(v[4], v[5]), cvt_pk_bf16(v[6], v[7]));
+        if constexpr (PAIR == kInterleaved) {
+            *reinterpret_cast<uint4 *>(p + m.off[0]) = make_uint4(a.x, a.y, b.x, b.y);
         } else {
-            if (n > 0) *reinterpret_cast<uint4 *>(p) = u;
+            *reinterpret_cast<uint2 *>(p + m.off[0]) = a;
+            *reinterpret_cast<uint2 *>(p + m.off[1]) = b;
         }
     }
 }
 
-// The lane's pairs turned by (cs, sn); pairs from nrot on pass unchanged.
+// The lane's four pairs turned by (cs, sn); those not rotated pass unchanged.
 template <int PAIR>
-__device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float (&cs)[8],
-                                       const float (&sn)[8], int nrot)
+__device__ __forceinline__ void rotate(float (&v)[8], const float (&cs)[4], const float (&sn)[4],
+                                       const LaneMap &m)
 {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float &u = PAIR == kInterleaved ? (i < 4 ? a[2 * i] : b[2 * i - 8]) : a[i];
-        float &v = PAIR == kInterleaved ? (i < 4 ? a[2 * i + 1] : b[2 * i - 7]) : b[i];
-        const float x = __builtin_fmaf(u, cs[i], -(v * sn[i]));
-        const float y = __builtin_fmaf(v, cs[i], u * sn[i]);
-        u = i < nrot ? x : u;
-        v = i < nrot ? y : v;
+    for (int i = 0; i < 4; ++i) {
+        float &a = v[PAIR == kInterleaved ? 2 * i : i];
+        float &b = v[PAIR == kInterleaved ? 2 * i + 1 : i + 4];
+        const bool turn = PAIR == kInterleaved ? i % 2 < m.rot[i / 2] : i < m.rot[0];
+        const float x = __builtin_fmaf(a, cs[i], -(b * sn[i]));
+        const float y = __builtin_fmaf(b, cs[i], a * sn[i]);
+        a = turn ? x : a;
+        b = turn ? y : b;
     }
 }
 
@@ -214,11 +215,11 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormRope a, Shape sh)
     constexpr bool NORM = MODE != NormRopeMode::ROPE;
     constexpr bool BWD = MODE == NormRopeMode::BACKWARD;
     extern __shared__ __attribute__((aligned(16))) float lds[];
-    const int lg = sh.lg, lph = 1 << lg, hpw = 64 >> lg, npad = 8 * lph;
+    const int lg = sh.lg, lph = 1 << lg, hpw = 64 >> lg, npad = 4 * lph;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     float2 *const tab = reinterpret_cast<float2 *>(lds) + wave * npad;
-    const LaneMap m = lane_map<PAIR>(lane & (lph - 1), a.D, a.R);
+    const LaneMap m = lane_map<F32, PAIR>(lane & (lph - 1), a.D, a.R);
     const int hg = lane >> lg;
     const uint32_t tokens = (uint32_t)(a.B * a.T);
     const float invD = 1.0f / (float)a.D;
@@ -234,93 +235,74 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormRope a, Shape sh)
     const float *const wp = side ? a.w[1] : a.w[0];
     const int units = (heads + hpw - 1) >> (6 - lg);
 
-    float wa[8], wb[8];
+    float wt[8];
     if constexpr (NORM) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) wa[i] = wb[i] = 1.0f;
+        for (int i = 0; i < 8; ++i) wt[i] = 1.0f;
         if (wp) {
-            widen<true>(load_raw<true, PAIR>(wp, m.off[0], m.n[0]), wa);
-            widen<true>(load_raw<true, PAIR>(wp, m.off[1], m.n[1]), wb);
+            Raw<true> r = {};
+            if (m.on[0]) {
+                r.u[0] = *reinterpret_cast<const uint4 *>(wp + m.off[0]);
+                r.u[1] = *reinterpret_cast<const uint4 *>(wp + m.off[1]);
+            }
+            widen<true>(r, wt);
         }
     }
-    float dwa[8] = {}, dwb[8] = {};      // backward: sums of g' x r
+    float dw[8] = {};                    // backward: sums of g' x r
 
     for (uint32_t tok = slot < sh.slots ? slot : tokens; tok < tokens; tok += sh.slots) {
         const int b = (int)(tok / (uint32_t)a.T), t = (int)tok - b * a.T;
         const int64_t x0 = b * xr.sb + t * xr.st, y0 = b * yr.sb + t * yr.st;
         const int64_t g0 = b * gr.sb + t * gr.st;
-        Raw<F32> xa, xb, ga, gb;
-        auto load = [&](int u, Raw<F32> &pa, Raw<F32> &pb, const HeadRows &v, int64_t at) {
+        Raw<F32> rx, rg;
+        auto load = [&](int u) {
             const int head = u * hpw + hg;
-            const bool live = head < heads;
-            at += head * v.sh;
-            pa = load_raw<F32, PAIR>(v.p, at + m.off[0], live ? m.n[0] : 0);
-            pb = load_raw<F32, PAIR>(v.p, at + m.off[1], live ? m.n[1] : 0);
+            rx = load_raw<F32, PAIR>(xr.p, x0 + head * xr.sh, m, head < heads);
+            if constexpr (BWD) rg = load_raw<F32, PAIR>(gr.p, g0 + head * gr.sh, m, head < heads);
         };
-        load(first, xa, xb, xr, x0);
-        if constexpr (BWD) load(first, ga, gb, gr, g0);
+        load(first);
         fill_table(a, b * a.pos_sb + (int64_t)t * a.axes, tab, npad, lane);
-        float cs[8], sn[8];
+        float cs[4], sn[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 v = tab[m.p0 + i];
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = tab[PAIR == kInterleaved ? m.p[i / 2] + i % 2 : m.p[0] + i];
             cs[i] = v.x;
             sn[i] = v.y;
         }
         for (int u = first; u < units; u += step) {
             const int head = u * hpw + hg;
-            const bool live = head < heads;
-            float va[8], vb[8], da[8], db[8];
-            widen(xa, va);
-            widen(xb, vb);
-            if constexpr (BWD) {
-                widen(ga, da);
-                widen(gb, db);
-            }
-            if (u + step < units) {
-                load(u + step, xa, xb, xr, x0);
-                if constexpr (BWD) load(u + step, ga, gb, gr, g0);
-            }
+            float v[8], d[8];
+            widen(rx, v);
+            if constexpr (BWD) widen(rg, d);
+            if (u + step < units) load(u + step);
             float r = 1.0f;
             if constexpr (NORM) {
                 float ss = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    ss = __builtin_fmaf(va[i], va[i], __builtin_fmaf(vb[i], vb[i], ss));
+                for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(v[i], v[i], ss);
                 r = rsqrtf(__builtin_fmaf(group_sum(ss, lg), invD, a.eps));
             }
             if constexpr (!BWD) {
                 if constexpr (NORM) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        va[i] = va[i] * r * wa[i];
-                        vb[i] = vb[i] * r * wb[i];
-                    }
+                    for (int i = 0; i < 8; ++i) v[i] = v[i] * r * wt[i];
                 }
-                rotate<PAIR>(va, vb, cs, sn, m.nrot);
+                rotate<PAIR>(v, cs, sn, m);
             } else {
-                rotate<PAIR>(da, db, cs, sn, m.nrot);
+                rotate<PAIR>(d, cs, sn, m);
                 float dot = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    va[i] *= r;
-                    vb[i] *= r;
-                    dwa[i] = __builtin_fmaf(da[i], va[i], dwa[i]);
-                    dwb[i] = __builtin_fmaf(db[i], vb[i], dwb[i]);
-                    da[i] *= wa[i];
-                    db[i] *= wb[i];
-                    dot = __builtin_fmaf(da[i], va[i], __builtin_fmaf(db[i], vb[i], dot));
+                    v[i] *= r;
+                    dw[i] = __builtin_fmaf(d[i], v[i], dw[i]);
+                    d[i] *= wt[i];
+                    dot = __builtin_fmaf(d[i], v[i], dot);
                 }
                 const float mean = group_sum(dot, lg) * invD;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    va[i] = r * __builtin_fmaf(-va[i], mean, da[i]);
-                    vb[i] = r * __builtin_fmaf(-vb[i], mean, db[i]);
-                }
+                for (int i = 0; i < 8; ++i) v[i] = r * __builtin_fmaf(-v[i], mean, d[i]);
             }
-            const int64_t at = y0 + head * yr.sh;
-            store_run<F32, PAIR>(yr.p, at + m.off[0], live ? m.n[0] : 0, va);
-            store_run<F32, PAIR>(yr.p, at + m.off[1], live ? m.n[1] : 0, vb);
+            store<F32, PAIR>(yr.p, y0 + head * yr.sh, m, head < heads, v);
         }
     }
     if constexpr (BWD) {
@@ -331,40 +313,45 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormRope a, Shape sh)
         for (int i = lane; i < a.D; i += 64) red[(wave * 2 + (side ^ 1)) * a.D + i] = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float va = dwa[i], vb = dwb[i];
-            for (int k = lph; k < 64; k <<= 1) {
-                va += __shfl_xor(va, k, 64);
-                vb += __shfl_xor(vb, k, 64);
-            }
-            float *const dst = red + (wave * 2 + side) * a.D;
-            if (hg == 0 && i < m.n[0]) dst[m.off[0] + i] = va;
-            if (hg == 0 && i < m.n[1]) dst[m.off[1] + i] = vb;
+            float s = dw[i];
+            for (int k = lph; k < 64; k <<= 1) s += __shfl_xor(s, k, 64);
+            if (hg == 0 && m.on[0]) red[(wave * 2 + side) * a.D + m.off[i / 4] + i % 4] = s;
         }
         __syncthreads();
         for (int i = threadIdx.x; i < 2 * a.D; i += 256) {
-            float v = 0.0f;
-            for (int k = 0; k < 4; ++k) v += red[k * 2 * a.D + i];
-            a.partial[(int64_t)blockIdx.x * 2 * a.D + i] = v;
+            float s = 0.0f;
+            for (int k = 0; k < 4; ++k) s += red[k * 2 * a.D + i];
+            a.partial[(int64_t)blockIdx.x * 2 * a.D + i] = s;
         }
     }
 }
 
 // dw[side][d] = the sum of `rows` partial rows, in fp64 and in a fixed order:
-// a workgroup takes 16 columns, its 16 thread rows every 16th partial row.
-__global__ __launch_bounds__(256) void weight_grad_kernel(const float *__restrict__ partial,
-                                                          int rows, int D, float *dw0, float *dw1)
+// a workgroup takes 16 columns, its 64 thread rows every 64th partial row, four
+// loads at a time; then halves are joined in LDS.
+__global__ __launch_bounds__(1024) void weight_grad_kernel(const float *__restrict__ partial,
+                                                           int rows, int D, float *dw0,
+                                                           float *dw1)
 {
-    __shared__ double sum[16][16];
+    __shared__ double sum[64][16];
     const int c = threadIdx.x & 15, k = threadIdx.x >> 4;
     const int col = blockIdx.x * 16 + c;      // 2 D is a multiple of 16
+    const float *const p = partial + col;
     double v = 0.0;
-    for (int i = k; i < rows; i += 16) v += (double)partial[(int64_t)i * 2 * D + col];
+    for (int i = k; i < rows; i += 256) {
+        float x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            x[u] = i + 64 * u < rows ? p[(int64_t)(i + 64 * u) * 2 * D] : 0.0f;
+        v += ((double)x[0] + (double)x[1]) + ((double)x[2] + (double)x[3]);
+    }
     sum[k][c] = v;
-    __syncthreads();
-    if (k != 0) return;
-    for (int i = 1; i < 16; ++i) v += sum[i][c];
+    for (int h = 32; h > 0; h >>= 1) {
+        __syncthreads();
+        if (k < h) sum[k][c] += sum[k + h][c];
+    }
     float *const dst = col < D ? dw0 : dw1;
-    if (dst) dst[col < D ? col : col - D] = (float)v;
+    if (k == 0 && dst) dst[col < D ? col : col - D] = (float)sum[0][c];
 }
 
 __global__ __launch_bounds__(256) void rope_tables_kernel(RopeDims dims, int axes, double theta,
@@ -387,11 +374,8 @@ void launch_pairing(const NormRope &a, const Shape &sh, unsigned grid, size_t ld
     if (!a.half)
         hipLaunchKernelGGL((norm_rope_kernel<F32, MODE, kInterleaved>), dim3(grid), dim3(256), lds,
                            stream, a, sh);
-    else if (a.R % 16 == 0)
-        hipLaunchKernelGGL((norm_rope_kernel<F32, MODE, kHalf8>), dim3(grid), dim3(256), lds,
-                           stream, a, sh);
     else
-        hipLaunchKernelGGL((norm_rope_kernel<F32, MODE, kHalf4>), dim3(grid), dim3(256), lds,
+        hipLaunchKernelGGL((norm_rope_kernel<F32, MODE, kHalf>), dim3(grid), dim3(256), lds,
                            stream, a, sh);
 }
 
@@ -412,12 +396,8 @@ hipError_t launch_norm_rope(NormRopeMode mode, const NormRope &a, hipStream_t st
 {
     const int64_t tokens = (int64_t)a.B * a.T;
     const bool bwd = mode == NormRopeMode::BACKWARD;
-    // lanes of a head: 16 channels each, half-split pairs and the channels
-    // that pass unchanged in lanes of their own
-    const int half = a.R / 2;
-    const int lanes = a.half ? (half + 7) / 8 + (a.D - a.R + 15) / 16 : (a.D + 15) / 16;
     Shape sh = {};
-    while ((1 << sh.lg) < lanes) ++sh.lg;
+    while ((8 << sh.lg) < a.D) ++sh.lg;      // 8 channels a lane
     const int hpw = 64 >> sh.lg;
     int64_t grid = 0;
     if (tokens > 0) {
@@ -434,7 +414,7 @@ hipError_t launch_norm_rope(NormRopeMode mode, const NormRope &a, hipStream_t st
         sh.slots = (int)(bwd ? std::min<int64_t>(tokens, kBackwardWaves / W)
                               : std::min<int64_t>(tokens, kMaxSlots));
         grid = ((int64_t)sh.slots * W + 3) / 4;
-        size_t lds = (size_t)4 * 8 * (1 << sh.lg) * sizeof(float2);
+        size_t lds = (size_t)4 * 4 * (1 << sh.lg) * sizeof(float2);
         if (bwd) lds = std::max(lds, (size_t)4 * 2 * a.D * sizeof(float));
         switch (mode) {
         case NormRopeMode::ROPE:
@@ -453,7 +433,7 @@ hipError_t launch_norm_rope(NormRopeMode mode, const NormRope &a, hipStream_t st
     }
     // the sum of the partial rows (none without tokens: zeros)
     if (bwd)
-        hipLaunchKernelGGL(weight_grad_kernel, dim3(2 * a.D / 16), dim3(256), 0, stream, a.partial,
+        hipLaunchKernelGGL(weight_grad_kernel, dim3(2 * a.D / 16), dim3(1024), 0, stream, a.partial,
                            (int)grid, a.D, a.dw[0], a.heads[1] ? a.dw[1] : nullptr);
     return bwd || tokens > 0 ? hipGetLastError() : hipSuccess;
 }
