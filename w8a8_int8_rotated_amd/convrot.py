@@ -229,18 +229,19 @@ def _launch(device, fn: str, stream, *args, scratch=()):
     a caller's stream the allocator must not hand them out again before that
     stream has passed the call."""
     if stream is None:
-        s = torch.cuda.current_stream(device)
+        # the raw handle: a Stream object costs as much as the launch's checks
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
     else:
-        s = stream
+        raw = stream.cuda_stream
         for t in scratch:
             if t is not None:
                 t.record_stream(stream)
     fun = getattr(library(), fn)
     if device.index == torch.cuda.current_device():
-        rc = fun(*args, ctypes.c_void_p(s.cuda_stream))
+        rc = fun(*args, raw)
     else:
         with torch.cuda.device(device):
-            rc = fun(*args, ctypes.c_void_p(s.cuda_stream))
+            rc = fun(*args, raw)
     _check(fn, rc)
 
 
@@ -905,9 +906,11 @@ def _heads_out(out, name, like, lead):
         if out is not None:
             raise ValueError(f"{name} given without its input")
         return None, None
+    H, D = like.shape[-2:]
     if out is None:
         out = torch.empty_like(like, memory_format=torch.contiguous_format)
-    H, D = like.shape[-2:]
+        T = lead[-1]
+        return out, _HEADS.pack(out.data_ptr(), H, 0, T * H * D, H * D, D)
     return out, _heads(out, name, like.dtype, lead, H, D)
 
 

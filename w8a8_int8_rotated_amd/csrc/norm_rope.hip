@@ -133,6 +133,13 @@ __device__ __forceinline__ void widen(const Raw<F32> &r, float (&v)[8])
     }
 }
 
+// Outputs are written past the caches that hold the inputs still to come (nt
+// stores): 300 against 309 us for 84 heads of 38656 tokens, 20.2 against 21.7 us for
+// 2381 tokens.  (nt loads too: 295 us, but 24.9 us.)
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
 template <bool F32, int PAIR>
 __device__ __forceinline__ void store(void *base, int64_t at, const LaneMap &m, bool live,
                                       const float (&v)[8])
@@ -140,17 +147,20 @@ __device__ __forceinline__ void store(void *base, int64_t at, const LaneMap &m, 
     if (!live || !m.on[0]) return;
     if constexpr (F32) {
         float *p = static_cast<float *>(base) + at;
-        *reinterpret_cast<float4 *>(p + m.off[0]) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4 *>(p + m.off[1]) = make_float4(v[4], v[5], v[6], v[7]);
+        __builtin_nontemporal_store((f32x4){v[0], v[1], v[2], v[3]},
+                                    reinterpret_cast<f32x4 *>(p + m.off[0]));
+        __builtin_nontemporal_store((f32x4){v[4], v[5], v[6], v[7]},
+                                    reinterpret_cast<f32x4 *>(p + m.off[1]));
     } else {
         uint16_t *p = static_cast<uint16_t *>(base) + at;
-        const uint2 a = make_uint2(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]));
-        const uint2 b = make_uint2(cvt_pk_bf16(v[4], v[5]), cvt_pk_bf16(v[6], v[7]));
+        const u32x2 a = {cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
+        const u32x2 b = {cvt_pk_bf16(v[4], v[5]), cvt_pk_bf16(v[6], v[7])};
         if constexpr (PAIR == kInterleaved) {
-            *reinterpret_cast<uint4 *>(p + m.off[0]) = make_uint4(a.x, a.y, b.x, b.y);
+            __builtin_nontemporal_store((u32x4){a.x, a.y, b.x, b.y},
+                                        reinterpret_cast<u32x4 *>(p + m.off[0]));
         } else {
-            *reinterpret_cast<uint2 *>(p + m.off[0]) = a;
-            *reinterpret_cast<uint2 *>(p + m.off[1]) = b;
+            __builtin_nontemporal_store(a, reinterpret_cast<u32x2 *>(p + m.off[0]));
+            __builtin_nontemporal_store(b, reinterpret_cast<u32x2 *>(p + m.off[1]));
         }
     }
 }
