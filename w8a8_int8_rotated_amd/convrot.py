@@ -264,9 +264,9 @@ def _on_device(device, **tensors):
     for name, t in tensors.items():
         if t is None:
             continue
-        if t.device.type != "cuda" or (device is not None and t.device != device):
-            raise ValueError(f"{name} must be a GPU tensor on {device or 'the GPU'}, "
-                             f"got {t.device}")
+        d = t.device
+        if d.type != "cuda" or (device is not None and d != device):
+            raise ValueError(f"{name} must be a GPU tensor on {device or 'the GPU'}, got {d}")
 
 
 def _need(t, name: str, dtypes, shape):
@@ -848,56 +848,60 @@ def convrot_rope_prepare(dims, head_dim: int, theta: float = 10000.0,
 # convrot_heads, laid out by struct: several times cheaper to fill per call than
 # a ctypes structure (a bytes object passes as the pointer)
 _HEADS = struct.Struct("Piiqqq")
+_Tensor = torch.Tensor
 assert _HEADS.size == ctypes.sizeof(convrot_heads)
 
 
-def _heads(t, name: str, dtype, lead, H, D: int) -> bytes:
-    """The C view of a tensor of per-head rows [*lead, H, D] (H None: any); any
-    strides with contiguous channels."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+def _heads(t, name: str, dtype, dims: int, B: int, T: int, H, D: int) -> bytes:
+    """The C view of a tensor of per-head rows [B, T, H, D], or with dims == 3
+    [T, H, D] (H None: any); any strides with contiguous channels."""
+    if not isinstance(t, _Tensor) or t.dtype != dtype:
         raise ValueError(f"{name} must be a {dtype} tensor")
-    shape = t.shape
-    if len(shape) != len(lead) + 2:
+    shape, st = t.shape, t.stride()
+    if len(st) != dims:
         raise ValueError(f"{name} must have as many dimensions as q")
-    if shape[:-2] != lead or shape[-1] != D or (H is not None and shape[-2] != H):
-        want = (*lead, "heads" if H is None else H, D)
+    h = shape[-2]
+    if shape[-1] != D or shape[-3] != T or (dims == 4 and shape[0] != B) \
+            or (H is not None and h != H):
+        want = (*((B,) if dims == 4 else ()), T, "heads" if H is None else H, D)
         raise ValueError(f"{name} must have shape {want}, got {tuple(shape)}")
-    st = t.stride()
     if st[-1] != 1:
         raise ValueError(f"{name} must have contiguous channels")
-    return _HEADS.pack(t.data_ptr(), shape[-2], 0, st[0] if len(st) == 4 else 0, st[-3], st[-2])
+    return _HEADS.pack(t.data_ptr(), h, 0, st[0] if dims == 4 else 0, st[-3], st[-2])
 
 
 def _heads_pair(q, k, rope, positions):
-    """The checks shared by the rope and norm calls: (B, T, position stride),
-    the leading shape and the views of q and k (None without k)."""
+    """The checks shared by the rope and norm calls: the leading dimensions
+    (dims, B, T), the batch stride of the positions and the views of q and k
+    (None without k)."""
     if not isinstance(rope, RopePlan):
         raise ValueError("rope must be a RopePlan from convrot_rope_prepare")
-    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
+    if not isinstance(q, _Tensor) or q.dim() not in (3, 4):
         raise ValueError("q must be a tensor [B, T, heads, D] or [T, heads, D]")
-    if q.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"q must be float32 or bfloat16, got {q.dtype}")
-    lead = q.shape[:-2]
-    B, T = lead if len(lead) == 2 else (1, lead[0])
-    D = rope.desc.head_dim
-    vq = _heads(q, "q", q.dtype, lead, None, D)
-    vk = None if k is None else _heads(k, "k", q.dtype, lead, None, D)
-    return B, T, _positions(positions, B, T, rope.desc.axes), lead, vq, vk
+    dtype = q.dtype
+    if dtype != torch.bfloat16 and dtype != torch.float32:
+        raise ValueError(f"q must be float32 or bfloat16, got {dtype}")
+    shape, D = q.shape, rope.desc.head_dim
+    dims = len(shape)
+    lead = (dims, shape[0] if dims == 4 else 1, shape[-3])
+    vq = _heads(q, "q", dtype, *lead, None, D)
+    vk = None if k is None else _heads(k, "k", dtype, *lead, None, D)
+    return lead, _positions(positions, lead[1], lead[2], rope.desc.axes), vq, vk
 
 
 def _positions(positions, B, T, axes):
-    if not isinstance(positions, torch.Tensor) \
-            or positions.dtype not in (torch.int32, torch.float32):
+    """The batch stride of checked positions."""
+    if not isinstance(positions, _Tensor) \
+            or (positions.dtype != torch.int32 and positions.dtype != torch.float32):
         raise ValueError("positions must be an int32 or float32 tensor")
-    shape = tuple(positions.shape)
-    if axes == 1 and shape in ((T,), (B, T)):
-        shape += (1,)
-    if shape not in ((T, axes), (B, T, axes)):
+    shape = positions.shape
+    if not (shape == (T, axes) or shape == (B, T, axes)
+            or (axes == 1 and shape in ((T,), (B, T)))):
         raise ValueError(f"positions must have shape {(T, axes)} or {(B, T, axes)}, got "
-                         f"{tuple(positions.shape)}")
+                         f"{tuple(shape)}")
     if not positions.is_contiguous():
         raise ValueError("positions must be contiguous")
-    return T * axes if len(shape) == 3 else 0
+    return T * axes if positions.numel() == B * T * axes else 0
 
 
 def _heads_out(out, name, like, lead):
@@ -909,9 +913,8 @@ def _heads_out(out, name, like, lead):
     H, D = like.shape[-2:]
     if out is None:
         out = torch.empty_like(like, memory_format=torch.contiguous_format)
-        T = lead[-1]
-        return out, _HEADS.pack(out.data_ptr(), H, 0, T * H * D, H * D, D)
-    return out, _heads(out, name, like.dtype, lead, H, D)
+        return out, _HEADS.pack(out.data_ptr(), H, 0, lead[2] * H * D, H * D, D)
+    return out, _heads(out, name, like.dtype, *lead, H, D)
 
 
 def convrot_rope_forward(q: torch.Tensor, k, rope: RopePlan, positions: torch.Tensor,
@@ -919,7 +922,8 @@ def convrot_rope_forward(q: torch.Tensor, k, rope: RopePlan, positions: torch.Te
     """(q_out, k_out): q and k [B, T, heads, D] turned by the tokens' positions
     [T, axes] or [B, T, axes] (int32 or float32); k may be None.  Out of place
     unless out_q is q.  inverse: by the negative angles, the backward pass."""
-    B, T, psb, lead, vq, vk = _heads_pair(q, k, rope, positions)
+    lead, psb, vq, vk = _heads_pair(q, k, rope, positions)
+    _, B, T = lead
     dev = rope.freq.device
     _on_device(dev, q=q, k=k, positions=positions, out_q=out_q, out_k=out_k)
     out_q, oq = _heads_out(out_q, "out_q", q, lead)
@@ -935,7 +939,8 @@ def convrot_qk_norm_rope_forward(q: torch.Tensor, k, w_q, w_k, rope: RopePlan,
                                  out_k=None, stream=None):
     """convrot_rope_forward of q * rsqrt(mean(q^2) + eps) * w_q over each head's
     channels and of k likewise; w_q, w_k float32 [D] or None."""
-    B, T, psb, lead, vq, vk = _heads_pair(q, k, rope, positions)
+    lead, psb, vq, vk = _heads_pair(q, k, rope, positions)
+    _, B, T = lead
     _opt(w_q, "w_q", torch.float32, (rope.head_dim,))
     _opt(w_k, "w_k", torch.float32, (rope.head_dim,))
     if k is None and w_k is not None:
@@ -961,13 +966,14 @@ def convrot_qk_norm_rope_backward(g_q: torch.Tensor, g_k, q: torch.Tensor, k, w_
     """(dq, dk, dw_q, dw_k) of convrot_qk_norm_rope_forward(q, k, ...) from the
     gradients g_q and g_k of its outputs."""
     lib = library()
-    B, T, psb, lead, vq, vk = _heads_pair(q, k, rope, positions)
+    lead, psb, vq, vk = _heads_pair(q, k, rope, positions)
+    _, B, T = lead
     D = rope.head_dim
     views = []
     for g, x, n in ((g_q, q, "g_q"), (g_k, k, "g_k")):
         if (g is None) != (x is None):
             raise ValueError(f"{n} must be given with its input and only then")
-        views.append(None if g is None else _heads(g, n, x.dtype, lead, x.shape[-2], D))
+        views.append(None if g is None else _heads(g, n, x.dtype, *lead, x.shape[-2], D))
     if k is None and w_k is not None:
         raise ValueError("w_k given without k")
     if k is None and dw_k is not None:
