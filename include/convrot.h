@@ -464,8 +464,8 @@ CONVROT_API size_t convrot_fp8_linear_workspace_bytes(int64_t M, int64_t K, int6
 /* Prepare a weight: W F32 or BF16 (quantised here, scale and codes as for the
  * activations with the amax of the 128 x 128 block), or CONVROT_F8E4M3 codes
  * with src_scale, device F32 [ceil(N / 128), K / 128] row-major (imported
- * unchanged; with POW2 they must be powers of two or 0, which is not checked
- * here).  Layout per `layout`, [N, K] or [K, N]; src_scale keeps its order
+ * unchanged; with POW2 they must be normal powers of two, or 0 where the block's
+ * codes are all 0, which is not checked here).  Layout per `layout`, [N, K] or [K, N]; src_scale keeps its order
  * either way.  out->codes, out->scale: caller allocations; out->scales selects
  * the kind.  Errors as for convrot_linear_prepare_weights. */
 CONVROT_API int convrot_fp8_prepare_weights(const void *W, int w_dtype, int layout,
@@ -536,7 +536,8 @@ CONVROT_API int convrot_rope_prepare(const int32_t *dims, int axes, int head_dim
  * data + b * batch_stride + t * token_stride + h * head_stride + d elements.
  * data and every stride are multiples of 16 bytes (EALIGN; the stride of an
  * extent of 1 is not looked at).  An output may be its input (same data and
- * strides); it may not overlap one otherwise, nor itself. */
+ * strides); it may not overlap one otherwise, nor itself (EINVAL for a zero
+ * stride over more than one row; inputs may be broadcast that way). */
 typedef struct convrot_heads {
     void *data;
     int32_t heads;

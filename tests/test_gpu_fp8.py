@@ -282,3 +282,76 @@ def test_pow2_import_refuses_other_scales(cr):
     with pytest.raises(ValueError, match="powers of two"):
         cr.convrot_fp8_prepare_weights(codes, src_scale=torch.full((1, 1), -2.0, device="cuda"),
                                        scales="pow2")
+
+
+# every tile shape, the two-launch plan, ragged edges, odd and even counts of k-blocks
+PLANS = [(100, 384, 528), (192, 256, 21504), (520, 128, 5376), (768, 384, 10880),
+         (1000, 256, 5376), (2041, 256, 5392), (4133, 640, 5392), (2500, 128, 16128)]
+
+
+@pytest.mark.parametrize("M,K,N", PLANS)
+def test_tile_plans(cr, M, K, N):
+    """Every output of the tiled kernels against the fp64 product of the library's
+    own codes and scales (checked against the definition above), on the GPU, with
+    the bound of the module's docstring; scales of a row differ by factors of up to
+    2^12 from block to block."""
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+    X = torch.randn(M, K, generator=g, device="cuda")
+    X = (X * torch.exp2(torch.randint(-6, 7, (M, K // 128, 1), generator=g, device="cuda"))
+         .expand(-1, -1, 128).reshape(M, K)).to(torch.bfloat16)
+    W = torch.randn(N, K, generator=g, device="cuda")
+    bias = torch.randn(N, generator=g, device="cuda")
+    for kind in ("f32", "pow2"):
+        pw = cr.convrot_fp8_prepare_weights(W, scales=kind)
+        q, s = cr.convrot_fp8_quantize(X, kind)
+        dec = lambda c, n: torch.from_numpy(untile(c.view(torch.int8), n, K).copy()).cuda() \
+            .view(F8).double()
+        xc, wc = dec(q, M), dec(pw.codes, N)
+        xd = xc * s[:, :M].t().double().repeat_interleave(128, 1)
+        wd = wc * pw.scale.double().repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)
+        ref, mag = xd @ wd.t() + bias.double(), xd.abs() @ wd.abs().t() + bias.double().abs()
+        top = lambda a: a.abs().view(a.shape[0], K // 8, 8).amax(-1)
+        cut = 7 * 2.0 ** -13 * (top(xd) @ top(wd).t())
+        for dt in (torch.bfloat16, torch.float32):
+            announce(f"fp8 plan {M}x{K}x{N} {kind} {dt}")
+            y = cr.convrot_fp8_linear_forward(X, pw, bias=bias, out_dtype=dt)
+            bound = (K + K // 128 + 4) * 2.0 ** -24 * mag
+            if dt == torch.bfloat16:
+                bound = bound + cut
+            bound = bound + (2.0 ** -8 if dt == torch.bfloat16 else 2.0 ** -24) * (ref.abs() + bound)
+            worst = float(((y.double() - ref).abs() / bound).max())
+            print(f"[parity] plan {M}x{K}x{N} {kind} {dt}: worst error {worst:.3f} of its bound",
+                  flush=True)
+            assert worst <= 1.0
+
+
+@pytest.mark.parametrize("M", [8, 200, 300])
+def test_non_finite_rows_fp32(cr, M):
+    """As above for the kernels behind fp32 outputs, where a NaN must not cross
+    from one k-block's scales or one tile into another token either."""
+    K, N = 384, 272
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(M))
+    pw = cr.convrot_fp8_prepare_weights(torch.randn(N, K, device="cuda"))
+    clean = cr.convrot_fp8_linear_forward(x.bfloat16().cuda(), pw, out_dtype=torch.float32)
+    x[M - 1, 200] = float("nan")
+    x[2, 7] = float("inf")
+    announce(f"fp8 non-finite fp32 M={M}")
+    y = cr.convrot_fp8_linear_forward(x.bfloat16().cuda(), pw, out_dtype=torch.float32)
+    assert bool(torch.isnan(y[[2, M - 1]]).all())
+    keep = [m for m in range(M) if m not in (2, M - 1)]
+    assert torch.equal(y[keep], clean[keep])
+
+
+def test_pow2_import_zero_scales(cr):
+    """A zero scale stands only for a block of zeros."""
+    codes = torch.zeros(128, 256, device="cuda")
+    codes[:, 128:] = 2.0
+    scale = torch.tensor([[0.0, 0.5]], device="cuda")
+    pw = cr.convrot_fp8_prepare_weights(codes.to(F8), src_scale=scale, scales="pow2")
+    for M in (1, 300):
+        announce(f"fp8 zero scale M={M}")
+        y = cr.convrot_fp8_linear_forward(torch.ones(M, 256, device="cuda").bfloat16(), pw)
+        assert bool((y == 128.0).all())
+    codes[5, 5] = 1.0
+    with pytest.raises(ValueError, match="scale is 0"):
+        cr.convrot_fp8_prepare_weights(codes.to(F8), src_scale=scale, scales="pow2")

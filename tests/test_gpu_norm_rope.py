@@ -407,3 +407,42 @@ def test_qkv_path(cr, fp8, B, T, out):
     size = pair_size(n, 64, "interleaved")
     half = 2.0 ** -8 if out == "bf16" else U
     close(back, n, 2.1 * half * size + 64 * U * size + 1e-40, "turned back")
+
+
+def test_broadcast_inputs_and_outputs(cr):
+    """Inputs may repeat rows with a zero stride; outputs may not."""
+    plan = cr.convrot_rope_prepare((64,), 64)
+    base = torch.randn(1, 7, 1, 64, device="cuda").bfloat16()
+    q = base.expand(3, 7, 4, 64)
+    pos = torch.arange(7, dtype=torch.int32, device="cuda").view(7, 1)
+    w = torch.randn(64, device="cuda")
+    announce("broadcast inputs")
+    y, _ = cr.convrot_qk_norm_rope_forward(q, None, w, None, plan, pos)
+    want, _ = cr.convrot_qk_norm_rope_forward(q.contiguous(), None, w, None, plan, pos)
+    assert torch.equal(y, want)
+    g = torch.randn(3, 7, 4, 64, device="cuda").bfloat16()
+    a = cr.convrot_qk_norm_rope_backward(g, None, q, None, w, None, plan, pos)
+    b = cr.convrot_qk_norm_rope_backward(g, None, q.contiguous(), None, w, None, plan, pos)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[2], b[2])
+    with pytest.raises(cr.ConvRotError):
+        cr.convrot_rope_forward(q, None, plan, pos, out_q=q)
+
+
+def test_two_streams_at_once(cr):
+    """Independent calls on two streams, each with its own workspace."""
+    c = Case(B=1, T=500, Hq=8, Hk=4, D=128, dims=(64, 64))
+    plan = c.plan(cr)
+    gq, gk = c.make(torch.Generator().manual_seed(2), 1.0)
+    args = (gq, gk, c.q, c.k, c.wq.cuda(), c.wk.cuda(), plan, c.posd)
+    want = cr.convrot_qk_norm_rope_backward(*args)
+    announce("two streams")
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(4):
+        for s in streams:
+            got.append(cr.convrot_qk_norm_rope_backward(*args, stream=s))
+    torch.cuda.synchronize()
+    for y in got:
+        for a, b in zip(y, want):
+            assert torch.equal(a, b)

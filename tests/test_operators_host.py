@@ -171,6 +171,9 @@ def test_rope_and_norm_refusals(cr):
     both(cr.EALIGN, qo=heads(cr, token_stride=8 * 128 + 4))
     both(cr.EALIGN, q=heads(cr, head_stride=129))
     both(cr.EINVAL, qo=heads(cr, token_stride=-1024))
+    both(cr.EINVAL, qo=heads(cr, head_stride=0))           # rows on top of each other
+    both(cr.EINVAL, qo=heads(cr, token_stride=0))
+    both(cr.EINVAL, B=2, qo=heads(cr, batch_stride=0))
     both(cr.EINVAL, k=heads(cr, H=2))                      # no output for k
     for bad in (dict(magic=0), dict(version=2), dict(axes=0), dict(axes=5), dict(head_dim=100),
                 dict(rotary_dim=130), dict(rotary_dim=63), dict(pairing=3),

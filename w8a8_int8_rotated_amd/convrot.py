@@ -749,10 +749,17 @@ def convrot_fp8_prepare_weights(W: torch.Tensor, layout: int = OUT_MAJOR,
     W = W.contiguous()
     _on_device(W.device, W=W, src_scale=src_scale)
     if src_scale is not None and scales == "pow2":
-        # load time: the one check that reads the tensor's values
+        # load time: the one check that reads the tensors' values
         bits = src_scale.view(torch.int32)
         if bool((((bits & 0x7FFFFF) != 0) | (bits < 0)).any()):
             raise ValueError("src_scale of a pow2 weight must hold powers of two or zeros")
+        if bool((bits == 0).any()):
+            # the matrix instruction reads a zero as 2^-127
+            c = W if layout == OUT_MAJOR else W.t()
+            used = torch.nn.functional.pad((c.view(torch.uint8) & 0x7F) != 0, (0, 0, 0, -N % 128))
+            used = used.view(-(-N // 128), 128, K // 128, 128).any(3).any(1)
+            if bool((used & (bits == 0)).any()):
+                raise ValueError("a block whose scale is 0 must hold zero codes")
     nbytes = lib.convrot_fp8_packed_bytes(N, K)
     if nbytes == 0:
         raise ConvRotError("convrot_fp8_prepare_weights", EUNSUPPORTED)

@@ -865,17 +865,21 @@ int convrot_rope_prepare(const int32_t *dims, int axes, int head_dim, double the
 }
 
 // A view of per-head rows (elements of es bytes) as the kernels take it.
+// An output's rows must be its own.
 static int head_rows(const convrot_heads *v, int heads, int64_t B, int64_t T, int es,
-                     convrot::HeadRows *out)
+                     convrot::HeadRows *out, bool written = false)
 {
     if (!v || v->heads != heads || v->reserved != 0) return CONVROT_EINVAL;
     if (B * T > 0 && !v->data) return CONVROT_EINVAL;
     const int64_t ext[3] = {B, T, heads};
     int64_t st[3] = {v->batch_stride, v->token_stride, v->head_stride};
     for (int i = 0; i < 3; ++i) {
-        if (ext[i] <= 1) st[i] = 0;
-        if ((st[i] * es) % 16 != 0) return CONVROT_EALIGN;
-        if (st[i] < 0) return CONVROT_EINVAL;
+        if (ext[i] <= 1) {
+            st[i] = 0;
+            continue;
+        }
+        if (st[i] < 0 || (written && st[i] == 0)) return CONVROT_EINVAL;
+        if (st[i] % (16 / es) != 0) return CONVROT_EALIGN;
     }
     if (!aligned16(v->data)) return CONVROT_EALIGN;
     *out = {v->data, st[0], st[1], st[2]};
@@ -923,7 +927,7 @@ static int norm_rope_side(convrot::NormRope *a, int side, const convrot_heads *x
     const int es = a->f32 ? 4 : 2;
     a->heads[side] = x->heads;
     int rc = head_rows(x, x->heads, a->B, a->T, es, &a->x[side]);
-    if (rc == CONVROT_OK) rc = head_rows(y, x->heads, a->B, a->T, es, &a->out[side]);
+    if (rc == CONVROT_OK) rc = head_rows(y, x->heads, a->B, a->T, es, &a->out[side], true);
     return rc;
 }
 

@@ -349,10 +349,22 @@ __global__ __launch_bounds__(512, 2) void fp8_gemm_kernel(
     const uint32_t vs = tok ? sgrp * 256 + lane * 4 : (lane & 1) * nkb * 4;
 
     // The stream of k-blocks: the next one to copy is k-block ikb of `is` (of
-    // nothing, zeros, beyond a tile's k-blocks and after the last tile)
+    // nothing, zeros, beyond a tile's k-blocks and after the last tile).  It turns
+    // to the next tile when it needs it, not at the end of the one before: with
+    // two k-blocks a tile, that tile is known only by then.
     Src is = src_of(m0, n0);
     int ikb = 0;
     auto copy_a = [&](uint8_t *dw, uint8_t *dx, float *ds) {
+        // (selects, not branches: a branch here would split the k-block into
+        // regions the additions get moved across)
+        const bool wrap = ikb == nkp;
+        is.w = wrap ? nxt.w : is.w;
+        is.x = wrap ? nxt.x : is.x;
+        is.s = wrap ? nxt.s : is.s;
+        is.wn = wrap ? nxt.wn : is.wn;
+        is.xn = wrap ? nxt.xn : is.xn;
+        is.sn = wrap ? nxt.sn : is.sn;
+        ikb = wrap ? (more ? 0 : INT_MAX / 2) : ikb;         // no more: past every k-block
         const bool none = ikb >= nkb;
         copy_tokens<CX>(is, none ? 0 : ikb, none, vx, odd, vs, dx + wave * CX * 1024,
                         ds + sgrp * 64);
@@ -361,16 +373,8 @@ __global__ __launch_bounds__(512, 2) void fp8_gemm_kernel(
     auto copy_b = [&](uint8_t *dw) {
         const bool none = ikb >= nkb;
         copy_weights<CH>(is, none ? 0 : ikb, none, vw1, dw + wave * CH * 1024);
-        // (selects, not branches: a branch here would split the k-block into
-        // regions the additions get moved across)
-        const bool wrap = ikb + 1 == nkp;
-        is.w = wrap ? nxt.w : is.w;
-        is.x = wrap ? nxt.x : is.x;
-        is.s = wrap ? nxt.s : is.s + (none ? 0 : s_step);
-        is.wn = wrap ? nxt.wn : is.wn;
-        is.xn = wrap ? nxt.xn : is.xn;
-        is.sn = wrap ? nxt.sn : is.sn;
-        ikb = wrap ? (more ? 0 : INT_MAX / 2) : ikb + 1;     // no more: past every k-block
+        is.s += none ? 0 : s_step;
+        ++ikb;
     };
 
     const int in_tile = r * 64 + ((g ^ lds_swz(r)) << 4);
