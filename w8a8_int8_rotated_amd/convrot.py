@@ -214,7 +214,7 @@ def _check(fn: str, rc: int):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
@@ -277,7 +277,7 @@ def _need(t, name: str, dtypes, shape):
     dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -700,6 +700,7 @@ class FP8Weights:
         self.desc = desc
         self.codes = codes
         self.scale = scale
+        self._ref = ctypes.byref(desc)
 
     @property
     def N(self):
@@ -710,7 +711,7 @@ class FP8Weights:
         return self.desc.K
 
     def ref(self):
-        return ctypes.byref(self.desc)
+        return self._ref
 
 
 def _fp8_weights(W, name: str):
@@ -809,6 +810,7 @@ class RopePlan:
         self.desc = desc
         self.freq = freq
         self.axis = axis
+        self._ref = ctypes.byref(desc)
 
     @property
     def axes(self):
@@ -819,7 +821,7 @@ class RopePlan:
         return self.desc.head_dim
 
     def ref(self):
-        return ctypes.byref(self.desc)
+        return self._ref
 
 
 def convrot_rope_prepare(dims, head_dim: int, theta: float = 10000.0,
@@ -1001,9 +1003,9 @@ def convrot_qk_norm_rope_backward(g_q: torch.Tensor, g_k, q: torch.Tensor, k, w_
         dw_k = torch.empty(D, dtype=torch.float32, device=dev)
     ws = _workspace(wsb, dev, workspace)
     _launch(dev, "convrot_qk_norm_rope_backward", stream, B, T, _dtype_tag(q.dtype), views[0],
-            vq, vdq, _ptr(w_q), _ptr(dw_q), views[1], vk, vdk, _ptr(w_k), _ptr(dw_k), eps, rope.ref(), _ptr(positions),
-            _dtype_tag(positions.dtype), psb, _ptr(ws), ws.numel() if ws is not None else 0,
-            scratch=(dq, dk, dw_q, dw_k, ws))
+            vq, vdq, _ptr(w_q), _ptr(dw_q), views[1], vk, vdk, _ptr(w_k), _ptr(dw_k), eps,
+            rope.ref(), _ptr(positions), _dtype_tag(positions.dtype), psb, _ptr(ws),
+            ws.numel() if ws is not None else 0, scratch=(dq, dk, dw_q, dw_k, ws))
     return dq, dk, dw_q, dw_k
 
 
