@@ -24,6 +24,7 @@ import collections
 import csv
 import hashlib
 import json
+import re
 import sys
 
 COPY_KERNEL = "__amd_rocclr_copyBuffer"
@@ -31,6 +32,7 @@ COPY_KERNEL = "__amd_rocclr_copyBuffer"
 
 def _short(name: str) -> str:
     name = name.replace("void ", "").replace("convrot::(anonymous namespace)::", "")
+    name = re.sub(r"\(\w+\)(?=\d)", "", name)      # an enumerator among the template arguments
     return name.split("(")[0]
 
 

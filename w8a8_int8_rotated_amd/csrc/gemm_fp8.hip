@@ -4,26 +4,42 @@
 // Both code matrices are K-tiled (common.hpp); a k-block of 128 inputs is two
 // consecutive 1 KiB tiles of each 16-row block.
 //
-// fp8_gemm_kernel (any scales).  The scale changes with every k-block, so each
-// block's sum is formed from zero by one v_mfma_f32_16x16x128_f8f6f4 and joined
-// by four fp32 fused multiply-adds per lane: 16 VALU cycles for 32 matrix
-// cycles, on the same SIMD.  A VALU instruction cannot name an accumulator
-// register, so the 128 sums of a lane have to sit in ordinary registers: 8 waves (two
-// per SIMD, 256 registers each) own 128 x 64 of a 256 (n) x 256 (m) tile, and one
-// wave's matrix instructions run under the other's additions.  The sums of row
-// tile i are joined while row tile i + 1 multiplies.
+// Any scales.  The scale changes with every k-block, so each block's sum is formed
+// from zero by one v_mfma_f32_16x16x128_f8f6f4 and joined by four fp32 fused
+// multiply-adds per lane: 16 VALU cycles for 32 matrix cycles, on the same SIMD.  A
+// VALU instruction cannot name an accumulator register, so the 128 sums of a lane
+// have to sit in ordinary registers: 8 waves (two per SIMD, 256 registers each) own
+// 128 x 64 of a 256 (n) x 256 (m) tile, and one wave's matrix instructions run under
+// the other's additions.  The sums of row tile i are joined while row tile i + 1
+// multiplies.
+//
+// Powers of two.  v_mfma_scale_f32_16x16x128_f8f6f4 applies both scales (their
+// exponent fields are its e8m0 operands) and keeps the sums: no additions.
+//
+// F32 outputs convert the codes to bf16 and use v_mfma_f32_16x16x32_bf16 (see
+// fp8.hip on the precision of the FP8 sums): half the matrix rate, the conversions
+// of the activations kept for a k-block.
 //
 // Copies go straight to LDS (buffer_load ... lds), one k-block (64 KiB) per stage,
-// two stages.  A wave walks a stage's 8 weight tiles with one operand in
-// registers and the next on its way; before the last one every wave has read
-// the stage, and a barrier there frees it for the k-block after next.  The copies of
-// a k-block so have one whole k-block (2048 matrix cycles) to land.  The stream
-// of k-blocks runs on across the tiles of a persistent workgroup.  With an odd
-// number of k-blocks a tile takes one more, of zeros.
+// two stages; see CONVROT_FP8_K_BLOCK for the turns at which halves of a stage
+// are freed and refilled.  The stream of k-blocks runs on across the tiles of a
+// persistent workgroup.  With an odd number of k-blocks a tile takes one more, of
+// zeros.
 //
-// F32 outputs (F32 = true) convert the codes to bf16 and use
-// v_mfma_f32_16x16x32_bf16 (see fp8.hip on the precision of the FP8 sums): half the
-// matrix rate, the conversions of the activations kept for a k-block.
+// At M = 38656, K = 5376, N = 16128 (6.70 TFLOP; the GEMM alone, bf16 outputs, by
+// step, any scales / powers of two):
+//   one wait and barrier per k-block, operands read after it       3.04 ms
+//   conflict-free LDS slots                                        3.00 ms
+//   next k-block's operands requested under the last row tile,
+//   weight scales through LDS (a scalar load made every LDS wait
+//   a full one)                                                    2.76 / 2.58 ms
+//   halves of a stage refilled 1.5 k-blocks ahead                  2.75 / 2.46 ms
+//   row tiles requested two ahead                                  2.69 / 2.40 ms
+// 2.5 and 2.8 PFLOP/s; the matrix cores are busy 0.62 and 0.71 of the time at
+// 1.77 GHz (the INT8 GEMM: 0.80 at 1.50 GHz: power sets their product).  LDS is the
+// next bound: a k-block costs 192 reads of 1 KiB and 64 KiB of copies, 2048 cycles
+// at 128 bytes a cycle, as many as its matrix instructions; a wave tile larger than
+// 128 x 64 would not fit its registers.
 #include "common.hpp"
 #include "gemm_common.hpp"
 
@@ -40,7 +56,7 @@ typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 constexpr int kKB = 128;        // inputs per k-block
-constexpr int kGroup = 4;       // tile-rows per L2 group
+constexpr int kGroup = 4;       // tile-rows per L2 group (2: 1% slower, 8: 1%, 16: 6%)
 
 // The slot of chunk c of row r in an LDS tile is c ^ lds_swz(r).  A 16 x 16 operand
 // read takes lane (r, g) to chunk g of row r; LDS serves ds_read_b128 in four
@@ -189,8 +205,9 @@ __device__ __forceinline__ void order_row_tile()
 
 // One k-block, in two halves.  Row tiles are requested two ahead (one ahead
 // leaves a wave that has its SIMD to itself waiting for LDS), so before the last
-// two row tiles of a half this wave has read all that the half needs; then it waits for its copies
-// but the last VM, and the barrier says that every wave has done both:
+// two row tiles of a half this wave has read all that the half needs; then it
+// waits for its copies but the last VM, and the barrier says that every wave has
+// done both:
 //  - at the first half's end the second half's weight rows have landed, and the
 //    first half's and the activations (in registers since the k-block's start)
 //    are free: COPY_A refills them for the k-block after next;
@@ -509,8 +526,10 @@ hipError_t launch_shape(int tn, int tm, const Fp8Gemm &g, int64_t m_base, int64_
 }
 
 // Tile shapes and the time of one tile per CU, in units of the largest shape's;
-// measured at K = 5376: bf16 outputs 56 us for 256 x 256 (any scales; M = 256 at
-// N = 5376 leaves one per CU), F32 outputs 70 us for 128 x 256.
+// measured at K = 5376: bf16 outputs 56 us for 256 x 256 (any scales), F32 outputs
+// 70 us for 128 x 256.  A 128 x 64 tile's k-block (18 us) is bound by the latency of
+// its copies and by LDS: four stages of it, or waves that split the k-blocks and
+// read half as much from LDS, took 17 to 20 us.
 struct TileShape {
     int tn, tm;
     double cost;
