@@ -465,8 +465,8 @@ CONVROT_API size_t convrot_fp8_linear_workspace_bytes(int64_t M, int64_t K, int6
  * activations with the amax of the 128 x 128 block), or CONVROT_F8E4M3 codes
  * with src_scale, device F32 [ceil(N / 128), K / 128] row-major (imported
  * unchanged; with POW2 they must be normal powers of two, or 0 where the block's
- * codes are all 0, which is not checked here).  Layout per `layout`, [N, K] or [K, N]; src_scale keeps its order
- * either way.  out->codes, out->scale: caller allocations; out->scales selects
+ * codes are all 0, which is not checked here).  Layout per `layout`, [N, K] or
+ * [K, N]; src_scale keeps its order either way.  out->codes, out->scale: caller allocations; out->scales selects
  * the kind.  Errors as for convrot_linear_prepare_weights. */
 CONVROT_API int convrot_fp8_prepare_weights(const void *W, int w_dtype, int layout,
                                             const float *src_scale, int64_t N, int64_t K,
@@ -547,7 +547,8 @@ typedef struct convrot_heads {
 
 /* Positions of the tokens: device, [B, T, axes] with batches pos_batch_stride
  * elements apart (0: one [T, axes] array for every batch), pos_dtype
- * CONVROT_I32 or CONVROT_F32 (fractional positions). */
+ * CONVROT_I32 or CONVROT_F32 (fractional positions).  4-byte alignment is
+ * enough for them, so one step's may be a slice of a longer array. */
 
 /* q_out = R q and k_out = R k; k and k_out may both be NULL.  dtype (of q, k
  * and their outputs): CONVROT_BF16 or CONVROT_F32.  CONVROT_ROPE_INVERSE turns

@@ -276,12 +276,10 @@ def test_graph_and_streams(cr, kind, M):
 
 def test_pow2_import_refuses_other_scales(cr):
     codes = torch.zeros(128, 128, device="cuda").to(F8)
-    with pytest.raises(ValueError, match="powers of two"):
-        cr.convrot_fp8_prepare_weights(codes, src_scale=torch.full((1, 1), 3.0, device="cuda"),
-                                       scales="pow2")
-    with pytest.raises(ValueError, match="powers of two"):
-        cr.convrot_fp8_prepare_weights(codes, src_scale=torch.full((1, 1), -2.0, device="cuda"),
-                                       scales="pow2")
+    for scale in (3.0, -2.0, float("inf"), float("nan")):
+        with pytest.raises(ValueError, match="powers of two"):
+            cr.convrot_fp8_prepare_weights(codes, scales="pow2",
+                                           src_scale=torch.full((1, 1), scale, device="cuda"))
 
 
 # every tile shape, the two-launch plan, ragged edges, odd and even counts of k-blocks

@@ -446,3 +446,18 @@ def test_two_streams_at_once(cr):
     for y in got:
         for a, b in zip(y, want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("pos,axes", [("i32", [24, 20, 20]), ("f32", [64])])
+def test_steps_of_a_longer_position_array(cr, pos, axes):
+    """One token per call, its positions a slice (at 4 or 12 bytes' offsets) of the
+    sequence's: the rows of the call over the whole sequence."""
+    c = Case(1, 9, 6, 2, 64, axes, pos=pos)
+    announce(f"position slices {c!r}")
+    plan, p = c.plan(cr), c.posd.reshape(9, len(axes))
+    whole = cr.convrot_qk_norm_rope_forward(c.q, c.k, c.wq.cuda(), c.wk.cuda(), plan, p)
+    for t in range(9):
+        step = cr.convrot_qk_norm_rope_forward(c.q[:, t:t + 1], c.k[:, t:t + 1], c.wq.cuda(),
+                                               c.wk.cuda(), plan, p[t:t + 1])
+        for y, z in zip(whole, step):
+            assert torch.equal(y[:, t:t + 1], z), t

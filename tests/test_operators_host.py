@@ -160,7 +160,7 @@ def test_rope_and_norm_refusals(cr):
     both(cr.EUNSUPPORTED, dt=cr.I8)
     both(cr.EUNSUPPORTED, pdt=cr.BF16)
     both(cr.EINVAL, pos=None)
-    both(cr.EALIGN, pos=ODD)
+    both(cr.EALIGN, pos=FAKE + 2)
     both(cr.EINVAL, psb=-1)
     both(cr.EINVAL, q=heads(cr, heads=0))
     both(cr.EUNSUPPORTED, q=heads(cr, heads=65537), qo=heads(cr, heads=65537))
@@ -227,7 +227,8 @@ def test_qkv_refusals(cr):
         assert f(hq=9) == cr.ELAYOUT and f(hq=0) == cr.EINVAL and f(hk=0) == cr.EINVAL
         assert f(r=rope_desc(cr, head_dim=64, rotary_dim=64)) == cr.ELAYOUT
         assert f(B=-1) == cr.EINVAL and f(B=1 << 40, T=1 << 40) == cr.EUNSUPPORTED
-        assert f(T=1 << 30) == cr.EUNSUPPORTED
+        assert f(T=1 << 30) == cr.EUNSUPPORTED and f(T=1 << 62) == cr.EUNSUPPORTED
+        assert f(pos=FAKE + 2) == cr.EALIGN
         assert f(X=None) == cr.EINVAL and f(Y=None) == cr.EINVAL and f(pos=None) == cr.EINVAL
         assert f(Y=ODD) == cr.EALIGN and f(X=ODD) == cr.EALIGN
         assert f(y=cr.I32) == cr.EUNSUPPORTED and f(eps=0.0) == cr.EINVAL

@@ -752,7 +752,7 @@ def convrot_fp8_prepare_weights(W: torch.Tensor, layout: int = OUT_MAJOR,
     if src_scale is not None and scales == "pow2":
         # load time: the one check that reads the tensors' values
         bits = src_scale.view(torch.int32)
-        if bool((((bits & 0x7FFFFF) != 0) | (bits < 0)).any()):
+        if bool((((bits & 0x7FFFFF) != 0) | (bits < 0) | (bits == 0x7F800000)).any()):
             raise ValueError("src_scale of a pow2 weight must hold powers of two or zeros")
         if bool((bits == 0).any()):
             # the matrix instruction reads a zero as 2^-127
@@ -772,7 +772,7 @@ def convrot_fp8_prepare_weights(W: torch.Tensor, layout: int = OUT_MAJOR,
     wsb = lib.convrot_fp8_prepare_workspace_bytes(N, K, tag, layout)
     ws = _workspace(wsb, W.device, None)
     _launch(W.device, "convrot_fp8_prepare_weights", stream, _ptr(W), tag, layout,
-            _ptr(src_scale), N, K, ctypes.byref(desc), _ptr(ws), wsb, scratch=(codes, scale, ws))
+            _ptr(src_scale), N, K, ctypes.byref(desc), _ptr(ws), wsb, scratch=(W, codes, scale, ws))
     fw = FP8Weights(desc, codes, scale)
     fw._ws = ws  # keep alive until the stream has consumed it
     return fw

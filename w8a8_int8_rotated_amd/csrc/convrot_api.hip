@@ -901,7 +901,8 @@ static int norm_rope_args(int64_t B, int64_t T, int dtype, const convrot_rope *r
     if (pos_batch_stride < 0) return CONVROT_EINVAL;
     if (B * T > 0) {
         if (!positions) return CONVROT_EINVAL;
-        if (!aligned16(positions)) return CONVROT_EALIGN;
+        // read value by value; a step's positions start anywhere in a longer array
+        if (reinterpret_cast<uintptr_t>(positions) % 4 != 0) return CONVROT_EALIGN;
     }
     a->B = (int)B;
     a->T = (int)T;
@@ -1063,7 +1064,8 @@ static int qkv_norm_rope_args(int64_t B, int64_t T, int64_t N, int heads_q, int 
                               int64_t pos_batch_stride, void *Y, int y_dtype,
                               convrot::NormRope *a)
 {
-    if (heads_q < 1 || heads_kv < 1) return CONVROT_EINVAL;
+    if (B < 0 || T < 0 || heads_q < 1 || heads_kv < 1) return CONVROT_EINVAL;
+    if (B >= kI32Bound || T >= kI32Bound) return CONVROT_EUNSUPPORTED;   // T * N below fits
     int rc = check_rope(rope);
     if (rc != CONVROT_OK) return rc;
     const int64_t D = rope->head_dim;

@@ -108,8 +108,8 @@ __global__ __launch_bounds__(256) void block_weights_kernel(const T *__restrict_
                                                             float *__restrict__ scale)
 {
     __shared__ float red[4];
-    const int n = blockIdx.y * 128 + (threadIdx.x >> 1);
-    const int k0 = blockIdx.x * 128 + (threadIdx.x & 1) * 64;
+    const int n = blockIdx.x * 128 + (threadIdx.x >> 1);
+    const int k0 = blockIdx.y * 128 + (threadIdx.x & 1) * 64;
     const bool live = n < N;
     auto at = [&](int i) -> float {
         if constexpr (sizeof(T) == 4) return W[(int64_t)n * K + k0 + i];
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(256) void block_weights_kernel(const T *__restrict_
     amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
     float s, inv;
     block_scale(amax, pow2, s, inv);
-    if (threadIdx.x == 0) scale[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = s;
+    if (threadIdx.x == 0) scale[(int64_t)blockIdx.x * gridDim.y + blockIdx.y] = s;
     if (!live) return;
     for (int i = 0; i < 64; i += 4)
         *reinterpret_cast<int *>(codes + tiled_offset(n, k0 + i, K)) =
@@ -306,7 +306,8 @@ hipError_t launch_skinny(const Fp8Gemm &g, int waves, hipStream_t stream)
 hipError_t launch_fp8_block_weights(const void *W, InType in, int64_t N, int64_t K, bool pow2,
                                     uint8_t *codes, float *scale, hipStream_t stream)
 {
-    const dim3 grid((unsigned)(K / 128), (unsigned)((N + 127) / 128));
+    // (the second extent is at most 65535 in a launch: N / 128 can be more)
+    const dim3 grid((unsigned)((N + 127) / 128), (unsigned)(K / 128));
     if (in == InType::F32)
         hipLaunchKernelGGL((block_weights_kernel<float>), grid, dim3(256), 0, stream,
                            static_cast<const float *>(W), (int)N, (int)K, pow2, codes, scale);
