@@ -1,8 +1,10 @@
 /*
  * convrot.h -- C ABI of libconvrot.so: the ConvRot W8A8 INT8 linear layer on
- * AMD Instinct MI355X (gfx950).
+ * AMD Instinct MI355X (gfx950), and beside it (in sections of their own below)
+ * the FP8 block-scaled linear, rotary positions and the norms of queries and
+ * keys.
  *
- * The method (what every entry point computes):
+ * The method (what the INT8 entry points compute):
  *   - Linear layers of the INT8 package are W8A8: INT8 activations times INT8
  *     weights, placed behind a block-diagonal Hadamard rotation (lehuy.net
  *     article on HyperFlow H3 Flash, "Cach nen hoat dong", second bullet).

@@ -32,7 +32,7 @@ COPY_KERNEL = "__amd_rocclr_copyBuffer"
 
 def _short(name: str) -> str:
     name = name.replace("void ", "").replace("convrot::(anonymous namespace)::", "")
-    name = re.sub(r"\(\w+\)(?=\d)", "", name)      # an enumerator among the template arguments
+    name = re.sub(r"\((?:\w+::)*\w+\)(?=\d)", "", name)      # an enumerator among the template arguments
     return name.split("(")[0]
 
 

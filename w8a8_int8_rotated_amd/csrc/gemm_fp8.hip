@@ -35,11 +35,10 @@
 //   a full one)                                                    2.76 / 2.58 ms
 //   halves of a stage refilled 1.5 k-blocks ahead                  2.75 / 2.46 ms
 //   row tiles requested two ahead                                  2.69 / 2.40 ms
-// 2.5 and 2.8 PFLOP/s; the matrix cores are busy 0.62 and 0.71 of the time at
-// 1.77 GHz (the INT8 GEMM: 0.80 at 1.50 GHz: power sets their product).  LDS is the
-// next bound: a k-block costs 192 reads of 1 KiB and 64 KiB of copies, 2048 cycles
-// at 128 bytes a cycle, as many as its matrix instructions; a wave tile larger than
-// 128 x 64 would not fit its registers.
+// 2.5 and 2.8 PFLOP/s; the matrix cores are busy 0.65 and 0.72 of the time at
+// 1.75 GHz.  LDS is the next bound: a k-block costs 192 reads of 1 KiB and 64 KiB
+// of copies, 2048 cycles at 128 bytes a cycle, as many as its matrix instructions;
+// a wave tile larger than 128 x 64 would not fit its registers.
 #include "common.hpp"
 #include "gemm_common.hpp"
 
