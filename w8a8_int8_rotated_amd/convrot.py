@@ -228,21 +228,23 @@ def _launch(device, fn: str, stream, *args, scratch=()):
     device's current stream).  scratch: tensors allocated here for the call; on
     a caller's stream the allocator must not hand them out again before that
     stream has passed the call."""
+    index = device.index
     if stream is None:
         # the raw handle: a Stream object costs as much as the launch's checks
-        raw = torch._C._cuda_getCurrentRawStream(device.index)
+        raw = torch._C._cuda_getCurrentRawStream(index)
     else:
         raw = stream.cuda_stream
         for t in scratch:
             if t is not None:
                 t.record_stream(stream)
-    fun = getattr(library(), fn)
-    if device.index == torch.cuda.current_device():
+    fun = getattr(_lib or library(), fn)
+    if index == torch.cuda.current_device():
         rc = fun(*args, raw)
     else:
         with torch.cuda.device(device):
             rc = fun(*args, raw)
-    _check(fn, rc)
+    if rc:
+        _check(fn, rc)
 
 
 _DTYPE_TAGS = {torch.float32: F32, torch.bfloat16: BF16, torch.int8: I8, torch.int32: I32,
@@ -261,6 +263,12 @@ def _on_device(device, **tensors):
     """Every tensor the library will dereference is a GPU tensor on `device`
     (any GPU when None).  Called after the shape and dtype checks, so a
     host-side caller sees those errors first."""
+    if device is not None and device.type == "cuda":
+        for t in tensors.values():
+            if t is not None and t.device != device:
+                break
+        else:
+            return
     for name, t in tensors.items():
         if t is None:
             continue
@@ -857,6 +865,7 @@ def convrot_rope_prepare(dims, head_dim: int, theta: float = 10000.0,
 # convrot_heads, laid out by struct: several times cheaper to fill per call than
 # a ctypes structure (a bytes object passes as the pointer)
 _HEADS = struct.Struct("Piiqqq")
+_pack_heads = _HEADS.pack
 _Tensor = torch.Tensor
 assert _HEADS.size == ctypes.sizeof(convrot_heads)
 
@@ -869,14 +878,19 @@ def _heads(t, name: str, dtype, dims: int, B: int, T: int, H, D: int) -> bytes:
     shape, st = t.shape, t.stride()
     if len(st) != dims:
         raise ValueError(f"{name} must have as many dimensions as q")
-    h = shape[-2]
-    if shape[-1] != D or shape[-3] != T or (dims == 4 and shape[0] != B) \
-            or (H is not None and h != H):
+    if dims == 4:
+        b, n, h, d = shape
+        sb, sn, sh, sd = st
+    else:
+        n, h, d = shape
+        sn, sh, sd = st
+        b, sb = B, 0
+    if d != D or n != T or b != B or (H is not None and h != H):
         want = (*((B,) if dims == 4 else ()), T, "heads" if H is None else H, D)
         raise ValueError(f"{name} must have shape {want}, got {tuple(shape)}")
-    if st[-1] != 1:
+    if sd != 1:
         raise ValueError(f"{name} must have contiguous channels")
-    return _HEADS.pack(t.data_ptr(), h, 0, st[0] if dims == 4 else 0, st[-3], st[-2])
+    return _pack_heads(t.data_ptr(), h, 0, sb, sn, sh)
 
 
 def _heads_pair(q, k, rope, positions):
@@ -919,10 +933,12 @@ def _heads_out(out, name, like, lead):
         if out is not None:
             raise ValueError(f"{name} given without its input")
         return None, None
-    H, D = like.shape[-2:]
+    shape = like.shape
+    H, D = shape[-2], shape[-1]
     if out is None:
         out = torch.empty_like(like, memory_format=torch.contiguous_format)
-        return out, _HEADS.pack(out.data_ptr(), H, 0, lead[2] * H * D, H * D, D)
+        HD = H * D
+        return out, _pack_heads(out.data_ptr(), H, 0, lead[2] * HD, HD, D)
     return out, _heads(out, name, like.dtype, *lead, H, D)
 
 
