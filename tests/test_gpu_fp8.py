@@ -212,10 +212,10 @@ def test_hooks_equal_forward(cr, kind, M):
 
 
 @pytest.mark.parametrize("kind", ["f32", "pow2"])
-@pytest.mark.parametrize("M", [4, 50, 300])
-def test_non_finite_rows_stay_alone(cr, kind, M):
+@pytest.mark.parametrize("M,N", [(4, 272), (50, 272), (300, 272), (520, 5392)])
+def test_non_finite_rows_stay_alone(cr, kind, M, N):
     """NaN and infinities make their own token's outputs NaN, no other's."""
-    K, N = 512, 272
+    K = 512
     rng = np.random.default_rng(5)
     x = rng.standard_normal((M, K)).astype(np.float32)
     pw = cr.convrot_fp8_prepare_weights(
@@ -223,7 +223,7 @@ def test_non_finite_rows_stay_alone(cr, kind, M):
     clean = cr.convrot_fp8_linear_forward(bf16(x).cuda(), pw)
     bad = {0: np.nan, 1: np.inf, M - 1: -np.inf}
     for m, v in bad.items():
-        x[m, 130 + m] = v
+        x[m, (130 + m) % K] = v
     announce(f"fp8 non-finite M={M} {kind}")
     y = cr.convrot_fp8_linear_forward(bf16(x).cuda(), pw)
     keep = [m for m in range(M) if m not in bad]
@@ -243,11 +243,11 @@ def test_zero_and_empty(cr):
 
 
 @pytest.mark.parametrize("kind", ["f32", "pow2"])
-@pytest.mark.parametrize("M", [2, 40, 520])
-def test_graph_and_streams(cr, kind, M):
+@pytest.mark.parametrize("M,N", [(2, 528), (40, 528), (520, 528), (1025, 5392)])
+def test_graph_and_streams(cr, kind, M, N):
     """Captured calls replay to the eager result, with eager work between the
     replays; a call on another stream gives it too."""
-    K, N = 640, 528
+    K = 640
     X = torch.randn(M, K, device="cuda").to(torch.bfloat16)
     pw = cr.convrot_fp8_prepare_weights(torch.randn(N, K, device="cuda"), scales=kind)
     want = cr.convrot_fp8_linear_forward(X, pw)
@@ -285,6 +285,10 @@ def test_pow2_import_refuses_other_scales(cr):
 # every tile shape, the two-launch plan, ragged edges, odd and even counts of k-blocks
 PLANS = [(100, 384, 528), (192, 256, 21504), (520, 128, 5376), (768, 384, 10880),
          (1000, 256, 5376), (2041, 256, 5392), (4133, 640, 5392), (2500, 128, 16128)]
+# few rows or few outputs: the shapes of the kernel whose waves split the k-blocks
+# (fewer k-blocks than waves, counts that 8 does not divide), and a long axis
+PLANS += [(43, 4224, 32), (37, 640, 272), (333, 1280, 272), (93, 1664, 1776), (64, 1152, 5392),
+          (70, 2176, 16144), (300, 896, 2064), (65, 21504, 48), (333, 1920, 5376)]
 
 
 @pytest.mark.parametrize("M,K,N", PLANS)
@@ -323,11 +327,11 @@ def test_tile_plans(cr, M, K, N):
             assert worst <= 1.0
 
 
-@pytest.mark.parametrize("M", [8, 200, 300])
-def test_non_finite_rows_fp32(cr, M):
+@pytest.mark.parametrize("M,N", [(8, 272), (200, 272), (300, 272), (520, 5392)])
+def test_non_finite_rows_fp32(cr, M, N):
     """As above for the kernels behind fp32 outputs, where a NaN must not cross
     from one k-block's scales or one tile into another token either."""
-    K, N = 384, 272
+    K = 384
     x = torch.randn(M, K, generator=torch.Generator().manual_seed(M))
     pw = cr.convrot_fp8_prepare_weights(torch.randn(N, K, device="cuda"))
     clean = cr.convrot_fp8_linear_forward(x.bfloat16().cuda(), pw, out_dtype=torch.float32)

@@ -179,8 +179,9 @@ struct Fp8Gemm {
 };
 bool fp8_fuses_quantize(int64_t M);
 hipError_t launch_fp8_gemm(const Fp8Gemm &g, hipStream_t stream);
-// The tiled kernels behind it (gemm_fp8.hip).
+// The tiled kernels behind it (gemm_fp8.hip), and an estimate of their time (us).
 hipError_t launch_fp8_tiles(const Fp8Gemm &g, hipStream_t stream);
+double fp8_tiles_us(const Fp8Gemm &g);
 
 // ------------------------------------------ norms and rotary positions ----
 // Per-head rows: element (b, t, h, d) at p + b sb + t st + h sh + d.

@@ -301,6 +301,23 @@ hipError_t launch_skinny(const Fp8Gemm &g, int waves, hipStream_t stream)
     return hipGetLastError();
 }
 
+// The shapes of the few-rows kernel on quantised rows and the time of one k-block
+// per wave, in us: each workgroup's 8 waves take nkb / 8 k-blocks in turn, whose
+// loads nothing covers but a CU's other workgroups.  Measured from N = 32, K = 15360
+// (a few workgroups) to N = 16128 (several a CU): within a fifth of
+//   3 us + rounds of workgroups over the CUs * ceil(nkb / 8) * us.
+// The tiles read each code less often but take nkb k-blocks in turn, so they win
+// where N and M give the CUs a tile each (N = 5376, K = 5376, bf16 outputs: 96 rows
+// 13.1 us, tiles 18.2 us; 333 rows 33 us, 18 us), and lose far below that (64 rows,
+// N = 1008, K = 18944: 14.0 us with 1 x 1, 31.5 us with 2 x 4, tiles 54.4 us).
+struct SkinnyShape {
+    int rt, mt;
+    double us;
+};
+constexpr SkinnyShape kSkinnyShapes[] = {{1, 1, 0.40}, {2, 1, 0.62}, {2, 2, 0.90}, {2, 4, 1.45}};
+constexpr double kSkinnyF32Us = 1.65;       // 2 x 4 with F32 outputs: the conversions
+constexpr int64_t kMaxGridY = 65535;
+
 } // namespace
 
 hipError_t launch_fp8_block_weights(const void *W, InType in, int64_t N, int64_t K, bool pow2,
@@ -330,11 +347,6 @@ hipError_t launch_fp8_quantize(const void *X, int64_t M, int64_t K, bool pow2, u
 
 bool fp8_fuses_quantize(int64_t M) { return M <= 16; }
 
-// Up to 64 rows the weights are read once whatever the kernel, and the tiles'
-// LDS pipeline is slower than loads straight to registers (64 rows at N = K = 5376:
-// 12.3 us against 16.9 us of the best tiles); from 65 rows on the tiles win (128
-// rows: 17.3 us against 17.8 us).  F32 outputs: 128 rows 18.2 us against 34.0 us,
-// 333 rows 33.7 us against 36.8 us, but 105 us against 81 us at N = 16128.
 hipError_t launch_fp8_gemm(const Fp8Gemm &g, hipStream_t stream)
 {
     if (!g.qx) {
@@ -349,10 +361,24 @@ hipError_t launch_fp8_gemm(const Fp8Gemm &g, hipStream_t stream)
         if (2 * blocks <= cus) return launch_skinny<1, 1, true>(g, 8, stream);
         return launch_skinny<2, 1, true>(g, 8, stream);
     }
-    if (g.M <= 16) return launch_skinny<2, 1, false>(g, 8, stream);
-    if (g.M <= 32) return launch_skinny<2, 2, false>(g, 8, stream);
-    if (g.M <= 64 || (g.f32_out && g.M <= 256)) return launch_skinny<2, 4, false>(g, 8, stream);
-    return launch_fp8_tiles(g, stream);
+    const int64_t cus = device_cu_count(), nb = g.N / 16, mb = (g.M + 15) / 16;
+    const int64_t steps = (g.K / 128 + 7) / 8;
+    double best_us = fp8_tiles_us(g);
+    int best = -1;
+    for (int i = 0; i < 4; ++i) {
+        const SkinnyShape &s = kSkinnyShapes[i];
+        const int64_t gx = (nb + s.rt - 1) / s.rt, gy = (mb + s.mt - 1) / s.mt;
+        const double step = i == 3 && g.f32_out ? kSkinnyF32Us : s.us;
+        const double us = 3.0 + (double)((gx * gy + cus - 1) / cus * steps) * step;
+        if (gy <= kMaxGridY && us < best_us) best = i, best_us = us;
+    }
+    switch (best) {
+    case 0: return launch_skinny<1, 1, false>(g, 8, stream);
+    case 1: return launch_skinny<2, 1, false>(g, 8, stream);
+    case 2: return launch_skinny<2, 2, false>(g, 8, stream);
+    case 3: return launch_skinny<2, 4, false>(g, 8, stream);
+    default: return launch_fp8_tiles(g, stream);
+    }
 }
 
 } // namespace convrot

@@ -538,7 +538,29 @@ constexpr TileShape kFp8Shapes[] = {{256, 256, 1.0}, {256, 128, 0.64}, {128, 256
 constexpr TileShape kBf16Shapes[] = {{128, 256, 1.0}, {128, 128, 0.61}, {128, 64, 0.49}};
 constexpr double kSecondLaunch = 0.06;
 
+// Rounds of one shape's tiles over the CUs, in units of the largest shape's tile.
+double shape_cost(const TileShape &s, int64_t rows, int64_t N, int64_t cus)
+{
+    const int64_t tiles = (rows + s.tm - 1) / s.tm * ((N + s.tn - 1) / s.tn);
+    return (double)((tiles + cus - 1) / cus) * s.cost;
+}
+
 } // namespace
+
+// Where the tiles compete with the few-rows kernel (one shape, a round or a few):
+// k-blocks in turn, 0.35 us each in a 128 x 64 tile (F32 outputs 0.69 us).  At
+// N = 1024 .. 5376: 9.2, 18.1, 36.1 and 61 us for 16, 42, 96 and 168 of them, F32
+// outputs 15.5, 33, 70.7 and 122 us; within a tenth of this.
+double fp8_tiles_us(const Fp8Gemm &g)
+{
+    const int64_t cus = device_cu_count();
+    double best = 1e30;
+    if (g.f32_out)
+        for (const TileShape &s : kBf16Shapes) best = std::min(best, shape_cost(s, g.M, g.N, cus));
+    else
+        for (const TileShape &s : kFp8Shapes) best = std::min(best, shape_cost(s, g.M, g.N, cus));
+    return 4.0 + best * (double)(g.K / kKB) * (g.f32_out ? 1.41 : 1.08);
+}
 
 // The plan with the least estimated time: one shape throughout, or whole rounds
 // of the largest shape and another one for the last rows (M = 4096 at
@@ -548,11 +570,7 @@ hipError_t launch_fp8_tiles(const Fp8Gemm &g, hipStream_t stream)
     const TileShape *const shapes = g.f32_out ? kBf16Shapes : kFp8Shapes;
     const int n_shapes = g.f32_out ? 3 : 6;
     const int64_t cus = device_cu_count();
-    auto cost = [&](int i, int64_t rows) {
-        const int64_t tiles = (rows + shapes[i].tm - 1) / shapes[i].tm *
-                              ((g.N + shapes[i].tn - 1) / shapes[i].tn);
-        return (double)((tiles + cus - 1) / cus) * shapes[i].cost;
-    };
+    auto cost = [&](int i, int64_t rows) { return shape_cost(shapes[i], rows, g.N, cus); };
     int best = 0;
     int64_t m1 = 0;                  // rows of the first launch (shape 0)
     double best_cost = 1e30;
