@@ -307,9 +307,9 @@ hipError_t launch_skinny(const Fp8Gemm &g, int waves, hipStream_t stream)
 // (a few workgroups) to N = 16128 (several a CU): within a fifth of
 //   3 us + rounds of workgroups over the CUs * ceil(nkb / 8) * us.
 // The tiles read each code less often but take nkb k-blocks in turn, so they win
-// where N and M give the CUs a tile each (N = 5376, K = 5376, bf16 outputs: 96 rows
-// 13.1 us, tiles 18.2 us; 333 rows 33 us, 18 us), and lose far below that (64 rows,
-// N = 1008, K = 18944: 14.0 us with 1 x 1, 31.5 us with 2 x 4, tiles 54.4 us).
+// where N and M give the CUs a tile each (128 rows, K = 5376, N = 16128: 20.4 us,
+// here 35.0 us), and lose far below that (96 rows, N = 5376: 18.2 us, here 13.1 us; 64
+// rows, N = 1008, K = 18944: 54.4 us, here 31.5 us with 2 x 4, 14.0 us with 1 x 1).
 struct SkinnyShape {
     int rt, mt;
     double us;

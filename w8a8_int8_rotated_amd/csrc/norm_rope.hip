@@ -182,25 +182,44 @@ __device__ __forceinline__ void rotate(float (&v)[8], const float (&cs)[4], cons
     }
 }
 
+// A token's positions as loaded (int32 or fp32), `axes` of them.
+struct Positions {
+    uint32_t v[4];
+};
+
+__device__ __forceinline__ Positions load_positions(const NormRope &a, int64_t at)
+{
+    Positions p = {};
+    const uint32_t *const src = static_cast<const uint32_t *>(a.pos) + at;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < a.axes) p.v[i] = src[i];
+    return p;
+}
+
+// The frequency (in revolutions per position unit) and axis of pair p.
+__device__ __forceinline__ void load_pair(const NormRope &a, int p, double &f, int &ax)
+{
+    f = a.freq[p] * 0.15915494309189535;
+    ax = min(max(a.axis[p], 0), a.axes - 1);
+}
+
 // cos and sin of the token's pairs into this wave's table; entries from R/2 up
-// to npad are never used in a rotation but are read.
-__device__ __forceinline__ void fill_table(const NormRope &a, int64_t pos_at, float2 *tab,
-                                           int npad, int lane)
+// to npad are never used in a rotation but are read.  (f, ax): pair `lane`.
+__device__ __forceinline__ void fill_table(const NormRope &a, const Positions &ps, double f, int ax,
+                                           float2 *tab, int npad, int lane)
 {
     const int half = a.R >> 1;
     double pos[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t at = pos_at + min(i, a.axes - 1);
-        pos[i] = a.pos_f32 ? (double)static_cast<const float *>(a.pos)[at]
-                           : (double)static_cast<const int32_t *>(a.pos)[at];
-    }
+    for (int i = 0; i < 4; ++i)
+        pos[i] = a.pos_f32 ? (double)__uint_as_float(ps.v[i]) : (double)(int)ps.v[i];
     for (int p = lane; p < npad; p += 64) {
         float s = 0.0f, c = 1.0f;
         if (p < half) {
-            const int ax = min(max(a.axis[p], 0), a.axes - 1);
+            if (p >= 64) load_pair(a, p, f, ax);
             const double x = ax == 0 ? pos[0] : ax == 1 ? pos[1] : ax == 2 ? pos[2] : pos[3];
-            double rev = x * a.freq[p] * 0.15915494309189535;
+            double rev = x * f;
             rev -= rint(rev);
             sincospif((float)(2.0 * rev), &s, &c);
             if (a.inverse) s = -s;
@@ -214,9 +233,10 @@ __device__ __forceinline__ void fill_table(const NormRope &a, int64_t pos_at, fl
 }
 
 // A launch's shape: W = wq + wk waves per token, wave w < wq on the queries'
-// units w, w + wq, ..., the others on the keys'; `slots` tokens at a time.
+// units w, w + wq, ..., the others on the keys'; `slots` tokens at a time, which
+// are db batches and dt tokens.
 struct Shape {
-    int lg, wq, wk, slots;
+    int lg, wq, wk, slots, db, dt;
 };
 
 template <bool F32, NormRopeMode MODE, int PAIR>
@@ -260,18 +280,46 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormRope a, Shape sh)
     }
     float dw[8] = {};                    // backward: sums of g' x r
 
-    for (uint32_t tok = slot < sh.slots ? slot : tokens; tok < tokens; tok += sh.slots) {
-        const int b = (int)(tok / (uint32_t)a.T), t = (int)tok - b * a.T;
-        const int64_t x0 = b * xr.sb + t * xr.st, y0 = b * yr.sb + t * yr.st;
-        const int64_t g0 = b * gr.sb + t * gr.st;
-        Raw<F32> rx, rg;
-        auto load = [&](int u) {
-            const int head = u * hpw + hg;
-            rx = load_raw<F32, PAIR>(xr.p, x0 + head * xr.sh, m, head < heads);
-            if constexpr (BWD) rg = load_raw<F32, PAIR>(gr.p, g0 + head * gr.sh, m, head < heads);
-        };
+    uint32_t tok = slot < sh.slots ? slot : tokens;
+    int b = (int)(tok / (uint32_t)a.T), t = (int)tok - b * a.T;
+    int64_t x0 = 0, y0 = 0, g0 = 0;
+    Raw<F32> rx, rg;
+    auto load = [&](int u) {
+        const int head = u * hpw + hg;
+        rx = load_raw<F32, PAIR>(xr.p, x0 + head * xr.sh, m, head < heads);
+        if constexpr (BWD) rg = load_raw<F32, PAIR>(gr.p, g0 + head * gr.sh, m, head < heads);
+    };
+    auto load_first = [&] {
+        x0 = b * xr.sb + t * xr.st;
+        y0 = b * yr.sb + t * yr.st;
+        g0 = b * gr.sb + t * gr.st;
         load(first);
-        fill_table(a, b * a.pos_sb + (int64_t)t * a.axes, tab, npad, lane);
+    };
+    // Loads return in order, so a token's positions are requested before its rows and
+    // the frequency of a lane's pair once a wave: the table is then evaluated while
+    // the rows are on their way (8 + 4 heads of 36135 tokens, backward: 76 us, 105 us
+    // with rows, positions and frequencies requested in this order for every token).
+    // Only a forward wave's first token has its rows first: with many heads it is its
+    // only one (84 heads of 38656 tokens: 313 us, 316 us).
+    double f = 0.0;
+    int ax = 0;
+    Positions ps = {};
+    auto load_token = [&] {
+        ps = load_positions(a, b * a.pos_sb + (int64_t)t * a.axes);
+        __builtin_amdgcn_sched_barrier(0);
+        load_first();
+    };
+    if (tok < tokens) {
+        if constexpr (!BWD) {
+            load_first();
+            __builtin_amdgcn_sched_barrier(0);
+            ps = load_positions(a, b * a.pos_sb + (int64_t)t * a.axes);
+        }
+        if (lane < a.R >> 1) load_pair(a, lane, f, ax);
+    }
+    while (tok < tokens) {
+        if constexpr (BWD) load_token();
+        fill_table(a, ps, f, ax, tab, npad, lane);
         float cs[4], sn[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -313,6 +361,13 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormRope a, Shape sh)
                 for (int i = 0; i < 8; ++i) v[i] = r * __builtin_fmaf(-v[i], mean, d[i]);
             }
             store<F32, PAIR>(yr.p, y0 + head * yr.sh, m, head < heads, v);
+        }
+        tok += sh.slots;
+        b += sh.db;
+        t += sh.dt;
+        if (t >= a.T) t -= a.T, ++b;
+        if constexpr (!BWD) {
+            if (tok < tokens) load_token();
         }
     }
     if constexpr (BWD) {
@@ -396,6 +451,8 @@ void launch_pairing(const NormRope &a, const Shape &sh, unsigned grid, size_t ld
 constexpr int64_t kWaves = 8192, kBackwardWaves = 4096;
 constexpr int kMaxSideWaves = 32;
 constexpr int64_t kMaxSlots = 1 << 22;
+constexpr int kFewUnits = 8;
+constexpr int64_t kFewUnitWaves = 16384;
 
 int64_t norm_rope_partial_rows(int64_t tokens)
 {
@@ -421,8 +478,15 @@ hipError_t launch_norm_rope(NormRopeMode mode, const NormRope &a, hipStream_t st
         sh.wq = waves(units0);
         sh.wk = waves(units1);
         const int W = sh.wq + sh.wk;
-        sh.slots = (int)(bwd ? std::min<int64_t>(tokens, kBackwardWaves / W)
-                              : std::min<int64_t>(tokens, kMaxSlots));
+        // A wave of few units spends more on its frequencies than on its rows, so it
+        // takes several tokens (2 + 2 units, 38274 tokens: 61.7 us, 70 us with a token a
+        // wave); one of many is better off with one (11 + 11 units, 38656 tokens:
+        // 317 us, 328 us with 16384 waves).
+        const int64_t most = bwd ? kBackwardWaves / W
+                             : units0 + units1 <= kFewUnits ? kFewUnitWaves / W : kMaxSlots;
+        sh.slots = (int)std::min<int64_t>(tokens, most);
+        sh.db = sh.slots / a.T;
+        sh.dt = sh.slots % a.T;
         grid = ((int64_t)sh.slots * W + 3) / 4;
         size_t lds = (size_t)4 * 4 * (1 << sh.lg) * sizeof(float2);
         if (bwd) lds = std::max(lds, (size_t)4 * 2 * a.D * sizeof(float));
