@@ -130,6 +130,10 @@ CASES = [
     dict(B=1, T=13, Hq=129, Hk=3, D=32, dims=(10, 6), layout="qkv"),
     dict(B=1, T=9, Hq=7, Hk=7, D=40, dims=(40,), pairing="half", dtype="bf16", layout="qkv"),
     dict(B=1, T=2100, Hq=4, Hk=2, D=64, dims=(24, 40), layout="qkv", pos="f32"),
+    # waves that take several tokens, from one batch to the next, or many batches apart
+    dict(B=3, T=6007, Hq=2, Hk=2, D=32, dims=(20, 12), pos="f32"),
+    dict(B=2500, T=8, Hq=3, Hk=1, D=64, dims=(64,), pairing="half", layout="bhtd", shared=True),
+    dict(B=1700, T=11, Hq=2, Hk=1, D=192, dims=(100, 92), dtype="f32"),
 ]
 
 
