@@ -357,3 +357,33 @@ def test_pow2_import_zero_scales(cr):
     codes[5, 5] = 1.0
     with pytest.raises(ValueError, match="scale is 0"):
         cr.convrot_fp8_prepare_weights(codes.to(F8), src_scale=scale, scales="pow2")
+
+
+def test_largest_extents(cr):
+    """The most rows, inputs and outputs that the shape limits allow (byte offsets
+    up to 2^31 in both code matrices, past it in the inputs and the output): rows and
+    columns at the corners against the same rows and weight blocks in a call of their
+    own.  Both calls form the same sum of each k-block; the K / 128 sums are then
+    added in two orders, and both outputs are rounded to bf16."""
+    M = N = 32752
+    K = 65536
+    announce(f"fp8 largest {M}x{K}x{N}")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    X = torch.randn(M, K, generator=g, device="cuda", dtype=torch.bfloat16)
+    W = torch.randn(N, K, generator=g, device="cuda", dtype=torch.bfloat16)
+    rows = torch.tensor([0, 1, 255, 16384, 32512, M - 1], device="cuda")
+    blocks = ((0, 128), (16384, 16512), (32640, N))
+    assert cr.convrot_fp8_packed_bytes(N + 16, K) == 0       # one row block more is refused
+    for kind in ("f32", "pow2"):
+        y = cr.convrot_fp8_linear_forward(X, cr.convrot_fp8_prepare_weights(W, scales=kind))
+        for a, b in blocks:
+            part = cr.convrot_fp8_prepare_weights(W[a:b].contiguous(), scales=kind)
+            want = cr.convrot_fp8_linear_forward(X[rows].contiguous(), part).double()
+            mag = X[rows].double().abs() @ W[a:b].double().abs().t()
+            # codes are within 1/16 of the values they stand for, products within 1/7
+            bound = 2 * (K // 128 + 8) * 2.0 ** -24 * (8 / 7) * mag
+            bound = bound + 2 * 2.0 ** -8 * (want.abs() + bound)
+            worst = float(((y[rows][:, a:b].double() - want).abs() / bound).max())
+            print(f"[parity] largest {kind} {a}: worst error {worst:.3f} of its bound", flush=True)
+            assert worst <= 1.0
+        del y

@@ -465,3 +465,27 @@ def test_steps_of_a_longer_position_array(cr, pos, axes):
                                                c.wk.cuda(), plan, p[t:t + 1])
         for y, z in zip(whole, step):
             assert torch.equal(y[:, t:t + 1], z), t
+
+
+def test_offsets_past_32_bits(cr):
+    """More than 2^31 elements of queries: the last tokens' rows, forward, inverse
+    and backward, are those of a call on these tokens alone."""
+    T, H, D = 140_000, 128, 128
+    announce("norm + rope, 2.3e9 elements")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q = torch.randn(T, H, D, generator=g, device="cuda", dtype=torch.bfloat16)
+    pos = torch.randint(0, 1000, (T, 3), generator=g, device="cuda", dtype=torch.int32)
+    w = torch.randn(D, generator=g, device="cuda")
+    plan = cr.convrot_rope_prepare([16, 56, 56], D)
+    for part in (slice(0, 3), slice(131_070, 131_075), slice(T - 5, T)):
+        x, p = q[part], pos[part].contiguous()
+        for run in (lambda q, pos: cr.convrot_rope_forward(q, None, plan, pos)[0],
+                    lambda q, pos: cr.convrot_rope_forward(q, None, plan, pos, inverse=True)[0],
+                    lambda q, pos: cr.convrot_qk_norm_rope_forward(q, None, w, None, plan, pos)[0],
+                    lambda q, pos: cr.convrot_qk_norm_rope_backward(
+                        q.flip(0) if q.shape[0] < T else G, None, q, None, w, None, plan, pos)[0]):
+            G = q.clone()
+            G[part] = x.flip(0)
+            whole = run(q, pos)
+            assert torch.equal(whole[part], run(x, p))
+            del G, whole
