@@ -485,12 +485,22 @@ CONVROT_API int convrot_fp8_linear_forward(const void *X, int64_t M,
 /* Its two stages, as test hooks: q K-tiled e4m3 codes (Mp x K bytes; padding
  * rows are left as they were) and s F32 [K / 128, Mp] (k-block major, Mp = M
  * rounded up to 16; padding columns are left as they were) of bf16 X [M, K];
- * and the product of such codes and scales with W. */
+ * and the product of such codes and scales with W.  convrot_fp8_gemm_dequant
+ * takes rows of either kind of scales with a weight of either kind;
+ * convrot_fp8_gemm_dequant_scales is told the rows' kind.  A POW2 weight and
+ * rows said to be POW2 run the arithmetic of that weight's forward, in which
+ * the matrix instruction reads the rows' scales' exponents alone: they must be
+ * normal powers of two, or 0 where the block's codes are all 0 (as
+ * convrot_fp8_quantize leaves them with POW2), which is not checked here. */
 CONVROT_API int convrot_fp8_quantize(const void *X, int64_t M, int64_t K, int scales, uint8_t *q,
                                      float *s, void *stream);
 CONVROT_API int convrot_fp8_gemm_dequant(const uint8_t *q, const float *s, int64_t M,
                                          const convrot_fp8_weights *W, const float *bias, void *Y,
                                          int y_dtype, void *stream);
+CONVROT_API int convrot_fp8_gemm_dequant_scales(const uint8_t *q, const float *s, int scales,
+                                                int64_t M, const convrot_fp8_weights *W,
+                                                const float *bias, void *Y, int y_dtype,
+                                                void *stream);
 
 /* ------------------------------------------------------------------ */
 /* norms and rotary positions of queries and keys                      */

@@ -387,3 +387,38 @@ def test_largest_extents(cr):
             print(f"[parity] largest {kind} {a}: worst error {worst:.3f} of its bound", flush=True)
             assert worst <= 1.0
         del y
+
+
+@pytest.mark.parametrize("rows_kind,kind", [("f32", "pow2"), ("pow2", "f32"), ("f32", "f32"),
+                                            ("pow2", "pow2")])
+@pytest.mark.parametrize("M,K,N", [(9, 640, 272), (40, 640, 272), (520, 256, 5392),
+                                   (1000, 384, 5392)])
+def test_gemm_dequant_takes_any_row_scales(cr, rows_kind, kind, M, K, N):
+    """Rows of either kind of scales by weights of either kind, in the few-rows
+    kernel and in tiles: the same product of codes and scales (the docstring's
+    bound)."""
+    rng = np.random.default_rng(M + N)
+    x, w = rows(rng, M, K), rng.standard_normal((N, K)).astype(np.float32)
+    bias = rng.standard_normal(N).astype(np.float32)
+    pw = cr.convrot_fp8_prepare_weights(torch.from_numpy(w).cuda(), scales=kind)
+    (xq, sx), (wq, sw) = quantize_rows(x, rows_kind), quantize_blocks(w, kind)
+    q, s = cr.convrot_fp8_quantize(bf16(x).cuda(), rows_kind)
+    for dt in (torch.bfloat16, torch.float32):
+        announce(f"fp8 gemm {M}x{K}x{N}: {rows_kind} rows, {kind} weight, {dt}")
+        y = cr.convrot_fp8_gemm_dequant(q, s, M, pw, bias=torch.from_numpy(bias).cuda(),
+                                        out_dtype=dt)
+        check(y, xq, sx, wq, sw, bias, f"gemm {M}x{K}x{N} {rows_kind}/{kind} {dt}")
+
+
+@pytest.mark.parametrize("kind", ["f32", "pow2"])
+@pytest.mark.parametrize("M,K,N", [(40, 640, 272), (520, 256, 5392), (1000, 384, 5392)])
+def test_stages_equal_forward(cr, kind, M, K, N):
+    """The two stages, told the rows' kind, are the forward bit for bit."""
+    rng = np.random.default_rng(M)
+    X = bf16(rows(rng, M, K)).cuda()
+    pw = cr.convrot_fp8_prepare_weights(torch.randn(N, K, device="cuda"), scales=kind)
+    q, s = cr.convrot_fp8_quantize(X, kind)
+    for dt in (torch.bfloat16, torch.float32):
+        announce(f"fp8 stages {M}x{K}x{N} {kind} {dt}")
+        y = cr.convrot_fp8_gemm_dequant(q, s, M, pw, out_dtype=dt, scales=kind)
+        assert torch.equal(y, cr.convrot_fp8_linear_forward(X, pw, out_dtype=dt))

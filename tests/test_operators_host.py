@@ -342,3 +342,21 @@ def test_norm_and_qkv_binding_refuse(cr):
         cr.convrot_rope_prepare((15,), 64)
     with pytest.raises(ValueError, match="device must be a GPU"):
         cr.convrot_rope_prepare((16,), 64, device="cpu")
+
+
+def test_gemm_dequant_rows_kind_refusals(cr):
+    lib = cr.library()
+    g = lambda d, kind=0, M=4, qx=FAKE, s=FAKE, y=0: lib.convrot_fp8_gemm_dequant_scales(
+        qx, s, kind, M, ctypes.byref(d), None, FAKE, y, None)
+    for kind in (0, 1):
+        for d in (fp8_desc(cr), fp8_desc(cr, scales=1)):
+            assert g(d, kind, M=0, qx=None) == cr.OK
+            assert g(d, kind, M=-1) == cr.EINVAL and g(d, kind, s=None) == cr.EINVAL
+            assert g(d, kind, s=ODD) == cr.EALIGN and g(d, kind, y=cr.I8) == cr.EUNSUPPORTED
+    assert g(fp8_desc(cr), 2) == cr.EINVAL and g(fp8_desc(cr), -1, M=0) == cr.EINVAL
+    assert g(fp8_desc(cr, magic=1), 2) == cr.ELAYOUT
+    q, s = torch.zeros(16, 256, dtype=torch.uint8), torch.zeros(2, 16)
+    with pytest.raises(ValueError, match="scales must be"):
+        cr.convrot_fp8_gemm_dequant(q, s, 4, fake_fp8(cr), scales="e8")
+    with pytest.raises(ValueError, match="GPU tensor"):
+        cr.convrot_fp8_gemm_dequant(q, s, 4, fake_fp8(cr), scales="pow2")

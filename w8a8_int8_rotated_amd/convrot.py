@@ -151,6 +151,8 @@ _SIGNATURES = {
     "convrot_fp8_quantize": (_c_int, [_c_p, _c_i64, _c_i64, _c_int, _c_p, _c_p, _c_p]),
     "convrot_fp8_gemm_dequant": (
         _c_int, [_c_p, _c_p, _c_i64, _FW, _c_p, _c_p, _c_int, _c_p]),
+    "convrot_fp8_gemm_dequant_scales": (
+        _c_int, [_c_p, _c_p, _c_int, _c_i64, _FW, _c_p, _c_p, _c_int, _c_p]),
     "convrot_rope_prepare": (
         _c_int, [ctypes.POINTER(ctypes.c_int32), _c_int, _c_int, ctypes.c_double, _c_int, _c_int,
                  _RP, _c_p]),
@@ -1210,9 +1212,14 @@ def convrot_fp8_quantize(X: torch.Tensor, scales: str = "f32", q=None, s=None, s
 
 
 def convrot_fp8_gemm_dequant(q: torch.Tensor, s: torch.Tensor, M: int, W: FP8Weights, bias=None,
-                             out_dtype: torch.dtype = torch.bfloat16, out=None, stream=None):
-    """Y [M, N] from the codes and scales of M rows (convrot_fp8_quantize)."""
+                             out_dtype: torch.dtype = torch.bfloat16, out=None, stream=None,
+                             scales: str = "f32"):
+    """Y [M, N] from the codes and scales of M rows (convrot_fp8_quantize), of
+    either kind.  scales='pow2' says that the rows' are powers of two or zeros
+    (not checked): with a 'pow2' weight that is its forward's arithmetic."""
     dev = _fp8_weights(W, "W")
+    if scales not in FP8_SCALES:
+        raise ValueError(f"scales must be one of {sorted(FP8_SCALES)}")
     _need(q, "q", torch.uint8, (padded_rows(M), W.K))
     _need(s, "s", torch.float32, (W.K // 128, padded_rows(M)))
     _opt(bias, "bias", torch.float32, (W.N,))
@@ -1220,8 +1227,8 @@ def convrot_fp8_gemm_dequant(q: torch.Tensor, s: torch.Tensor, M: int, W: FP8Wei
     _on_device(dev, q=q, s=s, bias=bias, out=out)
     if out is None:
         out = torch.empty((M, W.N), dtype=out_dtype, device=dev)
-    _launch(dev, "convrot_fp8_gemm_dequant", stream, _ptr(q), _ptr(s), M, W.ref(), _ptr(bias),
-            _ptr(out), _dtype_tag(out.dtype), scratch=(out,))
+    _launch(dev, "convrot_fp8_gemm_dequant_scales", stream, _ptr(q), _ptr(s), FP8_SCALES[scales],
+            M, W.ref(), _ptr(bias), _ptr(out), _dtype_tag(out.dtype), scratch=(out,))
     return out
 
 

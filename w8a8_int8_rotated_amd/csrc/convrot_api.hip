@@ -789,21 +789,33 @@ int convrot_fp8_quantize(const void *X, int64_t M, int64_t K, int scales, uint8_
                                                    s, static_cast<hipStream_t>(stream)));
 }
 
-int convrot_fp8_gemm_dequant(const uint8_t *q, const float *s, int64_t M,
-                             const convrot_fp8_weights *W, const float *bias, void *Y,
-                             int y_dtype, void *stream)
+// The matrix instruction may apply the rows' scales (reading their exponents
+// alone) only if both the rows' and the weight's are powers of two.
+int convrot_fp8_gemm_dequant_scales(const uint8_t *q, const float *s, int scales, int64_t M,
+                                    const convrot_fp8_weights *W, const float *bias, void *Y,
+                                    int y_dtype, void *stream)
 {
     int rc = check_fp8_weights(W);
     if (rc != CONVROT_OK) return rc;
+    if (!valid_fp8_scales(scales)) return CONVROT_EINVAL;
     if ((rc = check_rows(M, W->K)) != CONVROT_OK) return rc;
     if ((rc = check_out_dtype(y_dtype)) != CONVROT_OK) return rc;
     if (M == 0) return CONVROT_OK;
     if (!q || !s || !Y) return CONVROT_EINVAL;
     if (!aligned16(q) || !aligned16(s) || !aligned16(Y) || (bias && !aligned16(bias)))
         return CONVROT_EALIGN;
-    const convrot::Fp8Gemm g = {nullptr, q, s, W->codes, W->scale, bias, Y, M, W->N, W->K,
-                                W->scales == CONVROT_FP8_SCALE_POW2, y_dtype == CONVROT_F32};
+    const bool pow2 = scales == CONVROT_FP8_SCALE_POW2 && W->scales == CONVROT_FP8_SCALE_POW2;
+    const convrot::Fp8Gemm g = {nullptr, q, s, W->codes, W->scale, bias, Y, M, W->N, W->K, pow2,
+                                y_dtype == CONVROT_F32};
     return hip_status(convrot::launch_fp8_gemm(g, static_cast<hipStream_t>(stream)));
+}
+
+int convrot_fp8_gemm_dequant(const uint8_t *q, const float *s, int64_t M,
+                             const convrot_fp8_weights *W, const float *bias, void *Y,
+                             int y_dtype, void *stream)
+{
+    return convrot_fp8_gemm_dequant_scales(q, s, CONVROT_FP8_SCALE_F32, M, W, bias, Y, y_dtype,
+                                           stream);
 }
 
 // ---------------------------------------------------------------------------
