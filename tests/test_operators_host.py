@@ -360,3 +360,17 @@ def test_gemm_dequant_rows_kind_refusals(cr):
         cr.convrot_fp8_gemm_dequant(q, s, 4, fake_fp8(cr), scales="e8")
     with pytest.raises(ValueError, match="GPU tensor"):
         cr.convrot_fp8_gemm_dequant(q, s, 4, fake_fp8(cr), scales="pow2")
+
+
+def test_stream_of_another_device_refused(cr):
+    class Stream:
+        device = torch.device("cuda", 1)
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        cr.convrot_rope_prepare((16,), 64, device="cuda:0", stream=Stream())
+    X, plan = torch.zeros(32, 256, dtype=bf), fake_plan(cr)
+    for call in (lambda: cr.convrot_fp8_linear_forward(X, fake_fp8(cr), stream=Stream()),
+                 lambda: cr.convrot_fp8_prepare_weights(X, stream=Stream()),
+                 lambda: cr.convrot_fp8_quantize(X, stream=Stream()),
+                 lambda: cr.convrot_rope_forward(Q, Q, plan, P, stream=Stream())):
+        with pytest.raises(ValueError, match="GPU tensor on cuda:1"):
+            call()

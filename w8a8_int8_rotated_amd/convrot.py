@@ -225,20 +225,11 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _launch(device, fn: str, stream, *args, scratch=()):
-    """Call the library with `device` current, on `stream` (default: that
-    device's current stream).  scratch: tensors allocated here for the call; on
-    a caller's stream the allocator must not hand them out again before that
-    stream has passed the call."""
+def _launch(device, fn: str, *args):
+    """Call the library with `device` current, on that device's current stream."""
     index = device.index
-    if stream is None:
-        # the raw handle: a Stream object costs as much as the launch's checks
-        raw = torch._C._cuda_getCurrentRawStream(index)
-    else:
-        raw = stream.cuda_stream
-        for t in scratch:
-            if t is not None:
-                t.record_stream(stream)
+    # the raw handle: a Stream object costs as much as the launch's checks
+    raw = torch._C._cuda_getCurrentRawStream(index)
     fun = getattr(_lib or library(), fn)
     if index == torch.cuda.current_device():
         rc = fun(*args, raw)
@@ -247,6 +238,40 @@ def _launch(device, fn: str, stream, *args, scratch=()):
             rc = fun(*args, raw)
     if rc:
         _check(fn, rc)
+
+
+def _tensors(v):
+    """The tensors an argument or a result consists of."""
+    if isinstance(v, torch.Tensor):
+        yield v
+    elif isinstance(v, tuple):
+        for x in v:
+            yield from _tensors(x)
+    elif isinstance(v, (PreparedWeights, FP8Weights, RopePlan)):
+        yield from (t for t in vars(v).values() if isinstance(t, torch.Tensor))
+
+
+def _on_stream(fn, args: dict):
+    """fn(**args) on args["stream"], which must be ordered after whatever made the
+    arguments.  It is the current stream for the whole call, so that what the call
+    copies, reads back and allocates is ordered on it too; nothing of the call is
+    ordered against the stream that was current.  The allocator keeps the arguments'
+    memory until this stream has passed the call, and the results' (this stream's)
+    until the stream that was current has passed what it uses them for."""
+    stream = args.pop("stream")
+    device = args.get("device")
+    if device is not None and torch.device(device).index not in (None, stream.device.index):
+        raise ValueError(f"stream is on {stream.device}, device is {device}")
+    _on_device(stream.device,
+               **{n: t for n, t in args.items() if isinstance(t, torch.Tensor)})
+    current = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = fn(**args)
+    for t in _tensors(tuple(args.values())):
+        t.record_stream(stream)
+    for t in _tensors(out if isinstance(out, tuple) else (out,)):
+        t.record_stream(current)
+    return out
 
 
 _DTYPE_TAGS = {torch.float32: F32, torch.bfloat16: BF16, torch.int8: I8, torch.int32: I32,
@@ -744,6 +769,8 @@ def convrot_fp8_prepare_weights(W: torch.Tensor, layout: int = OUT_MAJOR,
     """Quantise and pack a weight (``[N, K]`` or ``[K, N]`` per layout) to e4m3
     with one scale per 128 x 128 block, float32 or (scales='pow2') a power of
     two; or import float8_e4m3fn codes with src_scale [ceil(N/128), K/128]."""
+    if stream is not None:
+        return _on_stream(convrot_fp8_prepare_weights, locals())
     lib = library()
     if not isinstance(W, torch.Tensor) or W.dim() != 2:
         raise ValueError("W must be a 2-D tensor")
@@ -781,8 +808,8 @@ def convrot_fp8_prepare_weights(W: torch.Tensor, layout: int = OUT_MAJOR,
     desc.codes, desc.scale, desc.scales = codes.data_ptr(), scale.data_ptr(), FP8_SCALES[scales]
     wsb = lib.convrot_fp8_prepare_workspace_bytes(N, K, tag, layout)
     ws = _workspace(wsb, W.device, None)
-    _launch(W.device, "convrot_fp8_prepare_weights", stream, _ptr(W), tag, layout,
-            _ptr(src_scale), N, K, ctypes.byref(desc), _ptr(ws), wsb, scratch=(W, codes, scale, ws))
+    _launch(W.device, "convrot_fp8_prepare_weights", _ptr(W), tag, layout,
+            _ptr(src_scale), N, K, ctypes.byref(desc), _ptr(ws), wsb)
     fw = FP8Weights(desc, codes, scale)
     fw._ws = ws  # keep alive until the stream has consumed it
     return fw
@@ -792,6 +819,8 @@ def convrot_fp8_linear_forward(X: torch.Tensor, W: FP8Weights, bias=None,
                                out_dtype: torch.dtype = torch.bfloat16, out=None,
                                workspace=None, stream=None) -> torch.Tensor:
     """Y [M, N] = X . W^T (+ bias) with X quantised to e4m3 per 128 inputs."""
+    if stream is not None:
+        return _on_stream(convrot_fp8_linear_forward, locals())
     lib = library()
     dev = _fp8_weights(W, "W")
     M = _rows(X, "X", W.K)
@@ -803,9 +832,8 @@ def convrot_fp8_linear_forward(X: torch.Tensor, W: FP8Weights, bias=None,
     if out is None:
         out = torch.empty((M, W.N), dtype=out_dtype, device=dev)
     ws = _workspace(wsb, dev, workspace)
-    _launch(dev, "convrot_fp8_linear_forward", stream, _ptr(X), M, W.ref(), _ptr(bias),
-            _ptr(out), _dtype_tag(out.dtype), _ptr(ws), ws.numel() if ws is not None else 0,
-            scratch=(out, ws))
+    _launch(dev, "convrot_fp8_linear_forward", _ptr(X), M, W.ref(), _ptr(bias),
+            _ptr(out), _dtype_tag(out.dtype), _ptr(ws), ws.numel() if ws is not None else 0)
     return out
 
 
@@ -841,6 +869,8 @@ def convrot_rope_prepare(dims, head_dim: int, theta: float = 10000.0,
     each even; together at most head_dim): pairs 'interleaved' (2p, 2p + 1) or
     'half' (p, p + R/2), every axis running through all frequencies
     (spectrum='axis') or the pairs sharing one spectrum ('whole')."""
+    if stream is not None:
+        return _on_stream(convrot_rope_prepare, locals())
     dims = [int(d) for d in dims]
     if not 1 <= len(dims) <= ROPE_MAX_AXES or any(d <= 0 or d % 2 for d in dims):
         raise ValueError(f"dims must be 1 to {ROPE_MAX_AXES} positive even numbers, got {dims}")
@@ -858,9 +888,9 @@ def convrot_rope_prepare(dims, head_dim: int, theta: float = 10000.0,
     axis = torch.empty(half, dtype=torch.int32, device=device)
     desc = convrot_rope()
     desc.freq, desc.axis = freq.data_ptr(), axis.data_ptr()
-    _launch(freq.device, "convrot_rope_prepare", stream, (ctypes.c_int32 * len(dims))(*dims),
+    _launch(freq.device, "convrot_rope_prepare", (ctypes.c_int32 * len(dims))(*dims),
             len(dims), head_dim, theta, ROPE_PAIRINGS[pairing], ROPE_SPECTRA[spectrum],
-            ctypes.byref(desc), scratch=(freq, axis))
+            ctypes.byref(desc))
     return RopePlan(desc, freq, axis)
 
 
@@ -949,15 +979,17 @@ def convrot_rope_forward(q: torch.Tensor, k, rope: RopePlan, positions: torch.Te
     """(q_out, k_out): q and k [B, T, heads, D] turned by the tokens' positions
     [T, axes] or [B, T, axes] (int32 or float32); k may be None.  Out of place
     unless out_q is q.  inverse: by the negative angles, the backward pass."""
+    if stream is not None:
+        return _on_stream(convrot_rope_forward, locals())
     lead, psb, vq, vk = _heads_pair(q, k, rope, positions)
     _, B, T = lead
     dev = rope.freq.device
     _on_device(dev, q=q, k=k, positions=positions, out_q=out_q, out_k=out_k)
     out_q, oq = _heads_out(out_q, "out_q", q, lead)
     out_k, ok = _heads_out(out_k, "out_k", k, lead)
-    _launch(dev, "convrot_rope_forward", stream, B, T, _dtype_tag(q.dtype), vq, oq, vk, ok,
+    _launch(dev, "convrot_rope_forward", B, T, _dtype_tag(q.dtype), vq, oq, vk, ok,
             rope.ref(), _ptr(positions), _dtype_tag(positions.dtype), psb,
-            ROPE_INVERSE if inverse else 0, scratch=(out_q, out_k))
+            ROPE_INVERSE if inverse else 0)
     return out_q, out_k
 
 
@@ -966,6 +998,8 @@ def convrot_qk_norm_rope_forward(q: torch.Tensor, k, w_q, w_k, rope: RopePlan,
                                  out_k=None, stream=None):
     """convrot_rope_forward of q * rsqrt(mean(q^2) + eps) * w_q over each head's
     channels and of k likewise; w_q, w_k float32 [D] or None."""
+    if stream is not None:
+        return _on_stream(convrot_qk_norm_rope_forward, locals())
     lead, psb, vq, vk = _heads_pair(q, k, rope, positions)
     _, B, T = lead
     _opt(w_q, "w_q", torch.float32, (rope.head_dim,))
@@ -976,9 +1010,9 @@ def convrot_qk_norm_rope_forward(q: torch.Tensor, k, w_q, w_k, rope: RopePlan,
     _on_device(dev, q=q, k=k, w_q=w_q, w_k=w_k, positions=positions, out_q=out_q, out_k=out_k)
     out_q, oq = _heads_out(out_q, "out_q", q, lead)
     out_k, ok = _heads_out(out_k, "out_k", k, lead)
-    _launch(dev, "convrot_qk_norm_rope_forward", stream, B, T, _dtype_tag(q.dtype), vq, oq,
+    _launch(dev, "convrot_qk_norm_rope_forward", B, T, _dtype_tag(q.dtype), vq, oq,
             _ptr(w_q), vk, ok, _ptr(w_k), eps, rope.ref(), _ptr(positions),
-            _dtype_tag(positions.dtype), psb, scratch=(out_q, out_k))
+            _dtype_tag(positions.dtype), psb)
     return out_q, out_k
 
 
@@ -992,6 +1026,8 @@ def convrot_qk_norm_rope_backward(g_q: torch.Tensor, g_k, q: torch.Tensor, k, w_
                                   stream=None):
     """(dq, dk, dw_q, dw_k) of convrot_qk_norm_rope_forward(q, k, ...) from the
     gradients g_q and g_k of its outputs."""
+    if stream is not None:
+        return _on_stream(convrot_qk_norm_rope_backward, locals())
     lib = library()
     lead, psb, vq, vk = _heads_pair(q, k, rope, positions)
     _, B, T = lead
@@ -1020,10 +1056,10 @@ def convrot_qk_norm_rope_backward(g_q: torch.Tensor, g_k, q: torch.Tensor, k, w_
     if dw_k is None and k is not None:
         dw_k = torch.empty(D, dtype=torch.float32, device=dev)
     ws = _workspace(wsb, dev, workspace)
-    _launch(dev, "convrot_qk_norm_rope_backward", stream, B, T, _dtype_tag(q.dtype), views[0],
+    _launch(dev, "convrot_qk_norm_rope_backward", B, T, _dtype_tag(q.dtype), views[0],
             vq, vdq, _ptr(w_q), _ptr(dw_q), views[1], vk, vdk, _ptr(w_k), _ptr(dw_k), eps,
             rope.ref(), _ptr(positions), _dtype_tag(positions.dtype), psb, _ptr(ws),
-            ws.numel() if ws is not None else 0, scratch=(dq, dk, dw_q, dw_k, ws))
+            ws.numel() if ws is not None else 0)
     return dq, dk, dw_q, dw_k
 
 
@@ -1034,6 +1070,8 @@ def convrot_qkv_forward(X: torch.Tensor, W, heads_q: int, heads_kv: int, w_q, w_
     """The QKV projection of X [M, K] or [B, T, K] with the norms and rotation
     of its queries and keys: [.., (heads_q + 2 heads_kv) D], queries, keys, then
     values.  W: PreparedWeights or FP8Weights."""
+    if stream is not None:
+        return _on_stream(convrot_qkv_forward, locals())
     lib = library()
     fp8 = isinstance(W, FP8Weights)
     dev = _fp8_weights(W, "W") if fp8 else _weights(W, "W")
@@ -1058,10 +1096,9 @@ def convrot_qkv_forward(X: torch.Tensor, W, heads_q: int, heads_kv: int, w_q, w_
         out = torch.empty((*X.shape[:-1], W.N), dtype=out_dtype, device=dev)
     ws = _workspace(wsb, dev, workspace)
     name = "convrot_fp8_qkv_forward" if fp8 else "convrot_qkv_forward"
-    _launch(dev, name, stream, _ptr(X), B, T, W.ref(), _ptr(bias), heads_q, heads_kv, _ptr(w_q),
+    _launch(dev, name, _ptr(X), B, T, W.ref(), _ptr(bias), heads_q, heads_kv, _ptr(w_q),
             _ptr(w_k), eps, rope.ref(), _ptr(positions), _dtype_tag(positions.dtype), psb,
-            _ptr(out), _dtype_tag(out.dtype), _ptr(ws), ws.numel() if ws is not None else 0,
-            scratch=(out, ws))
+            _ptr(out), _dtype_tag(out.dtype), _ptr(ws), ws.numel() if ws is not None else 0)
     return out
 
 
@@ -1192,6 +1229,8 @@ def convrot_gelu_bf16(u: torch.Tensor, out=None, stream=None) -> torch.Tensor:
 def convrot_fp8_quantize(X: torch.Tensor, scales: str = "f32", q=None, s=None, stream=None):
     """(q, s): the K-tiled e4m3 codes (Mp, K) uint8 of the bf16 rows X and their
     scales [K/128, Mp] float32."""
+    if stream is not None:
+        return _on_stream(convrot_fp8_quantize, locals())
     if not isinstance(X, torch.Tensor) or X.dim() != 2:
         raise ValueError("X must be a 2-D tensor [M, K]")
     M, K = X.shape
@@ -1206,8 +1245,8 @@ def convrot_fp8_quantize(X: torch.Tensor, scales: str = "f32", q=None, s=None, s
         q = torch.empty((Mp, K), dtype=torch.uint8, device=X.device)
     if s is None:
         s = torch.empty((K // 128, Mp), dtype=torch.float32, device=X.device)
-    _launch(X.device, "convrot_fp8_quantize", stream, _ptr(X), M, K, FP8_SCALES[scales], _ptr(q),
-            _ptr(s), scratch=(q, s))
+    _launch(X.device, "convrot_fp8_quantize", _ptr(X), M, K, FP8_SCALES[scales], _ptr(q),
+            _ptr(s))
     return q, s
 
 
@@ -1217,6 +1256,8 @@ def convrot_fp8_gemm_dequant(q: torch.Tensor, s: torch.Tensor, M: int, W: FP8Wei
     """Y [M, N] from the codes and scales of M rows (convrot_fp8_quantize), of
     either kind.  scales='pow2' says that the rows' are powers of two or zeros
     (not checked): with a 'pow2' weight that is its forward's arithmetic."""
+    if stream is not None:
+        return _on_stream(convrot_fp8_gemm_dequant, locals())
     dev = _fp8_weights(W, "W")
     if scales not in FP8_SCALES:
         raise ValueError(f"scales must be one of {sorted(FP8_SCALES)}")
@@ -1227,8 +1268,8 @@ def convrot_fp8_gemm_dequant(q: torch.Tensor, s: torch.Tensor, M: int, W: FP8Wei
     _on_device(dev, q=q, s=s, bias=bias, out=out)
     if out is None:
         out = torch.empty((M, W.N), dtype=out_dtype, device=dev)
-    _launch(dev, "convrot_fp8_gemm_dequant_scales", stream, _ptr(q), _ptr(s), FP8_SCALES[scales],
-            M, W.ref(), _ptr(bias), _ptr(out), _dtype_tag(out.dtype), scratch=(out,))
+    _launch(dev, "convrot_fp8_gemm_dequant_scales", _ptr(q), _ptr(s), FP8_SCALES[scales],
+            M, W.ref(), _ptr(bias), _ptr(out), _dtype_tag(out.dtype))
     return out
 
 
