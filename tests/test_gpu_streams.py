@@ -42,6 +42,11 @@ def calls(cr):
     w = torch.ones(64, device="cuda")
     x, q, gq = rand(300, 512), rand(300, 8, 64), rand(300, 8, 64)
     flat = lambda out: [t for t in (out if isinstance(out, tuple) else (out,)) if t is not None]
+    up, down = (cr.convrot_linear_prepare_weights(rand(*s), 128) for s in ((512, 512), (1024, 512)))
+    gu = cr.convrot_swiglu_prepare(rand(1024, 512), 128)
+    fa, fb = cr.convrot_lowrank_prepare(rand(128, 512), rand(1024, 128), 128)
+    a, b = rand(128, 512), rand(1024, 128)
+    qx, sx = cr.convrot_rotate_quantize(x, 128)
     return [
         ("fp8 linear", lambda x, **k: flat(cr.convrot_fp8_linear_forward(x, f8, **k)), x),
         ("fp8 quantise", lambda x, **k: flat(cr.convrot_fp8_quantize(x, **k))[1:], x[:288]),
@@ -55,6 +60,17 @@ def calls(cr):
          lambda x, **k: flat(cr.convrot_qkv_forward(x, i8, 8, 4, w, w, plan, pos, **k)), x),
         ("qkv fp8",
          lambda x, **k: flat(cr.convrot_qkv_forward(x, f8, 8, 4, w, w, plan, pos, **k)), x),
+        ("int8 linear", lambda x, **k: flat(cr.convrot_linear_forward(x, i8, **k)), x),
+        ("int8 mlp", lambda x, **k: flat(cr.convrot_mlp_forward(x, up, down, **k)), x),
+        ("swiglu mlp", lambda x, **k: flat(cr.convrot_swiglu_mlp_forward(x, gu, down, **k)), x),
+        ("low rank", lambda x, **k: flat(cr.lowrank_convrot_forward(x, fa, fb, **k)), x),
+        ("bf16 low rank", lambda x, **k: flat(cr.lowrank_bf16_forward(x, a, b, **k)), x),
+        ("rotate + quantise", lambda x, **k: flat(cr.convrot_rotate_quantize(x, 128, **k))[1:], x),
+        ("int8 gemm", lambda s, **k: flat(cr.convrot_gemm_dequant(qx, s, i8, **k)), sx),
+        ("factor 1", lambda s, **k: flat(cr.convrot_lowrank_factor1(qx, s, fa, **k))[1:], sx),
+        ("gelu", lambda x, **k: flat(cr.convrot_gelu_bf16(x, **k)), x),
+        ("swiglu", lambda x, **k: flat(cr.convrot_swiglu_bf16(x, **k)), x),
+        ("silu", lambda x, **k: flat(cr.convrot_silu_f32(x, **k)), x),
     ]
 
 
@@ -76,6 +92,25 @@ def test_strided_weight_on_a_side_stream(cr, busy, kind):
         with torch.cuda.stream(s):
             codes, scale = pw.codes.cpu(), pw.scale.cpu()
         assert torch.equal(codes, want.codes.cpu()) and torch.equal(scale, want.scale.cpu())
+
+
+@pytest.mark.parametrize("what", ["linear", "low rank", "swiglu"])
+def test_strided_int8_weight_on_a_side_stream(cr, busy, what):
+    w = torch.randn(2048, 4096, device="cuda")
+    b = torch.randn(128, 4096, device="cuda")
+    prep = {"linear": lambda w, b, **k: (cr.convrot_linear_prepare_weights(w, 128, **k),),
+            "low rank": lambda w, b, **k: cr.convrot_lowrank_prepare(w[:128], b, 128, **k),
+            "swiglu": lambda w, b, **k: (cr.convrot_swiglu_prepare(w, 128, **k),)}[what]
+    want = prep(w.t().contiguous(), b.t().contiguous())
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    announce(f"strided {what} weight on a side stream")
+    busy()
+    got = prep(w.t(), b.t(), stream=s)
+    with torch.cuda.stream(s):
+        got = [(p.codes.cpu(), p.scale.cpu()) for p in got]
+    for p, (codes, scale) in zip(want, got):
+        assert torch.equal(codes, p.codes.cpu()) and torch.equal(scale, p.scale.cpu())
 
 
 def test_pow2_import_reads_scales_on_the_callers_stream(cr, busy):
@@ -111,7 +146,7 @@ def test_plan_on_a_side_stream(cr, busy):
     assert torch.equal(plan.freq, want.freq) and torch.equal(plan.axis, want.axis)
 
 
-@pytest.mark.parametrize("i", range(7))
+@pytest.mark.parametrize("i", range(18))
 def test_memory_of_either_stream(cr, busy, i):
     name, call, x = calls(cr)[i]
     announce(f"streams: {name}")

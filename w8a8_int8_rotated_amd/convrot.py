@@ -265,6 +265,8 @@ def _on_stream(fn, args: dict):
     _on_device(stream.device,
                **{n: t for n, t in args.items() if isinstance(t, torch.Tensor)})
     current = torch.cuda.current_stream(stream.device)
+    if stream == current:
+        return fn(**args)
     with torch.cuda.stream(stream):
         out = fn(**args)
     for t in _tensors(tuple(args.values())):
@@ -416,6 +418,8 @@ def convrot_linear_prepare_weights(W: torch.Tensor, block: int, layout: int = OU
                                    stream=None, rotation: str = "sylvester") -> PreparedWeights:
     """Rotate + quantise + pack a weight (``[N, K]`` or ``[K, N]`` per layout)
     with the rotation kind ``'sylvester'`` or ``'regular'``."""
+    if stream is not None:
+        return _on_stream(convrot_linear_prepare_weights, locals())
     lib = library()
     if not isinstance(W, torch.Tensor) or W.dim() != 2:
         raise ValueError("W must be a 2-D tensor")
@@ -466,6 +470,8 @@ def convrot_lowrank_prepare(A: torch.Tensor, B: torch.Tensor, block: int, stream
     float32 or bfloat16) with lowrank_convrot_prepare_weights, which pads the
     rank with zero rows of A and zero columns of B to
     lowrank_padded_rank(r, block).  Returns two PreparedWeights."""
+    if stream is not None:
+        return _on_stream(convrot_lowrank_prepare, locals())
     lib = library()
     for t, name in ((A, "A"), (B, "B")):
         if not isinstance(t, torch.Tensor) or t.dim() != 2:
@@ -512,6 +518,8 @@ def convrot_lowrank_prepare(A: torch.Tensor, B: torch.Tensor, block: int, stream
 def convrot_linear_forward(X: torch.Tensor, W: PreparedWeights, bias=None,
                            out_dtype: torch.dtype = torch.bfloat16, out=None,
                            workspace=None, stream=None) -> torch.Tensor:
+    if stream is not None:
+        return _on_stream(convrot_linear_forward, locals())
     lib = library()
     dev = _weights(W, "W")
     M = _rows(X, "X", W.K)
@@ -536,6 +544,8 @@ def convrot_linear_forward_noalloc(X: torch.Tensor, W: PreparedWeights, bias=Non
     """convrot_linear_forward with the library's static device scratch as its
     workspace (the C call allocates nothing; pass `out` to allocate nothing
     here either).  Calls on one device must not overlap in time."""
+    if stream is not None:
+        return _on_stream(convrot_linear_forward_noalloc, locals())
     lib = library()
     dev = _weights(W, "W")
     M = _rows(X, "X", W.K)
@@ -553,6 +563,8 @@ def convrot_linear_forward_noalloc(X: torch.Tensor, W: PreparedWeights, bias=Non
 def lowrank_convrot_forward(X: torch.Tensor, A: PreparedWeights, B: PreparedWeights,
                             bias=None, out_dtype: torch.dtype = torch.bfloat16, out=None,
                             workspace=None, stream=None) -> torch.Tensor:
+    if stream is not None:
+        return _on_stream(lowrank_convrot_forward, locals())
     lib = library()
     dev = _weights(A, "A")
     if _weights(B, "B") != dev:
@@ -576,6 +588,8 @@ def lowrank_convrot_forward(X: torch.Tensor, A: PreparedWeights, B: PreparedWeig
 def convrot_mlp_forward(X: torch.Tensor, W_up: PreparedWeights, W_down: PreparedWeights,
                         bias_up=None, bias_down=None, out_dtype: torch.dtype = torch.bfloat16,
                         out=None, workspace=None, stream=None) -> torch.Tensor:
+    if stream is not None:
+        return _on_stream(convrot_mlp_forward, locals())
     lib = library()
     dev = _weights(W_up, "W_up")
     if _weights(W_down, "W_down") != dev:
@@ -608,6 +622,8 @@ def convrot_swiglu_prepare(W: torch.Tensor, block: int, src_scale: torch.Tensor 
     """Prepare a SwiGLU fc1 weight [2F, K] (gate rows, then up rows): float32 or
     bfloat16 weights, or int8 codes with src_scale [2F]; stored interleaved
     (SWIGLU_PAIRS) for the fused SwiGLU epilogue."""
+    if stream is not None:
+        return _on_stream(convrot_swiglu_prepare, locals())
     lib = library()
     if not isinstance(W, torch.Tensor) or W.dim() != 2 or W.shape[0] % 2:
         raise ValueError("W must be a 2-D tensor [2F, K]")
@@ -644,6 +660,8 @@ def convrot_swiglu_mlp_forward(X: torch.Tensor, W_gu: PreparedWeights, W_down: P
                                out_dtype: torch.dtype = torch.bfloat16, out=None,
                                workspace=None, stream=None) -> torch.Tensor:
     """Y = linear(swiglu(linear(X; W_gu) + bias_gu); W_down) + bias_down."""
+    if stream is not None:
+        return _on_stream(convrot_swiglu_mlp_forward, locals())
     lib = library()
     dev = _weights(W_gu, "W_gu")
     if _weights(W_down, "W_down") != dev:
@@ -670,6 +688,8 @@ def convrot_swiglu_mlp_forward(X: torch.Tensor, W_gu: PreparedWeights, W_down: P
 
 def convrot_swiglu_bf16(gu: torch.Tensor, out=None, stream=None) -> torch.Tensor:
     """g [M, F] = bf16(fp32(silu(gate)) * up) for gu [M, 2F] = gate | up."""
+    if stream is not None:
+        return _on_stream(convrot_swiglu_bf16, locals())
     lib = library()
     if not isinstance(gu, torch.Tensor) or gu.dim() != 2 or gu.shape[1] % 2:
         raise ValueError("gu must be a 2-D tensor [M, 2F]")
@@ -686,6 +706,8 @@ def convrot_swiglu_bf16(gu: torch.Tensor, out=None, stream=None) -> torch.Tensor
 
 def convrot_silu_f32(a: torch.Tensor, stream=None) -> torch.Tensor:
     """fp32(silu(a)) of bf16 values, as every SwiGLU path computes it."""
+    if stream is not None:
+        return _on_stream(convrot_silu_f32, locals())
     lib = library()
     if not isinstance(a, torch.Tensor) or a.dtype != torch.bfloat16:
         raise ValueError("a must be a bf16 tensor")
@@ -701,6 +723,8 @@ def lowrank_bf16_forward(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, bias
                          out=None, workspace=None, stream=None) -> torch.Tensor:
     """Comparison variant: bf16(bf16(X . A^T) . B^T + bias), bf16 factors
     A [r, K] and B [N, r], no rotation or quantisation."""
+    if stream is not None:
+        return _on_stream(lowrank_bf16_forward, locals())
     lib = library()
     for t, name in ((X, "X"), (A, "A"), (B, "B")):
         if not isinstance(t, torch.Tensor) or t.dim() != 2:
@@ -1127,6 +1151,8 @@ def convrot_rotate_quantize(X: torch.Tensor, block: int, q=None, s=None, stream=
     """Rotate + quantise the rows of X: (q, s), q the K-tiled codes (Mp, K).
     gelu: quantise bf16(GELU(X)) instead (bf16 X, 6144 < K <= 24576), as the
     MLP path does with its intermediate."""
+    if stream is not None:
+        return _on_stream(convrot_rotate_quantize, locals())
     lib = library()
     if not isinstance(X, torch.Tensor) or X.dim() != 2:
         raise ValueError("X must be a 2-D tensor [M, K]")
@@ -1150,6 +1176,8 @@ def convrot_rotate_quantize(X: torch.Tensor, block: int, q=None, s=None, stream=
 
 def convrot_gemm_i32(q_x: torch.Tensor, M: int, W: PreparedWeights, out=None, stream=None):
     """acc [M, N] int32 from K-tiled codes q_x of M rows."""
+    if stream is not None:
+        return _on_stream(convrot_gemm_i32, locals())
     lib = library()
     dev = _weights(W, "W")
     _codes(q_x, M, W.K, dev)
@@ -1167,6 +1195,8 @@ def convrot_gemm_dequant(q_x: torch.Tensor, s_x: torch.Tensor, W: PreparedWeight
                          swiglu: bool = False, stream=None):
     """Y [M, N] from K-tiled codes q_x and row scales s_x [M] (with swiglu, W a
     SwiGLU fc1 weight and Y = g [M, N/2])."""
+    if stream is not None:
+        return _on_stream(convrot_gemm_dequant, locals())
     lib = library()
     dev = _weights(W, "W")
     if not isinstance(s_x, torch.Tensor) or s_x.dim() != 1:
@@ -1191,6 +1221,8 @@ def convrot_lowrank_factor1(q_x: torch.Tensor, s_x: torch.Tensor, A: PreparedWei
                             q_h=None, s_h=None, stream=None):
     """Factor 1 of the low-rank chain with its output rotated and requantised:
     returns (q_h, s_h), q_h the K-tiled codes (Mp, r), s_h [M] f32."""
+    if stream is not None:
+        return _on_stream(convrot_lowrank_factor1, locals())
     lib = library()
     dev = _weights(A, "A")
     if not isinstance(s_x, torch.Tensor) or s_x.dim() != 1:
@@ -1213,6 +1245,8 @@ def convrot_lowrank_factor1(q_x: torch.Tensor, s_x: torch.Tensor, A: PreparedWei
 
 def convrot_gelu_bf16(u: torch.Tensor, out=None, stream=None) -> torch.Tensor:
     """bf16(GELU(u)) elementwise, as the MLP's up projection applies it."""
+    if stream is not None:
+        return _on_stream(convrot_gelu_bf16, locals())
     lib = library()
     if not isinstance(u, torch.Tensor) or u.dtype != torch.bfloat16:
         raise ValueError("u must be a bf16 tensor")
