@@ -422,3 +422,55 @@ def test_stages_equal_forward(cr, kind, M, K, N):
         announce(f"fp8 stages {M}x{K}x{N} {kind} {dt}")
         y = cr.convrot_fp8_gemm_dequant(q, s, M, pw, out_dtype=dt, scales=kind)
         assert torch.equal(y, cr.convrot_fp8_linear_forward(X, pw, out_dtype=dt))
+
+
+def product_bound(q, s, M, pw, bias, K, N):
+    """fp64 product of the library's codes and scales, its bound for fp32 outputs and
+    what bf16 outputs add to it (the module's docstring), on the GPU."""
+    dec = lambda c, n: torch.from_numpy(untile(c.view(torch.int8), n, K).copy()).cuda() \
+        .view(F8).double()
+    xd = dec(q, M) * s[:, :M].t().double().repeat_interleave(128, 1)
+    wd = dec(pw.codes, N) * pw.scale.double().repeat_interleave(128, 0)[:N] \
+        .repeat_interleave(128, 1)
+    ref, mag = xd @ wd.t(), xd.abs() @ wd.abs().t()
+    if bias is not None:
+        ref, mag = ref + bias.double(), mag + bias.double().abs()
+    top = lambda a: a.abs().view(a.shape[0], K // 8, 8).amax(-1)
+    return ref, (K + K // 128 + 4) * 2.0 ** -24 * mag, 7 * 2.0 ** -13 * (top(xd) @ top(wd).t())
+
+
+def check_product(y, ref, bound, cut, what):
+    bf = y.dtype == torch.bfloat16
+    bound = bound + cut if bf else bound
+    bound = bound + (2.0 ** -8 if bf else 2.0 ** -24) * (ref.abs() + bound)
+    worst = float(((y.double() - ref).abs() / bound).max())
+    print(f"[parity] {what}: worst error {worst:.3f} of its bound", flush=True)
+    assert worst <= 1.0
+
+
+# rows quantised by the product's kernel: 1, 2 and 4 row tiles a workgroup, counts of
+# 16-row blocks that these do not divide, fewer and more k-blocks than waves
+@pytest.mark.parametrize("kind", ["f32", "pow2"])
+@pytest.mark.parametrize("M", [1, 8, 16])
+@pytest.mark.parametrize("K,N", [(1152, 2064), (384, 5392), (1152, 5392), (384, 10256),
+                                 (384, 16144), (1152, 16144), (640, 17424), (384, 32272)])
+def test_few_rows(cr, kind, M, K, N):
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+    X = torch.randn(M, K, generator=g, device="cuda")
+    X = (X * torch.exp2(torch.randint(-6, 7, (M, K // 128, 1), generator=g, device="cuda"))
+         .expand(-1, -1, 128).reshape(M, K)).to(torch.bfloat16)
+    # blocks of 128 outputs differ in scale by factors up to 2^8
+    W = torch.randn(N, K, generator=g, device="cuda") * torch.exp2(
+        torch.randint(-4, 5, (-(-N // 128), 1), generator=g, device="cuda")
+        .repeat_interleave(128, 0)[:N].float())
+    bias = torch.randn(N, generator=g, device="cuda")
+    pw = cr.convrot_fp8_prepare_weights(W, scales=kind)
+    q, s = cr.convrot_fp8_quantize(X, kind)
+    for dt, b in ((torch.bfloat16, bias), (torch.bfloat16, None), (torch.float32, bias),
+                  (torch.float32, None)):
+        announce(f"fp8 few rows {M}x{K}x{N} {kind} {dt} bias={b is not None}")
+        buf = torch.full((M + 2, N), 3.0, dtype=dt, device="cuda")
+        cr.convrot_fp8_linear_forward(X, pw, bias=b, out=buf[:M])
+        assert bool((buf[M:] == 3.0).all())
+        check_product(buf[:M], *product_bound(q, s, M, pw, b, K, N),
+                      f"few rows {M}x{K}x{N} {kind} {dt}")
