@@ -355,14 +355,21 @@ hipError_t launch_fp8_gemm(const Fp8Gemm &g, hipStream_t stream)
 {
     if (!g.qx) {
         // Row tiles per workgroup, which shares one quantised k-block of the rows
-        // among them: 4 where that still gives one workgroup per CU (8 rows at
-        // N = 32256, K = 5376: 31.6 us, 34.6 us with 2; one row at N = 16128: 17.1 us,
-        // 17.7 us), 1 where 2 would leave most CUs without one (16 rows at
-        // N = 1024, K = 21504: 27.2 us, 30.1 us), else 2 (one row at N = K = 5376:
-        // 7.9 us, with 4 9.2 us, with 1 9.9 us).
+        // among them, by the rounds of workgroups over the CUs: 1 while that is one
+        // round, and of 2 and 4 the larger where it takes half the rounds.  Either
+        // side of each border at K = 5376, us with (1, 2 or 2, 4):
+        //   N = 4096:  one row 9.0, 9.3;   16 rows, F32 outputs  9.5, 11.4
+        //   N = 4608:         11.2, 10.2;                       16.3, 11.4
+        //   N = 8064:  one row 11.1, 13.9; 16 rows 12.0, 15.2
+        //   N = 10240:        15.9, 13.9;         20.2, 18.4
+        //   N = 16384: one row 18.5, 18.8; 16 rows 21.0, 18.5
+        //   N = 17408:        23.0, 25.4;         29.5, 29.2
+        //   N = 24576: one row 26.6, 28.6; 16 rows 33.0, 32.3
+        //   N = 32256:        34.0, 33.8;         42.3, 35.5
         const int64_t cus = device_cu_count(), blocks = g.N / 16;
-        if (blocks >= 4 * cus - 16) return launch_skinny<4, 1, true>(g, 8, stream);
-        if (2 * blocks <= cus) return launch_skinny<1, 1, true>(g, 8, stream);
+        auto rounds = [&](int64_t rt) { return ((blocks + rt - 1) / rt + cus - 1) / cus; };
+        if (rounds(1) == 1) return launch_skinny<1, 1, true>(g, 8, stream);
+        if (rounds(2) >= 2 * rounds(4)) return launch_skinny<4, 1, true>(g, 8, stream);
         return launch_skinny<2, 1, true>(g, 8, stream);
     }
     const int64_t cus = device_cu_count(), nb = g.N / 16, mb = (g.M + 15) / 16;
