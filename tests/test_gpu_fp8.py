@@ -450,10 +450,13 @@ def check_product(y, ref, bound, cut, what):
 
 # rows quantised by the product's kernel: 1, 2 and 4 row tiles a workgroup, counts of
 # 16-row blocks that these do not divide, fewer and more k-blocks than waves
+FEW_ROWS = [(1152, 2064), (384, 5392), (1152, 5392), (384, 10256), (384, 16144), (1152, 16144),
+            (640, 17424), (384, 32272)]
+
+
 @pytest.mark.parametrize("kind", ["f32", "pow2"])
 @pytest.mark.parametrize("M", [1, 8, 16])
-@pytest.mark.parametrize("K,N", [(1152, 2064), (384, 5392), (1152, 5392), (384, 10256),
-                                 (384, 16144), (1152, 16144), (640, 17424), (384, 32272)])
+@pytest.mark.parametrize("K,N", FEW_ROWS)
 def test_few_rows(cr, kind, M, K, N):
     g = torch.Generator(device="cuda").manual_seed(M + N)
     X = torch.randn(M, K, generator=g, device="cuda")
@@ -474,3 +477,30 @@ def test_few_rows(cr, kind, M, K, N):
         assert bool((buf[M:] == 3.0).all())
         check_product(buf[:M], *product_bound(q, s, M, pw, b, K, N),
                       f"few rows {M}x{K}x{N} {kind} {dt}")
+
+
+# whole rounds of the largest tiles, then the last rows in each of the other shapes, for
+# bf16 and F32 outputs (tests/test_fp8_plans.py asks the chooser which)
+TAILS = [(1185, 640, 15232), (574, 640, 14960), (1844, 384, 16704), (7390, 640, 3152),
+         (8965, 384, 2064), (5676, 640, 6672), (1400, 640, 1680), (8588, 384, 32), (90, 256, 1120),
+         (380, 640, 480)]
+
+
+@pytest.mark.parametrize("kind", ["f32", "pow2"])
+@pytest.mark.parametrize("M,K,N", TAILS)
+def test_tails(cr, kind, M, K, N):
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+    X = torch.randn(M, K, generator=g, device="cuda")
+    X = (X * torch.exp2(torch.randint(-6, 7, (M, K // 128, 1), generator=g, device="cuda"))
+         .expand(-1, -1, 128).reshape(M, K)).to(torch.bfloat16)
+    W = torch.randn(N, K, generator=g, device="cuda")
+    bias = torch.randn(N, generator=g, device="cuda")
+    pw = cr.convrot_fp8_prepare_weights(W, scales=kind)
+    q, s = cr.convrot_fp8_quantize(X, kind)
+    ref, bound, cut = product_bound(q, s, M, pw, bias, K, N)
+    for dt in (torch.bfloat16, torch.float32):
+        announce(f"fp8 tails {M}x{K}x{N} {kind} {dt}")
+        buf = torch.full((M + 2, N), 3.0, dtype=dt, device="cuda")
+        cr.convrot_fp8_linear_forward(X, pw, bias=bias, out=buf[:M])
+        assert bool((buf[M:] == 3.0).all())
+        check_product(buf[:M], ref, bound, cut, f"tails {M}x{K}x{N} {kind} {dt}")

@@ -179,9 +179,19 @@ struct Fp8Gemm {
 };
 bool fp8_fuses_quantize(int64_t M);
 hipError_t launch_fp8_gemm(const Fp8Gemm &g, hipStream_t stream);
-// The tiled kernels behind it (gemm_fp8.hip), and an estimate of their time (us).
-hipError_t launch_fp8_tiles(const Fp8Gemm &g, hipStream_t stream);
-double fp8_tiles_us(const Fp8Gemm &g);
+// Which kernels a product runs on `cus` CUs: the one for few rows with rt x mt tiles
+// of 16 x 16 a workgroup, or (rt 0) tn x tm tiles, the first `first` rows in the
+// largest ones and a launch of their own.  fused: bf16 rows.
+struct Fp8Plan {
+    int rt, mt, tn, tm;
+    int64_t first;
+};
+Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, bool f32_out, bool fused, int64_t cus);
+// The tiled kernels (gemm_fp8.hip): their plan, an estimate of their time (us) where
+// the kernel for few rows competes with them, and their launches.
+Fp8Plan fp8_tiles_plan(int64_t M, int64_t N, bool f32_out, int64_t cus);
+double fp8_tiles_us(int64_t M, int64_t N, int64_t K, bool f32_out, int64_t cus);
+hipError_t launch_fp8_tiles(const Fp8Gemm &g, const Fp8Plan &p, hipStream_t stream);
 
 // ------------------------------------------ norms and rotary positions ----
 // Per-head rows: element (b, t, h, d) at p + b sb + t st + h sh + d.

@@ -351,44 +351,53 @@ hipError_t launch_fp8_quantize(const void *X, int64_t M, int64_t K, bool pow2, u
 
 bool fp8_fuses_quantize(int64_t M) { return M <= 16; }
 
-hipError_t launch_fp8_gemm(const Fp8Gemm &g, hipStream_t stream)
+Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, bool f32_out, bool fused, int64_t cus)
 {
-    if (!g.qx) {
-        // Row tiles per workgroup, which shares one quantised k-block of the rows
-        // among them, by the rounds of workgroups over the CUs: 1 while that is one
-        // round, and of 2 and 4 the larger where it takes half the rounds.  Either
-        // side of each border at K = 5376, us with (1, 2 or 2, 4):
-        //   N = 4096:  one row 9.0, 9.3;   16 rows, F32 outputs  9.5, 11.4
-        //   N = 4608:         11.2, 10.2;                       16.3, 11.4
-        //   N = 8064:  one row 11.1, 13.9; 16 rows 12.0, 15.2
-        //   N = 10240:        15.9, 13.9;         20.2, 18.4
-        //   N = 16384: one row 18.5, 18.8; 16 rows 21.0, 18.5
-        //   N = 17408:        23.0, 25.4;         29.5, 29.2
-        //   N = 24576: one row 26.6, 28.6; 16 rows 33.0, 32.3
-        //   N = 32256:        34.0, 33.8;         42.3, 35.5
-        const int64_t cus = device_cu_count(), blocks = g.N / 16;
-        auto rounds = [&](int64_t rt) { return ((blocks + rt - 1) / rt + cus - 1) / cus; };
-        if (rounds(1) == 1) return launch_skinny<1, 1, true>(g, 8, stream);
-        if (rounds(2) >= 2 * rounds(4)) return launch_skinny<4, 1, true>(g, 8, stream);
-        return launch_skinny<2, 1, true>(g, 8, stream);
+    const int64_t nb = N / 16, mb = (M + 15) / 16;
+    // Row tiles per workgroup, which shares one quantised k-block of the rows
+    // among them, by the rounds of workgroups over the CUs: 1 while that is one
+    // round, and of 2 and 4 the larger where it takes half the rounds.  Either
+    // side of each border at K = 5376, us with (1, 2 or 2, 4):
+    //   N = 4096:  one row 9.0, 9.3;   16 rows, F32 outputs  9.5, 11.4
+    //   N = 4608:         11.2, 10.2;                       16.3, 11.4
+    //   N = 8064:  one row 11.1, 13.9; 16 rows 12.0, 15.2
+    //   N = 10240:        15.9, 13.9;         20.2, 18.4
+    //   N = 16384: one row 18.5, 18.8; 16 rows 21.0, 18.5
+    //   N = 17408:        23.0, 25.4;         29.5, 29.2
+    //   N = 24576: one row 26.6, 28.6; 16 rows 33.0, 32.3
+    //   N = 32256:        34.0, 33.8;         42.3, 35.5
+    if (fused) {
+        auto rounds = [&](int64_t rt) { return ((nb + rt - 1) / rt + cus - 1) / cus; };
+        const int rt = rounds(1) == 1 ? 1 : rounds(2) >= 2 * rounds(4) ? 4 : 2;
+        return {rt, 1, 0, 0, 0};
     }
-    const int64_t cus = device_cu_count(), nb = g.N / 16, mb = (g.M + 15) / 16;
-    const int64_t steps = (g.K / 128 + 7) / 8;
-    double best_us = fp8_tiles_us(g);
+    const int64_t steps = (K / 128 + 7) / 8;
+    double best_us = fp8_tiles_us(M, N, K, f32_out, cus);
     int best = -1;
     for (int i = 0; i < 4; ++i) {
         const SkinnyShape &s = kSkinnyShapes[i];
         const int64_t gx = (nb + s.rt - 1) / s.rt, gy = (mb + s.mt - 1) / s.mt;
-        const double step = i == 3 && g.f32_out ? kSkinnyF32Us : s.us;
+        const double step = i == 3 && f32_out ? kSkinnyF32Us : s.us;
         const double us = 3.0 + (double)((gx * gy + cus - 1) / cus * steps) * step;
         if (gy <= kMaxGridY && us < best_us) best = i, best_us = us;
     }
-    switch (best) {
-    case 0: return launch_skinny<1, 1, false>(g, 8, stream);
-    case 1: return launch_skinny<2, 1, false>(g, 8, stream);
-    case 2: return launch_skinny<2, 2, false>(g, 8, stream);
-    case 3: return launch_skinny<2, 4, false>(g, 8, stream);
-    default: return launch_fp8_tiles(g, stream);
+    if (best < 0) return fp8_tiles_plan(M, N, f32_out, cus);
+    return {kSkinnyShapes[best].rt, kSkinnyShapes[best].mt, 0, 0, 0};
+}
+
+hipError_t launch_fp8_gemm(const Fp8Gemm &g, hipStream_t stream)
+{
+    const Fp8Plan p = fp8_plan(g.M, g.N, g.K, g.f32_out, !g.qx, device_cu_count());
+    if (!g.qx)
+        return p.rt == 1   ? launch_skinny<1, 1, true>(g, 8, stream)
+               : p.rt == 2 ? launch_skinny<2, 1, true>(g, 8, stream)
+                           : launch_skinny<4, 1, true>(g, 8, stream);
+    switch (p.rt * p.mt) {
+    case 1: return launch_skinny<1, 1, false>(g, 8, stream);
+    case 2: return launch_skinny<2, 1, false>(g, 8, stream);
+    case 4: return launch_skinny<2, 2, false>(g, 8, stream);
+    case 8: return launch_skinny<2, 4, false>(g, 8, stream);
+    default: return launch_fp8_tiles(g, p, stream);
     }
 }
 

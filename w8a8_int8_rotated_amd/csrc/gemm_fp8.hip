@@ -551,51 +551,54 @@ double shape_cost(const TileShape &s, int64_t rows, int64_t N, int64_t cus)
 // k-blocks in turn, 0.35 us each in a 128 x 64 tile (F32 outputs 0.69 us).  At
 // N = 1024 .. 5376: 9.2, 18.1, 36.1 and 61 us for 16, 42, 96 and 168 of them, F32
 // outputs 15.5, 33, 70.7 and 122 us; within a tenth of this.
-double fp8_tiles_us(const Fp8Gemm &g)
+double fp8_tiles_us(int64_t M, int64_t N, int64_t K, bool f32_out, int64_t cus)
 {
-    const int64_t cus = device_cu_count();
     double best = 1e30;
-    if (g.f32_out)
-        for (const TileShape &s : kBf16Shapes) best = std::min(best, shape_cost(s, g.M, g.N, cus));
+    if (f32_out)
+        for (const TileShape &s : kBf16Shapes) best = std::min(best, shape_cost(s, M, N, cus));
     else
-        for (const TileShape &s : kFp8Shapes) best = std::min(best, shape_cost(s, g.M, g.N, cus));
-    return 4.0 + best * (double)(g.K / kKB) * (g.f32_out ? 1.41 : 1.08);
+        for (const TileShape &s : kFp8Shapes) best = std::min(best, shape_cost(s, M, N, cus));
+    return 4.0 + best * (double)(K / kKB) * (f32_out ? 1.41 : 1.08);
 }
 
 // The plan with the least estimated time: one shape throughout, or whole rounds
 // of the largest shape and another one for the last rows (M = 4096 at
 // N = K = 5376: 252 tiles of 256 x 256, then 1024 rows in 168 of 256 x 128).
-hipError_t launch_fp8_tiles(const Fp8Gemm &g, hipStream_t stream)
+Fp8Plan fp8_tiles_plan(int64_t M, int64_t N, bool f32_out, int64_t cus)
 {
-    const TileShape *const shapes = g.f32_out ? kBf16Shapes : kFp8Shapes;
-    const int n_shapes = g.f32_out ? 3 : 6;
-    const int64_t cus = device_cu_count();
-    auto cost = [&](int i, int64_t rows) { return shape_cost(shapes[i], rows, g.N, cus); };
+    const TileShape *const shapes = f32_out ? kBf16Shapes : kFp8Shapes;
+    const int n_shapes = f32_out ? 3 : 6;
+    auto cost = [&](int i, int64_t rows) { return shape_cost(shapes[i], rows, N, cus); };
     int best = 0;
     int64_t m1 = 0;                  // rows of the first launch (shape 0)
     double best_cost = 1e30;
     for (int i = 0; i < n_shapes; ++i) {
-        const double c = cost(i, g.M);
+        const double c = cost(i, M);
         if (c < best_cost) best = i, best_cost = c;
     }
-    const int64_t rows0 = (g.M - 1) / shapes[0].tm;      // whole tile-rows before the last
+    const int64_t rows0 = (M - 1) / shapes[0].tm;        // whole tile-rows before the last
     for (int64_t a = rows0; a > 0 && a > rows0 - 16; --a)
         for (int i = 1; i < n_shapes; ++i) {
-            const double c = cost(0, a * shapes[0].tm) + cost(i, g.M - a * shapes[0].tm) +
+            const double c = cost(0, a * shapes[0].tm) + cost(i, M - a * shapes[0].tm) +
                              kSecondLaunch;
             if (c < best_cost - 0.1) best = i, best_cost = c, m1 = a * shapes[0].tm;
         }
-    auto launch = [&](int i, int64_t base, int64_t rows) {
-        const int tn = shapes[i].tn, tm = shapes[i].tm;
+    return {0, 0, shapes[best].tn, shapes[best].tm, m1};
+}
+
+hipError_t launch_fp8_tiles(const Fp8Gemm &g, const Fp8Plan &p, hipStream_t stream)
+{
+    auto launch = [&](int tn, int tm, int64_t base, int64_t rows) {
         return g.f32_out ? launch_shape<kBf16>(tn, tm, g, base, rows, stream)
                : g.pow2  ? launch_shape<kPow2Scale>(tn, tm, g, base, rows, stream)
                          : launch_shape<kAnyScale>(tn, tm, g, base, rows, stream);
     };
-    if (m1 > 0) {
-        const hipError_t e = launch(0, 0, m1);
+    if (p.first > 0) {
+        const TileShape &s = g.f32_out ? kBf16Shapes[0] : kFp8Shapes[0];
+        const hipError_t e = launch(s.tn, s.tm, 0, p.first);
         if (e != hipSuccess) return e;
     }
-    return launch(best, m1, g.M - m1);
+    return launch(p.tn, p.tm, p.first, g.M - p.first);
 }
 
 } // namespace convrot
