@@ -20,18 +20,12 @@
 // magnitudes (rms), far below a bf16 output's rounding, so bf16 outputs use
 // them.  F32 outputs convert the codes to bf16, which holds every e4m3 value, and
 // use v_mfma_f32_16x16x32_bf16, whose sums keep 24 bits throughout.
-#include "common.hpp"
+#include "fp8_common.hpp"
 
 #include <algorithm>
 
 namespace convrot {
 namespace {
-
-typedef int v4i __attribute__((ext_vector_type(4)));
-typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float v4f __attribute__((ext_vector_type(4)));
-typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 constexpr float kMaxE4M3 = 448.0f;
 
@@ -87,16 +81,6 @@ __device__ __forceinline__ float max16(float v)
     CR_DPP_MAX(0x140);
 #undef CR_DPP_MAX
     return v;
-}
-
-// 8 e4m3 codes as bf16, exactly.
-__device__ __forceinline__ v8bf bf16_of_codes(int lo, int hi)
-{
-    const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
-    const v2bf b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
-    const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
-    const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
-    return (v8bf){a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
 // One 128 x 128 block of the weight per workgroup (load time only): thread t

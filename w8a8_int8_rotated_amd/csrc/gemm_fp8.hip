@@ -39,7 +39,7 @@
 // 1.75 GHz.  LDS is the next bound: a k-block costs 192 reads of 1 KiB and 64 KiB
 // of copies, 2048 cycles at 128 bytes a cycle, as many as its matrix instructions;
 // a wave tile larger than 128 x 64 would not fit its registers.
-#include "common.hpp"
+#include "fp8_common.hpp"
 #include "gemm_common.hpp"
 
 #include <algorithm>
@@ -47,12 +47,6 @@
 
 namespace convrot {
 namespace {
-
-typedef int v4i __attribute__((ext_vector_type(4)));
-typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float v4f __attribute__((ext_vector_type(4)));
-typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 constexpr int kKB = 128;        // inputs per k-block
 constexpr int kGroup = 4;       // tile-rows per L2 group (2: 1% slower, 8: 1%, 16: 6%)
@@ -87,16 +81,6 @@ __device__ __forceinline__ v8i frag(const uint8_t *__restrict__ tile)
     const v4i lo = *reinterpret_cast<const v4i *>(tile);
     const v4i hi = *reinterpret_cast<const v4i *>(tile + 1024);
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-
-// 8 e4m3 codes as bf16, exactly.
-__device__ __forceinline__ v8bf bf16_of_codes(int lo, int hi)
-{
-    const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
-    const v2bf b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
-    const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
-    const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
-    return (v8bf){a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
 // How a kernel multiplies: FP8 products joined by fp32 additions (any scales),
