@@ -37,6 +37,8 @@ import time
 ROOT = os.path.dirname(os.path.abspath(__file__))
 sys.path.insert(0, ROOT)
 
+from rocprof_summary import source_sha
+
 METRIC = "effective INT8 TOPS & % INT8 MFMA peak, ConvRot linear M=38656 K=5376"
 PEAK_INT8_TOPS = 5033.2      # MI355X dense INT8 MFMA: 256 CUs x 8192 ops/clk x 2.4 GHz (5.0 POP/s)
 PEAK_HBM_GBS = 8000.0        # MI355X HBM3E, 8 TB/s
@@ -110,13 +112,9 @@ def warmup_steps(args, step, torch):
     args.warmup = n
 
 
-def source_sha(path):
-    return hashlib.sha256(open(path, "rb").read()).hexdigest()
-
-
 def recorded_traffic(kernel, workload):
     """HBM bytes per launch from the committed counter summary, if it was
-    taken on the current kernel source."""
+    taken on the current kernel source and the headers it includes."""
     path = os.path.join(ROOT, "profiles", f"{kernel}_{workload}_pmc.md")
     if not os.path.exists(path):
         return None

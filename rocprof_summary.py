@@ -11,8 +11,9 @@
 
 `traffic` scales each counter by what it reads for the plain device copy of
 known size recorded in the same run (FETCH_SIZE and WRITE_SIZE are in KiB per
-dispatch), and records the SHA-256 of the kernel source so a reader (and
-bench.py) can tell whether the figure still applies to the current kernel.
+dispatch), and records the SHA-256 of the kernel source and of the headers it
+includes, so a reader (and bench.py) can tell whether the figure still applies to
+the current kernel.
 One call can launch several instantiations of a kernel (the GEMM sends its
 last tile-rows to a second launch); every instantiation matching --kernel is
 listed, and the per-call figure is the sum of their per-dispatch averages.
@@ -24,10 +25,27 @@ import collections
 import csv
 import hashlib
 import json
+import os
 import re
 import sys
 
 COPY_KERNEL = "__amd_rocclr_copyBuffer"
+
+
+def source_sha(path: str) -> str:
+    """SHA-256 of a kernel source followed by the headers beside it that it includes,
+    directly or through one another, each once, in the order they are named."""
+    folder, todo, seen, h = os.path.dirname(path), [path], set(), hashlib.sha256()
+    while todo:
+        f = todo.pop(0)
+        if f in seen or not os.path.exists(f):
+            continue
+        seen.add(f)
+        data = open(f, "rb").read()
+        h.update(data)
+        todo += [os.path.join(folder, n) for n in
+                 re.findall(r'^\s*#\s*include\s*"([^"]+)"', data.decode(), re.M)]
+    return h.hexdigest()
 
 
 def _short(name: str) -> str:
@@ -116,7 +134,7 @@ def traffic(args):
     sw = args.copy_bytes / (cw * 1024.0)
     rd = kf * 1024.0 * sf
     wr = kw * 1024.0 * sw
-    sha = hashlib.sha256(open(args.source, "rb").read()).hexdigest()
+    sha = source_sha(args.source)
     out = [f"# HBM traffic of `{args.kernel}` -- {args.workload}", "",
            "Commands (run from /tmp, repository at $R):", "", "```", args.command_fetch,
            args.command_write, "```", "",

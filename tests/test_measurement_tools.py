@@ -104,3 +104,28 @@ def test_recorded_traffic_only_for_the_current_source(tmp_path, monkeypatch):
     src.write_text("// version 2\n")                  # the kernel changed since
     assert bench.recorded_traffic("gemm_i8", "w") is None
 
+
+
+def test_recorded_traffic_only_for_the_current_headers(tmp_path, monkeypatch):
+    """A kernel is its source and the headers beside it that it includes, directly or
+    through one another: a change to any of them drops the recorded figure."""
+    import rocprof_summary
+    bench = _bench()
+    src, a, b = (tmp_path / n for n in ("gemm_i8.hip", "a.hpp", "b.hpp"))
+    src.write_text('#include "a.hpp"\n#include <vector>\n#include "elsewhere.h"\n')
+    a.write_text('#pragma once\n  #  include "b.hpp"\n')
+    b.write_text('#pragma once\n#include "a.hpp"\n// waits, version 1\n')
+    (tmp_path / "profiles").mkdir()
+    (tmp_path / "profiles" / "gemm_i8_w_pmc.md").write_text(
+        f"traffic_bytes_per_launch: 6.5e+09\n"
+        f"kernel_source_sha256: {rocprof_summary.source_sha(str(src))}\n")
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    monkeypatch.setattr(bench, "SOURCES", {"gemm_i8": str(src)})
+    assert bench.recorded_traffic("gemm_i8", "w") == 6.5e9
+    for f, text in ((b, '#pragma once\n#include "a.hpp"\n// waits, version 2\n'),
+                    (a, '#pragma once\n#include "b.hpp"\n// another\n')):
+        was = f.read_text()
+        f.write_text(text)
+        assert bench.recorded_traffic("gemm_i8", "w") is None
+        f.write_text(was)
+        assert bench.recorded_traffic("gemm_i8", "w") == 6.5e9
