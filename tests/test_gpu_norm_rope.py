@@ -489,3 +489,37 @@ def test_offsets_past_32_bits(cr):
             whole = run(q, pos)
             assert torch.equal(whole[part], run(x, p))
             del G, whole
+
+
+@pytest.mark.parametrize("pairing", ["interleaved", "half"])
+@pytest.mark.parametrize("pos", ["i32", "f32"])
+def test_far_positions_keep_fp32_accuracy(cr, pairing, pos):
+    """fp32 rows at positions to 10^6, with a zero row: rotation, norm with rotation and
+    its backward within the bounds of near positions (an fp32 angle would be off by 0.06
+    radians here).  fp32 positions are multiples of 0.24, the definition's own inputs."""
+    c = Case(B=1, T=64, Hq=2, Hk=1, D=128, dims=(64, 32, 32), pairing=pairing, dtype="f32",
+             pos=pos, far=20000 if pos == "i32" else 83000)
+    assert float(c.pos.max()) > 900_000
+    announce(f"far positions {c}")
+    c.q[0, 5] = 0
+    plan, wq, wk = c.plan(cr), c.wq.cuda(), c.wk.cuda()
+    for inverse, sign in ((False, 1.0), (True, -1.0)):
+        y, _ = cr.convrot_rope_forward(c.q, None, plan, c.posd, inverse=inverse)
+        x64 = c.q.double().cpu()
+        ref = c.rot(x64, sign)
+        close(y, ref, 16 * U * pair_size(x64, c.R, c.pairing) + c.half_step(ref) + 1e-40, "rope")
+    out = cr.convrot_qk_norm_rope_forward(c.q, c.k, wq, wk, plan, c.posd, eps=EPS)
+    for x, w, y in ((c.q, c.wq, out[0]), (c.k, c.wk, out[1])):
+        n, _ = norm(x.double().cpu(), w.double(), EPS)
+        ref = c.rot(n)
+        bound = (c.D / 16 + 32) * U * pair_size(n, c.R, c.pairing) + c.half_step(ref) + 1e-40
+        close(y, ref, bound, "norm + rope")
+    assert bool((out[0][0, 5] == 0).all())
+    gq, gk = c.make(torch.Generator().manual_seed(8), 0.1)
+    dq, dk, dwq, dwk = cr.convrot_qk_norm_rope_backward(gq, gk, c.q, c.k, wq, wk, plan, c.posd,
+                                                        eps=EPS)
+    chain = c.T * c.Hq + 64                  # as in test_norm_rope_backward
+    for g, x, w, dx, dw in ((gq, c.q, c.wq, dq, dwq), (gk, c.k, c.wk, dk, dwk)):
+        rdx, rdw, mag, dwmag = reference_backward(c, g, x, w)
+        close(dx, rdx, (c.D / 8 + 64) * U * mag + c.half_step(rdx) + 1e-40, "dx")
+        close(dw, rdw, (chain + c.D / 16 + 64) * U * dwmag + 1e-40, "dw")
