@@ -374,3 +374,13 @@ def test_stream_of_another_device_refused(cr):
                  lambda: cr.convrot_rope_forward(Q, Q, plan, P, stream=Stream())):
         with pytest.raises(ValueError, match="GPU tensor on cuda:1"):
             call()
+
+
+@pytest.mark.parametrize("N,K", [(64, 192), (24, 256), (64, 65664)])
+def test_fp8_import_refuses_shapes_before_values(cr, N, K):
+    """A shape that the library does not take is refused as such, whatever the scales."""
+    W = torch.zeros(N, K).to(torch.float8_e4m3fn)
+    for scales in ("f32", "pow2"):
+        with pytest.raises(cr.ConvRotError, match="convrot_fp8_prepare_weights"):
+            cr.convrot_fp8_prepare_weights(W, src_scale=torch.zeros(-(-N // 128), K // 128),
+                                           scales=scales)

@@ -808,6 +808,9 @@ def convrot_fp8_prepare_weights(W: torch.Tensor, layout: int = OUT_MAJOR,
     _opt(src_scale, "src_scale", torch.float32, (-(-N // 128), K // 128))
     if scales not in FP8_SCALES:
         raise ValueError(f"scales must be one of {sorted(FP8_SCALES)}")
+    nbytes = lib.convrot_fp8_packed_bytes(N, K)
+    if nbytes == 0:
+        raise ConvRotError("convrot_fp8_prepare_weights", EUNSUPPORTED)
     W = W.contiguous()
     _on_device(W.device, W=W, src_scale=src_scale)
     if src_scale is not None and scales == "pow2":
@@ -822,9 +825,6 @@ def convrot_fp8_prepare_weights(W: torch.Tensor, layout: int = OUT_MAJOR,
             used = used.view(-(-N // 128), 128, K // 128, 128).any(3).any(1)
             if bool((used & (bits == 0)).any()):
                 raise ValueError("a block whose scale is 0 must hold zero codes")
-    nbytes = lib.convrot_fp8_packed_bytes(N, K)
-    if nbytes == 0:
-        raise ConvRotError("convrot_fp8_prepare_weights", EUNSUPPORTED)
     tag = _dtype_tag(W.dtype)
     codes = torch.empty(nbytes, dtype=torch.uint8, device=W.device)
     scale = torch.empty((-(-N // 128), K // 128), dtype=torch.float32, device=W.device)
