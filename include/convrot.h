@@ -424,7 +424,11 @@ CONVROT_API int convrot_silu_f32(const uint16_t *a, int64_t n, float *s, void *s
  * Sums: F32 outputs are summed in fp32 throughout.  BF16 outputs use the FP8
  * matrix instructions, which cut each product to a multiple of 2^-13 of the
  * largest of its 8 neighbours' products before adding them (2e-6 of the sum of
- * magnitudes on Gaussian inputs) and add the rest in fp32.
+ * magnitudes on Gaussian inputs, rms) and add the rest in fp32.  The total error
+ * stays that of the rounding to bf16, but an output far smaller than the sum of its
+ * terms' magnitudes can be off by more than its own rounding (measured at K = 5376:
+ * 0.2 to 0.6% of the outputs by more than one unit in the last place).  Take F32
+ * outputs where small outputs matter.
  * The order of the sums depends on the shape, so a row slice of a call can
  * differ from the full call in the last bits of the fp32 sums; calls of the
  * same shape repeat bit for bit.  A NaN or an infinity among a token's inputs
@@ -468,8 +472,9 @@ CONVROT_API size_t convrot_fp8_linear_workspace_bytes(int64_t M, int64_t K, int6
  * with src_scale, device F32 [ceil(N / 128), K / 128] row-major (imported
  * unchanged; with POW2 they must be normal powers of two, or 0 where the block's
  * codes are all 0, which is not checked here).  Layout per `layout`, [N, K] or
- * [K, N]; src_scale keeps its order either way.  out->codes, out->scale: caller allocations; out->scales selects
- * the kind.  Errors as for convrot_linear_prepare_weights. */
+ * [K, N]; src_scale keeps its order either way.  out->codes, out->scale: caller
+ * allocations; out->scales selects the kind.  Errors as for
+ * convrot_linear_prepare_weights. */
 CONVROT_API int convrot_fp8_prepare_weights(const void *W, int w_dtype, int layout,
                                             const float *src_scale, int64_t N, int64_t K,
                                             convrot_fp8_weights *out, void *ws,

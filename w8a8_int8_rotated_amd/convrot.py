@@ -3,7 +3,13 @@
 Argument marshalling only: PyTorch provides device memory and the current HIP
 stream; every step of the forward path runs in the library's HIP kernels.
 The functions carry the C names.  If the library has not been built the first
-call raises -- there is no fallback implementation.
+call raises -- there is no fallback implementation.  They build no autograd graph,
+whatever their inputs require: where an entry has a backward pass here
+(convrot_rope_forward with inverse=True, convrot_qk_norm_rope_backward), a caller
+joins the two in a torch.autograd.Function of their own.
+
+stream=: the whole call, its copies and allocations among it, runs on that stream,
+which must be ordered after whatever made the arguments.
 """
 from __future__ import annotations
 
@@ -1001,8 +1007,9 @@ def _heads_out(out, name, like, lead):
 def convrot_rope_forward(q: torch.Tensor, k, rope: RopePlan, positions: torch.Tensor,
                          inverse: bool = False, out_q=None, out_k=None, stream=None):
     """(q_out, k_out): q and k [B, T, heads, D] turned by the tokens' positions
-    [T, axes] or [B, T, axes] (int32 or float32); k may be None.  Out of place
-    unless out_q is q.  inverse: by the negative angles, the backward pass."""
+    [T, axes] or [B, T, axes] (contiguous, int32 or float32); k may be None.  Out of
+    place unless out_q is q.  inverse: by the negative angles, the backward pass
+    (no autograd graph is built)."""
     if stream is not None:
         return _on_stream(convrot_rope_forward, locals())
     lead, psb, vq, vk = _heads_pair(q, k, rope, positions)
@@ -1021,7 +1028,8 @@ def convrot_qk_norm_rope_forward(q: torch.Tensor, k, w_q, w_k, rope: RopePlan,
                                  positions: torch.Tensor, eps: float = 1e-6, out_q=None,
                                  out_k=None, stream=None):
     """convrot_rope_forward of q * rsqrt(mean(q^2) + eps) * w_q over each head's
-    channels and of k likewise; w_q, w_k float32 [D] or None."""
+    channels and of k likewise; w_q, w_k float32 [D] or None.  No autograd graph is
+    built: convrot_qk_norm_rope_backward is the backward pass."""
     if stream is not None:
         return _on_stream(convrot_qk_norm_rope_forward, locals())
     lead, psb, vq, vk = _heads_pair(q, k, rope, positions)

@@ -17,9 +17,16 @@
 // largest one, and only the groups' sums are added in fp32 (measured with single
 // products: 2^16 + 2^3 is exact inside a group, 2^16 + 2^2 gives 2^16; across
 // groups 2^16 + 2^-7 is exact).  On Gaussian codes that is 2e-6 of the sum of
-// magnitudes (rms), far below a bf16 output's rounding, so bf16 outputs use
-// them.  F32 outputs convert the codes to bf16, which holds every e4m3 value, and
-// use v_mfma_f32_16x16x32_bf16, whose sums keep 24 bits throughout.
+// magnitudes (rms).  bf16 outputs use them, at twice the rate of the bf16
+// instructions: beside their own rounding (1.66e-3 of the outputs' rms) the cut does
+// not show in the total error, which stays 1.66e-3.  It does show in single outputs
+// whose terms cancel: at K = 5376, 1.2% of the outputs are not the bf16 value nearest
+// to the exact sum (2.6%, and 3.3% with power-of-two scales, where 1% of the channels
+// are 30 times larger; fp32 sums 0.01%), 0.2% (0.5%, 0.6%) are off by more than one
+// unit and 0.1% (0.2%, 0.3%) by more than 1% of their small value.  F32 outputs
+// convert the codes to bf16, which holds every e4m3 value, and use
+// v_mfma_f32_16x16x32_bf16, whose sums keep 24 bits throughout (1e-7 of the outputs'
+// rms).
 #include "fp8_common.hpp"
 
 #include <algorithm>
