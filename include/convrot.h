@@ -1,8 +1,8 @@
 /*
  * convrot.h -- C ABI of libconvrot.so: the ConvRot W8A8 INT8 linear layer on
  * AMD Instinct MI355X (gfx950), and beside it (in sections of their own below)
- * the FP8 block-scaled linear, rotary positions and the norms of queries and
- * keys.
+ * the FP8 block-scaled linear, rotary positions, the norms of queries and keys,
+ * and the residual's addition with the RMS norm in front of a projection.
  *
  * The method (what the INT8 entry points compute):
  *   - Linear layers of the INT8 package are W8A8: INT8 activations times INT8
@@ -623,6 +623,82 @@ CONVROT_API int convrot_fp8_qkv_forward(const void *X, int64_t B, int64_t T,
                                         const void *positions, int pos_dtype,
                                         int64_t pos_batch_stride, void *Y, int y_dtype, void *ws,
                                         size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------ */
+/* the residual's addition and the RMS norm in front of a projection   */
+/* ------------------------------------------------------------------ */
+
+/* For every row x of X [M, K]:
+ *   h = x + r, rounded to the residual's type (without a residual h = x);
+ *   n = (h * rsqrt(mean(h^2) + eps)) * w.
+ * All sums and products are fp32; h is rounded first and everything after uses the
+ * rounded value, so the norm of a stored h has the same bits.  (The sum of squares is
+ * fp32 too: channels beyond about 1e18 / sqrt(K) overflow it.)
+ *   x, residual   device [M, K], dense; x_dtype and res_dtype CONVROT_BF16 or _F32
+ *                 (an fp32 x takes an fp32 residual).  residual and residual_out may
+ *                 both be NULL: no addition (res_dtype is not looked at).
+ *   w             device F32 [K], or NULL (ones).  eps > 0, finite.
+ *   residual_out  h, of the residual's type; may be the residual, or x of that type.
+ * K % 8 == 0, K <= 32768, M < 2^31 (EUNSUPPORTED otherwise).  An output may stand in
+ * the place of an input of the same extent; otherwise outputs overlap neither inputs
+ * nor each other (EINVAL).  A row with a NaN or an infinity has NaN outputs (where it
+ * is rounded to INT8, its scale is NaN) and leaves the other rows alone. */
+
+/* y [M, K] = n, rounded once to y_dtype (CONVROT_BF16 or CONVROT_F32). */
+CONVROT_API int convrot_add_rms_norm_forward(const void *x, int x_dtype, const void *residual,
+                                             int res_dtype, const float *w, float eps, int64_t M,
+                                             int64_t K, void *residual_out, void *y, int y_dtype,
+                                             void *stream);
+
+/* The codes and scales of n, quantised from its fp32 values (never rounded to bf16):
+ * as convrot_rotate_quantize of the fp32 rows n (bit for bit) with its block and flags
+ * (0 or CONVROT_ROT_REGULAR), and e4m3 codes as convrot_fp8_quantize defines them,
+ * with its kind of scales.  K as for those calls, too. */
+CONVROT_API int convrot_add_rms_norm_rotate_quantize(const void *x, int x_dtype,
+                                                     const void *residual, int res_dtype,
+                                                     const float *w, float eps, int64_t M,
+                                                     int64_t K, int block, uint32_t flags,
+                                                     void *residual_out, int8_t *q, float *s,
+                                                     void *stream);
+CONVROT_API int convrot_add_rms_norm_fp8_quantize(const void *x, int x_dtype,
+                                                  const void *residual, int res_dtype,
+                                                  const float *w, float eps, int64_t M, int64_t K,
+                                                  int scales, void *residual_out, uint8_t *q,
+                                                  float *s, void *stream);
+
+/* Y [M, W->N] = linear(n; W) + bias: the two calls above, then the product (two
+ * launches; n itself is never written).  ws: convrot_linear_workspace_bytes(M, K, N, b)
+ * or convrot_fp8_norm_linear_workspace_bytes(M, K, N) bytes.  Y may not overlap
+ * residual_out.  Otherwise as convrot_linear_forward and convrot_fp8_linear_forward. */
+CONVROT_API size_t convrot_fp8_norm_linear_workspace_bytes(int64_t M, int64_t K, int64_t N);
+CONVROT_API int convrot_norm_linear_forward(const void *x, int x_dtype, const void *residual,
+                                            int res_dtype, const float *w, float eps, int64_t M,
+                                            const convrot_weights *W, const float *bias,
+                                            void *residual_out, void *Y, int y_dtype, void *ws,
+                                            size_t ws_bytes, void *stream);
+CONVROT_API int convrot_fp8_norm_linear_forward(const void *x, int x_dtype, const void *residual,
+                                                int res_dtype, const float *w, float eps,
+                                                int64_t M, const convrot_fp8_weights *W,
+                                                const float *bias, void *residual_out, void *Y,
+                                                int y_dtype, void *ws, size_t ws_bytes,
+                                                void *stream);
+
+/* The backward pass.  With q = rsqrt(mean(h^2) + eps), t = g w:
+ *   dh = g_h + q t - h q^3 mean(t h);   dw = sum over rows of g h q.
+ *   g     the gradient of n [M, K] (BF16 or F32); h as the forward stored it (x where
+ *         there was no residual); g_h: the gradient that reaches h along the residual
+ *         stream, of h's type, or NULL.
+ *   dh    the gradient of h, of h's type: the residual's, and x's.  dx: its bf16 copy,
+ *         for a bf16 x beside an fp32 residual (h_dtype F32), or NULL.
+ *   dw    F32 [K], written (not added to) in an order that does not change from call to
+ *         call, or NULL.  ws: convrot_add_rms_norm_workspace_bytes(M, K) bytes (partial
+ *         sums; not needed without dw).
+ * In place and overlaps as above (dh may be g, h or g_h of its type; dx may be g). */
+CONVROT_API size_t convrot_add_rms_norm_workspace_bytes(int64_t M, int64_t K);
+CONVROT_API int convrot_add_rms_norm_backward(const void *g, int g_dtype, const void *h,
+                                              int h_dtype, const void *g_h, const float *w,
+                                              float eps, int64_t M, int64_t K, void *dh, void *dx,
+                                              float *dw, void *ws, size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------ */
 /* comparison variant (not the W8A8 path)                              */

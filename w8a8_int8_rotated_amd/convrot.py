@@ -178,6 +178,26 @@ _SIGNATURES = {
     "convrot_fp8_qkv_forward": (
         _c_int, [_c_p, _c_i64, _c_i64, _FW, _c_p, _c_int, _c_int, _c_p, _c_p, ctypes.c_float, _RP,
                  _c_p, _c_int, _c_i64, _c_p, _c_int, _c_p, _c_sz, _c_p]),
+    "convrot_add_rms_norm_forward": (
+        _c_int, [_c_p, _c_int, _c_p, _c_int, _c_p, ctypes.c_float, _c_i64, _c_i64, _c_p, _c_p,
+                 _c_int, _c_p]),
+    "convrot_add_rms_norm_rotate_quantize": (
+        _c_int, [_c_p, _c_int, _c_p, _c_int, _c_p, ctypes.c_float, _c_i64, _c_i64, _c_int,
+                 ctypes.c_uint32, _c_p, _c_p, _c_p, _c_p]),
+    "convrot_add_rms_norm_fp8_quantize": (
+        _c_int, [_c_p, _c_int, _c_p, _c_int, _c_p, ctypes.c_float, _c_i64, _c_i64, _c_int, _c_p,
+                 _c_p, _c_p, _c_p]),
+    "convrot_fp8_norm_linear_workspace_bytes": (_c_sz, [_c_i64, _c_i64, _c_i64]),
+    "convrot_norm_linear_forward": (
+        _c_int, [_c_p, _c_int, _c_p, _c_int, _c_p, ctypes.c_float, _c_i64, _W, _c_p, _c_p, _c_p,
+                 _c_int, _c_p, _c_sz, _c_p]),
+    "convrot_fp8_norm_linear_forward": (
+        _c_int, [_c_p, _c_int, _c_p, _c_int, _c_p, ctypes.c_float, _c_i64, _FW, _c_p, _c_p, _c_p,
+                 _c_int, _c_p, _c_sz, _c_p]),
+    "convrot_add_rms_norm_workspace_bytes": (_c_sz, [_c_i64, _c_i64]),
+    "convrot_add_rms_norm_backward": (
+        _c_int, [_c_p, _c_int, _c_p, _c_int, _c_p, _c_p, ctypes.c_float, _c_i64, _c_i64, _c_p,
+                 _c_p, _c_p, _c_p, _c_sz, _c_p]),
     "convrot_probe_mfma_i8": (_c_int, [_c_i64, _c_p, _c_p, ctypes.POINTER(ctypes.c_int64),
                                        _c_p]),
     "convrot_probe_stream": (_c_int, [_c_p, _c_p, _c_i64, _c_int, _c_p]),
@@ -1132,6 +1152,198 @@ def convrot_qkv_forward(X: torch.Tensor, W, heads_q: int, heads_kv: int, w_q, w_
             _ptr(w_k), eps, rope.ref(), _ptr(positions), _dtype_tag(positions.dtype), psb,
             _ptr(out), _dtype_tag(out.dtype), _ptr(ws), ws.numel() if ws is not None else 0)
     return out
+
+
+# ------------------------- the residual's addition and the RMS norm ----
+
+_FLOATS = (torch.bfloat16, torch.float32)
+
+
+def _norm_args(x, w, residual, residual_out):
+    """The checks the forward calls share: (M, K, the residual's dtype or x's)."""
+    if not isinstance(x, _Tensor) or x.dim() < 1:
+        raise ValueError("x must be a tensor [.., K]")
+    shape = x.shape
+    K = shape[-1]
+    _need(x, "x", _FLOATS, shape)
+    _opt(w, "w", torch.float32, (K,))
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out given without residual")
+        return (x.numel() // K if K else 0), K, x.dtype
+    _need(residual, "residual", _FLOATS, shape)
+    if x.dtype == torch.float32 and residual.dtype != torch.float32:
+        raise ValueError("a float32 x takes a float32 residual")
+    _opt(residual_out, "residual_out", residual.dtype, shape)
+    return (x.numel() // K if K else 0), K, residual.dtype
+
+
+def convrot_add_rms_norm_forward(x: torch.Tensor, w, residual=None, eps: float = 1e-6,
+                                 out_dtype: torch.dtype = torch.bfloat16, out=None,
+                                 residual_out=None, stream=None):
+    """(y, h): h = x + residual in the residual's type (None without a residual) and
+    y = h * rsqrt(mean(h^2) + eps) * w over the last dimension; x and residual [.., K]
+    contiguous, w float32 [K] or None.  residual_out may be residual itself.  No autograd
+    graph is built: convrot_add_rms_norm_backward is the backward pass."""
+    if stream is not None:
+        return _on_stream(convrot_add_rms_norm_forward, locals())
+    M, K, rdt = _norm_args(x, w, residual, residual_out)
+    _opt(out, "out", _FLOATS, x.shape)
+    dev = x.device
+    _on_device(None, x=x)
+    _on_device(dev, w=w, residual=residual, out=out, residual_out=residual_out)
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype, device=dev)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(residual)
+    _launch(dev, "convrot_add_rms_norm_forward", _ptr(x), _dtype_tag(x.dtype), _ptr(residual),
+            _dtype_tag(rdt), _ptr(w), eps, M, K, _ptr(residual_out), _ptr(out),
+            _dtype_tag(out.dtype))
+    return out, residual_out
+
+
+def convrot_add_rms_norm_rotate_quantize(x: torch.Tensor, w, block: int, residual=None,
+                                         eps: float = 1e-6, rotation: str = "sylvester", q=None,
+                                         s=None, residual_out=None, stream=None):
+    """(q, s, h): the K-tiled INT8 codes (Mp, K) and row scales [M] of the rotated norm, as
+    convrot_gemm_dequant takes them."""
+    if stream is not None:
+        return _on_stream(convrot_add_rms_norm_rotate_quantize, locals())
+    M, K, rdt = _norm_args(x, w, residual, residual_out)
+    q = _codes(q, M, K, x.device) if q is not None else None
+    _opt(s, "s", torch.float32, (M,))
+    if rotation not in ROTATIONS:
+        raise ValueError(f"rotation must be one of {sorted(ROTATIONS)}")
+    dev = x.device
+    _on_device(None, x=x)
+    _on_device(dev, w=w, residual=residual, q=q, s=s, residual_out=residual_out)
+    if q is None:
+        q = _codes(None, M, K, dev)
+    if s is None:
+        s = torch.empty(M, dtype=torch.float32, device=dev)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(residual)
+    _launch(dev, "convrot_add_rms_norm_rotate_quantize", _ptr(x), _dtype_tag(x.dtype),
+            _ptr(residual), _dtype_tag(rdt), _ptr(w), eps, M, K, block, ROTATIONS[rotation],
+            _ptr(residual_out), _ptr(q), _ptr(s))
+    return q, s, residual_out
+
+
+def convrot_add_rms_norm_fp8_quantize(x: torch.Tensor, w, scales: str = "f32", residual=None,
+                                      eps: float = 1e-6, q=None, s=None, residual_out=None,
+                                      stream=None):
+    """(q, s, h): the K-tiled e4m3 codes (Mp, K) and scales [K/128, Mp] of the norm, as
+    convrot_fp8_gemm_dequant takes them."""
+    if stream is not None:
+        return _on_stream(convrot_add_rms_norm_fp8_quantize, locals())
+    M, K, rdt = _norm_args(x, w, residual, residual_out)
+    if scales not in FP8_SCALES:
+        raise ValueError(f"scales must be one of {sorted(FP8_SCALES)}")
+    Mp = padded_rows(M)
+    _opt(q, "q", torch.uint8, (Mp, K))
+    _opt(s, "s", torch.float32, (K // 128, Mp))
+    dev = x.device
+    _on_device(None, x=x)
+    _on_device(dev, w=w, residual=residual, q=q, s=s, residual_out=residual_out)
+    if q is None:
+        q = torch.empty((Mp, K), dtype=torch.uint8, device=dev)
+    if s is None:
+        s = torch.empty((K // 128, Mp), dtype=torch.float32, device=dev)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(residual)
+    _launch(dev, "convrot_add_rms_norm_fp8_quantize", _ptr(x), _dtype_tag(x.dtype),
+            _ptr(residual), _dtype_tag(rdt), _ptr(w), eps, M, K, FP8_SCALES[scales],
+            _ptr(residual_out), _ptr(q), _ptr(s))
+    return q, s, residual_out
+
+
+def convrot_fp8_norm_linear_workspace_bytes(M: int, K: int, N: int) -> int:
+    return library().convrot_fp8_norm_linear_workspace_bytes(M, K, N)
+
+
+def convrot_norm_linear_forward(x: torch.Tensor, w, W, residual=None, bias=None,
+                                eps: float = 1e-6, out_dtype: torch.dtype = torch.bfloat16,
+                                out=None, residual_out=None, workspace=None, stream=None):
+    """(Y, h): Y [.., N] = the linear W (PreparedWeights or FP8Weights) of the norm of
+    h = x + residual, quantised as it is formed."""
+    if stream is not None:
+        return _on_stream(convrot_norm_linear_forward, locals())
+    lib = library()
+    fp8 = isinstance(W, FP8Weights)
+    dev = _fp8_weights(W, "W") if fp8 else _weights(W, "W")
+    M, K, rdt = _norm_args(x, w, residual, residual_out)
+    if K != W.K:
+        raise ValueError(f"x must have {W.K} channels, got {K}")
+    shape = (*x.shape[:-1], W.N)
+    _opt(bias, "bias", torch.float32, (W.N,))
+    _opt(out, "out", _FLOATS, shape)
+    wsb = (lib.convrot_fp8_norm_linear_workspace_bytes(M, K, W.N) if fp8 else
+           lib.convrot_linear_workspace_bytes(M, K, W.N, W.block))
+    _check_workspace(wsb, workspace)
+    _on_device(dev, x=x, w=w, residual=residual, bias=bias, out=out, residual_out=residual_out,
+               workspace=workspace)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=dev)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(residual)
+    ws = _workspace(wsb, dev, workspace)
+    _launch(dev, "convrot_fp8_norm_linear_forward" if fp8 else "convrot_norm_linear_forward",
+            _ptr(x), _dtype_tag(x.dtype), _ptr(residual), _dtype_tag(rdt), _ptr(w), eps, M,
+            W.ref(), _ptr(bias), _ptr(residual_out), _ptr(out), _dtype_tag(out.dtype), _ptr(ws),
+            ws.numel() if ws is not None else 0)
+    return out, residual_out
+
+
+def convrot_add_rms_norm_workspace_bytes(M: int, K: int) -> int:
+    return library().convrot_add_rms_norm_workspace_bytes(M, K)
+
+
+def convrot_add_rms_norm_backward(g: torch.Tensor, h: torch.Tensor, w, g_h=None,
+                                  eps: float = 1e-6, x_dtype=None, dh=None, dx=None, dw=None,
+                                  workspace=None, stream=None):
+    """(dh, dx, dw) of convrot_add_rms_norm_forward from g, the gradient of y, and g_h, the
+    gradient that reaches h otherwise (or None).  dh is the residual's gradient, in h's type;
+    dx is x's: dh itself, or with x_dtype=torch.bfloat16 beside a float32 h its bf16 copy.
+    dw is None without w."""
+    if stream is not None:
+        return _on_stream(convrot_add_rms_norm_backward, locals())
+    lib = library()
+    if not isinstance(h, _Tensor) or h.dim() < 1:
+        raise ValueError("h must be a tensor [.., K]")
+    shape = h.shape
+    K = shape[-1]
+    _need(h, "h", _FLOATS, shape)
+    _need(g, "g", _FLOATS, shape)
+    _opt(g_h, "g_h", h.dtype, shape)
+    _opt(w, "w", torch.float32, (K,))
+    if x_dtype is not None and x_dtype != h.dtype \
+            and (x_dtype != torch.bfloat16 or h.dtype != torch.float32):
+        raise ValueError("x_dtype must be h's type, or bfloat16 beside a float32 h")
+    copy = x_dtype is not None and x_dtype != h.dtype
+    _opt(dh, "dh", h.dtype, shape)
+    if dx is not None and not copy:
+        raise ValueError("dx is dh unless x_dtype differs from h's type")
+    _opt(dx, "dx", torch.bfloat16, shape)
+    if w is None and dw is not None:
+        raise ValueError("dw given without w")
+    _opt(dw, "dw", torch.float32, (K,))
+    M = h.numel() // K if K else 0
+    wsb = lib.convrot_add_rms_norm_workspace_bytes(M, K) if w is not None else 0
+    _check_workspace(wsb, workspace)
+    dev = h.device
+    _on_device(None, h=h)
+    _on_device(dev, g=g, g_h=g_h, w=w, dh=dh, dx=dx, dw=dw, workspace=workspace)
+    if dh is None:
+        dh = torch.empty_like(h)
+    if copy and dx is None:
+        dx = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    if w is not None and dw is None:
+        dw = torch.empty(K, dtype=torch.float32, device=dev)
+    ws = _workspace(wsb, dev, workspace)
+    _launch(dev, "convrot_add_rms_norm_backward", _ptr(g), _dtype_tag(g.dtype), _ptr(h),
+            _dtype_tag(h.dtype), _ptr(g_h), _ptr(w), eps, M, K, _ptr(dh), _ptr(dx), _ptr(dw),
+            _ptr(ws), ws.numel() if ws is not None else 0)
+    return dh, dx if copy else dh, dw
 
 
 # ------------------------------------------------------------- hooks ----

@@ -2,6 +2,7 @@
 // sequencing.  Every check runs on the host before any launch; a call that
 // fails validation launches nothing.
 #include "convrot.h"
+#include "add_norm.hpp"
 #include "common.hpp"
 
 #include <atomic>
@@ -1130,6 +1131,290 @@ int convrot_fp8_qkv_forward(const void *X, int64_t B, int64_t T, const convrot_f
                                                   static_cast<hipStream_t>(stream)));
     log_call("convrot_fp8_qkv_forward", token_count(B, T), W ? W->N : 0, W ? W->K : 0, rc);
     return rc;
+}
+
+// ---------------------------------------------------------------------------
+// The residual's addition and the RMS norm.
+// ---------------------------------------------------------------------------
+
+// Whether an output may stand where an input does: in its place, or apart from it.
+static bool overlaps(const void *a, size_t na, const void *b, size_t nb)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && na > 0 && nb > 0 && x < y + nb && y < x + na;
+}
+static bool in_place_or_apart(const void *a, size_t na, const void *b, size_t nb)
+{
+    return (a == b && na == nb) || !overlaps(a, na, b, nb);
+}
+
+static bool is_float_dtype(int t) { return t == CONVROT_F32 || t == CONVROT_BF16; }
+static size_t dtype_bytes(int t) { return t == CONVROT_F32 ? 4u : 2u; }
+
+// Rows and channels of a norm; every byte count formed from them fits 64 bits.
+static int check_norm_shape(int64_t M, int64_t K, float eps)
+{
+    if (M < 0 || K <= 0) return CONVROT_EINVAL;
+    if (M >= kI32Bound || K > convrot::kMaxNormK || K % 8 != 0) return CONVROT_EUNSUPPORTED;
+    return check_eps(eps);
+}
+
+// The arguments the forward calls share, checked and gathered.  M > 0 or nothing but
+// the shape is looked at.
+static int add_norm_args(const void *x, int x_dtype, const void *residual, int res_dtype,
+                         const float *w, float eps, int64_t M, int64_t K, void *residual_out,
+                         convrot::AddNorm *a)
+{
+    int rc = check_norm_shape(M, K, eps);
+    if (rc != CONVROT_OK) return rc;
+    const bool add = residual != nullptr;
+    if (add != (residual_out != nullptr)) return CONVROT_EINVAL;
+    if (!is_float_dtype(x_dtype) || (add && !is_float_dtype(res_dtype)))
+        return CONVROT_EUNSUPPORTED;
+    if (add && x_dtype == CONVROT_F32 && res_dtype != CONVROT_F32) return CONVROT_EUNSUPPORTED;
+    *a = {};
+    a->x = x;
+    a->r = residual;
+    a->w = w;
+    a->h = residual_out;
+    a->M = M;
+    a->K = (int)K;
+    a->eps = eps;
+    a->x_f32 = x_dtype == CONVROT_F32;
+    a->r_f32 = add ? res_dtype == CONVROT_F32 : a->x_f32;
+    if (M == 0) return CONVROT_OK;
+    if (!x) return CONVROT_EINVAL;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(w) || !aligned16(residual_out))
+        return CONVROT_EALIGN;
+    const size_t n = (size_t)M * (size_t)K, nx = n * dtype_bytes(x_dtype);
+    if (add) {
+        const size_t nr = n * dtype_bytes(res_dtype);
+        if (!in_place_or_apart(residual_out, nr, residual, nr) ||
+            !in_place_or_apart(residual_out, nr, x, nx) ||
+            overlaps(residual_out, nr, w, (size_t)K * 4u))
+            return CONVROT_EINVAL;
+    }
+    return CONVROT_OK;
+}
+
+// An output of n bytes apart from the inputs and from residual_out.
+static bool apart_from_norm(const convrot::AddNorm &a, const void *out, size_t n)
+{
+    const size_t e = (size_t)a.M * (size_t)a.K;
+    const size_t nr = e * (a.r_f32 ? 4u : 2u);
+    return !overlaps(out, n, a.x, e * (a.x_f32 ? 4u : 2u)) && !overlaps(out, n, a.r, nr) &&
+           !overlaps(out, n, a.h, nr) && !overlaps(out, n, a.w, (size_t)a.K * 4u);
+}
+
+int convrot_add_rms_norm_forward(const void *x, int x_dtype, const void *residual, int res_dtype,
+                                 const float *w, float eps, int64_t M, int64_t K,
+                                 void *residual_out, void *y, int y_dtype, void *stream)
+{
+    convrot::AddNorm a;
+    int rc = add_norm_args(x, x_dtype, residual, res_dtype, w, eps, M, K, residual_out, &a);
+    if (rc != CONVROT_OK) return rc;
+    if ((rc = check_out_dtype(y_dtype)) != CONVROT_OK) return rc;
+    if (M == 0) return CONVROT_OK;
+    if (!y) return CONVROT_EINVAL;
+    if (!aligned16(y)) return CONVROT_EALIGN;
+    const size_t n = (size_t)M * (size_t)K, ny = n * dtype_bytes(y_dtype);
+    const size_t nr = n * (a.r_f32 ? 4u : 2u);
+    if (!in_place_or_apart(y, ny, x, n * dtype_bytes(x_dtype)) ||
+        !in_place_or_apart(y, ny, residual, nr) || overlaps(y, ny, residual_out, nr) ||
+        overlaps(y, ny, w, (size_t)K * 4u))
+        return CONVROT_EINVAL;
+    a.y = y;
+    a.y_f32 = y_dtype == CONVROT_F32;
+    return hip_status(convrot::launch_add_norm(convrot::NormOut::ROWS, a,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+int convrot_add_rms_norm_rotate_quantize(const void *x, int x_dtype, const void *residual,
+                                         int res_dtype, const float *w, float eps, int64_t M,
+                                         int64_t K, int block, uint32_t flags,
+                                         void *residual_out, int8_t *q, float *s, void *stream)
+{
+    convrot::AddNorm a;
+    int rc = add_norm_args(x, x_dtype, residual, res_dtype, w, eps, M, K, residual_out, &a);
+    if (rc != CONVROT_OK) return rc;
+    if ((flags & ~CONVROT_ROT_REGULAR) != 0) return CONVROT_EUNSUPPORTED;
+    if (!valid_block(block) || K % block != 0 || !valid_rotation(flags, block))
+        return CONVROT_EINVAL;
+    if (K % 128 != 0 || check_rows(M, K) != CONVROT_OK) return CONVROT_EUNSUPPORTED;
+    if (M == 0) return CONVROT_OK;
+    if (!q || !s) return CONVROT_EINVAL;
+    if (!aligned16(q) || !aligned16(s)) return CONVROT_EALIGN;
+    const size_t nq = codes_bytes(M, K), ns = (size_t)M * 4u;
+    if (!apart_from_norm(a, q, nq) || !apart_from_norm(a, s, ns) || overlaps(q, nq, s, ns))
+        return CONVROT_EINVAL;
+    a.q = reinterpret_cast<uint8_t *>(q);
+    a.s = s;
+    a.block = block;
+    a.regular = flags != 0;
+    a.inv_sqrt_b = inv_sqrt_block(block);
+    return hip_status(convrot::launch_add_norm(convrot::NormOut::ROTATED_I8, a,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+int convrot_add_rms_norm_fp8_quantize(const void *x, int x_dtype, const void *residual,
+                                      int res_dtype, const float *w, float eps, int64_t M,
+                                      int64_t K, int scales, void *residual_out, uint8_t *q,
+                                      float *s, void *stream)
+{
+    convrot::AddNorm a;
+    int rc = add_norm_args(x, x_dtype, residual, res_dtype, w, eps, M, K, residual_out, &a);
+    if (rc != CONVROT_OK) return rc;
+    if (!valid_fp8_scales(scales) || K % 128 != 0) return CONVROT_EINVAL;
+    if (check_rows(M, K) != CONVROT_OK) return CONVROT_EUNSUPPORTED;
+    if (M == 0) return CONVROT_OK;
+    if (!q || !s) return CONVROT_EINVAL;
+    if (!aligned16(q) || !aligned16(s)) return CONVROT_EALIGN;
+    const size_t nq = codes_bytes(M, K), ns = fp8_row_scales_bytes(M, K);
+    if (!apart_from_norm(a, q, nq) || !apart_from_norm(a, s, ns) || overlaps(q, nq, s, ns))
+        return CONVROT_EINVAL;
+    a.q = q;
+    a.s = s;
+    a.pow2 = scales == CONVROT_FP8_SCALE_POW2;
+    return hip_status(convrot::launch_add_norm(convrot::NormOut::FP8, a,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+size_t convrot_fp8_norm_linear_workspace_bytes(int64_t M, int64_t K, int64_t N)
+{
+    if (check_linear_shape(N, K, 128) != CONVROT_OK || check_rows(M, K) != CONVROT_OK) return 0;
+    return codes_bytes(M, K) + fp8_row_scales_bytes(M, K);
+}
+
+// What both paths check before anything is launched (W was checked).
+static int norm_linear_check(const convrot::AddNorm &a, int64_t N, const float *bias,
+                             const void *Y, int y_dtype, const void *ws, size_t ws_bytes,
+                             size_t need)
+{
+    int rc = check_rows(a.M, a.K);
+    if (rc != CONVROT_OK) return rc;
+    if ((rc = check_out_dtype(y_dtype)) != CONVROT_OK) return rc;
+    if (a.M == 0) return CONVROT_OK;
+    if (!Y) return CONVROT_EINVAL;
+    if (!aligned16(Y) || !aligned16(bias) || !aligned16(ws)) return CONVROT_EALIGN;
+    if (!ws || ws_bytes < need) return CONVROT_EWORKSPACE;
+    const size_t ny = (size_t)a.M * (size_t)N * dtype_bytes(y_dtype);
+    return overlaps(Y, ny, a.h, (size_t)a.M * (size_t)a.K * (a.r_f32 ? 4u : 2u))
+               ? CONVROT_EINVAL : CONVROT_OK;
+}
+
+static int norm_linear_impl(const void *x, int x_dtype, const void *residual, int res_dtype,
+                            const float *w, float eps, int64_t M, const convrot_weights *W,
+                            const float *bias, void *residual_out, void *Y, int y_dtype, void *ws,
+                            size_t ws_bytes, void *stream)
+{
+    int rc = check_weights(W);
+    if (rc != CONVROT_OK) return rc;
+    convrot::AddNorm a;
+    rc = add_norm_args(x, x_dtype, residual, res_dtype, w, eps, M, W->K, residual_out, &a);
+    if (rc == CONVROT_OK)
+        rc = norm_linear_check(a, W->N, bias, Y, y_dtype, ws, ws_bytes,
+                               convrot_linear_workspace_bytes(M, W->K, W->N, W->block));
+    if (rc != CONVROT_OK || M == 0) return rc;
+    Carve c(ws);
+    a.q = static_cast<uint8_t *>(c.take(codes_bytes(M, W->K)));
+    a.s = static_cast<float *>(c.take((size_t)M * 4u));
+    a.block = W->block;
+    a.regular = is_regular(W);
+    a.inv_sqrt_b = inv_sqrt_block(W->block);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipError_t e = convrot::launch_add_norm(convrot::NormOut::ROTATED_I8, a, st);
+    if (e == hipSuccess)
+        e = convrot::launch_gemm_i8(reinterpret_cast<const int8_t *>(a.q), W->codes, a.s, W->scale,
+                                    bias, Y, out_kind(y_dtype), M, W->N, W->K, st);
+    return hip_status(e);
+}
+
+int convrot_norm_linear_forward(const void *x, int x_dtype, const void *residual, int res_dtype,
+                                const float *w, float eps, int64_t M, const convrot_weights *W,
+                                const float *bias, void *residual_out, void *Y, int y_dtype,
+                                void *ws, size_t ws_bytes, void *stream)
+{
+    const int rc = norm_linear_impl(x, x_dtype, residual, res_dtype, w, eps, M, W, bias,
+                                    residual_out, Y, y_dtype, ws, ws_bytes, stream);
+    log_call("convrot_norm_linear_forward", M, W ? W->N : 0, W ? W->K : 0, rc);
+    return rc;
+}
+
+static int fp8_norm_linear_impl(const void *x, int x_dtype, const void *residual, int res_dtype,
+                                const float *w, float eps, int64_t M,
+                                const convrot_fp8_weights *W, const float *bias,
+                                void *residual_out, void *Y, int y_dtype, void *ws,
+                                size_t ws_bytes, void *stream)
+{
+    int rc = check_fp8_weights(W);
+    if (rc != CONVROT_OK) return rc;
+    convrot::AddNorm a;
+    rc = add_norm_args(x, x_dtype, residual, res_dtype, w, eps, M, W->K, residual_out, &a);
+    if (rc == CONVROT_OK)
+        rc = norm_linear_check(a, W->N, bias, Y, y_dtype, ws, ws_bytes,
+                               convrot_fp8_norm_linear_workspace_bytes(M, W->K, W->N));
+    if (rc != CONVROT_OK || M == 0) return rc;
+    Carve c(ws);
+    a.q = static_cast<uint8_t *>(c.take(codes_bytes(M, W->K)));
+    a.s = static_cast<float *>(c.take(fp8_row_scales_bytes(M, W->K)));
+    a.pow2 = W->scales == CONVROT_FP8_SCALE_POW2;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipError_t e = convrot::launch_add_norm(convrot::NormOut::FP8, a, st);
+    if (e == hipSuccess) {
+        const convrot::Fp8Gemm g = {nullptr, a.q, a.s, W->codes, W->scale, bias, Y, M, W->N, W->K,
+                                    a.pow2, y_dtype == CONVROT_F32};
+        e = convrot::launch_fp8_gemm(g, st);
+    }
+    return hip_status(e);
+}
+
+int convrot_fp8_norm_linear_forward(const void *x, int x_dtype, const void *residual,
+                                    int res_dtype, const float *w, float eps, int64_t M,
+                                    const convrot_fp8_weights *W, const float *bias,
+                                    void *residual_out, void *Y, int y_dtype, void *ws,
+                                    size_t ws_bytes, void *stream)
+{
+    const int rc = fp8_norm_linear_impl(x, x_dtype, residual, res_dtype, w, eps, M, W, bias,
+                                        residual_out, Y, y_dtype, ws, ws_bytes, stream);
+    log_call("convrot_fp8_norm_linear_forward", M, W ? W->N : 0, W ? W->K : 0, rc);
+    return rc;
+}
+
+size_t convrot_add_rms_norm_workspace_bytes(int64_t M, int64_t K)
+{
+    if (check_norm_shape(M, K, 1.0f) != CONVROT_OK) return 0;
+    return round_up((size_t)convrot::add_norm_partial_rows(M, K) * (size_t)K * 4u, kAlign);
+}
+
+int convrot_add_rms_norm_backward(const void *g, int g_dtype, const void *h, int h_dtype,
+                                  const void *g_h, const float *w, float eps, int64_t M, int64_t K,
+                                  void *dh, void *dx, float *dw, void *ws, size_t ws_bytes,
+                                  void *stream)
+{
+    const int rc = check_norm_shape(M, K, eps);
+    if (rc != CONVROT_OK) return rc;
+    if (!is_float_dtype(g_dtype) || !is_float_dtype(h_dtype)) return CONVROT_EUNSUPPORTED;
+    if (dx && h_dtype != CONVROT_F32) return CONVROT_EINVAL;
+    if (M == 0 && !dw) return CONVROT_OK;
+    if (M > 0 && (!g || !h || !dh)) return CONVROT_EINVAL;
+    const void *const all[] = {g, h, g_h, w, dh, dx, dw, ws};
+    for (const void *p : all)
+        if (!aligned16(p)) return CONVROT_EALIGN;
+    const size_t n = (size_t)M * (size_t)K, ng = n * dtype_bytes(g_dtype),
+                 nh = n * dtype_bytes(h_dtype), nk = (size_t)K * 4u;
+    const struct { const void *p; size_t n; } in[] = {{g, ng}, {h, nh}, {g_h, nh}};
+    for (const auto &i : in)
+        if (!in_place_or_apart(dh, nh, i.p, i.n) || !in_place_or_apart(dx, 2 * n, i.p, i.n) ||
+            overlaps(dw, nk, i.p, i.n))
+            return CONVROT_EINVAL;
+    if (overlaps(dh, nh, dx, 2 * n) || overlaps(dh, nh, dw, nk) || overlaps(dx, 2 * n, dw, nk) ||
+        overlaps(w, nk, dh, nh) || overlaps(w, nk, dx, 2 * n) || overlaps(w, nk, dw, nk))
+        return CONVROT_EINVAL;
+    const size_t need = dw ? convrot_add_rms_norm_workspace_bytes(M, K) : 0;
+    if (need > 0 && (!ws || ws_bytes < need)) return CONVROT_EWORKSPACE;
+    const convrot::AddNormGrad a = {g, h, g_h, w, dh, dx, dw, static_cast<float *>(ws), M, (int)K,
+                                    eps, g_dtype == CONVROT_F32, h_dtype == CONVROT_F32};
+    return hip_status(convrot::launch_add_norm_grad(a, static_cast<hipStream_t>(stream)));
 }
 
 static int lowrank_forward_impl(const void *X, int64_t M, const convrot_weights *A,
