@@ -2,7 +2,8 @@
  * convrot.h -- C ABI of libconvrot.so: the ConvRot W8A8 INT8 linear layer on
  * AMD Instinct MI355X (gfx950), and beside it (in sections of their own below)
  * the FP8 block-scaled linear, rotary positions, the norms of queries and keys,
- * and the residual's addition with the RMS norm in front of a projection.
+ * the residual's addition with the RMS norm in front of a projection, and a
+ * mixture-of-experts layer for a few tokens.
  *
  * The method (what the INT8 entry points compute):
  *   - Linear layers of the INT8 package are W8A8: INT8 activations times INT8
@@ -699,6 +700,83 @@ CONVROT_API int convrot_add_rms_norm_backward(const void *g, int g_dtype, const 
                                               int h_dtype, const void *g_h, const float *w,
                                               float eps, int64_t M, int64_t K, void *dh, void *dx,
                                               float *dw, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------ */
+/* a mixture-of-experts layer for a few tokens                         */
+/* ------------------------------------------------------------------ */
+
+/* For every token x of X [T, K] (bf16):
+ *   logits = x router^T, summed in fp64; the top_k experts of the largest logits, or
+ *   with a bias of the largest score + bias, ties to the lowest index (a NaN counts as
+ *   -infinity, -0 as 0); scores: softmax over the routed experts, or sigmoid, in fp64;
+ *   weights: the chosen scores, with CONVROT_MOE_RENORMALIZE divided by their sum (a sum
+ *   of 0 leaves them 0), times `scale`, rounded once to F32;
+ *   g_e = silu(G_e x) * (U_e x);  y = sum over the chosen e of weight_e D_e g_e, plus
+ *   D_e g_e of every shared expert.
+ * [G_e; U_e] [2F, K] and D_e [K, F] are e4m3 codes with an F32 scale per 128 x 128 block,
+ * as in the FP8 linear; activations are not quantised.  Sums are fp32; BF16 outputs round
+ * g to bf16, F32 outputs carry it in fp32.  Experts that no token chose are not read.
+ * The choice and the weights of a token do not depend on the other tokens; its output
+ * can differ in the last bits of the fp32 sums between batches.  Calls of the same
+ * arguments repeat bit for bit.  A token with a NaN or an infinity has NaN outputs and
+ * leaves the others alone.
+ * Any T: the experts' codes are read once for every 64 tokens, which suits few tokens. */
+#define CONVROT_MOE_MAGIC 0x454f4d43u /* "CMOE" little-endian */
+#define CONVROT_MOE_VERSION 1u
+#define CONVROT_MOE_MAX_EXPERTS 512
+#define CONVROT_MOE_MAX_SHARED 16
+#define CONVROT_MOE_MAX_TOP_K 32
+
+/* The prepared experts: a host struct holding caller-owned device pointers. */
+typedef struct convrot_moe_weights {
+    uint32_t magic;            /* CONVROT_MOE_MAGIC once prepared */
+    uint32_t version;          /* CONVROT_MOE_VERSION */
+    int32_t experts;           /* routed experts E, 1 .. CONVROT_MOE_MAX_EXPERTS */
+    int32_t shared;            /* experts S behind them that serve every token, 0 .. 16 */
+    int64_t K;                 /* channels: a multiple of 128, at most 65536 */
+    int64_t F;                 /* an expert's width: the same */
+    uint8_t *gate_up;          /* device, E + S times the K-tiled codes of [2F, K] */
+    float *gate_up_scale;      /* device, [E + S, 2F / 128, K / 128] */
+    uint8_t *down;             /* device, E + S times the K-tiled codes of [K, F] */
+    float *down_scale;         /* device, [E + S, K / 128, F / 128] */
+} convrot_moe_weights;
+
+/* Bytes of the codes and scales of n experts (n = E + S) of [2F, K] or [K, F]: rows R and
+ * inputs C of one.  0 for invalid shapes (2F * K < 2^31 and n <= 528 among them). */
+CONVROT_API size_t convrot_moe_packed_bytes(int64_t n, int64_t R, int64_t C);
+CONVROT_API size_t convrot_moe_scale_bytes(int64_t n, int64_t R, int64_t C);
+
+/* Prepare the experts: W_gate_up [E + S, 2F, K] (an expert's gate rows first) and W_down
+ * [E + S, K, F], device, dense, output-major: F32 or BF16 (quantised here as by
+ * convrot_fp8_prepare_weights, with its kind of scales), or CONVROT_F8E4M3 codes with both
+ * src_scales (imported unchanged; `scales` is not looked at).  out: experts, shared, K, F
+ * and the four pointers are set by the caller; magic and version are filled in. */
+CONVROT_API int convrot_moe_prepare_weights(const void *W_gate_up, const void *W_down, int w_dtype,
+                                            const float *src_scale_gate_up,
+                                            const float *src_scale_down, int scales,
+                                            convrot_moe_weights *out, void *stream);
+
+#define CONVROT_MOE_SCORE_SOFTMAX 0
+#define CONVROT_MOE_SCORE_SIGMOID 1
+#define CONVROT_MOE_RENORMALIZE 1u
+
+/* Workspace of the forward. */
+CONVROT_API size_t convrot_moe_workspace_bytes(int64_t T, const convrot_moe_weights *W, int top_k);
+
+/* Y [T, K] of the layer above.
+ *   X            device bf16 [T, K].
+ *   router       device [E, K], router_dtype CONVROT_BF16 or _F32; router_bias F32 [E] or
+ *                NULL (it acts on the choice alone).
+ *   score        CONVROT_MOE_SCORE_*; flags 0 or CONVROT_MOE_RENORMALIZE; scale finite.
+ *   Y            y_dtype CONVROT_BF16 or _F32.
+ *   ids, weights device [T, top_k] int32 and F32: the choices, the first the largest, and
+ *                their weights (outputs).  1 <= top_k <= min(E, CONVROT_MOE_MAX_TOP_K).
+ * Outputs overlap neither inputs nor each other (EINVAL). */
+CONVROT_API int convrot_moe_forward(const void *X, int64_t T, const void *router, int router_dtype,
+                                    const float *router_bias, const convrot_moe_weights *W,
+                                    int top_k, int score, uint32_t flags, float scale, void *Y,
+                                    int y_dtype, int32_t *ids, float *weights, void *ws,
+                                    size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------ */
 /* comparison variant (not the W8A8 path)                              */

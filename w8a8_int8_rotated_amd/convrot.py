@@ -39,6 +39,9 @@ ROPE_PAIRINGS = {"interleaved": 0, "half": 1}
 ROPE_SPECTRA = {"axis": 0, "whole": 1}
 ROPE_MAX_AXES = 4
 ROPE_INVERSE = 1
+MOE_MAGIC, MOE_VERSION = 0x454F4D43, 1
+MOE_SCORES = {"softmax": 0, "sigmoid": 1}
+MOE_RENORMALIZE = 1
 
 _c_i64 = ctypes.c_int64
 _c_int = ctypes.c_int
@@ -99,6 +102,22 @@ class convrot_heads(ctypes.Structure):
     ]
 
 
+class convrot_moe_weights(ctypes.Structure):
+    _fields_ = [
+        ("magic", ctypes.c_uint32),
+        ("version", ctypes.c_uint32),
+        ("experts", ctypes.c_int32),
+        ("shared", ctypes.c_int32),
+        ("K", ctypes.c_int64),
+        ("F", ctypes.c_int64),
+        ("gate_up", ctypes.c_void_p),
+        ("gate_up_scale", ctypes.c_void_p),
+        ("down", ctypes.c_void_p),
+        ("down_scale", ctypes.c_void_p),
+    ]
+
+
+_MW = ctypes.POINTER(convrot_moe_weights)
 _FW = ctypes.POINTER(convrot_fp8_weights)
 _RP = ctypes.POINTER(convrot_rope)
 _H = ctypes.c_void_p         # const convrot_heads * (byref, or packed bytes)
@@ -198,6 +217,14 @@ _SIGNATURES = {
     "convrot_add_rms_norm_backward": (
         _c_int, [_c_p, _c_int, _c_p, _c_int, _c_p, _c_p, ctypes.c_float, _c_i64, _c_i64, _c_p,
                  _c_p, _c_p, _c_p, _c_sz, _c_p]),
+    "convrot_moe_packed_bytes": (_c_sz, [_c_i64, _c_i64, _c_i64]),
+    "convrot_moe_scale_bytes": (_c_sz, [_c_i64, _c_i64, _c_i64]),
+    "convrot_moe_prepare_weights": (
+        _c_int, [_c_p, _c_p, _c_int, _c_p, _c_p, _c_int, _MW, _c_p]),
+    "convrot_moe_workspace_bytes": (_c_sz, [_c_i64, _MW, _c_int]),
+    "convrot_moe_forward": (
+        _c_int, [_c_p, _c_i64, _c_p, _c_int, _c_p, _MW, _c_int, _c_int, ctypes.c_uint32,
+                 ctypes.c_float, _c_p, _c_int, _c_p, _c_p, _c_p, _c_sz, _c_p]),
     "convrot_probe_mfma_i8": (_c_int, [_c_i64, _c_p, _c_p, ctypes.POINTER(ctypes.c_int64),
                                        _c_p]),
     "convrot_probe_stream": (_c_int, [_c_p, _c_p, _c_i64, _c_int, _c_p]),
@@ -273,7 +300,7 @@ def _tensors(v):
     elif isinstance(v, tuple):
         for x in v:
             yield from _tensors(x)
-    elif isinstance(v, (PreparedWeights, FP8Weights, RopePlan)):
+    elif isinstance(v, (PreparedWeights, FP8Weights, RopePlan, MoEWeights)):
         yield from (t for t in vars(v).values() if isinstance(t, torch.Tensor))
 
 
@@ -1344,6 +1371,134 @@ def convrot_add_rms_norm_backward(g: torch.Tensor, h: torch.Tensor, w, g_h=None,
             _dtype_tag(h.dtype), _ptr(g_h), _ptr(w), eps, M, K, _ptr(dh), _ptr(dx), _ptr(dw),
             _ptr(ws), ws.numel() if ws is not None else 0)
     return dh, dx if copy else dh, dw
+
+
+# ------------------------------------- mixture of experts for a few tokens ----
+
+class MoEWeights:
+    """The prepared experts of a layer: the C descriptor plus the tensors it points into."""
+
+    def __init__(self, desc: convrot_moe_weights, gate_up, gate_up_scale, down, down_scale):
+        self.desc = desc
+        self.gate_up, self.gate_up_scale = gate_up, gate_up_scale
+        self.down, self.down_scale = down, down_scale
+        self._ref = ctypes.byref(desc)
+
+    @property
+    def experts(self):
+        return self.desc.experts
+
+    @property
+    def shared(self):
+        return self.desc.shared
+
+    @property
+    def K(self):
+        return self.desc.K
+
+    @property
+    def F(self):
+        return self.desc.F
+
+    def ref(self):
+        return self._ref
+
+
+def convrot_moe_prepare_weights(W_gate_up: torch.Tensor, W_down: torch.Tensor, shared: int = 0,
+                                src_scale_gate_up=None, src_scale_down=None,
+                                scales: str = "f32", stream=None) -> MoEWeights:
+    """Pack the experts W_gate_up [E + S, 2F, K] (gate rows first) and W_down [E + S, K, F],
+    the last S = shared of which serve every token: float32 or bfloat16, quantised to e4m3
+    with a scale per 128 x 128 block, or float8_e4m3fn codes with their scales
+    [E + S, 2F/128, K/128] and [E + S, K/128, F/128]."""
+    if stream is not None:
+        return _on_stream(convrot_moe_prepare_weights, locals())
+    lib = library()
+    for t, n in ((W_gate_up, "W_gate_up"), (W_down, "W_down")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise ValueError(f"{n} must be a 3-D tensor")
+    n, K, F = W_down.shape
+    dt = W_down.dtype
+    if dt not in (torch.float32, torch.bfloat16, torch.float8_e4m3fn):
+        raise ValueError(f"weights must be float32, bfloat16 or float8_e4m3fn codes, got {dt}")
+    if W_gate_up.dtype != dt or tuple(W_gate_up.shape) != (n, 2 * F, K):
+        raise ValueError(f"W_gate_up must be {dt} of shape {(n, 2 * F, K)}, got "
+                         f"{W_gate_up.dtype} {tuple(W_gate_up.shape)}")
+    if not 0 <= shared < max(n, 1):
+        raise ValueError(f"shared must be from 0 to {max(n, 1) - 1}, got {shared}")
+    if scales not in FP8_SCALES:
+        raise ValueError(f"scales must be one of {sorted(FP8_SCALES)}")
+    for t, rc, name in ((src_scale_gate_up, (2 * F, K), "src_scale_gate_up"),
+                        (src_scale_down, (K, F), "src_scale_down")):
+        if (dt == torch.float8_e4m3fn) != (t is not None):
+            raise ValueError(f"{name} is required for float8_e4m3fn codes and only for them")
+        _opt(t, name, torch.float32, (n, rc[0] // 128, rc[1] // 128))
+    gub, db = lib.convrot_moe_packed_bytes(n, 2 * F, K), lib.convrot_moe_packed_bytes(n, K, F)
+    if gub == 0 or db == 0:
+        raise ConvRotError("convrot_moe_prepare_weights", EUNSUPPORTED)
+    dev = W_down.device
+    _on_device(None, W_down=W_down)
+    _on_device(dev, W_gate_up=W_gate_up, src_scale_gate_up=src_scale_gate_up,
+               src_scale_down=src_scale_down)
+    W_gate_up, W_down = W_gate_up.contiguous(), W_down.contiguous()
+    gate_up = torch.empty(gub, dtype=torch.uint8, device=dev)
+    down = torch.empty(db, dtype=torch.uint8, device=dev)
+    gus = torch.empty((n, 2 * F // 128, K // 128), dtype=torch.float32, device=dev)
+    ds = torch.empty((n, K // 128, F // 128), dtype=torch.float32, device=dev)
+    desc = convrot_moe_weights()
+    desc.experts, desc.shared, desc.K, desc.F = n - shared, shared, K, F
+    desc.gate_up, desc.gate_up_scale = gate_up.data_ptr(), gus.data_ptr()
+    desc.down, desc.down_scale = down.data_ptr(), ds.data_ptr()
+    _launch(dev, "convrot_moe_prepare_weights", _ptr(W_gate_up), _ptr(W_down), _dtype_tag(dt),
+            _ptr(src_scale_gate_up), _ptr(src_scale_down), FP8_SCALES[scales],
+            ctypes.byref(desc))
+    return MoEWeights(desc, gate_up, gus, down, ds)
+
+
+def convrot_moe_workspace_bytes(T: int, W: MoEWeights, top_k: int) -> int:
+    return library().convrot_moe_workspace_bytes(T, W.ref(), top_k)
+
+
+def convrot_moe_forward(X: torch.Tensor, router: torch.Tensor, W: MoEWeights, top_k: int,
+                        router_bias=None, score: str = "softmax", renormalize: bool = True,
+                        scale: float = 1.0, out_dtype: torch.dtype = torch.bfloat16, out=None,
+                        ids=None, weights=None, workspace=None, stream=None):
+    """(Y, ids, weights): the layer's output [T, K] for the bf16 tokens X [T, K], the experts
+    each token chose [T, top_k] (int32, the largest first) and their weights (float32).
+    router [E, K] bf16 or float32; router_bias float32 [E] acts on the choice alone.  Experts
+    that no token chose are not read; beyond 64 tokens they are read once for every 64."""
+    if stream is not None:
+        return _on_stream(convrot_moe_forward, locals())
+    if not isinstance(W, MoEWeights):
+        raise ValueError("W must be MoEWeights from convrot_moe_prepare_weights")
+    E, K = W.experts, W.K
+    T = _rows(X, "X", K)
+    _need(router, "router", _FLOATS, (E, K))
+    _opt(router_bias, "router_bias", torch.float32, (E,))
+    if score not in MOE_SCORES:
+        raise ValueError(f"score must be one of {sorted(MOE_SCORES)}")
+    if not 1 <= top_k <= E:
+        raise ValueError(f"top_k must be from 1 to {E}, got {top_k}")
+    _opt(out, "out", _FLOATS, (T, K))
+    _opt(ids, "ids", torch.int32, (T, top_k))
+    _opt(weights, "weights", torch.float32, (T, top_k))
+    wsb = convrot_moe_workspace_bytes(T, W, top_k)
+    _check_workspace(wsb, workspace)
+    dev = W.down.device
+    _on_device(dev, X=X, router=router, router_bias=router_bias, out=out, ids=ids,
+               weights=weights, workspace=workspace)
+    if out is None:
+        out = torch.empty((T, K), dtype=out_dtype, device=dev)
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    ws = _workspace(wsb, dev, workspace)
+    _launch(dev, "convrot_moe_forward", _ptr(X), T, _ptr(router), _dtype_tag(router.dtype),
+            _ptr(router_bias), W.ref(), top_k, MOE_SCORES[score],
+            MOE_RENORMALIZE if renormalize else 0, scale, _ptr(out), _dtype_tag(out.dtype),
+            _ptr(ids), _ptr(weights), _ptr(ws), ws.numel() if ws is not None else 0)
+    return out, ids, weights
 
 
 # ------------------------------------------------------------- hooks ----

@@ -4,6 +4,7 @@
 #include "convrot.h"
 #include "add_norm.hpp"
 #include "common.hpp"
+#include "moe.hpp"
 
 #include <atomic>
 #include <cmath>
@@ -1415,6 +1416,182 @@ int convrot_add_rms_norm_backward(const void *g, int g_dtype, const void *h, int
     const convrot::AddNormGrad a = {g, h, g_h, w, dh, dx, dw, static_cast<float *>(ws), M, (int)K,
                                     eps, g_dtype == CONVROT_F32, h_dtype == CONVROT_F32};
     return hip_status(convrot::launch_add_norm_grad(a, static_cast<hipStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// The mixture-of-experts layer.
+// ---------------------------------------------------------------------------
+
+static bool moe_shape(int64_t n, int64_t R, int64_t C)
+{
+    return n >= 1 && n <= CONVROT_MOE_MAX_EXPERTS + CONVROT_MOE_MAX_SHARED && R > 0 && C > 0 &&
+           R <= 2 * kMaxK && C <= kMaxK && R % 128 == 0 && C % 128 == 0 && R * C < kI32Bound;
+}
+
+size_t convrot_moe_packed_bytes(int64_t n, int64_t R, int64_t C)
+{
+    return moe_shape(n, R, C) ? (size_t)n * (size_t)R * (size_t)C : 0;
+}
+
+size_t convrot_moe_scale_bytes(int64_t n, int64_t R, int64_t C)
+{
+    return moe_shape(n, R, C) ? (size_t)n * (size_t)(R / 128) * (size_t)(C / 128) * 4u : 0;
+}
+
+// The caller's part of a descriptor.
+static int check_moe_shape(const convrot_moe_weights *W)
+{
+    if (W->experts < 1 || W->shared < 0 || W->K <= 0 || W->F <= 0) return CONVROT_EINVAL;
+    if (W->experts > CONVROT_MOE_MAX_EXPERTS || W->shared > CONVROT_MOE_MAX_SHARED ||
+        W->K > kMaxK || W->F > kMaxK || W->K % 128 != 0 || W->F % 128 != 0 ||
+        2 * W->F * W->K >= kI32Bound)
+        return CONVROT_EUNSUPPORTED;
+    if (!W->gate_up || !W->gate_up_scale || !W->down || !W->down_scale) return CONVROT_EINVAL;
+    return aligned16(W->gate_up) && aligned16(W->gate_up_scale) && aligned16(W->down) &&
+                   aligned16(W->down_scale) ? CONVROT_OK : CONVROT_EALIGN;
+}
+
+static int check_moe_weights(const convrot_moe_weights *W)
+{
+    if (!W) return CONVROT_EINVAL;
+    if (W->magic != CONVROT_MOE_MAGIC || W->version != CONVROT_MOE_VERSION) return CONVROT_ELAYOUT;
+    return check_moe_shape(W);
+}
+
+// n experts' [R, C] weights, one after another.
+static hipError_t moe_pack(const void *W, int w_dtype, const float *src_scale, bool pow2, int64_t n,
+                           int64_t R, int64_t C, uint8_t *codes, float *scale, hipStream_t s)
+{
+    const int64_t each = R * C, sc = (R / 128) * (C / 128);
+    hipError_t e = hipSuccess;
+    for (int64_t i = 0; i < n && e == hipSuccess; ++i) {
+        if (w_dtype == CONVROT_F8E4M3)
+            e = convrot::launch_tile_codes(static_cast<const int8_t *>(W) + i * each, false,
+                                           reinterpret_cast<int8_t *>(codes + i * each), R, C, s);
+        else
+            e = convrot::launch_fp8_block_weights(
+                static_cast<const char *>(W) + i * each * (int64_t)dtype_bytes(w_dtype),
+                w_dtype == CONVROT_F32 ? convrot::InType::F32 : convrot::InType::BF16, R, C, pow2,
+                codes + i * each, scale + i * sc, s);
+    }
+    if (e == hipSuccess && w_dtype == CONVROT_F8E4M3)
+        e = hipMemcpyAsync(scale, src_scale, (size_t)(n * sc) * 4u, hipMemcpyDeviceToDevice, s);
+    return e;
+}
+
+int convrot_moe_prepare_weights(const void *W_gate_up, const void *W_down, int w_dtype,
+                                const float *src_scale_gate_up, const float *src_scale_down,
+                                int scales, convrot_moe_weights *out, void *stream)
+{
+    if (!W_gate_up || !W_down || !out) return CONVROT_EINVAL;
+    int rc = check_moe_shape(out);
+    if (rc != CONVROT_OK) return rc;
+    if (w_dtype != CONVROT_F32 && w_dtype != CONVROT_BF16 && w_dtype != CONVROT_F8E4M3)
+        return CONVROT_EUNSUPPORTED;
+    const bool import = w_dtype == CONVROT_F8E4M3;
+    if (import != (src_scale_gate_up != nullptr) || import != (src_scale_down != nullptr) ||
+        (!import && !valid_fp8_scales(scales)))
+        return CONVROT_EINVAL;
+    if (!aligned16(W_gate_up) || !aligned16(W_down) || !aligned16(src_scale_gate_up) ||
+        !aligned16(src_scale_down))
+        return CONVROT_EALIGN;
+    const int64_t n = (int64_t)out->experts + out->shared;
+    const bool pow2 = scales == CONVROT_FP8_SCALE_POW2;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    hipError_t e = moe_pack(W_gate_up, w_dtype, src_scale_gate_up, pow2, n, 2 * out->F, out->K,
+                            out->gate_up, out->gate_up_scale, s);
+    if (e == hipSuccess)
+        e = moe_pack(W_down, w_dtype, src_scale_down, pow2, n, out->K, out->F, out->down,
+                     out->down_scale, s);
+    rc = hip_status(e);
+    if (rc != CONVROT_OK) return rc;
+    out->magic = CONVROT_MOE_MAGIC;
+    out->version = CONVROT_MOE_VERSION;
+    return CONVROT_OK;
+}
+
+static bool valid_top_k(const convrot_moe_weights *W, int top_k)
+{
+    return top_k >= 1 && top_k <= W->experts && top_k <= CONVROT_MOE_MAX_TOP_K;
+}
+
+size_t convrot_moe_workspace_bytes(int64_t T, const convrot_moe_weights *W, int top_k)
+{
+    if (T <= 0 || check_moe_weights(W) != CONVROT_OK || !valid_top_k(W, top_k)) return 0;
+    return convrot::moe_workspace_bytes((int)(T < convrot::kMoeTokens ? T : convrot::kMoeTokens),
+                                        W->experts, W->shared, top_k, (int)W->K, (int)W->F);
+}
+
+static int moe_forward_impl(const void *X, int64_t T, const void *router, int router_dtype,
+                            const float *router_bias, const convrot_moe_weights *W, int top_k,
+                            int score, uint32_t flags, float scale, void *Y, int y_dtype,
+                            int32_t *ids, float *weights, void *ws, size_t ws_bytes, void *stream)
+{
+    int rc = check_moe_weights(W);
+    if (rc != CONVROT_OK) return rc;
+    if (T < 0) return CONVROT_EINVAL;
+    if (T >= kI32Bound || !is_float_dtype(router_dtype) || !is_float_dtype(y_dtype) ||
+        (flags & ~CONVROT_MOE_RENORMALIZE) != 0)
+        return CONVROT_EUNSUPPORTED;
+    if (!valid_top_k(W, top_k) || !std::isfinite(scale) ||
+        (score != CONVROT_MOE_SCORE_SOFTMAX && score != CONVROT_MOE_SCORE_SIGMOID))
+        return CONVROT_EINVAL;
+    if (T == 0) return CONVROT_OK;
+    if (!X || !router || !Y || !ids || !weights) return CONVROT_EINVAL;
+    const void *const all[] = {X, router, router_bias, Y, ids, weights, ws};
+    for (const void *p : all)
+        if (!aligned16(p)) return CONVROT_EALIGN;
+    const size_t n = (size_t)T * (size_t)W->K, nk = (size_t)T * (size_t)top_k * 4u;
+    const struct { const void *p; size_t n; } in[] = {
+        {X, n * 2u}, {router, (size_t)W->experts * (size_t)W->K * dtype_bytes(router_dtype)},
+        {router_bias, (size_t)W->experts * 4u}},
+        out[] = {{Y, n * dtype_bytes(y_dtype)}, {ids, nk}, {weights, nk}};
+    for (int i = 0; i < 3; ++i)
+        for (int j = 0; j < 3; ++j)
+            if (overlaps(out[i].p, out[i].n, in[j].p, in[j].n) ||
+                (j < i && overlaps(out[i].p, out[i].n, out[j].p, out[j].n)))
+                return CONVROT_EINVAL;
+    if (!ws || ws_bytes < convrot_moe_workspace_bytes(T, W, top_k)) return CONVROT_EWORKSPACE;
+
+    convrot::Moe m = {};
+    m.router = router;
+    m.bias = router_bias;
+    m.gate_up = W->gate_up;
+    m.down = W->down;
+    m.gate_up_scale = W->gate_up_scale;
+    m.down_scale = W->down_scale;
+    m.E = W->experts;
+    m.S = W->shared;
+    m.top_k = top_k;
+    m.K = (int)W->K;
+    m.F = (int)W->F;
+    m.router_f32 = router_dtype == CONVROT_F32;
+    m.sigmoid = score == CONVROT_MOE_SCORE_SIGMOID;
+    m.renormalize = (flags & CONVROT_MOE_RENORMALIZE) != 0;
+    m.y_f32 = y_dtype == CONVROT_F32;
+    m.factor = (double)scale;
+    m.ws = ws;
+    hipError_t e = hipSuccess;
+    for (int64_t t = 0; t < T && e == hipSuccess; t += convrot::kMoeTokens) {
+        m.T = (int)(T - t < convrot::kMoeTokens ? T - t : convrot::kMoeTokens);
+        m.x = static_cast<const uint16_t *>(X) + t * W->K;
+        m.y = static_cast<char *>(Y) + t * W->K * (int64_t)dtype_bytes(y_dtype);
+        m.ids = ids + t * top_k;
+        m.weights = weights + t * top_k;
+        e = convrot::launch_moe(m, static_cast<hipStream_t>(stream));
+    }
+    return hip_status(e);
+}
+
+int convrot_moe_forward(const void *X, int64_t T, const void *router, int router_dtype,
+                        const float *router_bias, const convrot_moe_weights *W, int top_k,
+                        int score, uint32_t flags, float scale, void *Y, int y_dtype, int32_t *ids,
+                        float *weights, void *ws, size_t ws_bytes, void *stream)
+{
+    const int rc = moe_forward_impl(X, T, router, router_dtype, router_bias, W, top_k, score,
+                                    flags, scale, Y, y_dtype, ids, weights, ws, ws_bytes, stream);
+    log_call("convrot_moe_forward", T, W ? W->F : 0, W ? W->K : 0, rc);
+    return rc;
 }
 
 static int lowrank_forward_impl(const void *X, int64_t M, const convrot_weights *A,
