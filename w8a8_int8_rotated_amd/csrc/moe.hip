@@ -13,12 +13,17 @@
 //
 // Precision.  The logits are summed in fp64 (v_mfma_f64_16x16x4_f64): the choice of
 // experts then does not depend on the order of the sums, a batch or a shape.  g is
-// carried as two bf16 parts for bf16 outputs and as three, which hold an fp32 value
-// exactly, for F32 outputs.
+// rounded to bf16 for bf16 outputs, whose own rounding is as large (together 2.4e-3 of the
+// outputs' rms, 1.7e-3 with g exact); for F32 outputs it is carried as three bf16 parts,
+// which hold an fp32 value exactly.
 //
-// Kernels: router (partial logits over pieces of K), select (one workgroup: choices,
-// and for each chosen expert, a "unit", its tokens), gate_up, down.  For one token
-// every wave of gate_up makes the choice itself.
+// Loads.  A wave keeps a ring of D blocks of codes with their columns in registers: the
+// next block is requested as soon as one is used.  All loads of the ring go through
+// buffer resources, so that those past the end or of idle columns need no branch (they
+// read zeros, without memory traffic) and the compiler can count them.
+//
+// Kernels: router (partial logits over pieces of K), choose (a wave a token), gate_up,
+// down.  For one token every wave of gate_up makes the choice itself.
 #include "moe.hpp"
 
 #include "fp8_common.hpp"
@@ -34,23 +39,23 @@ typedef unsigned long long u64;
 
 constexpr int kMaxUnits = kMoeMaxExperts + kMoeMaxShared;
 
-// What select leaves for the experts' kernels.  Rows of g: those of the first unit, in
-// the order of its tokens, then those of the second, ...
+// A unit is an expert and the tokens that chose it.  gate_up finds its unit in the choices
+// and leaves it here for down.  Rows of g: an expert's lie behind those of the experts
+// before it, in the order of its tokens; the shared experts' behind all of them.
 struct Row {
     int token;
     float weight;
 };
 struct Units {
-    int count, pad;
     int expert[kMaxUnits];
     int base[kMaxUnits];                   // first of the unit's rows
-    u64 tokens[kMaxUnits];
+    u64 tokens[kMaxUnits];                 // none: not a unit
 };
 
 constexpr int kRouterPieces = 8, kRouterWaves = 8;
 
 struct Layout {
-    size_t logits, units, rows, g, partial, bytes;
+    size_t logits, units, rows, g, bytes;
 };
 
 // ------------------------------------------------------------- router ----
@@ -159,13 +164,14 @@ __device__ __forceinline__ double value_of(u64 k)
 
 // The choice of token t by one wave: lane j gets the j-th expert and its weight.  EP
 // experts a lane (expert lane + 64 i).  A round takes the wave's largest key and the
-// lowest expert that has it.
+// lowest expert that has it.  Without a bias the order is the logits', and scores are
+// formed of the chosen ones alone, where their sum does not need the others.
 template <int EP>
 __device__ __forceinline__ void choose(const Moe &m, const double *__restrict__ logits, int pieces,
                                        int t, int &id, float &weight)
 {
     const int lane = threadIdx.x & 63;
-    double p[EP];
+    double p[EP];                        // logits, or with a bias the scores
     u64 key[EP];
 #pragma unroll
     for (int i = 0; i < EP; ++i) p[i] = 0.0;
@@ -190,29 +196,29 @@ __device__ __forceinline__ void choose(const Moe &m, const double *__restrict__ 
         key[i] = lane + 64 * i < m.E ? order_of(p[i]) : 0;
         best = key[i] > best ? key[i] : best;
     }
-    if (m.sigmoid) {
+    double top = 0.0, sum = 1.0;
+    if (!m.sigmoid) {
+        top = value_of(wave_max(best));
+        if (m.bias || !m.renormalize) {
+            sum = 0.0;
 #pragma unroll
-        for (int i = 0; i < EP; ++i) p[i] = 1.0 / (1.0 + exp(-p[i]));
-    } else {
-        const double top = value_of(wave_max(best));
-        double sum = 0.0;
-#pragma unroll
-        for (int i = 0; i < EP; ++i) {
-            p[i] = exp(p[i] - top);
-            if (lane + 64 * i < m.E) sum += p[i];
+            for (int i = 0; i < EP; ++i)
+                if (lane + 64 * i < m.E) sum += exp(p[i] - top);
+            sum = wave_sum(sum);
         }
-        sum = wave_sum(sum);
-#pragma unroll
-        for (int i = 0; i < EP; ++i) p[i] /= sum;
     }
+    auto score = [&](double x) {
+        return m.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / sum;
+    };
     if (m.bias) {
 #pragma unroll
         for (int i = 0; i < EP; ++i) {
             const int e = lane + 64 * i;
+            p[i] = score(p[i]);
             if (e < m.E) key[i] = order_of(p[i] + (double)m.bias[e]);
         }
     }
-    double w = 0.0, total = 0.0;
+    double w = 0.0;
     id = 0;
     for (int j = 0; j < m.top_k; ++j) {
         best = 0;
@@ -220,7 +226,6 @@ __device__ __forceinline__ void choose(const Moe &m, const double *__restrict__ 
         for (int i = 0; i < EP; ++i) best = key[i] > best ? key[i] : best;
         best = wave_max(best);
         int e = -1;
-        double s = 0.0;
 #pragma unroll
         for (int i = 0; i < EP; ++i) {
             const u64 hit = __ballot(key[i] == best);
@@ -228,148 +233,115 @@ __device__ __forceinline__ void choose(const Moe &m, const double *__restrict__ 
             const int l = __builtin_ctzll(hit);
             e = 64 * i + l;
             const int2 u = __builtin_bit_cast(int2, p[i]);
-            s = __builtin_bit_cast(double, make_int2(__builtin_amdgcn_readlane(u.x, l),
-                                                     __builtin_amdgcn_readlane(u.y, l)));
+            const double s = __builtin_bit_cast(
+                double, make_int2(__builtin_amdgcn_readlane(u.x, l),
+                                  __builtin_amdgcn_readlane(u.y, l)));
             if (lane == l) key[i] = 0;
+            if (lane == j) id = e, w = s;
         }
-        total += s;
-        if (lane == j) id = e, w = s;
     }
-    if (m.renormalize) w = total == 0.0 ? 0.0 : w / total;
+    if (!m.bias) w = score(w);
+    if (m.renormalize) {
+        const double total = wave_sum(lane < m.top_k ? w : 0.0);
+        w = total == 0.0 ? 0.0 : w / total;
+    }
     weight = (float)(w * m.factor);
 }
 
-// The choices of several tokens, a wave for one after another, and the units.
 template <int EP>
-__global__ __launch_bounds__(1024) void select_kernel(Moe m, const double *__restrict__ logits,
-                                                      int pieces, Units *__restrict__ units,
-                                                      Row *__restrict__ rows)
+__global__ __launch_bounds__(64) void choose_kernel(Moe m, const double *__restrict__ logits,
+                                                    int pieces)
 {
-    __shared__ u64 tokens[kMoeMaxExperts];
-    __shared__ int unit_base[kMoeMaxExperts], wave_units[16], wave_rows[16];
-    __shared__ int ids[kMoeTokens * kMoeMaxTopK];
-    __shared__ float wts[kMoeTokens * kMoeMaxTopK];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    for (int i = threadIdx.x; i < kMoeMaxExperts; i += 1024) tokens[i] = 0;
-    __syncthreads();
-
-    for (int t = wave; t < m.T; t += 16) {
-        int id;
-        float w;
-        choose<EP>(m, logits, pieces, t, id, w);
-        if (lane < m.top_k) {
-            const int i = t * m.top_k + lane;
-            ids[i] = id;
-            wts[i] = w;
-            m.ids[i] = id;
-            m.weights[i] = w;
-            atomicOr(&tokens[id], 1ull << t);
-        }
-    }
-    __syncthreads();
-
-    // units: the chosen experts in order, their rows one after another
-    const int e = threadIdx.x;
-    const u64 mine = e < m.E ? tokens[e] : 0;
-    const u64 active = __ballot(mine != 0);
-    const int before = __popcll(active & ((1ull << lane) - 1));
-    int n = __popcll(mine);
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int up = __shfl_up(n, o, 64);
-        if (lane >= o) n += up;
-    }
-    if (lane == 63) {
-        wave_units[wave] = __popcll(active);
-        wave_rows[wave] = n;
-    }
-    __syncthreads();
-    int u = before, base = n - __popcll(mine), count = 0;
-    for (int k = 0; k < 16; ++k) {
-        if (k < wave) u += wave_units[k], base += wave_rows[k];
-        count += wave_units[k];
-    }
-    if (mine != 0) {
-        units->expert[u] = e;
-        units->base[u] = base;
-        units->tokens[u] = mine;
-        unit_base[e] = base;
-    }
-    const u64 all = m.T == 64 ? ~0ull : (1ull << m.T) - 1;
-    const int chosen = m.T * m.top_k;
-    if (e < m.S) {
-        units->expert[count + e] = m.E + e;
-        units->base[count + e] = chosen + e * m.T;
-        units->tokens[count + e] = all;
-    }
-    if (e == 0) units->count = count + m.S;
-    __syncthreads();
-    for (int i = threadIdx.x; i < chosen; i += 1024) {
-        const int t = i / m.top_k, x = ids[i];
-        rows[unit_base[x] + __popcll(tokens[x] & ((1ull << t) - 1))] = {t, wts[i]};
-    }
-    for (int i = threadIdx.x; i < m.S * m.T; i += 1024) rows[chosen + i] = {i % m.T, 1.0f};
+    int id;
+    float w;
+    choose<EP>(m, logits, pieces, blockIdx.x, id, w);
+    const int lane = threadIdx.x;
+    if (lane >= m.top_k) return;
+    m.ids[(int64_t)blockIdx.x * m.top_k + lane] = id;
+    m.weights[(int64_t)blockIdx.x * m.top_k + lane] = w;
 }
 
 // ------------------------------------------------------------ experts ----
+
+constexpr uint32_t kOut = 0x7f000000u;     // an offset beyond every range used here
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t range_of(const void *base, uint32_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes,
+                                             0x00020000);
+}
+__device__ __forceinline__ v4i load16(__amdgpu_buffer_rsrc_t p, uint32_t off)
+{
+    return __builtin_amdgcn_raw_buffer_load_b128(p, (int)off, 0, 0);
+}
+__device__ __forceinline__ float load4(__amdgpu_buffer_rsrc_t p, uint32_t off)
+{
+    return __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(p, (int)off, 0, 0));
+}
 
 // One 16 x 128 block of codes as two 16-byte pieces a lane.
 struct Block {
     v4i lo, hi;
 };
-__device__ __forceinline__ Block load_block(const uint8_t *p)
+__device__ __forceinline__ Block load_block(__amdgpu_buffer_rsrc_t p, uint32_t off)
 {
-    return {*reinterpret_cast<const v4i *>(p), *reinterpret_cast<const v4i *>(p + 1024)};
+    return {load16(p, off), load16(p, off + 1024)};
 }
 
-// 16 tokens' inputs of a block of 128: four pieces of 8 a lane.
+// 16 columns' inputs of a block of 128: four pieces of 8 a lane.
 struct Cols {
-    uint4 u[4];
+    v4i u[4];
 };
-__device__ __forceinline__ Cols load_cols(const uint16_t *p, bool on)
+__device__ __forceinline__ Cols load_cols(__amdgpu_buffer_rsrc_t p, uint32_t off)
 {
-    Cols c;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c.u[i] = make_uint4(0, 0, 0, 0);
-    if (on) {
-        c.u[0] = *reinterpret_cast<const uint4 *>(p);
-        c.u[1] = *reinterpret_cast<const uint4 *>(p + 8);
-        c.u[2] = *reinterpret_cast<const uint4 *>(p + 64);
-        c.u[3] = *reinterpret_cast<const uint4 *>(p + 72);
-    }
-    return c;
+    return {{load16(p, off), load16(p, off + 16), load16(p, off + 128), load16(p, off + 144)}};
 }
 
-__device__ __forceinline__ v4f block_sum(const Block &a, const Cols &b, v4f s)
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ u64 uniform(u64 v)
 {
-    s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf16_of_codes(a.lo[0], a.lo[1]),
-                                                __builtin_bit_cast(v8bf, b.u[0]), s, 0, 0, 0);
-    s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf16_of_codes(a.lo[2], a.lo[3]),
-                                                __builtin_bit_cast(v8bf, b.u[1]), s, 0, 0, 0);
-    s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf16_of_codes(a.hi[0], a.hi[1]),
-                                                __builtin_bit_cast(v8bf, b.u[2]), s, 0, 0, 0);
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf16_of_codes(a.hi[2], a.hi[3]),
-                                                   __builtin_bit_cast(v8bf, b.u[3]), s, 0, 0, 0);
+    return (u64)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
+           (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+}
+
+// The codes of a block as bf16, and its products with 16 columns added to s.
+struct Wide {
+    v8bf k[4];
+};
+__device__ __forceinline__ Wide widen(const Block &a)
+{
+    return {{bf16_of_codes(a.lo[0], a.lo[1]), bf16_of_codes(a.lo[2], a.lo[3]),
+             bf16_of_codes(a.hi[0], a.hi[1]), bf16_of_codes(a.hi[2], a.hi[3])}};
+}
+__device__ __forceinline__ v4f block_sum(const Wide &a, const Cols &b)
+{
+    v4f s = (v4f)(0.0f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.k[i], __builtin_bit_cast(v8bf, b.u[i]), s, 0,
+                                                    0, 0);
+    return s;
 }
 
 // g of one unit: a workgroup takes 16 gate and the same 16 up channels, its waves the
 // blocks of K in turn, D at a time.  Columns are the unit's rows, in up to CT tiles of
-// 16.  EP > 0: one token, whose choice every wave makes; the first workgroup leaves it
-// for the down projection.
+// 16.  blockIdx.y: with fewer choices than experts a choice, whose expert is taken up
+// where it comes first, else an expert; then the shared ones.
+// EP > 0: one token, whose choice every wave makes.
 template <int CT, int D, int EP>
-__global__ __launch_bounds__(256) void gate_up_kernel(Moe m, Units *__restrict__ units,
-                                                      Row *__restrict__ rows,
-                                                      uint16_t *__restrict__ g, int64_t plane,
-                                                      const double *__restrict__ logits,
-                                                      int pieces)
+__global__ __launch_bounds__(256, CT == 1 ? 3 : 2) void gate_up_kernel(
+    Moe m, Units *__restrict__ units, Row *__restrict__ rows, uint16_t *__restrict__ g,
+    int64_t plane, const double *__restrict__ logits, int pieces)
 {
     extern __shared__ float red[];                 // [wave][2][CT][256]
+    __shared__ u64 s_tokens;
+    __shared__ int s_less, s_first, s_row[16 * CT];
     const int u = blockIdx.y;
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int waves = blockDim.x >> 6;
     int expert, base, n;
+    int token[CT] = {};
     if constexpr (EP > 0) {
         int id;
         float w;
@@ -383,64 +355,116 @@ __global__ __launch_bounds__(256) void gate_up_kernel(Moe m, Units *__restrict__
             units->base[lane] = lane;
             units->tokens[lane] = 1;
             rows[lane] = {0, w};
-            if (lane == 0) units->count = m.top_k + m.S;
             if (lane < m.top_k) m.ids[lane] = id, m.weights[lane] = w;
         }
     } else {
-        if (u >= units->count) return;
-        expert = units->expert[u];
-        base = units->base[u];
-        n = __popcll(units->tokens[u]);
+        const int chosen = m.T * m.top_k, routed = min(chosen, m.E);
+        const bool shared = u >= routed;
+        expert = shared ? m.E + u - routed : chosen < m.E ? m.ids[u] : u;
+        u64 tokens = m.T == 64 ? ~0ull : (1ull << m.T) - 1;
+        base = chosen + (u - routed) * m.T;
+        if (!shared) {
+            if (threadIdx.x == 0) s_tokens = 0, s_less = 0, s_first = chosen;
+            __syncthreads();
+            for (int i0 = wave * 64; i0 < chosen; i0 += 64 * waves) {
+                const int i = i0 + lane, id = i < chosen ? m.ids[i] : kMaxUnits;
+                const int less = __popcll(__ballot(id < expert));
+                if (lane == 0 && less) atomicAdd(&s_less, less);
+                if (id == expert) {
+                    atomicOr(&s_tokens, 1ull << (i / m.top_k));
+                    atomicMin(&s_first, i);
+                }
+            }
+            __syncthreads();
+            tokens = s_tokens;
+            base = s_less;
+            if (chosen < m.E && s_first != u) tokens = 0;
+        }
+        if (blockIdx.x == 0) {
+            if (threadIdx.x == 0) {
+                units->expert[u] = expert;
+                units->base[u] = base;
+                units->tokens[u] = tokens;
+            }
+            if (shared) {
+                if ((int)threadIdx.x < m.T) rows[base + threadIdx.x] = {(int)threadIdx.x, 1.0f};
+            } else if (tokens != 0) {
+                for (int i = threadIdx.x; i < chosen; i += blockDim.x) {
+                    const int t = i / m.top_k;
+                    if (m.ids[i] == expert)
+                        rows[base + __popcll(tokens & ((1ull << t) - 1))] = {t, m.weights[i]};
+                }
+            }
+        }
+        if (tokens == 0) return;
+        n = __popcll(tokens);
+        // the tokens of this lane's rows
+        if ((int)threadIdx.x < m.T && ((tokens >> threadIdx.x) & 1))
+            s_row[__popcll(tokens & ((1ull << threadIdx.x) - 1))] = threadIdx.x;
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+            if (c * 16 + r < n) token[c] = s_row[c * 16 + r];
     }
+    expert = uniform(expert);
+    n = uniform(n);
     const int nkb = m.K >> 7, fb = blockIdx.x;
-    const int in_tile = r * 64 + ((q ^ ((r >> 2) & 3)) << 4);
-    const int64_t row_bytes = (int64_t)16 * m.K;
-    const uint8_t *const codes = m.gate_up + (int64_t)expert * 2 * m.F * m.K + in_tile;
-    const uint8_t *const gate = codes + fb * row_bytes, *const up = gate + (int64_t)m.F * m.K;
+    const uint32_t in_tile = r * 64 + ((q ^ ((r >> 2) & 3)) << 4);
+    const uint8_t *const codes = m.gate_up + ((int64_t)expert * 2 * m.F + fb * 16) * m.K;
+    const __amdgpu_buffer_rsrc_t gate = range_of(codes, 16 * m.K);
+    const __amdgpu_buffer_rsrc_t up = range_of(codes + (int64_t)m.F * m.K, 16 * m.K);
     const float *const sg = m.gate_up_scale +
                             ((int64_t)expert * (m.F >> 6) + (fb >> 3)) * nkb;
-    const float *const su = sg + (int64_t)(m.F >> 7) * nkb;
+    const __amdgpu_buffer_rsrc_t gate_scale = range_of(sg, nkb * 4);
+    const __amdgpu_buffer_rsrc_t up_scale = range_of(sg + (int64_t)(m.F >> 7) * nkb, nkb * 4);
+    const __amdgpu_buffer_rsrc_t xs = range_of(m.x, (uint32_t)(m.T * m.K * 2));
 
-    const uint16_t *col[CT];
+    uint32_t col[CT];
 #pragma unroll
-    for (int c = 0; c < CT; ++c) {
-        const bool on = c * 16 + r < n;
-        const int t = EP > 0 || !on ? 0 : rows[base + c * 16 + r].token;
-        col[c] = m.x + (int64_t)t * m.K + q * 16;
-    }
+    for (int c = 0; c < CT; ++c)
+        col[c] = c * 16 + r < n ? (uint32_t)(token[c] * m.K + q * 16) * 2 : kOut;
     v4f ag[CT], au[CT];
 #pragma unroll
     for (int c = 0; c < CT; ++c) ag[c] = au[c] = (v4f)(0.0f);
+    Block a[D], b[D];
+    Cols x[D];
+    float fg[D], fu[D];
+    int next = wave;                               // the block to request
+    auto request = [&](int d) {
+        const bool live = next < nkb;
+        const uint32_t at = live ? next * 2048 + in_tile : kOut;
+        a[d] = load_block(gate, at);
+        b[d] = load_block(up, at);
+        x[d] = load_cols(xs, live && r < n ? col[0] + next * 256 : kOut);
+        fg[d] = load4(gate_scale, live ? next * 4 : kOut);
+        fu[d] = load4(up_scale, live ? next * 4 : kOut);
+        next += waves;
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+        request(d);
+        __builtin_amdgcn_sched_barrier(0);
+    }
     for (int k0 = wave; k0 < nkb; k0 += waves * D) {
-        Block a[D], b[D];
-        Cols x[D];
-        float fg[D], fu[D];
 #pragma unroll
         for (int d = 0; d < D; ++d) {
-            const int kb = k0 + d * waves;
-            if (kb >= nkb) continue;
-            a[d] = load_block(gate + kb * 2048);
-            b[d] = load_block(up + kb * 2048);
-            x[d] = load_cols(col[0] + kb * 128, r < n);
-            fg[d] = sg[kb];
-            fu[d] = su[kb];
-        }
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            const int kb = k0 + d * waves;
-            if (kb >= nkb) continue;
+            const Wide wg = widen(a[d]), wu = widen(b[d]);
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
                 if (c > 0 && c * 16 >= n) continue;
-                if (c > 0) x[d] = load_cols(col[c] + kb * 128, c * 16 + r < n);
-                const v4f pg = block_sum(a[d], x[d], (v4f)(0.0f));
-                const v4f pu = block_sum(b[d], x[d], (v4f)(0.0f));
+                const int kb = k0 + d * waves;
+                if (c > 0)
+                    x[d] = load_cols(xs, kb < nkb && c * 16 + r < n ? col[c] + kb * 256 : kOut);
+                const v4f pg = block_sum(wg, x[d]);
+                const v4f pu = block_sum(wu, x[d]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     ag[c][i] = __builtin_fmaf(pg[i], fg[d], ag[c][i]);
                     au[c][i] = __builtin_fmaf(pu[i], fu[d], au[c][i]);
                 }
             }
+            request(d);
+            __builtin_amdgcn_sched_barrier(0);     // not all D uses first, then all requests
         }
     }
 #pragma unroll
@@ -461,11 +485,11 @@ __global__ __launch_bounds__(256) void gate_up_kernel(Moe m, Units *__restrict__
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = a[i] / (1.0f + expf(-a[i])) * b[i];
         uint16_t *p = g + (int64_t)(base + c * 16 + r) * m.F + fb * 16 + q * 4;
-        // the part that bf16 holds, then what it leaves
+        // the part that bf16 holds; for F32 outputs what it leaves, twice more
         for (int part = 1;; ++part) {
             const uint2 o = make_uint2(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]));
             *reinterpret_cast<uint2 *>(p) = o;
-            if (part == (m.y_f32 ? 3 : 2)) break;
+            if (part == (m.y_f32 ? 3 : 1)) break;
             v[0] -= bf16_lo(o.x);
             v[1] -= bf16_hi(o.x);
             v[2] -= bf16_lo(o.y);
@@ -475,193 +499,307 @@ __global__ __launch_bounds__(256) void gate_up_kernel(Moe m, Units *__restrict__
     }
 }
 
-__device__ __forceinline__ void store_y(const Moe &m, float *partial, int64_t o, v4f v)
+// The units, compacted into LDS by the whole workgroup: those of up to `light` rows from
+// the front, the others from the back of the same arrays (in reverse order).
+struct UnitList {
+    int expert[kMaxUnits], base[kMaxUnits];
+    u64 tokens[kMaxUnits];
+    int count, heavy;
+};
+__device__ __forceinline__ void list_units(const Units *__restrict__ units, int most, int light,
+                                           UnitList &l)
 {
-    if (partial)
-        *reinterpret_cast<v4f *>(partial + (int64_t)blockIdx.y * m.T * m.K + o) = v;
-    else if (m.y_f32)
+    const int lane = threadIdx.x & 63;
+    if (threadIdx.x < 64) {
+        int count = 0, heavy = 0;
+        for (int i = 0; i < most; i += 64) {
+            const int u = i + lane;
+            const u64 tokens = u < most ? units->tokens[u] : 0, below = (1ull << lane) - 1;
+            const bool many = __popcll(tokens) > light;
+            const u64 front = __ballot(tokens != 0 && !many), back = __ballot(many);
+            const int at = many ? kMaxUnits - 1 - heavy - __popcll(back & below)
+                                : count + __popcll(front & below);
+            if (tokens != 0) {
+                l.expert[at] = units->expert[u];
+                l.base[at] = units->base[u];
+                l.tokens[at] = tokens;
+            }
+            count += __popcll(front);
+            heavy += __popcll(back);
+        }
+        if (lane == 0) l.count = count, l.heavy = heavy;
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ void store_y(const Moe &m, int64_t o, v4f v)
+{
+    if (m.y_f32)
         *reinterpret_cast<v4f *>(static_cast<float *>(m.y) + o) = v;
     else
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(m.y) + o) =
             make_uint2(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]));
 }
 
-// y of 16 outputs for up to 16 tokens: a workgroup's waves take (unit, block of F) pairs
-// in turn, D at a time, of the units of its part (gridDim.y parts).  Columns are tokens,
-// zero where a token did not choose the unit, so that a token's sums over its experts
-// stay in one accumulator.  partial (or null): [part][T][K].
-template <int WAVES, int D, int PLANES>
-__global__ __launch_bounds__(64 * WAVES) void down_kernel(Moe m, const Units *__restrict__ units,
-                                                    const Row *__restrict__ rows,
-                                                    const uint16_t *__restrict__ g, int64_t plane,
-                                                    float *__restrict__ partial)
+// One expert's codes and scales of a workgroup's 16 outputs.
+struct DownRows {
+    __amdgpu_buffer_rsrc_t codes, scale;
+};
+__device__ __forceinline__ DownRows down_rows(const Moe &m, int64_t e, int nb)
 {
-    constexpr int waves = WAVES;
+    const int nkb = m.F >> 7;
+    return {range_of(m.down + (e * m.K + nb * 16) * m.F, 16 * m.F),
+            range_of(m.down_scale + (e * (m.K >> 7) + (nb >> 3)) * nkb, nkb * 4)};
+}
+
+// y of 16 outputs for up to 16 / PLANES tokens: the units' blocks of F are one sequence, of
+// which each of a workgroup's waves takes an even share.  Column p * (16 / PLANES) + t is part p of token t's g, zero where the
+// token did not choose the unit: a token's sums over its experts stay in one accumulator,
+// and its parts cost no further product.
+template <int WAVES, int D, int PLANES>
+__global__ __launch_bounds__(64 * WAVES, 4) void down_kernel(Moe m, const Units *__restrict__ units,
+                                                             int most,
+                                                             const Row *__restrict__ rows,
+                                                             const uint16_t *__restrict__ g,
+                                                             int64_t plane)
+{
+    constexpr int TP = 16 / PLANES;
     __shared__ float red[WAVES * 256];
+    __shared__ float weight[TP * (kMoeMaxTopK + kMoeMaxShared)];
+    __shared__ UnitList list;
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int part = r / TP, t = r - part * TP;
     const int nkb = m.F >> 7, nb = blockIdx.x;
-    const int count = units->count;
-    const int u0 = count * blockIdx.y / gridDim.y, u1 = count * (blockIdx.y + 1) / gridDim.y;
-    const int in_tile = r * 64 + ((q ^ ((r >> 2) & 3)) << 4);
+    const uint32_t in_tile = r * 64 + ((q ^ ((r >> 2) & 3)) << 4);
+    const __amdgpu_buffer_rsrc_t gs = range_of(g, (uint32_t)(plane * 2 * PLANES));
+    const uint32_t g0 = (uint32_t)(part * plane + q * 16) * 2;
+    for (int i = threadIdx.x; i < m.T * (m.top_k + m.S); i += 64 * WAVES)
+        weight[i] = rows[i].weight;
+    list_units(units, most, 64, list);
+    const int count = uniform(list.count);
 
     v4f acc = (v4f)(0.0f);
-    const int items = (u1 - u0) * nkb;
-    for (int i0 = wave; i0 < items; i0 += waves * D) {
+    if (count > 0) {
+        const int total = count * nkb;
+        const int i0 = (int)((int64_t)total * wave / WAVES);
+        const int i1 = (int)((int64_t)total * (wave + 1) / WAVES);
+        int u = i0 / nkb, kb = i0 - u * nkb, left = i1 - i0;
+        DownRows rw;
+        uint32_t col = 0;
+        float wu = 0.0f;
+        bool has = false;
+        auto enter = [&] {
+            const int at = min(u, count - 1);
+            rw = down_rows(m, uniform(list.expert[at]), nb);
+            const u64 tokens = uniform(list.tokens[at]);
+            has = part < PLANES && ((tokens >> t) & 1);
+            const int row = uniform(list.base[at]) + __popcll(tokens & ((1ull << t) - 1));
+            wu = has ? weight[row] : 0.0f;
+            col = g0 + (uint32_t)row * (uint32_t)m.F * 2;
+        };
+        enter();
         Block a[D];
-        Cols x[D][PLANES];
-        float w[D];
+        Cols x[D];
+        float w[D], f[D];
         bool on[D];
+        auto request = [&](int d) {
+            const bool live = left > 0;
+            a[d] = load_block(rw.codes, live ? kb * 2048 + in_tile : kOut);
+            on[d] = live && has;
+            x[d] = load_cols(gs, on[d] ? col + kb * 256 : kOut);
+            f[d] = load4(rw.scale, live ? kb * 4 : kOut);
+            w[d] = wu;
+            --left;
+            if (++kb == nkb) {
+                kb = 0;
+                ++u;
+                enter();
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
-            const int i = i0 + d * waves;
-            if (i >= items) continue;
-            const int u = u0 + i / nkb, kb = i % nkb;
-            const int64_t e = units->expert[u];
-            a[d] = load_block(m.down + e * m.K * m.F + (int64_t)nb * 16 * m.F + kb * 2048 +
-                              in_tile);
-            const float f = m.down_scale[(e * (m.K >> 7) + (nb >> 3)) * nkb + kb];
-            const u64 tokens = units->tokens[u];
-            on[d] = (tokens >> r) & 1;
-            const int row = units->base[u] + __popcll(tokens & ((1ull << r) - 1));
-            w[d] = 0.0f;
-            if (on[d]) w[d] = rows[row].weight * f;
+        for (int d = 0; d < D; ++d) request(d);
+        for (int i = i0; i < i1; i += D) {
 #pragma unroll
-            for (int k = 0; k < PLANES; ++k)
-                x[d][k] = load_cols(g + k * plane + (int64_t)row * m.F + kb * 128 + q * 16, on[d]);
-        }
+            for (int d = 0; d < D; ++d) {
+                const v4f s = block_sum(widen(a[d]), x[d]);
+                const float c = w[d] * f[d];
+                // a token that did not choose the expert takes nothing of it, codes of NaN
+                // included
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
-            if (i0 + d * waves >= items) continue;
-            v4f s = (v4f)(0.0f);
-#pragma unroll
-            for (int k = 0; k < PLANES; ++k) s = block_sum(a[d], x[d][k], s);
-            // a token that did not choose the expert takes nothing of it, codes of NaN
-            // included
-#pragma unroll
-            for (int k = 0; k < 4; ++k) acc[k] = on[d] ? __builtin_fmaf(s[k], w[d], acc[k]) : acc[k];
+                for (int k = 0; k < 4; ++k)
+                    acc[k] = on[d] ? __builtin_fmaf(s[k], c, acc[k]) : acc[k];
+                request(d);
+            }
         }
     }
     *reinterpret_cast<v4f *>(red + wave * 256 + lane * 4) = acc;
     __syncthreads();
-    if (wave > 0) return;
+    if (wave > 0 || part > 0 || t >= m.T) return;
     v4f v = (v4f)(0.0f);
-    for (int k = 0; k < waves; ++k) v += *reinterpret_cast<const v4f *>(red + k * 256 + lane * 4);
-    if (r < m.T) store_y(m, partial, (int64_t)r * m.K + nb * 16 + q * 4, v);
+    for (int k = 0; k < WAVES; ++k)
+#pragma unroll
+        for (int p = 0; p < PLANES; ++p)
+            v += *reinterpret_cast<const v4f *>(red + k * 256 + (lane + p * TP) * 4);
+    store_y(m, (int64_t)t * m.K + nb * 16 + q * 4, v);
 }
 
-// The same for more tokens: a wave takes whole units, whose rows are its columns (up to 4
-// tiles of 16), and adds each unit's sums, weighted, to its own [T][16] sums in LDS.
-template <int PLANES>
-__global__ __launch_bounds__(512) void down_many_kernel(Moe m, const Units *__restrict__ units,
-                                                        const Row *__restrict__ rows,
-                                                        const uint16_t *__restrict__ g,
-                                                        int64_t plane,
-                                                        float *__restrict__ partial)
+// The same for more tokens.  Columns are the parts of a unit's rows one after another:
+// column p * n + i is part p of row i.  A unit's sums, weighted, are added to the wave's own
+// [T][16] sums in LDS, part by part (two columns of one token are never added at once).
+// Units whose columns fit one tile of 16 make one sequence of blocks, of which each wave
+// takes an even share and its ring runs on from unit to unit; the others follow, up to CT
+// tiles in one pass over their codes.
+template <int D, int PLANES>
+__global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *__restrict__ units,
+                                                           int most, const Row *__restrict__ rows,
+                                                           const uint16_t *__restrict__ g,
+                                                           int64_t plane)
 {
-    constexpr int CT = kMoeTokens / 16, D = 2;
-    extern __shared__ float red[];                 // [wave][T][16]
+    constexpr int CT = 4, WAVES = 8;
+    extern __shared__ float red[];                 // [wave][T][16], rows
+    __shared__ UnitList list;
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int waves = blockDim.x >> 6;
     const int nkb = m.F >> 7, nb = blockIdx.x;
-    const int count = units->count;
-    const int u0 = count * blockIdx.y / gridDim.y, u1 = count * (blockIdx.y + 1) / gridDim.y;
-    const int in_tile = r * 64 + ((q ^ ((r >> 2) & 3)) << 4);
+    const uint32_t in_tile = r * 64 + ((q ^ ((r >> 2) & 3)) << 4);
+    const __amdgpu_buffer_rsrc_t gs = range_of(g, (uint32_t)(plane * 2 * PLANES));
     float *const mine = red + wave * m.T * 16;
+    Row *const lrows = reinterpret_cast<Row *>(red + WAVES * m.T * 16);
+    for (int i = threadIdx.x; i < m.T * (m.top_k + m.S); i += 64 * WAVES) lrows[i] = rows[i];
     for (int i = lane; i < m.T * 4; i += 64)
         *reinterpret_cast<v4f *>(mine + i * 4) = (v4f)(0.0f);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    list_units(units, most, 16 / PLANES, list);
 
-    for (int u = u0 + wave; u < u1; u += waves) {
-        const int64_t e = units->expert[u];
-        const int base = units->base[u], n = __popcll(units->tokens[u]);
-        const uint8_t *const codes = m.down + e * m.K * m.F + (int64_t)nb * 16 * m.F + in_tile;
-        const float *const sc = m.down_scale + (e * (m.K >> 7) + (nb >> 3)) * nkb;
-        v4f acc[CT];
-        Row row[CT];
+    // the sums of tile `first` of a unit of n rows from `base` on
+    auto flush = [&](const v4f &acc, int first, int base, int n) {
+        const int v = first + r, part = v / n;
+        const Row row = lrows[base + (part < PLANES ? v - part * n : 0)];
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-            acc[c] = (v4f)(0.0f);
-            row[c] = {0, 0.0f};
-            if (c * 16 + r < n) row[c] = rows[base + c * 16 + r];
-        }
-        const uint16_t *const x0 = g + (int64_t)(base + r) * m.F + q * 16;
-        for (int k0 = 0; k0 < nkb; k0 += D) {
-            Block a[D];
-            Cols x[D][PLANES];
-            float f[D];
+        for (int p = 0; p < PLANES; ++p) {
+            if (part == p) {
+                v4f *const to = reinterpret_cast<v4f *>(mine + row.token * 16 + q * 4);
+                v4f s = *to;
 #pragma unroll
-            for (int d = 0; d < D; ++d) {
-                const int kb = k0 + d;
-                if (kb >= nkb) continue;
-                a[d] = load_block(codes + kb * 2048);
-                f[d] = sc[kb];
-#pragma unroll
-                for (int k = 0; k < PLANES; ++k)
-                    x[d][k] = load_cols(x0 + k * plane + kb * 128, r < n);
+                for (int k = 0; k < 4; ++k) s[k] = __builtin_fmaf(acc[k], row.weight, s[k]);
+                *to = s;
             }
+            // LDS serves a wave in order; the compiler must keep that order
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        }
+    };
+    // byte offset of column `first` + r of such a unit, at its first block
+    auto column = [&](int first, int base, int n) -> uint32_t {
+        const int v = first + r, part = v / n;
+        return part < PLANES
+                   ? (uint32_t)(part * plane + (int64_t)(base + v - part * n) * m.F + q * 16) * 2
+                   : kOut;
+    };
+
+    const int count = uniform(list.count), heavy = uniform(list.heavy);
+    if (count > 0) {
+        const int total = count * nkb;
+        const int i0 = (int)((int64_t)total * wave / WAVES);
+        const int i1 = (int)((int64_t)total * (wave + 1) / WAVES);
+        Block a[D];
+        Cols x[D];
+        float f[D];
+        int u = i0 / nkb, kb = i0 - u * nkb, left = i1 - i0;   // to request
+        DownRows rw;
+        uint32_t col = 0;
+        auto enter = [&] {
+            const int at = min(u, count - 1);
+            rw = down_rows(m, uniform(list.expert[at]), nb);
+            col = column(0, uniform(list.base[at]), __popcll(uniform(list.tokens[at])));
+        };
+        enter();
+        auto request = [&](int d) {
+            const bool live = left > 0;
+            a[d] = load_block(rw.codes, live ? kb * 2048 + in_tile : kOut);
+            x[d] = load_cols(gs, live && col != kOut ? col + kb * 256 : kOut);
+            f[d] = load4(rw.scale, live ? kb * 4 : kOut);
+            --left;
+            if (++kb == nkb) {
+                kb = 0;
+                ++u;
+                enter();
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        int cu = u, ckb = kb;                                  // in use
+#pragma unroll
+        for (int d = 0; d < D; ++d) request(d);
+        v4f acc = (v4f)(0.0f);
+        for (int i = i0; i < i1; i += D) {
 #pragma unroll
             for (int d = 0; d < D; ++d) {
-                const int kb = k0 + d;
-                if (kb >= nkb) continue;
+                const v4f s = block_sum(widen(a[d]), x[d]);
 #pragma unroll
-                for (int c = 0; c < CT; ++c) {
-                    if (c > 0 && c * 16 >= n) continue;
-                    v4f s = (v4f)(0.0f);
-#pragma unroll
-                    for (int k = 0; k < PLANES; ++k) {
-                        if (c > 0)
-                            x[d][k] = load_cols(x0 + k * plane + (int64_t)c * 16 * m.F + kb * 128,
-                                                c * 16 + r < n);
-                        s = block_sum(a[d], x[d][k], s);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) acc[c][k] = __builtin_fmaf(s[k], f[d], acc[c][k]);
+                for (int k = 0; k < 4; ++k) acc[k] = __builtin_fmaf(s[k], f[d], acc[k]);
+                request(d);
+                if (i + d < i1 && (++ckb == nkb || i + d + 1 == i1)) {
+                    flush(acc, 0, uniform(list.base[cu]), __popcll(uniform(list.tokens[cu])));
+                    acc = (v4f)(0.0f);
+                    ckb = 0;
+                    ++cu;
                 }
             }
         }
+    }
+
+    const int total = heavy * nkb;
+    for (int i = (int)((int64_t)total * wave / WAVES),
+             end = (int)((int64_t)total * (wave + 1) / WAVES); i < end;) {
+        const int u = i / nkb, kb0 = i - u * nkb, kb1 = min(nkb, kb0 + end - i);
+        i += kb1 - kb0;
+        const int at = kMaxUnits - 1 - u;
+        const DownRows rw = down_rows(m, uniform(list.expert[at]), nb);
+        const int base = uniform(list.base[at]), n = __popcll(uniform(list.tokens[at]));
+        for (int c0 = 0; c0 < PLANES * n; c0 += 16 * CT) {
+            v4f acc[CT];
+            uint32_t col[CT];
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-            if (c * 16 + r >= n) continue;
-            v4f *const p = reinterpret_cast<v4f *>(mine + row[c].token * 16 + q * 4);
-            v4f v = *p;
+            for (int c = 0; c < CT; ++c) {
+                acc[c] = (v4f)(0.0f);
+                col[c] = column(c0 + c * 16, base, n);
+            }
+            Block a = load_block(rw.codes, kb0 * 2048 + in_tile);
+            float f = load4(rw.scale, kb0 * 4);
+            for (int kb = kb0; kb < kb1; ++kb) {
+                Cols x[CT];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = __builtin_fmaf(acc[c][k], row[c].weight, v[k]);
-            *p = v;
+                for (int c = 0; c < CT; ++c)
+                    x[c] = load_cols(gs, col[c] != kOut ? col[c] + kb * 256 : kOut);
+                const Wide w = widen(a);
+                const float fk = f;
+                const bool more = kb + 1 < kb1;
+                a = load_block(rw.codes, more ? (kb + 1) * 2048 + in_tile : kOut);
+                f = load4(rw.scale, more ? (kb + 1) * 4 : kOut);
+#pragma unroll
+                for (int c = 0; c < CT; ++c) {
+                    if (c0 + c * 16 >= PLANES * n) continue;
+                    const v4f s = block_sum(w, x[c]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) acc[c][k] = __builtin_fmaf(s[k], fk, acc[c][k]);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+                if (c0 + c * 16 < PLANES * n) flush(acc[c], c0 + c * 16, base, n);
         }
-        // LDS serves a wave in order; the next unit's sums may be another lane's
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < m.T * 4; i += blockDim.x) {
+    for (int i = threadIdx.x; i < m.T * 4; i += 64 * WAVES) {
         v4f v = (v4f)(0.0f);
-        for (int k = 0; k < waves; ++k)
+        for (int k = 0; k < WAVES; ++k)
             v += *reinterpret_cast<const v4f *>(red + k * m.T * 16 + i * 4);
-        store_y(m, partial, (int64_t)(i >> 2) * m.K + nb * 16 + (i & 3) * 4, v);
+        store_y(m, (int64_t)(i >> 2) * m.K + nb * 16 + (i & 3) * 4, v);
     }
 }
 
-// y = the sum of the parts, in order.
-__global__ __launch_bounds__(256) void join_parts_kernel(const float *__restrict__ partial,
-                                                         int parts, int64_t n, void *y, bool f32)
-{
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (i >= n) return;
-    v4f v = *reinterpret_cast<const v4f *>(partial + i);
-    for (int k = 1; k < parts; ++k) v += *reinterpret_cast<const v4f *>(partial + k * n + i);
-    if (f32)
-        *reinterpret_cast<v4f *>(static_cast<float *>(y) + i) = v;
-    else
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(y) + i) =
-            make_uint2(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]));
-}
-
-constexpr int kMaxParts = 8;
-
-Layout moe_layout(int T, int E, int S, int top_k, int K, int F)
+Layout moe_layout(int T, int E, int S, int top_k, int F)
 {
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     const size_t rows = (size_t)T * (top_k + S);
@@ -670,22 +808,21 @@ Layout moe_layout(int T, int E, int S, int top_k, int K, int F)
     l.units = l.logits + up((size_t)kRouterPieces * T * E * 8);
     l.rows = l.units + up(sizeof(Units));
     l.g = l.rows + up(rows * sizeof(Row));
-    l.partial = l.g + up(3 * rows * F * 2);
-    l.bytes = l.partial + up((size_t)kMaxParts * T * K * 4);
+    l.bytes = l.g + up(3 * rows * F * 2);
     return l;
 }
 
 } // namespace
 
-size_t moe_workspace_bytes(int T, int E, int S, int top_k, int K, int F)
+size_t moe_workspace_bytes(int T, int E, int S, int top_k, int F)
 {
-    return moe_layout(std::min(T, kMoeTokens), E, S, top_k, K, F).bytes;
+    return moe_layout(std::min(T, kMoeTokens), E, S, top_k, F).bytes;
 }
 
 hipError_t launch_moe(const Moe &m, hipStream_t stream)
 {
     if (m.T == 0) return hipSuccess;
-    const Layout l = moe_layout(m.T, m.E, m.S, m.top_k, m.K, m.F);
+    const Layout l = moe_layout(m.T, m.E, m.S, m.top_k, m.F);
     char *const ws = static_cast<char *>(m.ws);
     double *const logits = reinterpret_cast<double *>(ws + l.logits);
     Units *const units = reinterpret_cast<Units *>(ws + l.units);
@@ -710,40 +847,24 @@ hipError_t launch_moe(const Moe &m, hipStream_t stream)
                            stream, m, units, rows, g, plane, logits, pieces);
     };
     if (m.T == 1) {
-        by_experts([&](auto ep) { gate_up(gate_up_kernel<1, 4, decltype(ep)::value>, 1); });
+        by_experts([&](auto ep) { gate_up(gate_up_kernel<1, 3, decltype(ep)::value>, 1); });
     } else {
         by_experts([&](auto ep) {
-            hipLaunchKernelGGL((select_kernel<decltype(ep)::value>), dim3(1), dim3(1024), 0, stream,
-                               m, logits, pieces, units, rows);
+            hipLaunchKernelGGL((choose_kernel<decltype(ep)::value>), dim3(m.T), dim3(64), 0,
+                               stream, m, logits, pieces);
         });
-        if (m.T <= 16) gate_up(gate_up_kernel<1, 4, 0>, 1);
+        if (m.T <= 16) gate_up(gate_up_kernel<1, 3, 0>, 1);
         else gate_up(gate_up_kernel<4, 2, 0>, 4);
     }
 
-    const int blocks = m.K / 16;
-    const int parts = m.T == 1 ? 1 : std::max(1, std::min({kMaxParts, most, 1024 / blocks}));
-    float *const partial = parts > 1 ? reinterpret_cast<float *>(ws + l.partial) : nullptr;
-    if (m.T <= 16) {
-        auto down = [&](auto kernel, int waves) {
-            hipLaunchKernelGGL(kernel, dim3(blocks, parts), dim3(64 * waves), 0, stream, m, units,
-                               rows, g, plane, partial);
-        };
-        if (m.T == 1) m.y_f32 ? down(down_kernel<16, 1, 3>, 16) : down(down_kernel<16, 2, 2>, 16);
-        else m.y_f32 ? down(down_kernel<8, 2, 3>, 8) : down(down_kernel<8, 2, 2>, 8);
-    } else {
-        constexpr int DW = 8;
-        auto down = [&](auto kernel) {
-            hipLaunchKernelGGL(kernel, dim3(blocks, parts), dim3(64 * DW), DW * m.T * 64, stream, m,
-                               units, rows, g, plane, partial);
-        };
-        if (m.y_f32) down(down_many_kernel<3>);
-        else down(down_many_kernel<2>);
-    }
-    if (parts > 1) {
-        const int64_t n = (int64_t)m.T * m.K;
-        hipLaunchKernelGGL(join_parts_kernel, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0,
-                           stream, partial, parts, n, m.y, m.y_f32);
-    }
+    const dim3 blocks(m.K / 16);
+    if (m.T <= (m.y_f32 ? 5 : 16))
+        hipLaunchKernelGGL((m.y_f32 ? down_kernel<8, 3, 3> : down_kernel<8, 3, 1>), blocks,
+                           dim3(512), 0, stream, m, units, most, rows, g, plane);
+    else
+        hipLaunchKernelGGL((m.y_f32 ? down_many_kernel<3, 3> : down_many_kernel<4, 1>), blocks,
+                           dim3(512), m.T * (8 * 64 + (m.top_k + m.S) * sizeof(Row)), stream, m,
+                           units, most, rows, g, plane);
     return hipGetLastError();
 }
 
