@@ -1383,6 +1383,7 @@ class MoEWeights:
         self.gate_up, self.gate_up_scale = gate_up, gate_up_scale
         self.down, self.down_scale = down, down_scale
         self._ref = ctypes.byref(desc)
+        self._workspace = {}              # bytes by (tokens, top_k)
 
     @property
     def experts(self):
@@ -1482,7 +1483,9 @@ def convrot_moe_forward(X: torch.Tensor, router: torch.Tensor, W: MoEWeights, to
     _opt(out, "out", _FLOATS, (T, K))
     _opt(ids, "ids", torch.int32, (T, top_k))
     _opt(weights, "weights", torch.float32, (T, top_k))
-    wsb = convrot_moe_workspace_bytes(T, W, top_k)
+    wsb = W._workspace.get((T, top_k))
+    if wsb is None:
+        wsb = W._workspace[T, top_k] = convrot_moe_workspace_bytes(T, W, top_k)
     _check_workspace(wsb, workspace)
     dev = W.down.device
     _on_device(dev, X=X, router=router, router_bias=router_bias, out=out, ids=ids,

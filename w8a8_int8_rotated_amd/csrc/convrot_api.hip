@@ -1519,7 +1519,7 @@ size_t convrot_moe_workspace_bytes(int64_t T, const convrot_moe_weights *W, int 
 {
     if (T <= 0 || check_moe_weights(W) != CONVROT_OK || !valid_top_k(W, top_k)) return 0;
     return convrot::moe_workspace_bytes((int)(T < convrot::kMoeTokens ? T : convrot::kMoeTokens),
-                                        W->experts, W->shared, top_k, (int)W->F);
+                                        W->experts, W->shared, top_k, (int)W->K, (int)W->F);
 }
 
 static int moe_forward_impl(const void *X, int64_t T, const void *router, int router_dtype,

@@ -29,6 +29,7 @@
 #include "fp8_common.hpp"
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 namespace convrot {
@@ -55,7 +56,7 @@ struct Units {
 constexpr int kRouterPieces = 8, kRouterWaves = 8;
 
 struct Layout {
-    size_t logits, units, rows, g, bytes;
+    size_t logits, units, rows, g, partial, bytes;
 };
 
 // ------------------------------------------------------------- router ----
@@ -145,8 +146,12 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v)
 __device__ __forceinline__ u64 wave_max(u64 v)
 {
     const uint32_t hi = wave_max((uint32_t)(v >> 32));
-    const uint32_t lo = wave_max((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
-    return (u64)hi << 32 | lo;
+    const u64 have = __ballot((uint32_t)(v >> 32) == hi);
+    // mostly one lane has the largest upper half
+    if (__popcll(have) == 1)
+        return (u64)hi << 32 |
+               (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, __builtin_ctzll(have));
+    return (u64)hi << 32 | wave_max((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
 }
 
 // Doubles in the order of unsigned numbers; above 0 for every value, NaN as -infinity,
@@ -324,24 +329,138 @@ __device__ __forceinline__ v4f block_sum(const Wide &a, const Cols &b)
 }
 
 // g of one unit: a workgroup takes 16 gate and the same 16 up channels, its waves the
-// blocks of K in turn, D at a time.  Columns are the unit's rows, in up to CT tiles of
-// 16.  blockIdx.y: with fewer choices than experts a choice, whose expert is taken up
-// where it comes first, else an expert; then the shared ones.
-// EP > 0: one token, whose choice every wave makes.
-template <int CT, int D, int EP>
-__global__ __launch_bounds__(256, CT == 1 ? 3 : 2) void gate_up_kernel(
-    Moe m, Units *__restrict__ units, Row *__restrict__ rows, uint16_t *__restrict__ g,
-    int64_t plane, const double *__restrict__ logits, int pieces)
+// groups of P blocks of K in turn.  Columns are the unit's n rows, from row `base` of g on,
+// in up to CT tiles of 16; with P > 1 (up to 16 / P rows) column j * (16 / P) + i is row i's
+// part of the group's block j, so that one set of columns serves P blocks.  row_token: the
+// rows' tokens (null: token 0).
+template <int CT, int D, int P>
+__device__ __forceinline__ void gate_up(const Moe &m, int expert, int base, int n,
+                                        const int *row_token, float *red,
+                                        uint16_t *__restrict__ g, int64_t plane)
 {
-    extern __shared__ float red[];                 // [wave][2][CT][256]
-    __shared__ u64 s_tokens;
-    __shared__ int s_less, s_first, s_row[16 * CT];
-    const int u = blockIdx.y;
+    static_assert(CT == 1 || P == 1, "");
+    constexpr int CP = 16 / P;                     // columns of one block
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int waves = blockDim.x >> 6;
+    const int ri = r % CP, rj = r / CP;            // the lane's row (of a tile) and block
+    const int nkb = m.K >> 7, fb = blockIdx.x;
+    const uint32_t in_tile = r * 64 + ((q ^ ((r >> 2) & 3)) << 4);
+    const uint8_t *const codes = m.gate_up + ((int64_t)expert * 2 * m.F + fb * 16) * m.K;
+    const __amdgpu_buffer_rsrc_t gate = range_of(codes, 16 * m.K);
+    const __amdgpu_buffer_rsrc_t up = range_of(codes + (int64_t)m.F * m.K, 16 * m.K);
+    const float *const sg = m.gate_up_scale +
+                            ((int64_t)expert * (m.F >> 6) + (fb >> 3)) * nkb;
+    const __amdgpu_buffer_rsrc_t gate_scale = range_of(sg, nkb * 4);
+    const __amdgpu_buffer_rsrc_t up_scale = range_of(sg + (int64_t)(m.F >> 7) * nkb, nkb * 4);
+    const __amdgpu_buffer_rsrc_t xs = range_of(m.x, (uint32_t)(m.T * m.K * 2));
+
+    uint32_t col[CT];
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+        col[c] = c * 16 + ri < n
+                     ? (uint32_t)((row_token ? row_token[c * 16 + ri] : 0) * m.K + q * 16) * 2
+                     : kOut;
+    v4f ag[CT], au[CT];
+#pragma unroll
+    for (int c = 0; c < CT; ++c) ag[c] = au[c] = (v4f)(0.0f);
+    Block a[D][P], b[D][P];
+    Cols x[D];
+    float fg[D], fu[D];
+    const int step = waves * P;
+    int next = wave * P;                           // the group to request
+    auto request = [&](int d) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            const uint32_t at = next + j < nkb ? (next + j) * 2048 + in_tile : kOut;
+            a[d][j] = load_block(gate, at);
+            b[d][j] = load_block(up, at);
+        }
+        const int kb = next + rj;
+        x[d] = load_cols(xs, kb < nkb && ri < n ? col[0] + kb * 256 : kOut);
+        fg[d] = load4(gate_scale, kb < nkb ? kb * 4 : kOut);
+        fu[d] = load4(up_scale, kb < nkb ? kb * 4 : kOut);
+        next += step;
+        __builtin_amdgcn_sched_barrier(0);         // not all D uses first, then all requests
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d) request(d);
+    for (int k0 = wave * P; k0 < nkb; k0 += step * D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                const Wide wg = widen(a[d][j]), wu = widen(b[d][j]);
+#pragma unroll
+                for (int c = 0; c < CT; ++c) {
+                    if (c > 0 && c * 16 >= n) continue;
+                    const int kb = k0 + d * step;
+                    if (c > 0)
+                        x[d] = load_cols(xs, kb < nkb && c * 16 + r < n ? col[c] + kb * 256 : kOut);
+                    const v4f pg = block_sum(wg, x[d]);
+                    const v4f pu = block_sum(wu, x[d]);
+                    const bool on = rj == j;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        ag[c][i] = on ? __builtin_fmaf(pg[i], fg[d], ag[c][i]) : ag[c][i];
+                        au[c][i] = on ? __builtin_fmaf(pu[i], fu[d], au[c][i]) : au[c][i];
+                    }
+                }
+            }
+            request(d);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+        if (c > 0 && c * 16 >= n) continue;
+        *reinterpret_cast<v4f *>(red + ((wave * 2 + 0) * CT + c) * 256 + lane * 4) = ag[c];
+        *reinterpret_cast<v4f *>(red + ((wave * 2 + 1) * CT + c) * 256 + lane * 4) = au[c];
+    }
+    __syncthreads();
+    for (int c = wave; c * 16 < n; c += waves) {
+        if (rj > 0 || c * 16 + ri >= n) continue;
+        v4f a = (v4f)(0.0f), b = (v4f)(0.0f);
+        for (int k = 0; k < waves; ++k)
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                const float *const p = red + (k * 2 * CT + c) * 256 + (lane + j * CP) * 4;
+                a += *reinterpret_cast<const v4f *>(p);
+                b += *reinterpret_cast<const v4f *>(p + CT * 256);
+            }
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = a[i] / (1.0f + expf(-a[i])) * b[i];
+        uint16_t *p = g + (int64_t)(base + c * 16 + r) * m.F + fb * 16 + q * 4;
+        // the part that bf16 holds; for F32 outputs what it leaves, twice more
+        for (int part = 1;; ++part) {
+            const uint2 o = make_uint2(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]));
+            *reinterpret_cast<uint2 *>(p) = o;
+            if (part == (m.y_f32 ? 3 : 1)) break;
+            v[0] -= bf16_lo(o.x);
+            v[1] -= bf16_hi(o.x);
+            v[2] -= bf16_lo(o.y);
+            v[3] -= bf16_hi(o.y);
+            p += plane;
+        }
+    }
+}
+
+// blockIdx.y: with fewer choices than experts a choice, whose expert is taken up where it
+// comes first, else an expert; then the shared ones.  ROWS: the most rows of a unit.
+// EP > 0: one token, whose choice every wave makes.
+template <int ROWS, int EP>
+__global__ __launch_bounds__(256, 3) void gate_up_kernel(
+    Moe m, Units *__restrict__ units, Row *__restrict__ rows, uint16_t *__restrict__ g,
+    int64_t plane, const double *__restrict__ logits, int pieces)
+{
+    extern __shared__ float red[];                 // [wave][2][ROWS / 16][256]
+    __shared__ u64 s_tokens;
+    __shared__ int s_less, s_first, s_row[kMoeTokens];
+    const int u = blockIdx.y;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int waves = blockDim.x >> 6;
     int expert, base, n;
-    int token[CT] = {};
     if constexpr (EP > 0) {
         int id;
         float w;
@@ -398,105 +517,27 @@ __global__ __launch_bounds__(256, CT == 1 ? 3 : 2) void gate_up_kernel(
         }
         if (tokens == 0) return;
         n = __popcll(tokens);
-        // the tokens of this lane's rows
+        // the tokens of the rows
         if ((int)threadIdx.x < m.T && ((tokens >> threadIdx.x) & 1))
             s_row[__popcll(tokens & ((1ull << threadIdx.x) - 1))] = threadIdx.x;
         __syncthreads();
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-            if (c * 16 + r < n) token[c] = s_row[c * 16 + r];
     }
     expert = uniform(expert);
     n = uniform(n);
-    const int nkb = m.K >> 7, fb = blockIdx.x;
-    const uint32_t in_tile = r * 64 + ((q ^ ((r >> 2) & 3)) << 4);
-    const uint8_t *const codes = m.gate_up + ((int64_t)expert * 2 * m.F + fb * 16) * m.K;
-    const __amdgpu_buffer_rsrc_t gate = range_of(codes, 16 * m.K);
-    const __amdgpu_buffer_rsrc_t up = range_of(codes + (int64_t)m.F * m.K, 16 * m.K);
-    const float *const sg = m.gate_up_scale +
-                            ((int64_t)expert * (m.F >> 6) + (fb >> 3)) * nkb;
-    const __amdgpu_buffer_rsrc_t gate_scale = range_of(sg, nkb * 4);
-    const __amdgpu_buffer_rsrc_t up_scale = range_of(sg + (int64_t)(m.F >> 7) * nkb, nkb * 4);
-    const __amdgpu_buffer_rsrc_t xs = range_of(m.x, (uint32_t)(m.T * m.K * 2));
+    const int *const row_token = EP > 0 ? nullptr : s_row;
+    if (ROWS == 8 || n <= 8) gate_up<1, 2, 2>(m, expert, base, n, row_token, red, g, plane);
+    if constexpr (ROWS == 16) {
+        if (n > 8) gate_up<1, 3, 1>(m, expert, base, n, row_token, red, g, plane);
+    } else if constexpr (ROWS == 64) {
+        if (n > 16) gate_up<4, 2, 1>(m, expert, base, n, row_token, red, g, plane);
+        else if (n > 8) gate_up<1, 3, 1>(m, expert, base, n, row_token, red, g, plane);
+    }
+}
 
-    uint32_t col[CT];
-#pragma unroll
-    for (int c = 0; c < CT; ++c)
-        col[c] = c * 16 + r < n ? (uint32_t)(token[c] * m.K + q * 16) * 2 : kOut;
-    v4f ag[CT], au[CT];
-#pragma unroll
-    for (int c = 0; c < CT; ++c) ag[c] = au[c] = (v4f)(0.0f);
-    Block a[D], b[D];
-    Cols x[D];
-    float fg[D], fu[D];
-    int next = wave;                               // the block to request
-    auto request = [&](int d) {
-        const bool live = next < nkb;
-        const uint32_t at = live ? next * 2048 + in_tile : kOut;
-        a[d] = load_block(gate, at);
-        b[d] = load_block(up, at);
-        x[d] = load_cols(xs, live && r < n ? col[0] + next * 256 : kOut);
-        fg[d] = load4(gate_scale, live ? next * 4 : kOut);
-        fu[d] = load4(up_scale, live ? next * 4 : kOut);
-        next += waves;
-    };
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-        request(d);
-        __builtin_amdgcn_sched_barrier(0);
-    }
-    for (int k0 = wave; k0 < nkb; k0 += waves * D) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            const Wide wg = widen(a[d]), wu = widen(b[d]);
-#pragma unroll
-            for (int c = 0; c < CT; ++c) {
-                if (c > 0 && c * 16 >= n) continue;
-                const int kb = k0 + d * waves;
-                if (c > 0)
-                    x[d] = load_cols(xs, kb < nkb && c * 16 + r < n ? col[c] + kb * 256 : kOut);
-                const v4f pg = block_sum(wg, x[d]);
-                const v4f pu = block_sum(wu, x[d]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    ag[c][i] = __builtin_fmaf(pg[i], fg[d], ag[c][i]);
-                    au[c][i] = __builtin_fmaf(pu[i], fu[d], au[c][i]);
-                }
-            }
-            request(d);
-            __builtin_amdgcn_sched_barrier(0);     // not all D uses first, then all requests
-        }
-    }
-#pragma unroll
-    for (int c = 0; c < CT; ++c) {
-        if (c > 0 && c * 16 >= n) continue;
-        *reinterpret_cast<v4f *>(red + ((wave * 2 + 0) * CT + c) * 256 + lane * 4) = ag[c];
-        *reinterpret_cast<v4f *>(red + ((wave * 2 + 1) * CT + c) * 256 + lane * 4) = au[c];
-    }
-    __syncthreads();
-    for (int c = wave; c * 16 < n; c += waves) {
-        v4f a = (v4f)(0.0f), b = (v4f)(0.0f);
-        for (int k = 0; k < waves; ++k) {
-            a += *reinterpret_cast<const v4f *>(red + ((k * 2 + 0) * CT + c) * 256 + lane * 4);
-            b += *reinterpret_cast<const v4f *>(red + ((k * 2 + 1) * CT + c) * 256 + lane * 4);
-        }
-        if (c * 16 + r >= n) continue;
-        float v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = a[i] / (1.0f + expf(-a[i])) * b[i];
-        uint16_t *p = g + (int64_t)(base + c * 16 + r) * m.F + fb * 16 + q * 4;
-        // the part that bf16 holds; for F32 outputs what it leaves, twice more
-        for (int part = 1;; ++part) {
-            const uint2 o = make_uint2(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]));
-            *reinterpret_cast<uint2 *>(p) = o;
-            if (part == (m.y_f32 ? 3 : 1)) break;
-            v[0] -= bf16_lo(o.x);
-            v[1] -= bf16_hi(o.x);
-            v[2] -= bf16_lo(o.y);
-            v[3] -= bf16_hi(o.y);
-            p += plane;
-        }
-    }
+// This wave's share of n things: of all waves of the workgroups that sum the same outputs.
+__device__ __forceinline__ int share(int n, int waves, int wave)
+{
+    return (int)((int64_t)n * ((int)blockIdx.y * waves + wave) / ((int)gridDim.y * waves));
 }
 
 // The units, compacted into LDS by the whole workgroup: those of up to `light` rows from
@@ -532,9 +573,12 @@ __device__ __forceinline__ void list_units(const Units *__restrict__ units, int 
     __syncthreads();
 }
 
-__device__ __forceinline__ void store_y(const Moe &m, int64_t o, v4f v)
+// 4 outputs of y, or of this workgroup's part of the units (partial: [part][T][K]).
+__device__ __forceinline__ void store_y(const Moe &m, float *partial, int64_t o, v4f v)
 {
-    if (m.y_f32)
+    if (partial)
+        *reinterpret_cast<v4f *>(partial + (int64_t)blockIdx.y * m.T * m.K + o) = v;
+    else if (m.y_f32)
         *reinterpret_cast<v4f *>(static_cast<float *>(m.y) + o) = v;
     else
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(m.y) + o) =
@@ -552,25 +596,25 @@ __device__ __forceinline__ DownRows down_rows(const Moe &m, int64_t e, int nb)
             range_of(m.down_scale + (e * (m.K >> 7) + (nb >> 3)) * nkb, nkb * 4)};
 }
 
-// y of 16 outputs for up to 16 / PLANES tokens: the units' blocks of F are one sequence, of
-// which each of a workgroup's waves takes an even share.  Column p * (16 / PLANES) + t is part p of token t's g, zero where the
-// token did not choose the unit: a token's sums over its experts stay in one accumulator,
-// and its parts cost no further product.
-template <int WAVES, int D, int PLANES>
-__global__ __launch_bounds__(64 * WAVES, 4) void down_kernel(Moe m, const Units *__restrict__ units,
-                                                             int most,
-                                                             const Row *__restrict__ rows,
-                                                             const uint16_t *__restrict__ g,
-                                                             int64_t plane)
+// y of 16 outputs for up to CP = 16 / (P PLANES) tokens: the units' blocks of F, in groups
+// of P, are one sequence, of which each wave takes an even share.  Column
+// (j PLANES + p) CP + t is, for the group's block j, part p of token t's g, zero where the
+// token did not choose the unit: a token's sums over its experts stay in one place, and
+// its parts and the group's further blocks need no further columns.
+template <int D, int P, int PLANES>
+__global__ __launch_bounds__(512, 4) void down_kernel(Moe m, const Units *__restrict__ units,
+                                                      int most, const Row *__restrict__ rows,
+                                                      const uint16_t *__restrict__ g,
+                                                      int64_t plane, float *__restrict__ partial)
 {
-    constexpr int TP = 16 / PLANES;
+    constexpr int WAVES = 8, CP = 16 / (P * PLANES);
     __shared__ float red[WAVES * 256];
-    __shared__ float weight[TP * (kMoeMaxTopK + kMoeMaxShared)];
+    __shared__ float weight[CP * (kMoeMaxTopK + kMoeMaxShared)];
     __shared__ UnitList list;
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int part = r / TP, t = r - part * TP;
-    const int nkb = m.F >> 7, nb = blockIdx.x;
+    const int t = r % CP, part = r / CP % PLANES, rj = r / CP / PLANES;
+    const int nkb = m.F >> 7, nb = blockIdx.x, groups = (nkb + P - 1) / P;
     const uint32_t in_tile = r * 64 + ((q ^ ((r >> 2) & 3)) << 4);
     const __amdgpu_buffer_rsrc_t gs = range_of(g, (uint32_t)(plane * 2 * PLANES));
     const uint32_t g0 = (uint32_t)(part * plane + q * 16) * 2;
@@ -580,11 +624,10 @@ __global__ __launch_bounds__(64 * WAVES, 4) void down_kernel(Moe m, const Units 
     const int count = uniform(list.count);
 
     v4f acc = (v4f)(0.0f);
-    if (count > 0) {
-        const int total = count * nkb;
-        const int i0 = (int)((int64_t)total * wave / WAVES);
-        const int i1 = (int)((int64_t)total * (wave + 1) / WAVES);
-        int u = i0 / nkb, kb = i0 - u * nkb, left = i1 - i0;
+    const int total = count * groups;
+    const int i0 = share(total, WAVES, wave), i1 = share(total, WAVES, wave + 1);
+    if (i0 < i1) {
+        int u = i0 / groups, kb = (i0 - u * groups) * P, left = i1 - i0;
         DownRows rw;
         uint32_t col = 0;
         float wu = 0.0f;
@@ -593,25 +636,29 @@ __global__ __launch_bounds__(64 * WAVES, 4) void down_kernel(Moe m, const Units 
             const int at = min(u, count - 1);
             rw = down_rows(m, uniform(list.expert[at]), nb);
             const u64 tokens = uniform(list.tokens[at]);
-            has = part < PLANES && ((tokens >> t) & 1);
+            has = rj < P && ((tokens >> t) & 1);
             const int row = uniform(list.base[at]) + __popcll(tokens & ((1ull << t) - 1));
             wu = has ? weight[row] : 0.0f;
             col = g0 + (uint32_t)row * (uint32_t)m.F * 2;
         };
         enter();
-        Block a[D];
+        Block a[D][P];
         Cols x[D];
         float w[D], f[D];
         bool on[D];
         auto request = [&](int d) {
             const bool live = left > 0;
-            a[d] = load_block(rw.codes, live ? kb * 2048 + in_tile : kOut);
-            on[d] = live && has;
-            x[d] = load_cols(gs, on[d] ? col + kb * 256 : kOut);
-            f[d] = load4(rw.scale, live ? kb * 4 : kOut);
+#pragma unroll
+            for (int j = 0; j < P; ++j)
+                a[d][j] = load_block(rw.codes,
+                                     live && kb + j < nkb ? (kb + j) * 2048 + in_tile : kOut);
+            on[d] = live && has && kb + rj < nkb;
+            x[d] = load_cols(gs, on[d] ? col + (kb + rj) * 256 : kOut);
+            f[d] = load4(rw.scale, on[d] ? (kb + rj) * 4 : kOut);
             w[d] = wu;
             --left;
-            if (++kb == nkb) {
+            kb += P;
+            if (kb >= nkb) {
                 kb = 0;
                 ++u;
                 enter();
@@ -623,41 +670,47 @@ __global__ __launch_bounds__(64 * WAVES, 4) void down_kernel(Moe m, const Units 
         for (int i = i0; i < i1; i += D) {
 #pragma unroll
             for (int d = 0; d < D; ++d) {
-                const v4f s = block_sum(widen(a[d]), x[d]);
                 const float c = w[d] * f[d];
-                // a token that did not choose the expert takes nothing of it, codes of NaN
-                // included
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    acc[k] = on[d] ? __builtin_fmaf(s[k], c, acc[k]) : acc[k];
+                for (int j = 0; j < P; ++j) {
+                    const v4f s = block_sum(widen(a[d][j]), x[d]);
+                    // a token that did not choose the expert takes nothing of it, codes of
+                    // NaN included
+                    const bool take = on[d] && rj == j;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        acc[k] = take ? __builtin_fmaf(s[k], c, acc[k]) : acc[k];
+                }
                 request(d);
             }
         }
     }
     *reinterpret_cast<v4f *>(red + wave * 256 + lane * 4) = acc;
     __syncthreads();
-    if (wave > 0 || part > 0 || t >= m.T) return;
+    if (wave > 0 || r >= CP || t >= m.T) return;
     v4f v = (v4f)(0.0f);
     for (int k = 0; k < WAVES; ++k)
 #pragma unroll
-        for (int p = 0; p < PLANES; ++p)
-            v += *reinterpret_cast<const v4f *>(red + k * 256 + (lane + p * TP) * 4);
-    store_y(m, (int64_t)t * m.K + nb * 16 + q * 4, v);
+        for (int p = 0; p < P * PLANES; ++p)
+            v += *reinterpret_cast<const v4f *>(red + k * 256 + (lane + p * CP) * 4);
+    store_y(m, partial, (int64_t)t * m.K + nb * 16 + q * 4, v);
 }
 
 // The same for more tokens.  Columns are the parts of a unit's rows one after another:
 // column p * n + i is part p of row i.  A unit's sums, weighted, are added to the wave's own
 // [T][16] sums in LDS, part by part (two columns of one token are never added at once).
-// Units whose columns fit one tile of 16 make one sequence of blocks, of which each wave
-// takes an even share and its ring runs on from unit to unit; the others follow, up to CT
-// tiles in one pass over their codes.
-template <int D, int PLANES>
+// Units whose columns fit 16 / P make one sequence of groups of P blocks (columns
+// j * (16 / P) .. belong to the group's block j), of which each wave takes an even share
+// and its ring runs on from unit to unit; the others follow, up to CT tiles of 16 in one
+// pass over their codes.
+template <int D, int P, int PLANES>
 __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *__restrict__ units,
                                                            int most, const Row *__restrict__ rows,
                                                            const uint16_t *__restrict__ g,
-                                                           int64_t plane)
+                                                           int64_t plane,
+                                                           float *__restrict__ partial)
 {
-    constexpr int CT = 4, WAVES = 8;
+    constexpr int CT = 4, WAVES = 8, CP = 16 / P;
     extern __shared__ float red[];                 // [wave][T][16], rows
     __shared__ UnitList list;
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
@@ -670,11 +723,11 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
     for (int i = threadIdx.x; i < m.T * (m.top_k + m.S); i += 64 * WAVES) lrows[i] = rows[i];
     for (int i = lane; i < m.T * 4; i += 64)
         *reinterpret_cast<v4f *>(mine + i * 4) = (v4f)(0.0f);
-    list_units(units, most, 16 / PLANES, list);
+    list_units(units, most, CP / PLANES, list);
 
-    // the sums of tile `first` of a unit of n rows from `base` on
-    auto flush = [&](const v4f &acc, int first, int base, int n) {
-        const int v = first + r, part = v / n;
+    // adds to the sums of column v of a unit of n rows from `base` on (v past its columns: none)
+    auto flush = [&](const v4f &acc, int v, int base, int n) {
+        const int part = v / n;
         const Row row = lrows[base + (part < PLANES ? v - part * n : 0)];
 #pragma unroll
         for (int p = 0; p < PLANES; ++p) {
@@ -690,57 +743,71 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
             __builtin_amdgcn_wave_barrier();
         }
     };
-    // byte offset of column `first` + r of such a unit, at its first block
-    auto column = [&](int first, int base, int n) -> uint32_t {
-        const int v = first + r, part = v / n;
+    // byte offset of column v of such a unit, at its first block
+    auto column = [&](int v, int base, int n) -> uint32_t {
+        const int part = v / n;
         return part < PLANES
                    ? (uint32_t)(part * plane + (int64_t)(base + v - part * n) * m.F + q * 16) * 2
                    : kOut;
     };
 
     const int count = uniform(list.count), heavy = uniform(list.heavy);
-    if (count > 0) {
-        const int total = count * nkb;
-        const int i0 = (int)((int64_t)total * wave / WAVES);
-        const int i1 = (int)((int64_t)total * (wave + 1) / WAVES);
-        Block a[D];
+    const int groups = (nkb + P - 1) / P, rj = r / CP;
+    const int light = count * groups;
+    const int i0 = share(light, WAVES, wave), i1 = share(light, WAVES, wave + 1);
+    if (i0 < i1) {
+        Block a[D][P];
         Cols x[D];
         float f[D];
-        int u = i0 / nkb, kb = i0 - u * nkb, left = i1 - i0;   // to request
+        int u = i0 / groups, kb = (i0 - u * groups) * P, left = i1 - i0;   // to request
         DownRows rw;
         uint32_t col = 0;
         auto enter = [&] {
             const int at = min(u, count - 1);
             rw = down_rows(m, uniform(list.expert[at]), nb);
-            col = column(0, uniform(list.base[at]), __popcll(uniform(list.tokens[at])));
+            col = column(r % CP, uniform(list.base[at]), __popcll(uniform(list.tokens[at])));
         };
         enter();
+        int cu = u, ckb = kb;                                              // in use
         auto request = [&](int d) {
             const bool live = left > 0;
-            a[d] = load_block(rw.codes, live ? kb * 2048 + in_tile : kOut);
-            x[d] = load_cols(gs, live && col != kOut ? col + kb * 256 : kOut);
-            f[d] = load4(rw.scale, live ? kb * 4 : kOut);
+#pragma unroll
+            for (int j = 0; j < P; ++j)
+                a[d][j] = load_block(rw.codes,
+                                     live && kb + j < nkb ? (kb + j) * 2048 + in_tile : kOut);
+            const bool on = live && kb + rj < nkb;
+            x[d] = load_cols(gs, on && col != kOut ? col + (kb + rj) * 256 : kOut);
+            f[d] = load4(rw.scale, on ? (kb + rj) * 4 : kOut);
             --left;
-            if (++kb == nkb) {
+            kb += P;
+            if (kb >= nkb) {
                 kb = 0;
                 ++u;
                 enter();
             }
             __builtin_amdgcn_sched_barrier(0);
         };
-        int cu = u, ckb = kb;                                  // in use
 #pragma unroll
         for (int d = 0; d < D; ++d) request(d);
         v4f acc = (v4f)(0.0f);
         for (int i = i0; i < i1; i += D) {
 #pragma unroll
             for (int d = 0; d < D; ++d) {
-                const v4f s = block_sum(widen(a[d]), x[d]);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) acc[k] = __builtin_fmaf(s[k], f[d], acc[k]);
+                for (int j = 0; j < P; ++j) {
+                    const v4f s = block_sum(widen(a[d][j]), x[d]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        acc[k] = rj == j ? __builtin_fmaf(s[k], f[d], acc[k]) : acc[k];
+                }
                 request(d);
-                if (i + d < i1 && (++ckb == nkb || i + d + 1 == i1)) {
-                    flush(acc, 0, uniform(list.base[cu]), __popcll(uniform(list.tokens[cu])));
+                ckb += P;
+                if (i + d < i1 && (ckb >= nkb || i + d + 1 == i1)) {
+                    const int base = uniform(list.base[cu]);
+                    const int n = __popcll(uniform(list.tokens[cu]));
+#pragma unroll
+                    for (int j = 0; j < P; ++j)
+                        flush(acc, rj == j ? r % CP : PLANES * n, base, n);
                     acc = (v4f)(0.0f);
                     ckb = 0;
                     ++cu;
@@ -750,8 +817,7 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
     }
 
     const int total = heavy * nkb;
-    for (int i = (int)((int64_t)total * wave / WAVES),
-             end = (int)((int64_t)total * (wave + 1) / WAVES); i < end;) {
+    for (int i = share(total, WAVES, wave), end = share(total, WAVES, wave + 1); i < end;) {
         const int u = i / nkb, kb0 = i - u * nkb, kb1 = min(nkb, kb0 + end - i);
         i += kb1 - kb0;
         const int at = kMaxUnits - 1 - u;
@@ -763,7 +829,7 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
                 acc[c] = (v4f)(0.0f);
-                col[c] = column(c0 + c * 16, base, n);
+                col[c] = column(c0 + c * 16 + r, base, n);
             }
             Block a = load_block(rw.codes, kb0 * 2048 + in_tile);
             float f = load4(rw.scale, kb0 * 4);
@@ -787,7 +853,7 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
             }
 #pragma unroll
             for (int c = 0; c < CT; ++c)
-                if (c0 + c * 16 < PLANES * n) flush(acc[c], c0 + c * 16, base, n);
+                if (c0 + c * 16 < PLANES * n) flush(acc[c], c0 + c * 16 + r, base, n);
         }
     }
     __syncthreads();
@@ -795,11 +861,28 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
         v4f v = (v4f)(0.0f);
         for (int k = 0; k < WAVES; ++k)
             v += *reinterpret_cast<const v4f *>(red + k * m.T * 16 + i * 4);
-        store_y(m, (int64_t)(i >> 2) * m.K + nb * 16 + (i & 3) * 4, v);
+        store_y(m, partial, (int64_t)(i >> 2) * m.K + nb * 16 + (i & 3) * 4, v);
     }
 }
 
-Layout moe_layout(int T, int E, int S, int top_k, int F)
+// y = the sum of the parts, in order.
+__global__ __launch_bounds__(256) void join_parts_kernel(const float *__restrict__ partial,
+                                                         int parts, int64_t n, void *y, bool f32)
+{
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    v4f v = *reinterpret_cast<const v4f *>(partial + i);
+    for (int k = 1; k < parts; ++k) v += *reinterpret_cast<const v4f *>(partial + k * n + i);
+    if (f32)
+        *reinterpret_cast<v4f *>(static_cast<float *>(y) + i) = v;
+    else
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(y) + i) =
+            make_uint2(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]));
+}
+
+constexpr int kMaxParts = 8;
+
+Layout moe_layout(int T, int E, int S, int top_k, int K, int F)
 {
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     const size_t rows = (size_t)T * (top_k + S);
@@ -808,21 +891,43 @@ Layout moe_layout(int T, int E, int S, int top_k, int F)
     l.units = l.logits + up((size_t)kRouterPieces * T * E * 8);
     l.rows = l.units + up(sizeof(Units));
     l.g = l.rows + up(rows * sizeof(Row));
-    l.bytes = l.g + up(3 * rows * F * 2);
+    l.partial = l.g + up(3 * rows * F * 2);
+    l.bytes = l.partial + up((size_t)kMaxParts * T * K * 4);
     return l;
+}
+
+// Parts of the units whose sums a second kernel joins: the CUs hold two workgroups each,
+// and a round that they do not fill reads more slowly.  64 tokens, 64 experts of
+// K = 5376, F = 1408 (336 workgroups a part), us with 1, 2, 3, 4, 6 parts and without the
+// join (5 us): 143, 120, 114, 126, 124; 23 tokens, 40 experts of K = 2560, F = 640, F32 (160
+// workgroups a part): 33.8, 35.9, 27.4, 32.0, 32.8.  The bytes are those of the experts that
+// the tokens are expected to choose.
+int down_parts(const Moe &m)
+{
+    const double units = m.E * (1.0 - std::pow(1.0 - (double)m.top_k / m.E, m.T)) + m.S;
+    const double us = units * m.K * m.F / 5.1e6;
+    const int blocks = m.K / 16, round = 2 * device_cu_count();
+    int best = 1;
+    double least = 0.0;
+    for (int p = 1; p <= kMaxParts; ++p) {
+        const int rounds = (blocks * p + round - 1) / round;
+        const double t = us * rounds * round / (blocks * p) + (p > 1 ? 8.0 : 0.0);
+        if (p == 1 || t < least) best = p, least = t;
+    }
+    return best;
 }
 
 } // namespace
 
-size_t moe_workspace_bytes(int T, int E, int S, int top_k, int F)
+size_t moe_workspace_bytes(int T, int E, int S, int top_k, int K, int F)
 {
-    return moe_layout(std::min(T, kMoeTokens), E, S, top_k, F).bytes;
+    return moe_layout(std::min(T, kMoeTokens), E, S, top_k, K, F).bytes;
 }
 
 hipError_t launch_moe(const Moe &m, hipStream_t stream)
 {
     if (m.T == 0) return hipSuccess;
-    const Layout l = moe_layout(m.T, m.E, m.S, m.top_k, m.F);
+    const Layout l = moe_layout(m.T, m.E, m.S, m.top_k, m.K, m.F);
     char *const ws = static_cast<char *>(m.ws);
     double *const logits = reinterpret_cast<double *>(ws + l.logits);
     Units *const units = reinterpret_cast<Units *>(ws + l.units);
@@ -847,24 +952,33 @@ hipError_t launch_moe(const Moe &m, hipStream_t stream)
                            stream, m, units, rows, g, plane, logits, pieces);
     };
     if (m.T == 1) {
-        by_experts([&](auto ep) { gate_up(gate_up_kernel<1, 3, decltype(ep)::value>, 1); });
+        by_experts([&](auto ep) { gate_up(gate_up_kernel<8, decltype(ep)::value>, 1); });
     } else {
         by_experts([&](auto ep) {
             hipLaunchKernelGGL((choose_kernel<decltype(ep)::value>), dim3(m.T), dim3(64), 0,
                                stream, m, logits, pieces);
         });
-        if (m.T <= 16) gate_up(gate_up_kernel<1, 3, 0>, 1);
-        else gate_up(gate_up_kernel<4, 2, 0>, 4);
+        if (m.T <= 8) gate_up(gate_up_kernel<8, 0>, 1);
+        else if (m.T <= 16) gate_up(gate_up_kernel<16, 0>, 1);
+        else gate_up(gate_up_kernel<64, 0>, 4);
     }
 
-    const dim3 blocks(m.K / 16);
-    if (m.T <= (m.y_f32 ? 5 : 16))
-        hipLaunchKernelGGL((m.y_f32 ? down_kernel<8, 3, 3> : down_kernel<8, 3, 1>), blocks,
-                           dim3(512), 0, stream, m, units, most, rows, g, plane);
-    else
-        hipLaunchKernelGGL((m.y_f32 ? down_many_kernel<3, 3> : down_many_kernel<4, 1>), blocks,
-                           dim3(512), m.T * (8 * 64 + (m.top_k + m.S) * sizeof(Row)), stream, m,
-                           units, most, rows, g, plane);
+    const int parts = down_parts(m);
+    float *const partial = parts > 1 ? reinterpret_cast<float *>(ws + l.partial) : nullptr;
+    auto down = [&](auto kernel, size_t lds) {
+        hipLaunchKernelGGL(kernel, dim3(m.K / 16, parts), dim3(512), lds, stream, m, units, most,
+                           rows, g, plane, partial);
+    };
+    const size_t many = m.T * (8 * 64 + (m.top_k + m.S) * sizeof(Row));
+    if (m.y_f32) m.T <= 5 ? down(down_kernel<3, 1, 3>, 0) : down(down_many_kernel<3, 1, 3>, many);
+    else if (m.T <= 8) down(down_kernel<2, 2, 1>, 0);
+    else if (m.T <= 16) down(down_kernel<3, 1, 1>, 0);
+    else down(down_many_kernel<2, 2, 1>, many);
+    if (parts > 1) {
+        const int64_t n = (int64_t)m.T * m.K;
+        hipLaunchKernelGGL(join_parts_kernel, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0,
+                           stream, partial, parts, n, m.y, m.y_f32);
+    }
     return hipGetLastError();
 }
 

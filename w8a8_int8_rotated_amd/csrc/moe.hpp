@@ -25,7 +25,7 @@ struct Moe {
     void *ws;                              // moe_workspace_bytes
 };
 // For passes of up to T tokens.
-size_t moe_workspace_bytes(int T, int E, int S, int top_k, int F);
+size_t moe_workspace_bytes(int T, int E, int S, int top_k, int K, int F);
 hipError_t launch_moe(const Moe &m, hipStream_t stream);
 
 } // namespace convrot
