@@ -4,6 +4,7 @@
 #include "convrot.h"
 #include "add_norm.hpp"
 #include "common.hpp"
+#include "gemm_i8_few.hpp"
 #include "moe.hpp"
 
 #include <atomic>
@@ -133,6 +134,18 @@ int check_out_dtype(int y_dtype)
 convrot::OutKind out_kind(int y_dtype)
 {
     return y_dtype == CONVROT_F32 ? convrot::OutKind::F32 : convrot::OutKind::BF16;
+}
+
+// A product of codes with the plain epilogue: up to kFewRows rows in the kernel for few
+// rows (M = 5, K = 5376, N = 16128: @@FEW@@).
+hipError_t product_i8(const int8_t *qx, const float *sx, int64_t M, const convrot_weights *W,
+                      const float *bias, void *Y, int y_dtype, hipStream_t s)
+{
+    if (M <= convrot::kFewRows)
+        return convrot::launch_gemm_i8_few(qx, W->codes, sx, W->scale, bias, Y,
+                                           y_dtype == CONVROT_F32, M, W->N, W->K, s);
+    return convrot::launch_gemm_i8(qx, W->codes, sx, W->scale, bias, Y, out_kind(y_dtype), M, W->N,
+                                   W->K, s);
 }
 
 // Bump allocator over a caller workspace.
@@ -403,8 +416,7 @@ static int linear_forward_impl(const void *X, int64_t M, const convrot_weights *
                                             is_regular(W),
                                             inv_sqrt_block(W->block), qx, sx, s);
     if (e == hipSuccess)
-        e = convrot::launch_gemm_i8(qx, W->codes, sx, W->scale, bias, Y, out_kind(y_dtype), M,
-                                    W->N, W->K, s);
+        e = product_i8(qx, sx, M, W, bias, Y, y_dtype, s);
     return hip_status(e);
 }
 
@@ -1325,8 +1337,7 @@ static int norm_linear_impl(const void *x, int x_dtype, const void *residual, in
     hipStream_t st = static_cast<hipStream_t>(stream);
     hipError_t e = convrot::launch_add_norm(convrot::NormOut::ROTATED_I8, a, st);
     if (e == hipSuccess)
-        e = convrot::launch_gemm_i8(reinterpret_cast<const int8_t *>(a.q), W->codes, a.s, W->scale,
-                                    bias, Y, out_kind(y_dtype), M, W->N, W->K, st);
+        e = product_i8(reinterpret_cast<const int8_t *>(a.q), a.s, M, W, bias, Y, y_dtype, st);
     return hip_status(e);
 }
 
@@ -1817,10 +1828,12 @@ int convrot_gemm_dequant(const int8_t *q_x, const float *s_x, int64_t M,
     if (!q_x || !s_x || !Y) return CONVROT_EINVAL;
     if (!aligned16(q_x) || !aligned16(s_x) || !aligned16(Y) || (bias && !aligned16(bias)))
         return CONVROT_EALIGN;
+    if (!gelu && !swiglu)
+        return hip_status(product_i8(q_x, s_x, M, W, bias, Y, y_dtype,
+                                     static_cast<hipStream_t>(stream)));
     return hip_status(convrot::launch_gemm_i8(
         q_x, W->codes, s_x, W->scale, bias, Y,
-        swiglu ? convrot::OutKind::SWIGLU_BF16
-               : gelu ? convrot::OutKind::GELU_BF16 : out_kind(y_dtype),
+        swiglu ? convrot::OutKind::SWIGLU_BF16 : convrot::OutKind::GELU_BF16,
         M, W->N, W->K, static_cast<hipStream_t>(stream)));
 }
 

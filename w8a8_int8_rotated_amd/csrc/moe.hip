@@ -370,6 +370,7 @@ __device__ __forceinline__ void gate_up(const Moe &m, int expert, int base, int 
     const int step = waves * P;
     int next = wave * P;                           // the group to request
     auto request = [&](int d) {
+        if (next >= nkb) return;
 #pragma unroll
         for (int j = 0; j < P; ++j) {
             const uint32_t at = next + j < nkb ? (next + j) * 2048 + in_tile : kOut;
@@ -388,6 +389,7 @@ __device__ __forceinline__ void gate_up(const Moe &m, int expert, int base, int 
     for (int k0 = wave * P; k0 < nkb; k0 += step * D) {
 #pragma unroll
         for (int d = 0; d < D; ++d) {
+            if (k0 + d * step >= nkb) break;
 #pragma unroll
             for (int j = 0; j < P; ++j) {
                 const Wide wg = widen(a[d][j]), wu = widen(b[d][j]);
@@ -529,7 +531,7 @@ __global__ __launch_bounds__(256, 3) void gate_up_kernel(
     if constexpr (ROWS == 16) {
         if (n > 8) gate_up<1, 3, 1>(m, expert, base, n, row_token, red, g, plane);
     } else if constexpr (ROWS == 64) {
-        if (n > 16) gate_up<4, 2, 1>(m, expert, base, n, row_token, red, g, plane);
+        if (n > 16) gate_up<4, 1, 1>(m, expert, base, n, row_token, red, g, plane);
         else if (n > 8) gate_up<1, 3, 1>(m, expert, base, n, row_token, red, g, plane);
     }
 }
@@ -647,12 +649,11 @@ __global__ __launch_bounds__(512, 4) void down_kernel(Moe m, const Units *__rest
         float w[D], f[D];
         bool on[D];
         auto request = [&](int d) {
-            const bool live = left > 0;
+            if (left <= 0) return;
 #pragma unroll
             for (int j = 0; j < P; ++j)
-                a[d][j] = load_block(rw.codes,
-                                     live && kb + j < nkb ? (kb + j) * 2048 + in_tile : kOut);
-            on[d] = live && has && kb + rj < nkb;
+                a[d][j] = load_block(rw.codes, kb + j < nkb ? (kb + j) * 2048 + in_tile : kOut);
+            on[d] = has && kb + rj < nkb;
             x[d] = load_cols(gs, on[d] ? col + (kb + rj) * 256 : kOut);
             f[d] = load4(rw.scale, on[d] ? (kb + rj) * 4 : kOut);
             w[d] = wu;
@@ -670,6 +671,7 @@ __global__ __launch_bounds__(512, 4) void down_kernel(Moe m, const Units *__rest
         for (int i = i0; i < i1; i += D) {
 #pragma unroll
             for (int d = 0; d < D; ++d) {
+                if (i + d >= i1) break;
                 const float c = w[d] * f[d];
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
@@ -770,12 +772,11 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
         enter();
         int cu = u, ckb = kb;                                              // in use
         auto request = [&](int d) {
-            const bool live = left > 0;
+            if (left <= 0) return;
 #pragma unroll
             for (int j = 0; j < P; ++j)
-                a[d][j] = load_block(rw.codes,
-                                     live && kb + j < nkb ? (kb + j) * 2048 + in_tile : kOut);
-            const bool on = live && kb + rj < nkb;
+                a[d][j] = load_block(rw.codes, kb + j < nkb ? (kb + j) * 2048 + in_tile : kOut);
+            const bool on = kb + rj < nkb;
             x[d] = load_cols(gs, on && col != kOut ? col + (kb + rj) * 256 : kOut);
             f[d] = load4(rw.scale, on ? (kb + rj) * 4 : kOut);
             --left;
@@ -793,6 +794,7 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
         for (int i = i0; i < i1; i += D) {
 #pragma unroll
             for (int d = 0; d < D; ++d) {
+                if (i + d >= i1) break;
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
                     const v4f s = block_sum(widen(a[d][j]), x[d]);
@@ -802,7 +804,7 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
                 }
                 request(d);
                 ckb += P;
-                if (i + d < i1 && (ckb >= nkb || i + d + 1 == i1)) {
+                if (ckb >= nkb || i + d + 1 == i1) {
                     const int base = uniform(list.base[cu]);
                     const int n = __popcll(uniform(list.tokens[cu]));
 #pragma unroll
@@ -970,8 +972,8 @@ hipError_t launch_moe(const Moe &m, hipStream_t stream)
                            rows, g, plane, partial);
     };
     const size_t many = m.T * (8 * 64 + (m.top_k + m.S) * sizeof(Row));
-    if (m.y_f32) m.T <= 5 ? down(down_kernel<3, 1, 3>, 0) : down(down_many_kernel<3, 1, 3>, many);
-    else if (m.T <= 8) down(down_kernel<2, 2, 1>, 0);
+    if (m.y_f32) m.T <= 5 ? down(down_kernel<3, 1, 3>, 0) : down(down_many_kernel<2, 1, 3>, many);
+    else if (m.T <= 8) down(down_kernel<1, 2, 1>, 0);
     else if (m.T <= 16) down(down_kernel<3, 1, 1>, 0);
     else down(down_many_kernel<2, 2, 1>, many);
     if (parts > 1) {
