@@ -23,21 +23,48 @@
 namespace convrot {
 namespace {
 
-constexpr uint32_t kOut = 0x7f000000u;   // an offset beyond every range used here
+// an element offset beyond every range used here, whose byte offset still fits 32 bits
+constexpr uint32_t kPast = 0x1fc00000u;
+constexpr uint32_t kOut = 4 * kPast;
 
-// 8 channels as loaded, bf16 or fp32.
+// 8 channels as loaded, bf16 or fp32: 4 from element e0 and 4 from e1 of a range.  RUNS: e1
+// is anywhere (neighbouring lanes then hold neighbouring runs, so that loads of fp32 rows
+// cover whole cache lines); otherwise e1 = e0 + 4.  AUX: the cache policy (2: past the caches).
 template <bool F32> struct Raw {
     v4i u[F32 ? 2 : 1];
 };
 
-template <bool F32>
-__device__ __forceinline__ Raw<F32> load8(__amdgpu_buffer_rsrc_t rows, uint32_t off)
+template <bool F32, bool RUNS, int AUX>
+__device__ __forceinline__ Raw<F32> load8(__amdgpu_buffer_rsrc_t rows, uint32_t e0, uint32_t e1)
 {
     Raw<F32> r;
-    r.u[0] = __builtin_amdgcn_raw_buffer_load_b128(rows, (int)off, 0, 0);
-    if constexpr (F32)
-        r.u[1] = __builtin_amdgcn_raw_buffer_load_b128(rows, (int)off + 16, 0, 0);
+    if constexpr (F32) {
+        r.u[0] = __builtin_amdgcn_raw_buffer_load_b128(rows, (int)(e0 * 4), 0, AUX);
+        r.u[1] = __builtin_amdgcn_raw_buffer_load_b128(rows, (int)(e1 * 4), 0, AUX);
+    } else if constexpr (RUNS) {
+        const v2i a = __builtin_amdgcn_raw_buffer_load_b64(rows, (int)(e0 * 2), 0, AUX);
+        const v2i b = __builtin_amdgcn_raw_buffer_load_b64(rows, (int)(e1 * 2), 0, AUX);
+        r.u[0] = (v4i){a[0], a[1], b[0], b[1]};
+    } else {
+        r.u[0] = __builtin_amdgcn_raw_buffer_load_b128(rows, (int)(e0 * 2), 0, AUX);
+    }
     return r;
+}
+
+template <bool RUNS, int AUX, bool F32>
+__device__ __forceinline__ void store8(const Raw<F32> &r, __amdgpu_buffer_rsrc_t rows, uint32_t e0,
+                                       uint32_t e1)
+{
+    if constexpr (F32) {
+        __builtin_amdgcn_raw_buffer_store_b128(r.u[0], rows, (int)(e0 * 4), 0, AUX);
+        __builtin_amdgcn_raw_buffer_store_b128(r.u[1], rows, (int)(e1 * 4), 0, AUX);
+    } else if constexpr (RUNS) {
+        const v4i u = r.u[0];
+        __builtin_amdgcn_raw_buffer_store_b64((v2i){u[0], u[1]}, rows, (int)(e0 * 2), 0, AUX);
+        __builtin_amdgcn_raw_buffer_store_b64((v2i){u[2], u[3]}, rows, (int)(e1 * 2), 0, AUX);
+    } else {
+        __builtin_amdgcn_raw_buffer_store_b128(r.u[0], rows, (int)(e0 * 2), 0, AUX);
+    }
 }
 
 template <bool F32> __device__ __forceinline__ void widen(const Raw<F32> &r, float (&v)[8])
@@ -69,15 +96,6 @@ template <bool F32> __device__ __forceinline__ Raw<F32> narrow(const float (&v)[
     return r;
 }
 
-template <bool F32>
-__device__ __forceinline__ void store8(const Raw<F32> &r, __amdgpu_buffer_rsrc_t rows,
-                                       uint32_t off)
-{
-    __builtin_amdgcn_raw_buffer_store_b128(r.u[0], rows, (int)off, 0, 0);
-    if constexpr (F32)
-        __builtin_amdgcn_raw_buffer_store_b128(r.u[1], rows, (int)off + 16, 0, 0);
-}
-
 // Sum and maximum over a half-wave.
 #define CR_DPP(v, CTRL)                                                                           \
     __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true))
@@ -103,9 +121,10 @@ constexpr int kRows = 0, kFp8 = 2;
 // so that a store of codes covers whole cache lines of the K-tiled layout (two rows
 // of a 16-row block are neighbours in it).  A pair of rows is split over W waves of
 // at most SPR steps; a workgroup holds blockDim / 64 / W pairs.
-template <bool XF, bool RF, int MODE, int SPR>
+template <bool XF, bool RF, int MODE, int SPR, int AUX>
 __global__ __launch_bounds__(1024) void add_norm_kernel(AddNorm a, int W)
 {
+    constexpr bool RUNS = MODE == kRows && RF;
     constexpr bool I8 = MODE != kRows && MODE != kFp8;
     constexpr int B = I8 ? MODE & ~1 : 64, ROT = I8 ? MODE & 1 : 0, LPB = B / 8;
     constexpr int NSTAGE = B == 64 ? 3 : B == 128 ? 4 : 5;
@@ -123,11 +142,13 @@ __global__ __launch_bounds__(1024) void add_norm_kernel(AddNorm a, int W)
     const int rows = row0 < a.M ? (int)min(a.M - row0, (int64_t)2) : 0;
     const bool in = row < a.M;
     const int chunk = I8 ? chunk_of_lane(hl % LPB) : 0;
-    const int lane_off = I8 ? (hl / LPB) * B + chunk * 8 : hl * 8;
-    // element offset of this lane in step t (kOut past the row's end or the last row)
-    auto at = [&](int t, int es) -> uint32_t {
-        const int e = ((part + W * t) << 8) + lane_off;
-        return in && e < K ? (uint32_t)((half * K + e) * es) : kOut;
+    const int lane_off = I8 ? (hl / LPB) * B + chunk * 8 : hl * (RUNS ? 4 : 8);
+    const int run = RUNS ? 128 : 4;                  // from the lane's first run to the second
+    // this lane's element in step t, of a pair of rows and of one row (kPast past the end)
+    auto element = [&](int t) { return ((part + W * t) << 8) + lane_off; };
+    auto at = [&](int t, int o) -> uint32_t {
+        const int e = element(t) + o;
+        return in && e < K ? (uint32_t)(half * K + e) : kPast;
     };
     auto range = [&](const void *p, int es) {
         return row_rsrc(static_cast<const char *>(p) + first * K * es, rows * K * es);
@@ -140,19 +161,20 @@ __global__ __launch_bounds__(1024) void add_norm_kernel(AddNorm a, int W)
         const __amdgpu_buffer_rsrc_t xs = range(a.x, XS);
 #pragma unroll
         for (int t = 0; t < SPR; ++t)
-            if (t < mine) xr[t] = load8<XF>(xs, at(t, XS));
+            if (t < mine) xr[t] = load8<XF, RUNS, AUX>(xs, at(t, 0), at(t, run));
     }
     if (add) {
         const __amdgpu_buffer_rsrc_t rs = range(a.r, RS);
 #pragma unroll
         for (int t = 0; t < SPR; ++t)
-            if (t < mine) rr[t] = load8<RF>(rs, at(t, RS));
+            if (t < mine) rr[t] = load8<RF, RUNS, AUX>(rs, at(t, 0), at(t, run));
     }
     // the weights of this lane's channels, requested with the rows
     const __amdgpu_buffer_rsrc_t ws = row_rsrc(a.w ? a.w : a.x, a.w ? K * 4 : 0);
     auto load_w = [&](int t) {
-        const int e = ((part + W * t) << 8) + lane_off;
-        return load8<true>(ws, e < K ? (uint32_t)(e * 4) : kOut);
+        const int e = element(t);
+        return load8<true, RUNS, 0>(ws, e < K ? (uint32_t)e : kPast,
+                                    e + run < K ? (uint32_t)(e + run) : kPast);
     };
     constexpr bool EARLY = SPR <= 4;
     Raw<true> wr[EARLY ? SPR : 1];
@@ -162,7 +184,7 @@ __global__ __launch_bounds__(1024) void add_norm_kernel(AddNorm a, int W)
             if (t < mine) wr[t] = load_w(t);
     }
 
-    float v[SPR][8], sum = 0.0f;
+    float v[SPR][8], part_sum[2] = {};
     const __amdgpu_buffer_rsrc_t hs = range(add ? a.h : a.x, add ? RS : 0);
 #pragma unroll
     for (int t = 0; t < SPR; ++t) {
@@ -174,13 +196,17 @@ __global__ __launch_bounds__(1024) void add_norm_kernel(AddNorm a, int W)
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[t][j] += r[j];
             const Raw<RF> h = narrow<RF>(v[t]);
-            store8<RF>(h, hs, at(t, RS));
+            store8<RUNS, AUX>(h, hs, at(t, 0), at(t, run));
             widen<RF>(h, v[t]);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(v[t][j], v[t][j], sum);
+        for (int j = 0; j < 8; ++j)
+            part_sum[j / 4] = __builtin_fmaf(v[t][j], v[t][j], part_sum[j / 4]);
     }
-    sum = half_sum(sum);
+    // one tree over the runs of 4 channels, whichever lane holds which: every output form
+    // of the same rows has the same bits
+    float sum = RUNS ? half_sum(part_sum[0]) + half_sum(part_sum[1])
+                     : half_sum(part_sum[0] + part_sum[1]);
     if (W > 1) {
         if (hl == 0) red[0][wave][half] = sum;
         __syncthreads();
@@ -202,12 +228,12 @@ __global__ __launch_bounds__(1024) void add_norm_kernel(AddNorm a, int W)
             const __amdgpu_buffer_rsrc_t ys = range(a.y, 4);
 #pragma unroll
             for (int t = 0; t < SPR; ++t)
-                if (t < mine) store8<true>(narrow<true>(v[t]), ys, at(t, 4));
+                if (t < mine) store8<RUNS, AUX>(narrow<true>(v[t]), ys, at(t, 0), at(t, run));
         } else {
             const __amdgpu_buffer_rsrc_t ys = range(a.y, 2);
 #pragma unroll
             for (int t = 0; t < SPR; ++t)
-                if (t < mine) store8<false>(narrow<false>(v[t]), ys, at(t, 2));
+                if (t < mine) store8<RUNS, AUX>(narrow<false>(v[t]), ys, at(t, 0), at(t, run));
         }
         return;
     }
@@ -216,9 +242,8 @@ __global__ __launch_bounds__(1024) void add_norm_kernel(AddNorm a, int W)
         row_rsrc(a.q + (first & ~int64_t(15)) * K, rows ? 16 * K : 0);
     const uint32_t q_off = (uint32_t)tiled_offset(row & 15, lane_off, K);
     auto store_codes = [&](int t, int lo, int hi) {
-        const int e = ((part + W * t) << 8) + lane_off;
         __builtin_amdgcn_raw_buffer_store_b64(
-            (v2i){lo, hi}, qs, in && e < K ? (int)((part + W * t) * 4096 + q_off) : (int)kOut, 0,
+            (v2i){lo, hi}, qs, in && element(t) < K ? (int)((part + W * t) * 4096 + q_off) : (int)kOut, 0,
             0);
     };
     if constexpr (MODE == kFp8) {
@@ -273,6 +298,17 @@ __global__ __launch_bounds__(1024) void add_norm_kernel(AddNorm a, int W)
     }
 }
 
+// Rows out and backward: a call that moves more than the last-level cache holds reads and
+// writes past the caches (AUX = 2).  us without and with that, K = 5376, bf16 rows and
+// residual, bf16 rows and fp32 residual:
+//   forward   3121 rows  23.9  26.6   36.2  37.0;   6242  49.4  49.1    76.8  69.8;
+//            24966       195   183    285   268
+//   backward  3121       31.1  36.2   47.9  50.9;   6242  60.6  61.8   105    94;
+//            24966       222   218    408   376
+// Codes gain nothing (38656 rows to INT8: 411, 436): an fp32 residual is read there in
+// pieces of 16 of every 32 bytes, the other half from the caches.
+constexpr int64_t kPastCaches = (int64_t)1 << 28;
+
 template <bool XF, bool RF, int MODE>
 void launch_steps(const AddNorm &a, hipStream_t stream)
 {
@@ -280,12 +316,15 @@ void launch_steps(const AddNorm &a, hipStream_t stream)
     const int spr = steps <= 32 ? 2 : steps <= 64 ? 4 : 8;
     const int W = (steps + spr - 1) / spr, pairs = std::max(1, 4 / W);
     const dim3 grid((unsigned)((a.M + 2 * pairs - 1) / (2 * pairs))), block(64 * W * pairs);
-    if (spr == 2)
-        hipLaunchKernelGGL((add_norm_kernel<XF, RF, MODE, 2>), grid, block, 0, stream, a, W);
-    else if (spr == 4)
-        hipLaunchKernelGGL((add_norm_kernel<XF, RF, MODE, 4>), grid, block, 0, stream, a, W);
-    else
-        hipLaunchKernelGGL((add_norm_kernel<XF, RF, MODE, 8>), grid, block, 0, stream, a, W);
+    auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a, W); };
+    if (spr == 2) {
+        const int bytes = (XF ? 4 : 2) + (a.r ? RF ? 8 : 4 : 0) + (a.y_f32 ? 4 : 2);
+        if (MODE == kRows && a.M * a.K * bytes >= kPastCaches)
+            launch(add_norm_kernel<XF, RF, MODE, 2, MODE == kRows ? 2 : 0>);
+        else
+            launch(add_norm_kernel<XF, RF, MODE, 2, 0>);
+    } else if (spr == 4) launch(add_norm_kernel<XF, RF, MODE, 4, 0>);
+    else launch(add_norm_kernel<XF, RF, MODE, 8, 0>);
 }
 
 template <int MODE> void launch_types(const AddNorm &a, hipStream_t stream)
@@ -295,47 +334,15 @@ template <int MODE> void launch_types(const AddNorm &a, hipStream_t stream)
     else launch_steps<false, false, MODE>(a, stream);
 }
 
-// Backward.  A wave step is 512 channels of one row, 8 a lane: two runs of 4, each
-// neighbouring its neighbour's, so that loads of fp32 rows cover whole cache lines
-// too.  A row is split over W waves of at most SPR steps; a workgroup holds `pairs`
-// rows at a time and walks the rows, the next one's loads on their way while it
-// finishes the last, and keeps its sums of dw in registers.
-template <bool F32>
-__device__ __forceinline__ void load_runs(__amdgpu_buffer_rsrc_t row, uint32_t e0, uint32_t e1,
-                                          Raw<F32> &r)
-{
-    if constexpr (F32) {
-        r.u[0] = __builtin_amdgcn_raw_buffer_load_b128(row, (int)(e0 * 4), 0, 0);
-        r.u[1] = __builtin_amdgcn_raw_buffer_load_b128(row, (int)(e1 * 4), 0, 0);
-    } else {
-        const v2i a = __builtin_amdgcn_raw_buffer_load_b64(row, (int)(e0 * 2), 0, 0);
-        const v2i b = __builtin_amdgcn_raw_buffer_load_b64(row, (int)(e1 * 2), 0, 0);
-        r.u[0] = (v4i){a[0], a[1], b[0], b[1]};
-    }
-}
-
-template <bool F32>
-__device__ __forceinline__ void store_runs(const Raw<F32> &r, __amdgpu_buffer_rsrc_t row,
-                                           uint32_t e0, uint32_t e1)
-{
-    if constexpr (F32) {
-        __builtin_amdgcn_raw_buffer_store_b128(r.u[0], row, (int)(e0 * 4), 0, 0);
-        __builtin_amdgcn_raw_buffer_store_b128(r.u[1], row, (int)(e1 * 4), 0, 0);
-    } else {
-        __builtin_amdgcn_raw_buffer_store_b64((v2i){r.u[0][0], r.u[0][1]}, row, (int)(e0 * 2), 0,
-                                              0);
-        __builtin_amdgcn_raw_buffer_store_b64((v2i){r.u[0][2], r.u[0][3]}, row, (int)(e1 * 2), 0,
-                                              0);
-    }
-}
-
+// Backward.  A wave step is 512 channels of one row, 8 a lane in two runs of 4.  A row is
+// split over W waves of at most SPR steps; a workgroup holds `pairs` rows at a time and
+// walks the rows, the next one's loads on their way while it finishes the last, and keeps
+// its sums of dw in registers.
 constexpr int kGradStep = 512;
-// element offset past every row, whose byte offset still fits 32 bits
-constexpr uint32_t kPast = 0x1fc00000u;
 
 // LEAN (rows of many steps a wave): no loads ahead, gh and w read where they are
 // needed; the registers hold g, h and dw.
-template <bool GF, bool HF, int SPR>
+template <bool GF, bool HF, int SPR, int AUX>
 __global__ __launch_bounds__(1024) void add_norm_grad_kernel(AddNormGrad a, int W)
 {
     constexpr int GS = GF ? 4 : 2, HS = HF ? 4 : 2;
@@ -355,9 +362,7 @@ __global__ __launch_bounds__(1024) void add_norm_grad_kernel(AddNormGrad a, int 
     float dw[SPR][8], wk[LEAN ? 1 : SPR][8];
     const __amdgpu_buffer_rsrc_t ws = row_rsrc(a.w ? a.w : a.h, a.w ? K * 4 : 0);
     auto load_w = [&](int t, float (&w)[8]) {
-        Raw<true> r;
-        load_runs<true>(ws, e0[t], e1[t], r);
-        widen<true>(r, w);
+        widen<true>(load8<true, true, 0>(ws, e0[t], e1[t]), w);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (!a.w) w[j] = 1.0f;
@@ -383,16 +388,16 @@ __global__ __launch_bounds__(1024) void add_norm_grad_kernel(AddNormGrad a, int 
         const __amdgpu_buffer_rsrc_t gs = row_of(a.g, row, GS), hs = row_of(a.h, row, HS);
 #pragma unroll
         for (int t = 0; t < SPR; ++t)
-            if (t < mine) load_runs<HF>(hs, e0[t], e1[t], h[t]);
+            if (t < mine) h[t] = load8<HF, true, AUX>(hs, e0[t], e1[t]);
 #pragma unroll
         for (int t = 0; t < SPR; ++t)
-            if (t < mine) load_runs<GF>(gs, e0[t], e1[t], g[t]);
+            if (t < mine) g[t] = load8<GF, true, AUX>(gs, e0[t], e1[t]);
         if constexpr (!LEAN) {
             if (!more) return;
             const __amdgpu_buffer_rsrc_t ms = row_of(a.gh, row, HS);
 #pragma unroll
             for (int t = 0; t < SPR; ++t)
-                if (t < mine) load_runs<HF>(ms, e0[t], e1[t], gh[t]);
+                if (t < mine) gh[t] = load8<HF, true, AUX>(ms, e0[t], e1[t]);
         }
     };
 
@@ -456,11 +461,7 @@ __global__ __launch_bounds__(1024) void add_norm_grad_kernel(AddNormGrad a, int 
             widen<GF>(gc[t], gv);
             if constexpr (LEAN) {
                 load_w(t, w);
-                if (more) {
-                    Raw<HF> r;
-                    load_runs<HF>(ms, e0[t], e1[t], r);
-                    widen<HF>(r, m);
-                }
+                if (more) widen<HF>(load8<HF, true, AUX>(ms, e0[t], e1[t]), m);
             } else if (more) {
                 widen<HF>(mc[t], m);
             }
@@ -471,8 +472,8 @@ __global__ __launch_bounds__(1024) void add_norm_grad_kernel(AddNormGrad a, int 
                                       -(hv[j] * c));
                 if (more) d[j] += m[j];
             }
-            store_runs<HF>(narrow<HF>(d), ds, e0[t], e1[t]);
-            if (HF && a.dx) store_runs<false>(narrow<false>(d), xs, e0[t], e1[t]);
+            store8<true, AUX>(narrow<HF>(d), ds, e0[t], e1[t]);
+            if (HF && a.dx) store8<true, AUX>(narrow<false>(d), xs, e0[t], e1[t]);
         }
     }
     if (!a.dw) return;
@@ -482,7 +483,7 @@ __global__ __launch_bounds__(1024) void add_norm_grad_kernel(AddNormGrad a, int 
     if (pairs == 1) {
 #pragma unroll
         for (int t = 0; t < SPR; ++t)
-            if (t < mine) store_runs<true>(narrow<true>(dw[t]), out, e0[t], e1[t]);
+            if (t < mine) store8<true, 0>(narrow<true>(dw[t]), out, e0[t], e1[t]);
         return;
     }
 #pragma unroll
@@ -543,7 +544,7 @@ GradShape grad_shape(int64_t M, int64_t K)
     // small beside the rows
     const int64_t rows = (M + g.pairs - 1) / g.pairs;
     const int64_t held = 256 * std::max(1, 16 / (g.W * g.pairs));
-    g.grid = std::min(held, std::max<int64_t>((rows + 3) / 4, std::min<int64_t>(rows, 64)));
+    g.grid = std::min(held, std::max<int64_t>((rows + 5) / 6, std::min<int64_t>(rows, 64)));
     return g;
 }
 
@@ -574,10 +575,16 @@ hipError_t launch_add_norm_grad(const AddNormGrad &a, hipStream_t stream)
         };
         auto types = [&](auto spr) {
             constexpr int S = decltype(spr)::value;
-            if (a.g_f32) a.h_f32 ? launch(add_norm_grad_kernel<true, true, S>)
-                                 : launch(add_norm_grad_kernel<true, false, S>);
-            else a.h_f32 ? launch(add_norm_grad_kernel<false, true, S>)
-                         : launch(add_norm_grad_kernel<false, false, S>);
+            auto past = [&](auto aux) {
+                constexpr int A = decltype(aux)::value;
+                if (a.g_f32) a.h_f32 ? launch(add_norm_grad_kernel<true, true, S, A>)
+                                     : launch(add_norm_grad_kernel<true, false, S, A>);
+                else a.h_f32 ? launch(add_norm_grad_kernel<false, true, S, A>)
+                             : launch(add_norm_grad_kernel<false, false, S, A>);
+            };
+            const int bytes = (a.g_f32 ? 4 : 2) + (a.h_f32 ? 4 : 2) * (a.gh ? 3 : 2) + (a.dx ? 2 : 0);
+            if (a.M * a.K * bytes >= kPastCaches) past(std::integral_constant<int, 2>{});
+            else past(std::integral_constant<int, 0>{});
         };
         if (g.spr == 1) types(std::integral_constant<int, 1>{});
         else if (g.spr == 2) types(std::integral_constant<int, 2>{});
