@@ -113,6 +113,14 @@ CASES = [
     dict(T=64, K=1024, F=384, E=16, k=4, S=1, bias=True, score="sigmoid"),
     dict(T=64, K=640, F=256, E=64, k=1, out="f32"),
     dict(T=65, K=512, F=256, E=12, k=3, S=1),
+    dict(T=64, K=256, F=384, E=40, k=32, S=16),
+    dict(T=64, K=384, F=256, E=40, k=32, S=16, out="f32"),
+    dict(T=3, K=384, F=128, E=300, k=12, S=2, score="sigmoid", bias=True),
+    dict(T=4, K=512, F=640, E=6, k=5, S=1, out="f32"),
+    dict(T=8, K=2048, F=1024, E=70, k=8, bias=True),
+    dict(T=9, K=640, F=384, E=143, k=3),
+    dict(T=26, K=384, F=512, E=59, k=9, S=1, score="sigmoid", out="f32"),
+    dict(T=60, K=2560, F=128, E=20, k=4, S=1, router="f32"),
     dict(T=200, K=384, F=128, E=9, k=2, out="f32", router="f32"),
 ]
 

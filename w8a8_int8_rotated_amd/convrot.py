@@ -1186,6 +1186,18 @@ def convrot_qkv_forward(X: torch.Tensor, W, heads_q: int, heads_kv: int, w_q, w_
 _FLOATS = (torch.bfloat16, torch.float32)
 
 
+def _new(like: torch.Tensor, dtype: torch.dtype) -> torch.Tensor:
+    """A new tensor of the contiguous `like`'s shape (empty_like is the cheaper call)."""
+    return torch.empty_like(like) if like.dtype == dtype else \
+        torch.empty(like.shape, dtype=dtype, device=like.device)
+
+
+def _gpu_of(t: torch.Tensor):
+    """A tensor's device for _on_device; None, so that it refuses the tensor, off the GPU."""
+    d = t.device
+    return d if d.type == "cuda" else None
+
+
 def _norm_args(x, w, residual, residual_out):
     """The checks the forward calls share: (M, K, the residual's dtype or x's)."""
     if not isinstance(x, _Tensor) or x.dim() < 1:
@@ -1216,11 +1228,10 @@ def convrot_add_rms_norm_forward(x: torch.Tensor, w, residual=None, eps: float =
         return _on_stream(convrot_add_rms_norm_forward, locals())
     M, K, rdt = _norm_args(x, w, residual, residual_out)
     _opt(out, "out", _FLOATS, x.shape)
-    dev = x.device
-    _on_device(None, x=x)
-    _on_device(dev, w=w, residual=residual, out=out, residual_out=residual_out)
+    dev = _gpu_of(x)
+    _on_device(dev, x=x, w=w, residual=residual, out=out, residual_out=residual_out)
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype, device=dev)
+        out = _new(x, out_dtype)
     if residual is not None and residual_out is None:
         residual_out = torch.empty_like(residual)
     _launch(dev, "convrot_add_rms_norm_forward", _ptr(x), _dtype_tag(x.dtype), _ptr(residual),
@@ -1241,9 +1252,8 @@ def convrot_add_rms_norm_rotate_quantize(x: torch.Tensor, w, block: int, residua
     _opt(s, "s", torch.float32, (M,))
     if rotation not in ROTATIONS:
         raise ValueError(f"rotation must be one of {sorted(ROTATIONS)}")
-    dev = x.device
-    _on_device(None, x=x)
-    _on_device(dev, w=w, residual=residual, q=q, s=s, residual_out=residual_out)
+    dev = _gpu_of(x)
+    _on_device(dev, x=x, w=w, residual=residual, q=q, s=s, residual_out=residual_out)
     if q is None:
         q = _codes(None, M, K, dev)
     if s is None:
@@ -1269,9 +1279,8 @@ def convrot_add_rms_norm_fp8_quantize(x: torch.Tensor, w, scales: str = "f32", r
     Mp = padded_rows(M)
     _opt(q, "q", torch.uint8, (Mp, K))
     _opt(s, "s", torch.float32, (K // 128, Mp))
-    dev = x.device
-    _on_device(None, x=x)
-    _on_device(dev, w=w, residual=residual, q=q, s=s, residual_out=residual_out)
+    dev = _gpu_of(x)
+    _on_device(dev, x=x, w=w, residual=residual, q=q, s=s, residual_out=residual_out)
     if q is None:
         q = torch.empty((Mp, K), dtype=torch.uint8, device=dev)
     if s is None:
@@ -1357,9 +1366,8 @@ def convrot_add_rms_norm_backward(g: torch.Tensor, h: torch.Tensor, w, g_h=None,
     M = h.numel() // K if K else 0
     wsb = lib.convrot_add_rms_norm_workspace_bytes(M, K) if w is not None else 0
     _check_workspace(wsb, workspace)
-    dev = h.device
-    _on_device(None, h=h)
-    _on_device(dev, g=g, g_h=g_h, w=w, dh=dh, dx=dx, dw=dw, workspace=workspace)
+    dev = _gpu_of(h)
+    _on_device(dev, h=h, g=g, g_h=g_h, w=w, dh=dh, dx=dx, dw=dw, workspace=workspace)
     if dh is None:
         dh = torch.empty_like(h)
     if copy and dx is None:
@@ -1491,7 +1499,7 @@ def convrot_moe_forward(X: torch.Tensor, router: torch.Tensor, W: MoEWeights, to
     _on_device(dev, X=X, router=router, router_bias=router_bias, out=out, ids=ids,
                weights=weights, workspace=workspace)
     if out is None:
-        out = torch.empty((T, K), dtype=out_dtype, device=dev)
+        out = _new(X, out_dtype)
     if ids is None:
         ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
     if weights is None:

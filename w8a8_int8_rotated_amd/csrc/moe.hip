@@ -54,6 +54,7 @@ struct Units {
 };
 
 constexpr int kRouterPieces = 8, kRouterWaves = 8;
+constexpr int kGateWaves = 4, kOwnChoice = kGateWaves;     // tokens that gate_up chooses for itself
 
 struct Layout {
     size_t logits, units, rows, g, partial, bytes;
@@ -342,7 +343,7 @@ __device__ __forceinline__ void gate_up(const Moe &m, int expert, int base, int 
     constexpr int CP = 16 / P;                     // columns of one block
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int waves = blockDim.x >> 6;
+    constexpr int waves = kGateWaves;
     const int ri = r % CP, rj = r / CP;            // the lane's row (of a tile) and block
     const int nkb = m.K >> 7, fb = blockIdx.x;
     const uint32_t in_tile = r * 64 + ((q ^ ((r >> 2) & 3)) << 4);
@@ -412,22 +413,23 @@ __device__ __forceinline__ void gate_up(const Moe &m, int expert, int base, int 
             request(d);
         }
     }
+    // tile by tile, in two buffers in turn: a tile's sums are read before the next but one's
+    // are written
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
-        if (c > 0 && c * 16 >= n) continue;
-        *reinterpret_cast<v4f *>(red + ((wave * 2 + 0) * CT + c) * 256 + lane * 4) = ag[c];
-        *reinterpret_cast<v4f *>(red + ((wave * 2 + 1) * CT + c) * 256 + lane * 4) = au[c];
-    }
-    __syncthreads();
-    for (int c = wave; c * 16 < n; c += waves) {
-        if (rj > 0 || c * 16 + ri >= n) continue;
+        if (c > 0 && c * 16 >= n) break;
+        float *const buf = red + (c & 1) * waves * 512;
+        *reinterpret_cast<v4f *>(buf + (wave * 2 + 0) * 256 + lane * 4) = ag[c];
+        *reinterpret_cast<v4f *>(buf + (wave * 2 + 1) * 256 + lane * 4) = au[c];
+        __syncthreads();
+        if (wave != c || rj > 0 || c * 16 + ri >= n) continue;
         v4f a = (v4f)(0.0f), b = (v4f)(0.0f);
         for (int k = 0; k < waves; ++k)
 #pragma unroll
             for (int j = 0; j < P; ++j) {
-                const float *const p = red + (k * 2 * CT + c) * 256 + (lane + j * CP) * 4;
+                const float *const p = buf + k * 512 + (lane + j * CP) * 4;
                 a += *reinterpret_cast<const v4f *>(p);
-                b += *reinterpret_cast<const v4f *>(p + CT * 256);
+                b += *reinterpret_cast<const v4f *>(p + 256);
             }
         float v[4];
 #pragma unroll
@@ -449,46 +451,77 @@ __device__ __forceinline__ void gate_up(const Moe &m, int expert, int base, int 
 
 // blockIdx.y: with fewer choices than experts a choice, whose expert is taken up where it
 // comes first, else an expert; then the shared ones.  ROWS: the most rows of a unit.
-// EP > 0: one token, whose choice every wave makes.
+// EP > 0: up to kOwnChoice tokens, whose choices the workgroup makes itself, a wave a token
+// (of a single token every wave, and no wave waits for another).
 template <int ROWS, int EP>
-__global__ __launch_bounds__(256, 3) void gate_up_kernel(
+__global__ __launch_bounds__(64 * kGateWaves, 3) void gate_up_kernel(
     Moe m, Units *__restrict__ units, Row *__restrict__ rows, uint16_t *__restrict__ g,
     int64_t plane, const double *__restrict__ logits, int pieces)
 {
-    extern __shared__ float red[];                 // [wave][2][ROWS / 16][256]
+    extern __shared__ float red[];                 // [1 or 2 tiles of 16 rows][wave][2][256]
     __shared__ u64 s_tokens;
     __shared__ int s_less, s_first, s_row[kMoeTokens];
+    __shared__ int s_ids[EP > 0 ? kOwnChoice * kMoeMaxTopK : 1];
+    __shared__ float s_weights[EP > 0 ? kOwnChoice * kMoeMaxTopK : 1];
     const int u = blockIdx.y;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int waves = blockDim.x >> 6;
-    int expert, base, n;
+    int expert = 0, base = 0, n = 0;
+    bool single = false;
     if constexpr (EP > 0) {
-        int id;
-        float w;
-        choose<EP>(m, logits, pieces, 0, id, w);
-        if (lane >= m.top_k) id = m.E + lane - m.top_k, w = 1.0f;
-        expert = __builtin_amdgcn_readlane(id, u);
-        base = u;
-        n = 1;
-        if (blockIdx.x == 0 && u == 0 && wave == 0 && lane < m.top_k + m.S) {
-            units->expert[lane] = id;
-            units->base[lane] = lane;
-            units->tokens[lane] = 1;
-            rows[lane] = {0, w};
-            if (lane < m.top_k) m.ids[lane] = id, m.weights[lane] = w;
+        single = m.T == 1;
+        if (single) {
+            int id;
+            float w;
+            choose<EP>(m, logits, pieces, 0, id, w);
+            if (lane >= m.top_k) id = m.E + lane - m.top_k, w = 1.0f;
+            expert = __builtin_amdgcn_readlane(id, u);
+            base = u;
+            n = 1;
+            if (blockIdx.x == 0 && u == 0 && wave == 0 && lane < m.top_k + m.S) {
+                units->expert[lane] = id;
+                units->base[lane] = lane;
+                units->tokens[lane] = 1;
+                rows[lane] = {0, w};
+                if (lane < m.top_k) m.ids[lane] = id, m.weights[lane] = w;
+            }
         }
-    } else {
+    }
+    if (!single) {
         const int chosen = m.T * m.top_k, routed = min(chosen, m.E);
         const bool shared = u >= routed;
-        expert = shared ? m.E + u - routed : chosen < m.E ? m.ids[u] : u;
+        if constexpr (EP > 0) {
+            if (!shared) {
+                if (wave < m.T) {
+                    int id;
+                    float w;
+                    choose<EP>(m, logits, pieces, wave, id, w);
+                    const int i = wave * m.top_k + lane;
+                    if (lane < m.top_k) {
+                        s_ids[i] = id;
+                        s_weights[i] = w;
+                        if (blockIdx.x == 0 && u == 0) m.ids[i] = id, m.weights[i] = w;
+                    }
+                }
+                __syncthreads();
+            }
+        }
+        auto id_of = [&](int i) {
+            if constexpr (EP > 0) return s_ids[i];
+            else return m.ids[i];
+        };
+        auto weight_of = [&](int i) {
+            if constexpr (EP > 0) return s_weights[i];
+            else return m.weights[i];
+        };
+        expert = shared ? m.E + u - routed : chosen < m.E ? id_of(u) : u;
         u64 tokens = m.T == 64 ? ~0ull : (1ull << m.T) - 1;
         base = chosen + (u - routed) * m.T;
         if (!shared) {
             if (threadIdx.x == 0) s_tokens = 0, s_less = 0, s_first = chosen;
             __syncthreads();
-            for (int i0 = wave * 64; i0 < chosen; i0 += 64 * waves) {
-                const int i = i0 + lane, id = i < chosen ? m.ids[i] : kMaxUnits;
+            for (int i0 = wave * 64; i0 < chosen; i0 += 64 * kGateWaves) {
+                const int i = i0 + lane, id = i < chosen ? id_of(i) : kMaxUnits;
                 const int less = __popcll(__ballot(id < expert));
                 if (lane == 0 && less) atomicAdd(&s_less, less);
                 if (id == expert) {
@@ -510,10 +543,10 @@ __global__ __launch_bounds__(256, 3) void gate_up_kernel(
             if (shared) {
                 if ((int)threadIdx.x < m.T) rows[base + threadIdx.x] = {(int)threadIdx.x, 1.0f};
             } else if (tokens != 0) {
-                for (int i = threadIdx.x; i < chosen; i += blockDim.x) {
+                for (int i = threadIdx.x; i < chosen; i += 64 * kGateWaves) {
                     const int t = i / m.top_k;
-                    if (m.ids[i] == expert)
-                        rows[base + __popcll(tokens & ((1ull << t) - 1))] = {t, m.weights[i]};
+                    if (id_of(i) == expert)
+                        rows[base + __popcll(tokens & ((1ull << t) - 1))] = {t, weight_of(i)};
                 }
             }
         }
@@ -526,7 +559,7 @@ __global__ __launch_bounds__(256, 3) void gate_up_kernel(
     }
     expert = uniform(expert);
     n = uniform(n);
-    const int *const row_token = EP > 0 ? nullptr : s_row;
+    const int *const row_token = single ? nullptr : s_row;
     if (ROWS == 8 || n <= 8) gate_up<1, 2, 2>(m, expert, base, n, row_token, red, g, plane);
     if constexpr (ROWS == 16) {
         if (n > 8) gate_up<1, 3, 1>(m, expert, base, n, row_token, red, g, plane);
@@ -542,35 +575,38 @@ __device__ __forceinline__ int share(int n, int waves, int wave)
     return (int)((int64_t)n * ((int)blockIdx.y * waves + wave) / ((int)gridDim.y * waves));
 }
 
-// The units, compacted into LDS by the whole workgroup: those of up to `light` rows from
-// the front, the others from the back of the same arrays (in reverse order).
+// The units, compacted into LDS by the whole workgroup in three classes by their rows: up to
+// few, up to some, more; class c is order[first[c]] .. order[first[c + 1]].
 struct UnitList {
-    int expert[kMaxUnits], base[kMaxUnits];
     u64 tokens[kMaxUnits];
-    int count, heavy;
+    short expert[kMaxUnits], base[kMaxUnits], order[kMaxUnits];
+    int first[4];
 };
-__device__ __forceinline__ void list_units(const Units *__restrict__ units, int most, int light,
-                                           UnitList &l)
+static_assert(kMoeTokens * (kMoeMaxTopK + kMoeMaxShared) < 32768, "rows fit short");
+__device__ __forceinline__ void list_units(const Units *__restrict__ units, int most, int few,
+                                           int some, UnitList &l)
 {
     const int lane = threadIdx.x & 63;
+    for (int u = threadIdx.x; u < most; u += blockDim.x) {
+        l.tokens[u] = units->tokens[u];
+        l.expert[u] = (short)units->expert[u];
+        l.base[u] = (short)units->base[u];
+    }
+    __syncthreads();
     if (threadIdx.x < 64) {
-        int count = 0, heavy = 0;
-        for (int i = 0; i < most; i += 64) {
-            const int u = i + lane;
-            const u64 tokens = u < most ? units->tokens[u] : 0, below = (1ull << lane) - 1;
-            const bool many = __popcll(tokens) > light;
-            const u64 front = __ballot(tokens != 0 && !many), back = __ballot(many);
-            const int at = many ? kMaxUnits - 1 - heavy - __popcll(back & below)
-                                : count + __popcll(front & below);
-            if (tokens != 0) {
-                l.expert[at] = units->expert[u];
-                l.base[at] = units->base[u];
-                l.tokens[at] = tokens;
+        int at = 0;
+        for (int c = 0; c < 3; ++c) {
+            if (lane == 0) l.first[c] = at;
+            for (int i = 0; i < most; i += 64) {
+                const int u = i + lane;
+                const int n = u < most ? __popcll(l.tokens[u]) : 0;
+                const bool in = c == 0 ? n > 0 && n <= few : c == 1 ? n > few && n <= some : n > some;
+                const u64 have = __ballot(in);
+                if (in) l.order[at + __popcll(have & ((1ull << lane) - 1))] = (short)u;
+                at += __popcll(have);
             }
-            count += __popcll(front);
-            heavy += __popcll(back);
         }
-        if (lane == 0) l.count = count, l.heavy = heavy;
+        if (lane == 0) l.first[3] = at;
     }
     __syncthreads();
 }
@@ -622,8 +658,8 @@ __global__ __launch_bounds__(512, 4) void down_kernel(Moe m, const Units *__rest
     const uint32_t g0 = (uint32_t)(part * plane + q * 16) * 2;
     for (int i = threadIdx.x; i < m.T * (m.top_k + m.S); i += 64 * WAVES)
         weight[i] = rows[i].weight;
-    list_units(units, most, 64, list);
-    const int count = uniform(list.count);
+    list_units(units, most, kMoeTokens, kMoeTokens, list);
+    const int count = uniform(list.first[1]);
 
     v4f acc = (v4f)(0.0f);
     const int total = count * groups;
@@ -635,7 +671,7 @@ __global__ __launch_bounds__(512, 4) void down_kernel(Moe m, const Units *__rest
         float wu = 0.0f;
         bool has = false;
         auto enter = [&] {
-            const int at = min(u, count - 1);
+            const int at = uniform(list.order[min(u, count - 1)]);
             rw = down_rows(m, uniform(list.expert[at]), nb);
             const u64 tokens = uniform(list.tokens[at]);
             has = rj < P && ((tokens >> t) & 1);
@@ -701,18 +737,18 @@ __global__ __launch_bounds__(512, 4) void down_kernel(Moe m, const Units *__rest
 // The same for more tokens.  Columns are the parts of a unit's rows one after another:
 // column p * n + i is part p of row i.  A unit's sums, weighted, are added to the wave's own
 // [T][16] sums in LDS, part by part (two columns of one token are never added at once).
-// Units whose columns fit 16 / P make one sequence of groups of P blocks (columns
-// j * (16 / P) .. belong to the group's block j), of which each wave takes an even share
-// and its ring runs on from unit to unit; the others follow, up to CT tiles of 16 in one
-// pass over their codes.
-template <int D, int P, int PLANES>
+// Units whose columns fit 16 / P, P = 2 or 1, make one sequence of groups of P blocks
+// (columns j * (16 / P) .. belong to the group's block j), of which each wave takes an even
+// share and its ring runs on from unit to unit; the others follow, up to CT tiles of 16 in
+// one pass over their codes.
+template <int PLANES>
 __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *__restrict__ units,
                                                            int most, const Row *__restrict__ rows,
                                                            const uint16_t *__restrict__ g,
                                                            int64_t plane,
                                                            float *__restrict__ partial)
 {
-    constexpr int CT = 4, WAVES = 8, CP = 16 / P;
+    constexpr int CT = 4, WAVES = 8;
     extern __shared__ float red[];                 // [wave][T][16], rows
     __shared__ UnitList list;
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
@@ -725,7 +761,7 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
     for (int i = threadIdx.x; i < m.T * (m.top_k + m.S); i += 64 * WAVES) lrows[i] = rows[i];
     for (int i = lane; i < m.T * 4; i += 64)
         *reinterpret_cast<v4f *>(mine + i * 4) = (v4f)(0.0f);
-    list_units(units, most, CP / PLANES, list);
+    list_units(units, most, PLANES == 1 ? 8 : 0, 16 / PLANES, list);
 
     // adds to the sums of column v of a unit of n rows from `base` on (v past its columns: none)
     auto flush = [&](const v4f &acc, int v, int base, int n) {
@@ -753,11 +789,13 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
                    : kOut;
     };
 
-    const int count = uniform(list.count), heavy = uniform(list.heavy);
-    const int groups = (nkb + P - 1) / P, rj = r / CP;
-    const int light = count * groups;
-    const int i0 = share(light, WAVES, wave), i1 = share(light, WAVES, wave + 1);
-    if (i0 < i1) {
+    // the units of class c, whose columns fit 16 / P
+    auto run = [&](auto p, auto depth, int c) {
+        constexpr int P = decltype(p)::value, D = decltype(depth)::value, CP = 16 / P;
+        const int from = uniform(list.first[c]), count = uniform(list.first[c + 1]) - from;
+        const int groups = (nkb + P - 1) / P, rj = r / CP, total = count * groups;
+        const int i0 = share(total, WAVES, wave), i1 = share(total, WAVES, wave + 1);
+        if (i0 >= i1) return;
         Block a[D][P];
         Cols x[D];
         float f[D];
@@ -765,7 +803,7 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
         DownRows rw;
         uint32_t col = 0;
         auto enter = [&] {
-            const int at = min(u, count - 1);
+            const int at = uniform(list.order[from + min(u, count - 1)]);
             rw = down_rows(m, uniform(list.expert[at]), nb);
             col = column(r % CP, uniform(list.base[at]), __popcll(uniform(list.tokens[at])));
         };
@@ -805,8 +843,9 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
                 request(d);
                 ckb += P;
                 if (ckb >= nkb || i + d + 1 == i1) {
-                    const int base = uniform(list.base[cu]);
-                    const int n = __popcll(uniform(list.tokens[cu]));
+                    const int at = uniform(list.order[from + cu]);
+                    const int base = uniform(list.base[at]);
+                    const int n = __popcll(uniform(list.tokens[at]));
 #pragma unroll
                     for (int j = 0; j < P; ++j)
                         flush(acc, rj == j ? r % CP : PLANES * n, base, n);
@@ -816,13 +855,16 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
                 }
             }
         }
-    }
+    };
+    // (three parts of a row in two groups of columns leave room for two rows only)
+    if constexpr (PLANES == 1) run(std::integral_constant<int, 2>{}, std::integral_constant<int, 2>{}, 0);
+    run(std::integral_constant<int, 1>{}, std::integral_constant<int, 2>{}, 1);
 
-    const int total = heavy * nkb;
+    const int from = uniform(list.first[2]), total = (uniform(list.first[3]) - from) * nkb;
     for (int i = share(total, WAVES, wave), end = share(total, WAVES, wave + 1); i < end;) {
         const int u = i / nkb, kb0 = i - u * nkb, kb1 = min(nkb, kb0 + end - i);
         i += kb1 - kb0;
-        const int at = kMaxUnits - 1 - u;
+        const int at = uniform(list.order[from + u]);
         const DownRows rw = down_rows(m, uniform(list.expert[at]), nb);
         const int base = uniform(list.base[at]), n = __popcll(uniform(list.tokens[at]));
         for (int c0 = 0; c0 < PLANES * n; c0 += 16 * CT) {
@@ -948,12 +990,17 @@ hipError_t launch_moe(const Moe &m, hipStream_t stream)
         else if (m.E <= 256) launch(std::integral_constant<int, 4>{});
         else launch(std::integral_constant<int, 8>{});
     };
-    constexpr int GW = 4;
-    auto gate_up = [&](auto kernel, int tiles) {
-        hipLaunchKernelGGL(kernel, dim3(m.F / 16, most), dim3(64 * GW), GW * 2 * tiles * 1024,
-                           stream, m, units, rows, g, plane, logits, pieces);
+    const int tiles = m.F / 16;
+    auto gate_up = [&](auto kernel, int buffers) {
+        hipLaunchKernelGGL(kernel, dim3(tiles, most), dim3(64 * kGateWaves),
+                           buffers * kGateWaves * 2 * 1024, stream, m, units, rows, g, plane,
+                           logits, pieces);
     };
-    if (m.T == 1) {
+    // The experts' own workgroups choose while they are one round of the CUs (three a CU),
+    // since each pays for it: us a call with that and with the kernel of its own, 3 tokens of
+    // 5 experts of 256 x 896: 23.4, 26.6; 2 tokens of 45 experts, 8 each, of 2944 x 1792 (1792
+    // workgroups): 61.9, 57.3.
+    if (m.T == 1 || (m.T <= kOwnChoice && tiles * most <= 3 * device_cu_count())) {
         by_experts([&](auto ep) { gate_up(gate_up_kernel<8, decltype(ep)::value>, 1); });
     } else {
         by_experts([&](auto ep) {
@@ -962,7 +1009,7 @@ hipError_t launch_moe(const Moe &m, hipStream_t stream)
         });
         if (m.T <= 8) gate_up(gate_up_kernel<8, 0>, 1);
         else if (m.T <= 16) gate_up(gate_up_kernel<16, 0>, 1);
-        else gate_up(gate_up_kernel<64, 0>, 4);
+        else gate_up(gate_up_kernel<64, 0>, 2);
     }
 
     const int parts = down_parts(m);
@@ -972,10 +1019,12 @@ hipError_t launch_moe(const Moe &m, hipStream_t stream)
                            rows, g, plane, partial);
     };
     const size_t many = m.T * (8 * 64 + (m.top_k + m.S) * sizeof(Row));
-    if (m.y_f32) m.T <= 5 ? down(down_kernel<3, 1, 3>, 0) : down(down_many_kernel<2, 1, 3>, many);
+    static_assert(kMoeTokens * (8 * 64 + (kMoeMaxTopK + kMoeMaxShared) * sizeof(Row)) +
+                          sizeof(UnitList) <= 65536, "LDS of down_many_kernel");
+    if (m.y_f32) m.T <= 5 ? down(down_kernel<3, 1, 3>, 0) : down(down_many_kernel<3>, many);
     else if (m.T <= 8) down(down_kernel<1, 2, 1>, 0);
     else if (m.T <= 16) down(down_kernel<3, 1, 1>, 0);
-    else down(down_many_kernel<2, 2, 1>, many);
+    else down(down_many_kernel<1>, many);
     if (parts > 1) {
         const int64_t n = (int64_t)m.T * m.K;
         hipLaunchKernelGGL(join_parts_kernel, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0,
