@@ -634,7 +634,8 @@ CONVROT_API int convrot_fp8_qkv_forward(const void *X, int64_t B, int64_t T,
  *   n = (h * rsqrt(mean(h^2) + eps)) * w.
  * All sums and products are fp32; h is rounded first and everything after uses the
  * rounded value, so the norm of a stored h has the same bits.  (The sum of squares is
- * fp32 too: channels beyond about 1e18 / sqrt(K) overflow it.)
+ * fp32 too: a row whose root mean square is beyond about 1.8e19 / sqrt(K) overflows it and
+ * has outputs of 0 or NaN.)
  *   x, residual   device [M, K], dense; x_dtype and res_dtype CONVROT_BF16 or _F32
  *                 (an fp32 x takes an fp32 residual).  residual and residual_out may
  *                 both be NULL: no addition (res_dtype is not looked at).
@@ -685,7 +686,7 @@ CONVROT_API int convrot_fp8_norm_linear_forward(const void *x, int x_dtype, cons
                                                 void *stream);
 
 /* The backward pass.  With q = rsqrt(mean(h^2) + eps), t = g w:
- *   dh = g_h + q t - h q^3 mean(t h);   dw = sum over rows of g h q.
+ *   dh = g_h + q (t - h q mean(t h q));   dw = sum over rows of g h q.
  *   g     the gradient of n [M, K] (BF16 or F32); h as the forward stored it (x where
  *         there was no residual); g_h: the gradient that reaches h along the residual
  *         stream, of h's type, or NULL.
@@ -718,8 +719,8 @@ CONVROT_API int convrot_add_rms_norm_backward(const void *g, int g_dtype, const 
  * g to bf16, F32 outputs carry it in fp32.  Experts that no token chose are not read.
  * The choice and the weights of a token do not depend on the other tokens; its output
  * can differ in the last bits of the fp32 sums between batches.  Calls of the same
- * arguments repeat bit for bit.  A token with a NaN or an infinity has NaN outputs and
- * leaves the others alone.
+ * arguments repeat bit for bit.  A token with a NaN or an infinity has outputs that are NaN
+ * or infinite and leaves the others alone.
  * Any T: the experts' codes are read once for every 64 tokens, which suits few tokens. */
 #define CONVROT_MOE_MAGIC 0x454f4d43u /* "CMOE" little-endian */
 #define CONVROT_MOE_VERSION 1u

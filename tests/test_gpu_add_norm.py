@@ -125,12 +125,34 @@ def test_non_finite_rows_stay_alone(cr, bad):
     assert torch.equal(y0[others], y1[others]) and torch.equal(h0[others], h1[others])
     assert bool(y1[4].isnan().any()) and bool(y1[5].isnan().any())
     W = cr.convrot_linear_prepare_weights(rows(3, 256, K, F32) * 0.02, 128)
-    F = cr.convrot_fp8_prepare_weights(rows(3, 256, K, F32) * 0.02)
-    for weights in (W, F):
-        a, _ = cr.convrot_norm_linear_forward(x, w, weights, r)
-        b, _ = cr.convrot_norm_linear_forward(xb, w, weights, r)
-        assert torch.equal(a[others], b[others])
-        assert bool(b[4].isnan().all()) and bool(b[5].isnan().all())
+    F, P = (cr.convrot_fp8_prepare_weights(rows(3, 256, K, F32) * 0.02, scales=s)
+            for s in ("f32", "pow2"))
+    for weights in (W, F, P):
+        for n in (M, 9):                             # tiles, and the kernels for few rows
+            for out in (BF16, F32):
+                a, _ = cr.convrot_norm_linear_forward(x[:n], w, weights, r[:n], out_dtype=out)
+                b, _ = cr.convrot_norm_linear_forward(xb[:n], w, weights, r[:n], out_dtype=out)
+                assert torch.equal(a[others[:n - 2]], b[others[:n - 2]])
+                assert bool(b[4].isnan().all()) and bool(b[5].isnan().all())
+
+
+@pytest.mark.parametrize("eps", [1e-30, 1e-38, 2e-45])
+def test_tiny_eps(cr, eps):
+    """A zero row is 0 times a large number, forward and backward, not 0 times infinity."""
+    K = 256
+    x, w, g = torch.zeros(3, K, device="cuda"), weight(K), rows(1, 3, K, F32) * 1e-9
+    x[1] = 1e-25
+    x[2, 3] = -2.0
+    y, _ = cr.convrot_add_rms_norm_forward(x, w, eps=eps, out_dtype=F32)
+    assert bool((y[0] == 0).all()) and bool(y.isfinite().all())
+    dh, _, dw = cr.convrot_add_rms_norm_backward(g, x, w, eps=eps)
+    assert not bool(dh.isnan().any()) and bool(dw.isfinite().all())
+    v = x[2].double()
+    q = 1 / ((v * v).mean() + eps).sqrt()
+    t = g[2].double() * w.double()
+    d = q * (t - v * q * (t * v * q).mean())
+    size = q * (t.abs() + (v * q).abs() * (t * v * q).abs().mean())
+    assert bool(((dh[2].double() - d).abs() <= size * 2.0 ** -15 + 2.0 ** -130).all())
 
 
 BLOCKS = [(64, "sylvester"), (128, "sylvester"), (256, "sylvester"), (64, "regular"),
@@ -425,3 +447,15 @@ def test_offsets_past_32_bits(cr):
     dh, _, dw = cr.convrot_add_rms_norm_backward(y, h, None, g_h=h, dh=h)
     d2, _, _ = cr.convrot_add_rms_norm_backward(a, b, None, g_h=b)
     assert torch.equal(dh[-4:], d2) and dw is None
+
+
+def test_more_rows_than_a_grid_dimension_holds(cr):
+    """A grid of more than 2^32 threads in a row: every row against a second call in parts."""
+    M, K = 2 ** 27 + 37, 8
+    x = torch.empty(M, K, dtype=BF16, device="cuda")
+    x.view(torch.int16).copy_(torch.arange(K, device="cuda", dtype=torch.int16) + 0x3f80)
+    x[:, 3] = (torch.arange(M, device="cuda") % 251).to(BF16)
+    y, _ = cr.convrot_add_rms_norm_forward(x, None)
+    for at in range(0, M, 2 ** 25 + 8):
+        part, _ = cr.convrot_add_rms_norm_forward(x[at:at + 2 ** 25 + 8], None)
+        assert torch.equal(y[at:at + 2 ** 25 + 8], part)

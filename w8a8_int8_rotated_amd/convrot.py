@@ -1187,7 +1187,9 @@ _FLOATS = (torch.bfloat16, torch.float32)
 
 
 def _new(like: torch.Tensor, dtype: torch.dtype) -> torch.Tensor:
-    """A new tensor of the contiguous `like`'s shape (empty_like is the cheaper call)."""
+    """A new output of the contiguous `like`'s shape (empty_like is the cheaper call)."""
+    if dtype not in _FLOATS:
+        raise ValueError(f"out_dtype must be bfloat16 or float32, got {dtype}")
     return torch.empty_like(like) if like.dtype == dtype else \
         torch.empty(like.shape, dtype=dtype, device=like.device)
 
@@ -1319,6 +1321,8 @@ def convrot_norm_linear_forward(x: torch.Tensor, w, W, residual=None, bias=None,
     _on_device(dev, x=x, w=w, residual=residual, bias=bias, out=out, residual_out=residual_out,
                workspace=workspace)
     if out is None:
+        if out_dtype not in _FLOATS:
+            raise ValueError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
         out = torch.empty(shape, dtype=out_dtype, device=dev)
     if residual is not None and residual_out is None:
         residual_out = torch.empty_like(residual)

@@ -5,13 +5,17 @@
 //              out: n (bf16 or fp32), or the codes that the INT8 or the FP8 linear
 //              multiplies: v = H_b n, amax, rint(v 127 / amax); or per 128 channels
 //              e4m3(n / s)
-//   backward:  t = g w;  dh = gh + q t - h q^3 mean(t h);  dw = sum_m g h q
+//   backward:  t = g w;  dh = gh + q (t - h q mean(t h q));  dw = sum_m g h q
 //
 // Bound: memory.  Every row is read once and every result written once; h is held
 // in registers between its sum of squares and its use.  All arithmetic is fp32; h is
 // rounded to its own type first and everything after uses the rounded value, so the
 // norm of a stored h gives the same bits.  8-bit outputs are quantised from the fp32
 // n, without a rounding to bf16 in between.
+//
+// Measured (us; K = 5376, bf16 rows beside an fp32 residual stream): 38656 rows forward 414
+// (6.0 TB/s of 12 bytes a channel), to INT8 codes 411 (5.6 TB/s), backward with bf16
+// gradients and dx 582 (5.7 TB/s of 16 bytes); 5 rows 3.5, a launch's length.
 #include "add_norm.hpp"
 
 #include "fp8_common.hpp"
@@ -137,7 +141,8 @@ __global__ __launch_bounds__(1024) void add_norm_kernel(AddNorm a, int W)
     const int grp = wave / W, part = wave - grp * W, pairs = waves / W;
     const int K = a.K, steps = (K + 255) >> 8;
     const int mine = (steps - part + W - 1) / W;     // steps of this wave
-    const int64_t row0 = 2 * ((int64_t)blockIdx.x * pairs + grp), row = row0 + half;
+    const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    const int64_t row0 = 2 * (block * pairs + grp), row = row0 + half;
     const int64_t first = row0 < a.M ? row0 : 0;
     const int rows = row0 < a.M ? (int)min(a.M - row0, (int64_t)2) : 0;
     const bool in = row < a.M;
@@ -315,7 +320,10 @@ void launch_steps(const AddNorm &a, hipStream_t stream)
     const int steps = (a.K + 255) / 256;
     const int spr = steps <= 32 ? 2 : steps <= 64 ? 4 : 8;
     const int W = (steps + spr - 1) / spr, pairs = std::max(1, 4 / W);
-    const dim3 grid((unsigned)((a.M + 2 * pairs - 1) / (2 * pairs))), block(64 * W * pairs);
+    // a grid dimension holds less than 2^32 threads
+    const int64_t blocks = (a.M + 2 * pairs - 1) / (2 * pairs), kWide = 1 << 21;
+    const dim3 grid((unsigned)std::min(blocks, kWide), (unsigned)((blocks + kWide - 1) / kWide));
+    const dim3 block(64 * W * pairs);
     auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a, W); };
     if (spr == 2) {
         const int bytes = (XF ? 4 : 2) + (a.r ? RF ? 8 : 4 : 0) + (a.y_f32 ? 4 : 2);
@@ -449,7 +457,8 @@ __global__ __launch_bounds__(1024) void add_norm_grad_kernel(AddNormGrad a, int 
             }
         }
         const float q = rsqrtf(s1 * invK + a.eps);
-        const float c = (s2 * invK) * (q * q) * q;
+        // (through h q, which is bounded: q^3 need not be finite)
+        const float c = (s2 * invK) * q;
         const __amdgpu_buffer_rsrc_t ds = row_of(a.dh, row, HS);
         const __amdgpu_buffer_rsrc_t xs = a.dx ? row_of(a.dx, row, 2) : row_rsrc(a.dh, 0);
         const __amdgpu_buffer_rsrc_t ms = row_of(more ? a.gh : a.h, row, HS);
@@ -467,9 +476,9 @@ __global__ __launch_bounds__(1024) void add_norm_grad_kernel(AddNormGrad a, int 
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                dw[t][j] = __builtin_fmaf(gv[j], hv[j] * q, dw[t][j]);
-                d[j] = __builtin_fmaf(gv[j] * (LEAN ? w[j] : wk[LEAN ? 0 : t][j]), q,
-                                      -(hv[j] * c));
+                const float hq = hv[j] * q;
+                dw[t][j] = __builtin_fmaf(gv[j], hq, dw[t][j]);
+                d[j] = q * __builtin_fmaf(-hq, c, gv[j] * (LEAN ? w[j] : wk[LEAN ? 0 : t][j]));
                 if (more) d[j] += m[j];
             }
             store8<true, AUX>(narrow<HF>(d), ds, e0[t], e1[t]);

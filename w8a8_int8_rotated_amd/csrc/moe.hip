@@ -18,12 +18,17 @@
 // which hold an fp32 value exactly.
 //
 // Loads.  A wave keeps a ring of D blocks of codes with their columns in registers: the
-// next block is requested as soon as one is used.  All loads of the ring go through
-// buffer resources, so that those past the end or of idle columns need no branch (they
-// read zeros, without memory traffic) and the compiler can count them.
+// next block is requested as soon as one is used.  Idle columns read past the end of a
+// buffer resource, which gives zeros without a branch; blocks past the wave's share are not
+// requested at all (a request past the end takes its turn all the same: 5 tokens of 46
+// experts 89 us with those, 82 without).
 //
-// Kernels: router (partial logits over pieces of K), choose (a wave a token), gate_up,
-// down.  For one token every wave of gate_up makes the choice itself.
+// Kernels: router (partial logits over pieces of K), choose (a wave a token; for a few
+// tokens gate_up's workgroups choose for themselves), gate_up, down, and where down was
+// split a join.  Measured, the kernels of a call and in brackets the chosen experts' codes
+// at the 5.1 TB/s of a large copy, us: 64 tokens, 6 of 64 experts of 5376 x 1408 each: 280
+// [283]; 5 tokens, 4 of 32 of them and a shared one: 85 [74]; one token, 8 of 128 experts of
+// 2048 x 768: 20.5 [7.5], three launches whose shortest takes 4.2.
 #include "moe.hpp"
 
 #include "fp8_common.hpp"
