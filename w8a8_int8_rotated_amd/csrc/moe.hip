@@ -47,7 +47,10 @@ constexpr int kMaxUnits = kMoeMaxExperts + kMoeMaxShared;
 
 // A unit is an expert and the tokens that chose it.  gate_up finds its unit in the choices
 // and leaves it here for down.  Rows of g: an expert's lie behind those of the experts
-// before it, in the order of its tokens; the shared experts' behind all of them.
+// before it, in the order of its tokens; the shared experts' behind all of them.  In memory a
+// unit's n rows are [F / 128][16 pieces][n][8 inputs]: a block of 128 inputs is one run, and so
+// is a piece of all rows (a load takes its time for the cache lines that it touches; row by
+// row each lane of 16 touches one of its own).
 struct Row {
     int token;
     float weight;
@@ -299,13 +302,14 @@ __device__ __forceinline__ Block load_block(__amdgpu_buffer_rsrc_t p, uint32_t o
     return {load16(p, off), load16(p, off + 1024)};
 }
 
-// 16 columns' inputs of a block of 128: four pieces of 8 a lane.
+// 16 columns' inputs of a block of 128: four pieces of 8 a lane, step bytes apart.
 struct Cols {
     v4i u[4];
 };
-__device__ __forceinline__ Cols load_cols(__amdgpu_buffer_rsrc_t p, uint32_t off)
+__device__ __forceinline__ Cols load_cols(__amdgpu_buffer_rsrc_t p, uint32_t off, uint32_t step)
 {
-    return {{load16(p, off), load16(p, off + 16), load16(p, off + 128), load16(p, off + 144)}};
+    return {{load16(p, off), load16(p, off + step), load16(p, off + 8 * step),
+             load16(p, off + 9 * step)}};
 }
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -384,7 +388,7 @@ __device__ __forceinline__ void gate_up(const Moe &m, int expert, int base, int 
             b[d][j] = load_block(up, at);
         }
         const int kb = next + rj;
-        x[d] = load_cols(xs, kb < nkb && ri < n ? col[0] + kb * 256 : kOut);
+        x[d] = load_cols(xs, kb < nkb && ri < n ? col[0] + kb * 256 : kOut, 16);
         fg[d] = load4(gate_scale, kb < nkb ? kb * 4 : kOut);
         fu[d] = load4(up_scale, kb < nkb ? kb * 4 : kOut);
         next += step;
@@ -404,7 +408,8 @@ __device__ __forceinline__ void gate_up(const Moe &m, int expert, int base, int 
                     if (c > 0 && c * 16 >= n) continue;
                     const int kb = k0 + d * step;
                     if (c > 0)
-                        x[d] = load_cols(xs, kb < nkb && c * 16 + r < n ? col[c] + kb * 256 : kOut);
+                        x[d] = load_cols(xs, kb < nkb && c * 16 + r < n ? col[c] + kb * 256 : kOut,
+                                         16);
                     const v4f pg = block_sum(wg, x[d]);
                     const v4f pu = block_sum(wu, x[d]);
                     const bool on = rj == j;
@@ -439,7 +444,8 @@ __device__ __forceinline__ void gate_up(const Moe &m, int expert, int base, int 
         float v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = a[i] / (1.0f + expf(-a[i])) * b[i];
-        uint16_t *p = g + (int64_t)(base + c * 16 + r) * m.F + fb * 16 + q * 4;
+        uint16_t *p = g + (int64_t)base * m.F +
+                      ((fb * 2 + (q >> 1)) * n + c * 16 + r) * 8 + (q & 1) * 4;
         // the part that bf16 holds; for F32 outputs what it leaves, twice more
         for (int part = 1;; ++part) {
             const uint2 o = make_uint2(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]));
@@ -660,7 +666,7 @@ __global__ __launch_bounds__(512, 4) void down_kernel(Moe m, const Units *__rest
     const int nkb = m.F >> 7, nb = blockIdx.x, groups = (nkb + P - 1) / P;
     const uint32_t in_tile = r * 64 + ((q ^ ((r >> 2) & 3)) << 4);
     const __amdgpu_buffer_rsrc_t gs = range_of(g, (uint32_t)(plane * 2 * PLANES));
-    const uint32_t g0 = (uint32_t)(part * plane + q * 16) * 2;
+    const uint32_t g0 = (uint32_t)(part * plane) * 2;
     for (int i = threadIdx.x; i < m.T * (m.top_k + m.S); i += 64 * WAVES)
         weight[i] = rows[i].weight;
     list_units(units, most, kMoeTokens, kMoeTokens, list);
@@ -672,7 +678,7 @@ __global__ __launch_bounds__(512, 4) void down_kernel(Moe m, const Units *__rest
     if (i0 < i1) {
         int u = i0 / groups, kb = (i0 - u * groups) * P, left = i1 - i0;
         DownRows rw;
-        uint32_t col = 0;
+        uint32_t col = 0, piece = 0;
         float wu = 0.0f;
         bool has = false;
         auto enter = [&] {
@@ -680,9 +686,11 @@ __global__ __launch_bounds__(512, 4) void down_kernel(Moe m, const Units *__rest
             rw = down_rows(m, uniform(list.expert[at]), nb);
             const u64 tokens = uniform(list.tokens[at]);
             has = rj < P && ((tokens >> t) & 1);
-            const int row = uniform(list.base[at]) + __popcll(tokens & ((1ull << t) - 1));
-            wu = has ? weight[row] : 0.0f;
-            col = g0 + (uint32_t)row * (uint32_t)m.F * 2;
+            const int base = uniform(list.base[at]);
+            const int row = __popcll(tokens & ((1ull << t) - 1));
+            wu = has ? weight[base + row] : 0.0f;
+            piece = __popcll(tokens) * 16;
+            col = g0 + (uint32_t)base * (uint32_t)m.F * 2 + 2 * q * piece + row * 16;
         };
         enter();
         Block a[D][P];
@@ -695,7 +703,7 @@ __global__ __launch_bounds__(512, 4) void down_kernel(Moe m, const Units *__rest
             for (int j = 0; j < P; ++j)
                 a[d][j] = load_block(rw.codes, kb + j < nkb ? (kb + j) * 2048 + in_tile : kOut);
             on[d] = has && kb + rj < nkb;
-            x[d] = load_cols(gs, on[d] ? col + (kb + rj) * 256 : kOut);
+            x[d] = load_cols(gs, on[d] ? col + (kb + rj) * 16 * piece : kOut, piece);
             f[d] = load4(rw.scale, on[d] ? (kb + rj) * 4 : kOut);
             w[d] = wu;
             --left;
@@ -742,10 +750,14 @@ __global__ __launch_bounds__(512, 4) void down_kernel(Moe m, const Units *__rest
 // The same for more tokens.  Columns are the parts of a unit's rows one after another:
 // column p * n + i is part p of row i.  A unit's sums, weighted, are added to the wave's own
 // [T][16] sums in LDS, part by part (two columns of one token are never added at once).
-// Units whose columns fit 16 / P, P = 2 or 1, make one sequence of groups of P blocks
-// (columns j * (16 / P) .. belong to the group's block j), of which each wave takes an even
-// share and its ring runs on from unit to unit; the others follow, up to CT tiles of 16 in
-// one pass over their codes.
+// Units whose columns fit 8 (one part) make one sequence of groups of two blocks (columns
+// 8 .. 15 belong to the group's second block), those whose columns fit two tiles of 16 one of
+// single blocks; of a sequence each wave takes an even share and its ring runs on from unit
+// to unit.  The others follow, up to CT tiles in one pass over their codes.  Bound: memory
+// and what a wave can keep in flight beside the columns: 64 tokens, 6 of 64 experts of
+// 5376 x 1408: bf16 102 us (4.8 TB/s of codes), F32 185.  (Units of two tiles outside the
+// ring, a block at a time: F32 215; 64 tokens, 8 of 24 experts of 4096 x 1024, bf16: a call
+// of 127 us, 116 so.)
 template <int PLANES>
 __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *__restrict__ units,
                                                            int most, const Row *__restrict__ rows,
@@ -766,11 +778,18 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
     for (int i = threadIdx.x; i < m.T * (m.top_k + m.S); i += 64 * WAVES) lrows[i] = rows[i];
     for (int i = lane; i < m.T * 4; i += 64)
         *reinterpret_cast<v4f *>(mine + i * 4) = (v4f)(0.0f);
-    list_units(units, most, PLANES == 1 ? 8 : 0, 16 / PLANES, list);
+    list_units(units, most, PLANES == 1 ? 8 : 0, 32 / PLANES, list);
 
+    // the part that column v of a unit of n rows belongs to (PLANES or more: none)
+    auto part_of = [](int v, int n) {
+        int part = 0;
+#pragma unroll
+        for (int p = 1; p <= PLANES; ++p) part += v >= p * n;
+        return part;
+    };
     // adds to the sums of column v of a unit of n rows from `base` on (v past its columns: none)
     auto flush = [&](const v4f &acc, int v, int base, int n) {
-        const int part = v / n;
+        const int part = part_of(v, n);
         const Row row = lrows[base + (part < PLANES ? v - part * n : 0)];
 #pragma unroll
         for (int p = 0; p < PLANES; ++p) {
@@ -788,29 +807,36 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
     };
     // byte offset of column v of such a unit, at its first block
     auto column = [&](int v, int base, int n) -> uint32_t {
-        const int part = v / n;
+        const int part = part_of(v, n);
         return part < PLANES
-                   ? (uint32_t)(part * plane + (int64_t)(base + v - part * n) * m.F + q * 16) * 2
+                   ? (uint32_t)(part * plane + (int64_t)base * m.F) * 2 +
+                         (2 * q * n + v - part * n) * 16
                    : kOut;
     };
 
-    // the units of class c, whose columns fit 16 / P
-    auto run = [&](auto p, auto depth, int c) {
-        constexpr int P = decltype(p)::value, D = decltype(depth)::value, CP = 16 / P;
+    // the units of class c, whose columns fit 16 / P, with P = 1 also two tiles of 16
+    auto run = [&](auto p, int c) {
+        constexpr int P = decltype(p)::value, D = 2, CP = 16 / P, TILES = P == 1 ? 2 : 1;
         const int from = uniform(list.first[c]), count = uniform(list.first[c + 1]) - from;
         const int groups = (nkb + P - 1) / P, rj = r / CP, total = count * groups;
         const int i0 = share(total, WAVES, wave), i1 = share(total, WAVES, wave + 1);
         if (i0 >= i1) return;
         Block a[D][P];
-        Cols x[D];
+        Cols x[D][TILES];
         float f[D];
+        bool two[D];                                   // the block's unit takes two tiles
         int u = i0 / groups, kb = (i0 - u * groups) * P, left = i1 - i0;   // to request
         DownRows rw;
-        uint32_t col = 0;
+        uint32_t col[TILES], piece = 0;
+        bool wide = false;
         auto enter = [&] {
             const int at = uniform(list.order[from + min(u, count - 1)]);
             rw = down_rows(m, uniform(list.expert[at]), nb);
-            col = column(r % CP, uniform(list.base[at]), __popcll(uniform(list.tokens[at])));
+            const int base = uniform(list.base[at]), n = __popcll(uniform(list.tokens[at]));
+            piece = n * 16;
+            wide = TILES > 1 && PLANES * n > 16;
+#pragma unroll
+            for (int c = 0; c < TILES; ++c) col[c] = column(c * 16 + r % CP, base, n);
         };
         enter();
         int cu = u, ckb = kb;                                              // in use
@@ -820,7 +846,12 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
             for (int j = 0; j < P; ++j)
                 a[d][j] = load_block(rw.codes, kb + j < nkb ? (kb + j) * 2048 + in_tile : kOut);
             const bool on = kb + rj < nkb;
-            x[d] = load_cols(gs, on && col != kOut ? col + (kb + rj) * 256 : kOut);
+            two[d] = wide;
+#pragma unroll
+            for (int c = 0; c < TILES; ++c)
+                if (c == 0 || wide)
+                    x[d][c] = load_cols(
+                        gs, on && col[c] != kOut ? col[c] + (kb + rj) * 16 * piece : kOut, piece);
             f[d] = load4(rw.scale, on ? (kb + rj) * 4 : kOut);
             --left;
             kb += P;
@@ -833,17 +864,25 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
         };
 #pragma unroll
         for (int d = 0; d < D; ++d) request(d);
-        v4f acc = (v4f)(0.0f);
+        v4f acc[TILES];
+#pragma unroll
+        for (int c = 0; c < TILES; ++c) acc[c] = (v4f)(0.0f);
         for (int i = i0; i < i1; i += D) {
 #pragma unroll
             for (int d = 0; d < D; ++d) {
                 if (i + d >= i1) break;
+                const bool both = two[d];
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
-                    const v4f s = block_sum(widen(a[d][j]), x[d]);
+                    const Wide w = widen(a[d][j]);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        acc[k] = rj == j ? __builtin_fmaf(s[k], f[d], acc[k]) : acc[k];
+                    for (int c = 0; c < TILES; ++c) {
+                        if (c > 0 && !both) continue;
+                        const v4f s = block_sum(w, x[d][c]);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            acc[c][k] = rj == j ? __builtin_fmaf(s[k], f[d], acc[c][k]) : acc[c][k];
+                    }
                 }
                 request(d);
                 ckb += P;
@@ -851,10 +890,17 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
                     const int at = uniform(list.order[from + cu]);
                     const int base = uniform(list.base[at]);
                     const int n = __popcll(uniform(list.tokens[at]));
+                    if constexpr (P == 2) {
 #pragma unroll
-                    for (int j = 0; j < P; ++j)
-                        flush(acc, rj == j ? r % CP : PLANES * n, base, n);
-                    acc = (v4f)(0.0f);
+                        for (int k = 0; k < 4; ++k)            // columns 8 apart: row_ror:8
+                            acc[0][k] += __int_as_float(CR_DPP_I(__float_as_int(acc[0][k]), 0x128));
+                    }
+#pragma unroll
+                    for (int c = 0; c < TILES; ++c) {
+                        if (c > 0 && !both) continue;
+                        flush(acc[c], rj == 0 ? c * 16 + r : PLANES * n, base, n);
+                        acc[c] = (v4f)(0.0f);
+                    }
                     ckb = 0;
                     ++cu;
                 }
@@ -862,8 +908,8 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
         }
     };
     // (three parts of a row in two groups of columns leave room for two rows only)
-    if constexpr (PLANES == 1) run(std::integral_constant<int, 2>{}, std::integral_constant<int, 2>{}, 0);
-    run(std::integral_constant<int, 1>{}, std::integral_constant<int, 2>{}, 1);
+    if constexpr (PLANES == 1) run(std::integral_constant<int, 2>{}, 0);
+    run(std::integral_constant<int, 1>{}, 1);
 
     const int from = uniform(list.first[2]), total = (uniform(list.first[3]) - from) * nkb;
     for (int i = share(total, WAVES, wave), end = share(total, WAVES, wave + 1); i < end;) {
@@ -886,7 +932,7 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
                 Cols x[CT];
 #pragma unroll
                 for (int c = 0; c < CT; ++c)
-                    x[c] = load_cols(gs, col[c] != kOut ? col[c] + kb * 256 : kOut);
+                    x[c] = load_cols(gs, col[c] != kOut ? col[c] + kb * 256 * n : kOut, n * 16);
                 const Wide w = widen(a);
                 const float fk = f;
                 const bool more = kb + 1 < kb1;
