@@ -48,9 +48,10 @@ constexpr int kMaxUnits = kMoeMaxExperts + kMoeMaxShared;
 // A unit is an expert and the tokens that chose it.  gate_up finds its unit in the choices
 // and leaves it here for down.  Rows of g: an expert's lie behind those of the experts
 // before it, in the order of its tokens; the shared experts' behind all of them.  In memory a
-// unit's n rows are [F / 128][16 pieces][n][8 inputs]: a block of 128 inputs is one run, and so
-// is a piece of all rows (a load takes its time for the cache lines that it touches; row by
-// row each lane of 16 touches one of its own).
+// unit's n rows, in `planes` parts of bf16 each (one, or three for F32 outputs), are
+// [F / 8][planes][n][8]: a block of 128 inputs is one run of memory, and 8 inputs of all rows
+// are neighbours in it.  (A load takes its time for the cache lines that it touches; row by
+// row each of 16 lanes touches one of its own.  down of 64 tokens so 94.5 us, 102 by rows.)
 struct Row {
     int token;
     float weight;
@@ -346,7 +347,7 @@ __device__ __forceinline__ v4f block_sum(const Wide &a, const Cols &b)
 template <int CT, int D, int P>
 __device__ __forceinline__ void gate_up(const Moe &m, int expert, int base, int n,
                                         const int *row_token, float *red,
-                                        uint16_t *__restrict__ g, int64_t plane)
+                                        uint16_t *__restrict__ g)
 {
     static_assert(CT == 1 || P == 1, "");
     constexpr int CP = 16 / P;                     // columns of one block
@@ -444,18 +445,19 @@ __device__ __forceinline__ void gate_up(const Moe &m, int expert, int base, int 
         float v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = a[i] / (1.0f + expf(-a[i])) * b[i];
-        uint16_t *p = g + (int64_t)base * m.F +
-                      ((fb * 2 + (q >> 1)) * n + c * 16 + r) * 8 + (q & 1) * 4;
+        const int planes = m.y_f32 ? 3 : 1;
+        uint16_t *p = g + (int64_t)base * planes * m.F +
+                      ((fb * 2 + (q >> 1)) * planes * n + c * 16 + r) * 8 + (q & 1) * 4;
         // the part that bf16 holds; for F32 outputs what it leaves, twice more
         for (int part = 1;; ++part) {
             const uint2 o = make_uint2(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]));
             *reinterpret_cast<uint2 *>(p) = o;
-            if (part == (m.y_f32 ? 3 : 1)) break;
+            if (part == planes) break;
             v[0] -= bf16_lo(o.x);
             v[1] -= bf16_hi(o.x);
             v[2] -= bf16_lo(o.y);
             v[3] -= bf16_hi(o.y);
-            p += plane;
+            p += n * 8;
         }
     }
 }
@@ -467,7 +469,7 @@ __device__ __forceinline__ void gate_up(const Moe &m, int expert, int base, int 
 template <int ROWS, int EP>
 __global__ __launch_bounds__(64 * kGateWaves, 3) void gate_up_kernel(
     Moe m, Units *__restrict__ units, Row *__restrict__ rows, uint16_t *__restrict__ g,
-    int64_t plane, const double *__restrict__ logits, int pieces)
+    const double *__restrict__ logits, int pieces)
 {
     extern __shared__ float red[];                 // [1 or 2 tiles of 16 rows][wave][2][256]
     __shared__ u64 s_tokens;
@@ -571,12 +573,12 @@ __global__ __launch_bounds__(64 * kGateWaves, 3) void gate_up_kernel(
     expert = uniform(expert);
     n = uniform(n);
     const int *const row_token = single ? nullptr : s_row;
-    if (ROWS == 8 || n <= 8) gate_up<1, 2, 2>(m, expert, base, n, row_token, red, g, plane);
+    if (ROWS == 8 || n <= 8) gate_up<1, 2, 2>(m, expert, base, n, row_token, red, g);
     if constexpr (ROWS == 16) {
-        if (n > 8) gate_up<1, 3, 1>(m, expert, base, n, row_token, red, g, plane);
+        if (n > 8) gate_up<1, 3, 1>(m, expert, base, n, row_token, red, g);
     } else if constexpr (ROWS == 64) {
-        if (n > 16) gate_up<4, 1, 1>(m, expert, base, n, row_token, red, g, plane);
-        else if (n > 8) gate_up<1, 3, 1>(m, expert, base, n, row_token, red, g, plane);
+        if (n > 16) gate_up<4, 1, 1>(m, expert, base, n, row_token, red, g);
+        else if (n > 8) gate_up<1, 3, 1>(m, expert, base, n, row_token, red, g);
     }
 }
 
@@ -654,7 +656,7 @@ template <int D, int P, int PLANES>
 __global__ __launch_bounds__(512, 4) void down_kernel(Moe m, const Units *__restrict__ units,
                                                       int most, const Row *__restrict__ rows,
                                                       const uint16_t *__restrict__ g,
-                                                      int64_t plane, float *__restrict__ partial)
+                                                      float *__restrict__ partial)
 {
     constexpr int WAVES = 8, CP = 16 / (P * PLANES);
     __shared__ float red[WAVES * 256];
@@ -665,8 +667,7 @@ __global__ __launch_bounds__(512, 4) void down_kernel(Moe m, const Units *__rest
     const int t = r % CP, part = r / CP % PLANES, rj = r / CP / PLANES;
     const int nkb = m.F >> 7, nb = blockIdx.x, groups = (nkb + P - 1) / P;
     const uint32_t in_tile = r * 64 + ((q ^ ((r >> 2) & 3)) << 4);
-    const __amdgpu_buffer_rsrc_t gs = range_of(g, (uint32_t)(plane * 2 * PLANES));
-    const uint32_t g0 = (uint32_t)(part * plane) * 2;
+    const __amdgpu_buffer_rsrc_t gs = range_of(g, m.T * (m.top_k + m.S) * m.F * 2 * PLANES);
     for (int i = threadIdx.x; i < m.T * (m.top_k + m.S); i += 64 * WAVES)
         weight[i] = rows[i].weight;
     list_units(units, most, kMoeTokens, kMoeTokens, list);
@@ -689,8 +690,9 @@ __global__ __launch_bounds__(512, 4) void down_kernel(Moe m, const Units *__rest
             const int base = uniform(list.base[at]);
             const int row = __popcll(tokens & ((1ull << t) - 1));
             wu = has ? weight[base + row] : 0.0f;
-            piece = __popcll(tokens) * 16;
-            col = g0 + (uint32_t)base * (uint32_t)m.F * 2 + 2 * q * piece + row * 16;
+            const int n = __popcll(tokens);
+            piece = PLANES * n * 16;
+            col = base * m.F * 2 * PLANES + 2 * q * piece + (part * n + row) * 16;
         };
         enter();
         Block a[D][P];
@@ -762,7 +764,6 @@ template <int PLANES>
 __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *__restrict__ units,
                                                            int most, const Row *__restrict__ rows,
                                                            const uint16_t *__restrict__ g,
-                                                           int64_t plane,
                                                            float *__restrict__ partial)
 {
     constexpr int CT = 4, WAVES = 8;
@@ -772,7 +773,7 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nkb = m.F >> 7, nb = blockIdx.x;
     const uint32_t in_tile = r * 64 + ((q ^ ((r >> 2) & 3)) << 4);
-    const __amdgpu_buffer_rsrc_t gs = range_of(g, (uint32_t)(plane * 2 * PLANES));
+    const __amdgpu_buffer_rsrc_t gs = range_of(g, m.T * (m.top_k + m.S) * m.F * 2 * PLANES);
     float *const mine = red + wave * m.T * 16;
     Row *const lrows = reinterpret_cast<Row *>(red + WAVES * m.T * 16);
     for (int i = threadIdx.x; i < m.T * (m.top_k + m.S); i += 64 * WAVES) lrows[i] = rows[i];
@@ -807,10 +808,8 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
     };
     // byte offset of column v of such a unit, at its first block
     auto column = [&](int v, int base, int n) -> uint32_t {
-        const int part = part_of(v, n);
-        return part < PLANES
-                   ? (uint32_t)(part * plane + (int64_t)base * m.F) * 2 +
-                         (2 * q * n + v - part * n) * 16
+        return v < PLANES * n
+                   ? (uint32_t)(base * m.F * 2 * PLANES + (2 * q * PLANES * n + v) * 16)
                    : kOut;
     };
 
@@ -833,7 +832,7 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
             const int at = uniform(list.order[from + min(u, count - 1)]);
             rw = down_rows(m, uniform(list.expert[at]), nb);
             const int base = uniform(list.base[at]), n = __popcll(uniform(list.tokens[at]));
-            piece = n * 16;
+            piece = PLANES * n * 16;
             wide = TILES > 1 && PLANES * n > 16;
 #pragma unroll
             for (int c = 0; c < TILES; ++c) col[c] = column(c * 16 + r % CP, base, n);
@@ -918,6 +917,7 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
         const int at = uniform(list.order[from + u]);
         const DownRows rw = down_rows(m, uniform(list.expert[at]), nb);
         const int base = uniform(list.base[at]), n = __popcll(uniform(list.tokens[at]));
+        const uint32_t piece = PLANES * n * 16;
         for (int c0 = 0; c0 < PLANES * n; c0 += 16 * CT) {
             v4f acc[CT];
             uint32_t col[CT];
@@ -932,7 +932,7 @@ __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *_
                 Cols x[CT];
 #pragma unroll
                 for (int c = 0; c < CT; ++c)
-                    x[c] = load_cols(gs, col[c] != kOut ? col[c] + kb * 256 * n : kOut, n * 16);
+                    x[c] = load_cols(gs, col[c] != kOut ? col[c] + kb * 16 * piece : kOut, piece);
                 const Wide w = widen(a);
                 const float fk = f;
                 const bool more = kb + 1 < kb1;
@@ -1028,7 +1028,6 @@ hipError_t launch_moe(const Moe &m, hipStream_t stream)
     Units *const units = reinterpret_cast<Units *>(ws + l.units);
     Row *const rows = reinterpret_cast<Row *>(ws + l.rows);
     uint16_t *const g = reinterpret_cast<uint16_t *>(ws + l.g);
-    const int64_t plane = (int64_t)m.T * (m.top_k + m.S) * m.F;
     const int most = std::min(m.T * m.top_k, m.E) + m.S;      // units
 
     // at most two runs of 32 inputs a wave up to K = 4096
@@ -1044,7 +1043,7 @@ hipError_t launch_moe(const Moe &m, hipStream_t stream)
     const int tiles = m.F / 16;
     auto gate_up = [&](auto kernel, int buffers) {
         hipLaunchKernelGGL(kernel, dim3(tiles, most), dim3(64 * kGateWaves),
-                           buffers * kGateWaves * 2 * 1024, stream, m, units, rows, g, plane,
+                           buffers * kGateWaves * 2 * 1024, stream, m, units, rows, g,
                            logits, pieces);
     };
     // The experts' own workgroups choose while they are one round of the CUs (three a CU),
@@ -1067,7 +1066,7 @@ hipError_t launch_moe(const Moe &m, hipStream_t stream)
     float *const partial = parts > 1 ? reinterpret_cast<float *>(ws + l.partial) : nullptr;
     auto down = [&](auto kernel, size_t lds) {
         hipLaunchKernelGGL(kernel, dim3(m.K / 16, parts), dim3(512), lds, stream, m, units, most,
-                           rows, g, plane, partial);
+                           rows, g, partial);
     };
     const size_t many = m.T * (8 * 64 + (m.top_k + m.S) * sizeof(Row));
     static_assert(kMoeTokens * (8 * 64 + (kMoeMaxTopK + kMoeMaxShared) * sizeof(Row)) +
