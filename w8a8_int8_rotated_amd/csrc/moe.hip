@@ -45,8 +45,8 @@ typedef unsigned long long u64;
 
 constexpr int kMaxUnits = kMoeMaxExperts + kMoeMaxShared;
 
-// A unit is an expert and the tokens that chose it.  gate_up finds its unit in the choices
-// and leaves it here for down.  Rows of g: an expert's lie behind those of the experts
+// A unit is an expert and the tokens that chose it: choose leaves a set of tokens for every
+// expert, gate_up finds its unit from them and leaves it here for down.  Rows of g: an expert's lie behind those of the experts
 // before it, in the order of its tokens; the shared experts' behind all of them.  In memory a
 // unit's n rows, in `planes` parts of bf16 each (one, or three for F32 outputs), are
 // [F / 8][planes][n][8]: a block of 128 inputs is one run of memory, and 8 inputs of all rows
@@ -66,7 +66,7 @@ constexpr int kRouterPieces = 8, kRouterWaves = 8;
 constexpr int kGateWaves = 4, kOwnChoice = kGateWaves;     // tokens that gate_up chooses for itself
 
 struct Layout {
-    size_t logits, units, rows, g, partial, bytes;
+    size_t logits, sets, units, rows, g, partial, bytes;
 };
 
 // ------------------------------------------------------------- router ----
@@ -75,8 +75,11 @@ struct Layout {
 // inputs 8 q .. 8 q + 7 of a run of expert r and of token r, one of them per product.
 template <bool RF32>
 __global__ __launch_bounds__(64 * kRouterWaves) void router_kernel(Moe m,
-                                                                   double *__restrict__ logits)
+                                                                   double *__restrict__ logits,
+                                                                   u64 *__restrict__ sets)
 {
+    if (blockIdx.x + blockIdx.y + blockIdx.z == 0)        // choose sets bits in them
+        for (int e = threadIdx.x; e < m.E; e += 64 * kRouterWaves) sets[e] = 0;
     __shared__ double red[kRouterWaves][256];
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4, wave = threadIdx.x >> 6;
     const int e0 = blockIdx.x * 16, t0 = blockIdx.z * 16, runs = m.K >> 5;
@@ -141,6 +144,15 @@ __device__ __forceinline__ double wave_sum(double v)
                                                   __builtin_amdgcn_readlane(u.y, l)));
     }
     return s;
+}
+__device__ __forceinline__ int wave_sum(int v)
+{
+    v += CR_DPP_I(v, 0xB1);
+    v += CR_DPP_I(v, 0x4E);
+    v += CR_DPP_I(v, 0x141);
+    v += CR_DPP_I(v, 0x140);
+    return (__builtin_amdgcn_readlane(v, 0) + __builtin_amdgcn_readlane(v, 16)) +
+           (__builtin_amdgcn_readlane(v, 32) + __builtin_amdgcn_readlane(v, 48));
 }
 __device__ __forceinline__ uint32_t wave_max(uint32_t v)
 {
@@ -265,7 +277,7 @@ __device__ __forceinline__ void choose(const Moe &m, const double *__restrict__ 
 
 template <int EP>
 __global__ __launch_bounds__(64) void choose_kernel(Moe m, const double *__restrict__ logits,
-                                                    int pieces)
+                                                    int pieces, u64 *__restrict__ sets)
 {
     int id;
     float w;
@@ -274,6 +286,7 @@ __global__ __launch_bounds__(64) void choose_kernel(Moe m, const double *__restr
     if (lane >= m.top_k) return;
     m.ids[(int64_t)blockIdx.x * m.top_k + lane] = id;
     m.weights[(int64_t)blockIdx.x * m.top_k + lane] = w;
+    atomicOr(sets + id, 1ull << blockIdx.x);               // bits: no order
 }
 
 // ------------------------------------------------------------ experts ----
@@ -342,11 +355,11 @@ __device__ __forceinline__ v4f block_sum(const Wide &a, const Cols &b)
 // g of one unit: a workgroup takes 16 gate and the same 16 up channels, its waves the
 // groups of P blocks of K in turn.  Columns are the unit's n rows, from row `base` of g on,
 // in up to CT tiles of 16; with P > 1 (up to 16 / P rows) column j * (16 / P) + i is row i's
-// part of the group's block j, so that one set of columns serves P blocks.  row_token: the
-// rows' tokens (null: token 0).
+// part of the group's block j, so that one set of columns serves P blocks.  token: of row
+// `lane`.
 template <int CT, int D, int P>
 __device__ __forceinline__ void gate_up(const Moe &m, int expert, int base, int n,
-                                        const int *row_token, float *red,
+                                        int token, float *red,
                                         uint16_t *__restrict__ g)
 {
     static_assert(CT == 1 || P == 1, "");
@@ -368,10 +381,10 @@ __device__ __forceinline__ void gate_up(const Moe &m, int expert, int base, int 
 
     uint32_t col[CT];
 #pragma unroll
-    for (int c = 0; c < CT; ++c)
-        col[c] = c * 16 + ri < n
-                     ? (uint32_t)((row_token ? row_token[c * 16 + ri] : 0) * m.K + q * 16) * 2
-                     : kOut;
+    for (int c = 0; c < CT; ++c) {
+        const int from = __shfl(token, c * 16 + ri, 64);
+        col[c] = c * 16 + ri < n ? (uint32_t)(from * m.K + q * 16) * 2 : kOut;
+    }
     v4f ag[CT], au[CT];
 #pragma unroll
     for (int c = 0; c < CT; ++c) ag[c] = au[c] = (v4f)(0.0f);
@@ -469,117 +482,85 @@ __device__ __forceinline__ void gate_up(const Moe &m, int expert, int base, int 
 template <int ROWS, int EP>
 __global__ __launch_bounds__(64 * kGateWaves, 3) void gate_up_kernel(
     Moe m, Units *__restrict__ units, Row *__restrict__ rows, uint16_t *__restrict__ g,
-    const double *__restrict__ logits, int pieces)
+    const double *__restrict__ logits, int pieces, const u64 *__restrict__ sets)
 {
     extern __shared__ float red[];                 // [1 or 2 tiles of 16 rows][wave][2][256]
-    __shared__ u64 s_tokens;
-    __shared__ int s_less, s_first, s_row[kMoeTokens];
     __shared__ int s_ids[EP > 0 ? kOwnChoice * kMoeMaxTopK : 1];
     __shared__ float s_weights[EP > 0 ? kOwnChoice * kMoeMaxTopK : 1];
-    const int u = blockIdx.y;
+    const int u = blockIdx.y, chosen = m.T * m.top_k, routed = min(chosen, m.E);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int expert = 0, base = 0, n = 0;
-    bool single = false;
+    const bool shared = u >= routed, single = EP > 0 && m.T == 1;
+    int expert = m.E + u - routed, base = chosen + (u - routed) * m.T;
+    u64 tokens = m.T == 64 ? ~0ull : (1ull << m.T) - 1;
+    int id = 0;
+    float weight = 1.0f;
     if constexpr (EP > 0) {
-        single = m.T == 1;
-        if (single) {
-            int id;
-            float w;
-            choose<EP>(m, logits, pieces, 0, id, w);
-            if (lane >= m.top_k) id = m.E + lane - m.top_k, w = 1.0f;
-            expert = __builtin_amdgcn_readlane(id, u);
-            base = u;
-            n = 1;
-            if (blockIdx.x == 0 && u == 0 && wave == 0 && lane < m.top_k + m.S) {
-                units->expert[lane] = id;
-                units->base[lane] = lane;
-                units->tokens[lane] = 1;
-                rows[lane] = {0, w};
-                if (lane < m.top_k) m.ids[lane] = id, m.weights[lane] = w;
-            }
-        }
-    }
-    if (!single) {
-        const int chosen = m.T * m.top_k, routed = min(chosen, m.E);
-        const bool shared = u >= routed;
-        if constexpr (EP > 0) {
-            if (!shared) {
-                if (wave < m.T) {
-                    int id;
-                    float w;
-                    choose<EP>(m, logits, pieces, wave, id, w);
+        if (!shared) {
+            if (single || wave < m.T) choose<EP>(m, logits, pieces, single ? 0 : wave, id, weight);
+            if (single) {
+                expert = __builtin_amdgcn_readlane(id, u);
+                weight = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(weight), u));
+                base = u;
+            } else {
+                if (wave < m.T && lane < m.top_k) {
                     const int i = wave * m.top_k + lane;
-                    if (lane < m.top_k) {
-                        s_ids[i] = id;
-                        s_weights[i] = w;
-                        if (blockIdx.x == 0 && u == 0) m.ids[i] = id, m.weights[i] = w;
-                    }
+                    s_ids[i] = id;
+                    s_weights[i] = weight;
+                    if (blockIdx.x == 0 && u == 0) m.ids[i] = id, m.weights[i] = weight;
                 }
                 __syncthreads();
-            }
-        }
-        auto id_of = [&](int i) {
-            if constexpr (EP > 0) return s_ids[i];
-            else return m.ids[i];
-        };
-        auto weight_of = [&](int i) {
-            if constexpr (EP > 0) return s_weights[i];
-            else return m.weights[i];
-        };
-        expert = shared ? m.E + u - routed : chosen < m.E ? id_of(u) : u;
-        u64 tokens = m.T == 64 ? ~0ull : (1ull << m.T) - 1;
-        base = chosen + (u - routed) * m.T;
-        if (!shared) {
-            if (threadIdx.x == 0) s_tokens = 0, s_less = 0, s_first = chosen;
-            __syncthreads();
-            for (int i0 = wave * 64; i0 < chosen; i0 += 64 * kGateWaves) {
-                const int i = i0 + lane, id = i < chosen ? id_of(i) : kMaxUnits;
-                const int less = __popcll(__ballot(id < expert));
-                if (lane == 0 && less) atomicAdd(&s_less, less);
-                if (id == expert) {
-                    atomicOr(&s_tokens, 1ull << (i / m.top_k));
-                    atomicMin(&s_first, i);
-                }
-            }
-            __syncthreads();
-            tokens = s_tokens;
-            base = s_less;
-            if (chosen < m.E && s_first != u) tokens = 0;
-        }
-        if (blockIdx.x == 0) {
-            if (threadIdx.x == 0) {
-                units->expert[u] = expert;
-                units->base[u] = base;
-                units->tokens[u] = tokens;
-            }
-            if (shared) {
-                if ((int)threadIdx.x < m.T) rows[base + threadIdx.x] = {(int)threadIdx.x, 1.0f};
-            } else if (tokens != 0) {
-                for (int i = threadIdx.x; i < chosen; i += 64 * kGateWaves) {
-                    const int t = i / m.top_k;
-                    if (id_of(i) == expert)
-                        rows[base + __popcll(tokens & ((1ull << t) - 1))] = {t, weight_of(i)};
+                expert = uniform(chosen < m.E ? s_ids[u] : u);
+                tokens = 0;
+                base = 0;
+                for (int i0 = 0; i0 < chosen; i0 += 64) {
+                    const int i = i0 + lane, e = i < chosen ? s_ids[i] : kMaxUnits;
+                    base += __popcll(__ballot(e < expert));
+                    for (u64 hit = __ballot(e == expert); hit; hit &= hit - 1)
+                        tokens |= 1ull << ((i0 + __builtin_ctzll(hit)) / m.top_k);
                 }
             }
         }
-        if (tokens == 0) return;
-        n = __popcll(tokens);
-        // the tokens of the rows
-        if ((int)threadIdx.x < m.T && ((tokens >> threadIdx.x) & 1))
-            s_row[__popcll(tokens & ((1ull << threadIdx.x) - 1))] = threadIdx.x;
-        __syncthreads();
+    } else if (!shared) {
+        if (chosen < m.E) expert = uniform(m.ids[u]);
+        else expert = u;
+        tokens = uniform(sets[expert]);
+        int before = 0;
+        for (int e = lane; e < expert; e += 64) before += __popcll(sets[e]);
+        base = wave_sum(before);
     }
-    expert = uniform(expert);
-    n = uniform(n);
-    const int *const row_token = single ? nullptr : s_row;
-    if (ROWS == 8 || n <= 8) gate_up<1, 2, 2>(m, expert, base, n, row_token, red, g);
+    // a choice whose expert an earlier token chose too is not a unit of its own
+    if (!shared && !single && chosen < m.E && tokens != 0 && __builtin_ctzll(tokens) != u / m.top_k)
+        tokens = 0;
+    const int n = uniform((int)__popcll(tokens));
+    const int rank = __popcll(tokens & ((1ull << lane) - 1));
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        units->expert[u] = expert;
+        units->base[u] = base;
+        units->tokens[u] = tokens;
+    }
+    if (tokens == 0) return;
+    // lane i gets the token of row i (the lanes of no row go behind them)
+    const int to = (tokens >> lane) & 1 ? rank : n + lane - rank;
+    const int token = __builtin_amdgcn_ds_permute(to * 4, lane);
+    if (ROWS == 8 || n <= 8) gate_up<1, 2, 2>(m, expert, base, n, token, red, g);
     if constexpr (ROWS == 16) {
-        if (n > 8) gate_up<1, 3, 1>(m, expert, base, n, row_token, red, g);
+        if (n > 8) gate_up<1, 3, 1>(m, expert, base, n, token, red, g);
     } else if constexpr (ROWS == 64) {
-        if (n > 16) gate_up<4, 1, 1>(m, expert, base, n, row_token, red, g);
-        else if (n > 8) gate_up<1, 3, 1>(m, expert, base, n, row_token, red, g);
+        if (n > 16) gate_up<4, 1, 1>(m, expert, base, n, token, red, g);
+        else if (n > 8) gate_up<1, 3, 1>(m, expert, base, n, token, red, g);
     }
+    // the unit's rows for down
+    if (blockIdx.x > 0 || wave > 0 || lane >= m.T || !((tokens >> lane) & 1)) return;
+    if (!shared && !single)
+        for (int j = lane * m.top_k; j < (lane + 1) * m.top_k; ++j) {
+            const int e = EP > 0 ? s_ids[j] : m.ids[j];
+            const float w = EP > 0 ? s_weights[j] : m.weights[j];
+            if (e == expert) weight = w;
+        }
+    else if (single && !shared)
+        m.ids[u] = expert, m.weights[u] = weight;
+    rows[base + rank] = {lane, weight};
 }
 
 // This wave's share of n things: of all waves of the workgroups that sum the same outputs.
@@ -983,7 +964,8 @@ Layout moe_layout(int T, int E, int S, int top_k, int K, int F)
     const size_t rows = (size_t)T * (top_k + S);
     Layout l;
     l.logits = 0;
-    l.units = l.logits + up((size_t)kRouterPieces * T * E * 8);
+    l.sets = l.logits + up((size_t)kRouterPieces * T * E * 8);
+    l.units = l.sets + up((size_t)E * 8);
     l.rows = l.units + up(sizeof(Units));
     l.g = l.rows + up(rows * sizeof(Row));
     l.partial = l.g + up(3 * rows * F * 2);
@@ -1025,6 +1007,7 @@ hipError_t launch_moe(const Moe &m, hipStream_t stream)
     const Layout l = moe_layout(m.T, m.E, m.S, m.top_k, m.K, m.F);
     char *const ws = static_cast<char *>(m.ws);
     double *const logits = reinterpret_cast<double *>(ws + l.logits);
+    u64 *const sets = reinterpret_cast<u64 *>(ws + l.sets);
     Units *const units = reinterpret_cast<Units *>(ws + l.units);
     Row *const rows = reinterpret_cast<Row *>(ws + l.rows);
     uint16_t *const g = reinterpret_cast<uint16_t *>(ws + l.g);
@@ -1034,7 +1017,7 @@ hipError_t launch_moe(const Moe &m, hipStream_t stream)
     const int pieces = std::min(kRouterPieces, (m.K / 32 + 2 * kRouterWaves - 1) / (2 * kRouterWaves));
     hipLaunchKernelGGL(m.router_f32 ? router_kernel<true> : router_kernel<false>,
                        dim3((m.E + 15) / 16, pieces, (m.T + 15) / 16), dim3(64 * kRouterWaves), 0,
-                       stream, m, logits);
+                       stream, m, logits, sets);
     auto by_experts = [&](auto launch) {
         if (m.E <= 128) launch(std::integral_constant<int, 2>{});
         else if (m.E <= 256) launch(std::integral_constant<int, 4>{});
@@ -1044,7 +1027,7 @@ hipError_t launch_moe(const Moe &m, hipStream_t stream)
     auto gate_up = [&](auto kernel, int buffers) {
         hipLaunchKernelGGL(kernel, dim3(tiles, most), dim3(64 * kGateWaves),
                            buffers * kGateWaves * 2 * 1024, stream, m, units, rows, g,
-                           logits, pieces);
+                           logits, pieces, sets);
     };
     // The experts' own workgroups choose while they are one round of the CUs (three a CU),
     // since each pays for it: us a call with that and with the kernel of its own, 3 tokens of
@@ -1055,7 +1038,7 @@ hipError_t launch_moe(const Moe &m, hipStream_t stream)
     } else {
         by_experts([&](auto ep) {
             hipLaunchKernelGGL((choose_kernel<decltype(ep)::value>), dim3(m.T), dim3(64), 0,
-                               stream, m, logits, pieces);
+                               stream, m, logits, pieces, sets);
         });
         if (m.T <= 8) gate_up(gate_up_kernel<8, 0>, 1);
         else if (m.T <= 16) gate_up(gate_up_kernel<16, 0>, 1);
