@@ -26,9 +26,9 @@
 // Kernels: router (partial logits over pieces of K), choose (a wave a token; for a few
 // tokens gate_up's workgroups choose for themselves), gate_up, down, and where down was
 // split a join.  Measured, the kernels of a call and in brackets the chosen experts' codes
-// at the 5.1 TB/s of a large copy, us: 64 tokens, 6 of 64 experts of 5376 x 1408 each: 280
+// at the 5.1 TB/s of a large copy, us: 64 tokens, 6 of 64 experts of 5376 x 1408 each: 272
 // [283]; 5 tokens, 4 of 32 of them and a shared one: 85 [74]; one token, 8 of 128 experts of
-// 2048 x 768: 20.5 [7.5], three launches whose shortest takes 4.2.
+// 2048 x 768: 20.9 [7.5], three launches whose shortest takes 4.4.
 #include "moe.hpp"
 
 #include "fp8_common.hpp"
@@ -738,9 +738,8 @@ __global__ __launch_bounds__(512, 4) void down_kernel(Moe m, const Units *__rest
 // single blocks; of a sequence each wave takes an even share and its ring runs on from unit
 // to unit.  The others follow, up to CT tiles in one pass over their codes.  Bound: memory
 // and what a wave can keep in flight beside the columns: 64 tokens, 6 of 64 experts of
-// 5376 x 1408: bf16 102 us (4.8 TB/s of codes), F32 185.  (Units of two tiles outside the
-// ring, a block at a time: F32 215; 64 tokens, 8 of 24 experts of 4096 x 1024, bf16: a call
-// of 127 us, 116 so.)
+// 5376 x 1408: bf16 95 us (5.1 TB/s of codes), F32 outputs 143.  (Units of two tiles outside
+// the ring, a block at a time: F32 205, with g by rows then; 175 in the ring.)
 template <int PLANES>
 __global__ __launch_bounds__(512, 4) void down_many_kernel(Moe m, const Units *__restrict__ units,
                                                            int most, const Row *__restrict__ rows,
