@@ -122,6 +122,10 @@ CASES = [
     dict(T=26, K=384, F=512, E=59, k=9, S=1, score="sigmoid", out="f32"),
     dict(T=60, K=2560, F=128, E=20, k=4, S=1, router="f32"),
     dict(T=200, K=384, F=128, E=9, k=2, out="f32", router="f32"),
+    dict(T=3, K=256, F=128, E=300, k=32),
+    dict(T=4, K=384, F=128, E=40, k=32, S=2, bias=True),
+    dict(T=37, K=640, F=384, E=12, k=3, S=1, out="f32"),
+    dict(T=64, K=512, F=640, E=8, k=3),
 ]
 
 
