@@ -389,7 +389,7 @@ __device__ __forceinline__ void gate_up(const Moe &m, int expert, int base, int 
 #pragma unroll
     for (int c = 0; c < CT; ++c) ag[c] = au[c] = (v4f)(0.0f);
     Block a[D][P], b[D][P];
-    Cols x[D];
+    Cols x[D][CT];
     float fg[D], fu[D];
     const int step = waves * P;
     int next = wave * P;                           // the group to request
@@ -402,7 +402,10 @@ __device__ __forceinline__ void gate_up(const Moe &m, int expert, int base, int 
             b[d][j] = load_block(up, at);
         }
         const int kb = next + rj;
-        x[d] = load_cols(xs, kb < nkb && ri < n ? col[0] + kb * 256 : kOut, 16);
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+            if (c == 0 || c * 16 < n)
+                x[d][c] = load_cols(xs, kb < nkb && c * 16 + ri < n ? col[c] + kb * 256 : kOut, 16);
         fg[d] = load4(gate_scale, kb < nkb ? kb * 4 : kOut);
         fu[d] = load4(up_scale, kb < nkb ? kb * 4 : kOut);
         next += step;
@@ -416,23 +419,22 @@ __device__ __forceinline__ void gate_up(const Moe &m, int expert, int base, int 
             if (k0 + d * step >= nkb) break;
 #pragma unroll
             for (int j = 0; j < P; ++j) {
-                const Wide wg = widen(a[d][j]), wu = widen(b[d][j]);
+                const bool on = rj == j;
+                // gate, then up: one of them widened at a time
+                auto add = [&](const Block &codes, float f, v4f (&acc)[CT]) {
+                    const Wide w = widen(codes);
 #pragma unroll
-                for (int c = 0; c < CT; ++c) {
-                    if (c > 0 && c * 16 >= n) continue;
-                    const int kb = k0 + d * step;
-                    if (c > 0)
-                        x[d] = load_cols(xs, kb < nkb && c * 16 + r < n ? col[c] + kb * 256 : kOut,
-                                         16);
-                    const v4f pg = block_sum(wg, x[d]);
-                    const v4f pu = block_sum(wu, x[d]);
-                    const bool on = rj == j;
+                    for (int c = 0; c < CT; ++c) {
+                        if (c > 0 && c * 16 >= n) continue;
+                        const v4f s = block_sum(w, x[d][c]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        ag[c][i] = on ? __builtin_fmaf(pg[i], fg[d], ag[c][i]) : ag[c][i];
-                        au[c][i] = on ? __builtin_fmaf(pu[i], fu[d], au[c][i]) : au[c][i];
+                        for (int i = 0; i < 4; ++i)
+                            acc[c][i] = on ? __builtin_fmaf(s[i], f, acc[c][i]) : acc[c][i];
                     }
-                }
+                };
+                add(a[d][j], fg[d], ag);
+                if constexpr (CT > 1) __builtin_amdgcn_sched_barrier(0);
+                add(b[d][j], fu[d], au);
             }
             request(d);
         }
@@ -543,11 +545,15 @@ __global__ __launch_bounds__(64 * kGateWaves, 3) void gate_up_kernel(
     // lane i gets the token of row i (the lanes of no row go behind them)
     const int to = (tokens >> lane) & 1 ? rank : n + lane - rank;
     const int token = __builtin_amdgcn_ds_permute(to * 4, lane);
+    // the deepest rings that 168 registers hold (three waves a SIMD): 64 tokens, 2 of 8 experts
+    // of 4096 x 2048, us with two tiles in the ring and with the further tiles loaded where they
+    // are used: 32.7, 40
     if (ROWS == 8 || n <= 8) gate_up<1, 2, 2>(m, expert, base, n, token, red, g);
     if constexpr (ROWS == 16) {
         if (n > 8) gate_up<1, 3, 1>(m, expert, base, n, token, red, g);
     } else if constexpr (ROWS == 64) {
-        if (n > 16) gate_up<4, 1, 1>(m, expert, base, n, token, red, g);
+        if (n > 32) gate_up<4, 1, 1>(m, expert, base, n, token, red, g);
+        else if (n > 16) gate_up<2, 2, 1>(m, expert, base, n, token, red, g);
         else if (n > 8) gate_up<1, 3, 1>(m, expert, base, n, token, red, g);
     }
     // the unit's rows for down
