@@ -1,4 +1,4 @@
-"""The INT8 product for up to 16 rows: equal bits to the integer definition and, row by row,
+"""The INT8 product for up to 64 rows: equal bits to the integer definition and, row by row,
 to the tiled kernel (a call of more rows), over its row tiles a workgroup and ragged ends."""
 import numpy as np
 import pytest
@@ -19,7 +19,8 @@ def cr():
 # N: one, two and four blocks of 16 outputs a workgroup on 256 CUs, and blocks left over in the
 # last; K: fewer 64-wide tiles than waves, ragged shares, many
 SHAPES = [(16, 128), (48, 256), (4096, 128), (4112, 640), (8208, 384), (16400, 256), (16128, 5376),
-          (21520, 128), (528, 65536 // 2)]
+          (21520, 128), (528, 65536 // 2),
+          (24592, 256)]
 
 
 @pytest.mark.parametrize("bias", [False, True])
@@ -32,15 +33,16 @@ def test_against_integers_and_the_tiled_kernel(cr, N, K, out, bias):
     W = cr.convrot_linear_prepare_weights(codes, 64, src_scale=torch.rand(N, generator=g,
                                                                           device="cuda") * 1e-3)
     b = torch.randn(N, generator=g, device="cuda") if bias else None
-    for M in (1, 5, 16):
+    for M in (1, 5, 16, 17, 32, 33, 50, 64):
         announce(f"few rows M={M} N={N} K={K} {out} bias={bias}")
-        q = rng.integers(-127, 128, (17, K)).astype(np.int8)
-        s = to_dev(rng.random(17).astype(np.float32))
-        tiled = to_dev(tile(q))                       # 17 rows: the tiled kernel
-        few = tiled.reshape(-1)[:16 * K].clone().view(16, K)
-        if M < 16:                                    # padding rows may hold anything
+        q = rng.integers(-127, 128, (65, K)).astype(np.int8)
+        s = to_dev(rng.random(65).astype(np.float32))
+        tiled = to_dev(tile(q))                       # 65 rows: the tiled kernel
+        Mp = padded_rows(M)
+        few = tiled.reshape(-1)[:Mp * K].clone().view(Mp, K)
+        if M < Mp:                                    # padding rows may hold anything
             flat = few.reshape(-1)
-            flat[torch.from_numpy(tiled_index(16, K)[M:].reshape(-1)).cuda()] = -128
+            flat[torch.from_numpy(tiled_index(Mp, K)[M:].reshape(-1)).cuda()] = -128
         whole = torch.full((M + 2, N), 7.0, dtype=out, device="cuda")
         y = cr.convrot_gemm_dequant(few, s[:M].contiguous(), W, b, out=whole[:M])
         assert bool((whole[M:] == 7).all())
@@ -55,10 +57,10 @@ def test_against_integers_and_the_tiled_kernel(cr, N, K, out, bias):
 def test_linear_few_rows(cr):
     """The whole linear: a row alone equals the same row of a larger batch."""
     K, N = 1280, 528
-    x = torch.randn(40, K, device="cuda").to(torch.bfloat16)
+    x = torch.randn(70, K, device="cuda").to(torch.bfloat16)
     W = cr.convrot_linear_prepare_weights(torch.randn(N, K, device="cuda") * 0.02, 128)
     b = torch.randn(N, device="cuda")
     full = cr.convrot_linear_forward(x, W, bias=b)
-    for M in (1, 2, 15, 16):
+    for M in (1, 2, 15, 16, 17, 33, 64):
         assert torch.equal(cr.convrot_linear_forward(x[:M].contiguous(), W, bias=b), full[:M])
     assert padded_rows(16) == 16

@@ -61,13 +61,11 @@ int hip_status(hipError_t e)
     return CONVROT_EHIP;
 }
 
-// A product of codes with the plain epilogue.  Up to kFewRows rows in the kernel for few rows;
-// 16 rows there and in tiles, us a call: K = 5376, N = 5376, 16128, 32256: 11.3, 18.0; 16.6,
-// 32.3; 31.1, 38.8; K = 21504, N = 5376: 25.2, 104; K = 2048, N = 4096: the call's 11.2 either way.
+// The kernel for few rows where it is the faster one; the bits are the same.
 hipError_t product_i8(const int8_t *qx, const float *sx, int64_t M, const convrot_weights *W,
                       const float *bias, void *Y, int y_dtype, hipStream_t s)
 {
-    if (M <= kFewRows)
+    if (few_rows(M, W->N))
         return launch_gemm_i8_few(qx, W->codes, sx, W->scale, bias, Y, y_dtype == CONVROT_F32, M,
                                   W->N, W->K, s);
     return launch_gemm_i8(qx, W->codes, sx, W->scale, bias, Y, out_kind(y_dtype), M, W->N, W->K, s);
