@@ -981,8 +981,8 @@ Layout moe_layout(int T, int E, int S, int top_k, int K, int F)
 // Parts of the units whose sums a second kernel joins: the CUs hold two workgroups each,
 // and a round that they do not fill reads more slowly.  64 tokens, 64 experts of
 // K = 5376, F = 1408 (336 workgroups a part), us with 1, 2, 3, 4, 6 parts and without the
-// join (5 us): 143, 120, 114, 126, 124; 23 tokens, 40 experts of K = 2560, F = 640, F32 (160
-// workgroups a part): 33.8, 35.9, 27.4, 32.0, 32.8.  The bytes are those of the experts that
+// join (5 us): 120, 101, 95, 103, 101; 23 tokens, 40 experts of K = 2560, F = 640, F32 (160
+// workgroups a part): 25.5, 25.9, 20.8, 23.2, 23.1.  The bytes are those of the experts that
 // the tokens are expected to choose.
 int down_parts(const Moe &m)
 {
@@ -1036,8 +1036,8 @@ hipError_t launch_moe(const Moe &m, hipStream_t stream)
     };
     // The experts' own workgroups choose while they are one round of the CUs (three a CU),
     // since each pays for it: us a call with that and with the kernel of its own, 3 tokens of
-    // 5 experts of 256 x 896: 23.4, 26.6; 2 tokens of 45 experts, 8 each, of 2944 x 1792 (1792
-    // workgroups): 61.9, 57.3.
+    // 5 experts of 256 x 896: 21.7, 25.2; 2 tokens of 45 experts, 8 each, of 2944 x 1792 (1792
+    // workgroups): 62.2, 57.8.
     if (m.T == 1 || (m.T <= kOwnChoice && tiles * most <= 3 * device_cu_count())) {
         by_experts([&](auto ep) { gate_up(gate_up_kernel<8, decltype(ep)::value>, 1); });
     } else {
