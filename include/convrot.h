@@ -644,7 +644,9 @@ CONVROT_API int convrot_fp8_qkv_forward(const void *X, int64_t B, int64_t T,
  * K % 8 == 0, K <= 32768, M < 2^31 (EUNSUPPORTED otherwise).  An output may stand in
  * the place of an input of the same extent; otherwise outputs overlap neither inputs
  * nor each other (EINVAL).  A row with a NaN or an infinity has NaN outputs (where it
- * is rounded to INT8, its scale is NaN) and leaves the other rows alone. */
+ * is rounded to INT8, its scale is NaN) and leaves the other rows alone.  A w with a NaN or
+ * an infinity reaches every row: its channel of n is not finite, and where n is rounded to
+ * INT8 the row's scale is not. */
 
 /* y [M, K] = n, rounded once to y_dtype (CONVROT_BF16 or CONVROT_F32). */
 CONVROT_API int convrot_add_rms_norm_forward(const void *x, int x_dtype, const void *residual,

@@ -459,3 +459,31 @@ def test_more_rows_than_a_grid_dimension_holds(cr):
     for at in range(0, M, 2 ** 25 + 8):
         part, _ = cr.convrot_add_rms_norm_forward(x[at:at + 2 ** 25 + 8], None)
         assert torch.equal(y[at:at + 2 ** 25 + 8], part)
+
+
+@pytest.mark.parametrize("K", [256, 1280, 5376, 8448, 16640])
+@pytest.mark.parametrize("block,rotation", BLOCKS, ids=str)
+def test_non_finite_weights_reach_every_row(cr, block, rotation, K):
+    """A NaN in the norm's weight, or infinities that meet as NaN in a block's rotation (an odd
+    number of minus signs over four of its channels), show in the outputs of the INT8 form as
+    in those of the others: no row looks finite."""
+    x, w = rows(1, 18, K, BF16), weight(K)
+    x[:, :4] = 1
+    bad = []
+    for at in (0, K // 2 + 3, K - 1):
+        wb = w.clone()
+        wb[at] = float("nan")
+        bad.append(wb)
+    wb = w.clone()
+    wb[:4] = torch.tensor([1.0, 1, 1, -1], device="cuda") * float("inf")
+    bad.append(wb)
+    W8 = cr.convrot_linear_prepare_weights(rows(3, 64, K, F32) * 0.02, block, rotation=rotation)
+    F = cr.convrot_fp8_prepare_weights(rows(3, 64, K, F32) * 0.02)
+    for wb in bad:
+        y, _ = cr.convrot_add_rms_norm_forward(x, wb)
+        assert not bool(y.isfinite().all(1).any())
+        _, s, _ = cr.convrot_add_rms_norm_rotate_quantize(x, wb, block, rotation=rotation)
+        assert bool(s.isnan().all())
+        for W in (W8, F):
+            y, _ = cr.convrot_norm_linear_forward(x, wb, W)
+            assert bool(y.isnan().all())

@@ -100,7 +100,9 @@ template <bool F32> __device__ __forceinline__ Raw<F32> narrow(const float (&v)[
     return r;
 }
 
-// Sum and maximum over a half-wave.
+// Sum and maximum over a half-wave.  The maximum keeps a NaN (v_maximum3_f32): a weight of NaN
+// makes a NaN of its whole block, and a maximum that dropped it would leave the row a finite
+// scale and codes of 0.
 #define CR_DPP(v, CTRL)                                                                           \
     __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true))
 __device__ __forceinline__ float half_sum(float v)
@@ -111,10 +113,17 @@ __device__ __forceinline__ float half_sum(float v)
     v += CR_DPP(v, 0x140);
     return v + __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(v), 0x401F));
 }
+__device__ __forceinline__ float max_or_nan(float a, float b)
+{
+    return __builtin_elementwise_maximum(a, b);
+}
 __device__ __forceinline__ float half_max(float v)
 {
-    v = max16(v);
-    return fmaxf(v, __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(v), 0x401F)));
+    v = max_or_nan(v, CR_DPP(v, 0xB1));
+    v = max_or_nan(v, CR_DPP(v, 0x4E));
+    v = max_or_nan(v, CR_DPP(v, 0x141));
+    v = max_or_nan(v, CR_DPP(v, 0x140));
+    return max_or_nan(v, __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(v), 0x401F)));
 }
 
 // Outputs of the forward kernel: rows, e4m3 codes, or INT8 codes of blocks of b
@@ -278,19 +287,20 @@ __global__ __launch_bounds__(1024) void add_norm_kernel(AddNorm a, int W)
             if (t >= mine) continue;
             rotate_chunk<B, ROT>(v[t], csign);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[t][j]));
+            for (int j = 0; j < 8; ++j) m = max_or_nan(m, fabsf(v[t][j]));
         }
         m = half_max(m);
         if (W > 1) {
             if (hl == 0) red[1][wave][half] = m;
             __syncthreads();
             m = 0.0f;
-            for (int k = 0; k < W; ++k) m = fmaxf(m, red[1][grp * W + k][half]);
+            for (int k = 0; k < W; ++k) m = max_or_nan(m, red[1][grp * W + k][half]);
         }
         const float inv = m > 0.0f ? __fdiv_rn(127.0f, m) : 0.0f;
         // the Sylvester sign trick leaves the upper lanes' values negated
         const float invs = ROT == 0 && (__builtin_popcount(chunk) & 1) ? -inv : inv;
-        // a row that is not finite gets a scale of NaN, and so NaN outputs
+        // a row that is not finite gets a scale of NaN (infinities of n alone an infinite one:
+        // infinity times the codes' 0), and so NaN outputs
         if (part == 0 && hl == 0 && in)
             a.s[row] = sum < __builtin_inff() ? __fmul_rn(__fdiv_rn(m, 127.0f), a.inv_sqrt_b)
                                               : __builtin_nanf("");
