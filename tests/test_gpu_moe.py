@@ -386,3 +386,26 @@ def test_pre_norm_layers(cr, T):
         ref, bound = layer(n, ex, ids64, w64, 0, BF16)
         assert bool(((y.double() - ref).abs() <= bound).all())
         x, h = y, h2
+
+
+@pytest.mark.parametrize("T", [1, 5, 12, 20, 40])
+def test_values_past_bf16(cr, T):
+    """F32 outputs carry g up to the largest fp32 value, which is beyond bf16's: even tokens have
+    a g of that value at every channel, odd ones a quarter of it, the last (of several) an
+    infinite one, whose outputs are not finite.  Only channel 0 of g is summed, so outputs are
+    off by the additions of its three parts: 2^-22."""
+    K = F = 128
+    gu, dn = torch.zeros(1, 2 * F, K, device="cuda"), torch.zeros(1, K, F, device="cuda")
+    gu[:, :, 0], dn[:, :, 0] = 1, 1
+    gus, dns = torch.empty(1, 2, 1, device="cuda"), torch.full((1, 1, 1), 2.0 ** -120, device="cuda")
+    gus[0, 0], gus[0, 1] = 2.0 ** 63, (2 - 2.0 ** -23) * 2.0 ** 64
+    W = cr.convrot_moe_prepare_weights(gu.to(FP8), dn.to(FP8), 0, gus, dns)
+    x = torch.zeros(T, K, dtype=BF16, device="cuda")
+    x[0::2, 0], x[1::2, 0] = 1, 0.5
+    if T > 1:
+        x[-1, 0] = 2
+    n = max(T - 1, 1)
+    y, _, _ = cr.convrot_moe_forward(x, torch.zeros(1, K, device="cuda"), W, 1, out_dtype=F32)
+    ref = x.double()[:, :1] ** 2 * ((2 - 2.0 ** -23) * 2.0 ** 7)
+    assert bool(((y[:n].double() - ref[:n]).abs() <= ref[:n] * 2.0 ** -22).all())
+    assert not bool(y[n:].isfinite().any())

@@ -15,7 +15,7 @@
 // experts then does not depend on the order of the sums, a batch or a shape.  g is
 // rounded to bf16 for bf16 outputs, whose own rounding is as large (together 2.4e-3 of the
 // outputs' rms, 1.7e-3 with g exact); for F32 outputs it is carried as three bf16 parts,
-// which hold an fp32 value exactly.
+// which hold an fp32 value of 2^-110 or more exactly, and a smaller one to 2^-133.
 //
 // Loads.  A wave keeps a ring of D blocks of codes with their columns in registers: the
 // next block is requested as soon as one is used.  Idle columns read past the end of a
@@ -44,6 +44,7 @@ typedef double v4d __attribute__((ext_vector_type(4)));
 typedef unsigned long long u64;
 
 constexpr int kMaxUnits = kMoeMaxExperts + kMoeMaxShared;
+constexpr float kMaxBf16 = 0x1.fep127f;
 
 // A unit is an expert and the tokens that chose it: choose leaves a set of tokens for every
 // expert, gate_up finds its unit from them and leaves it here for down.  Rows of g: an expert's lie behind those of the experts
@@ -463,9 +464,15 @@ __device__ __forceinline__ void gate_up(const Moe &m, int expert, int base, int 
         const int planes = m.y_f32 ? 3 : 1;
         uint16_t *p = g + (int64_t)base * planes * m.F +
                       ((fb * 2 + (q >> 1)) * planes * n + c * 16 + r) * 8 + (q & 1) * 4;
-        // the part that bf16 holds; for F32 outputs what it leaves, twice more
+        // the part that bf16 holds; for F32 outputs what it leaves, twice more.  A part that others
+        // follow stays within bf16's largest value: rounded past it, it would be infinite and
+        // what it leaves minus infinity
         for (int part = 1;; ++part) {
-            const uint2 o = make_uint2(cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]));
+            const float most = part < planes ? kMaxBf16 : __builtin_inff();
+            float c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[i] = fabsf(v[i]) > most ? copysignf(most, v[i]) : v[i];
+            const uint2 o = make_uint2(cvt_pk_bf16(c[0], c[1]), cvt_pk_bf16(c[2], c[3]));
             *reinterpret_cast<uint2 *>(p) = o;
             if (part == planes) break;
             v[0] -= bf16_lo(o.x);
