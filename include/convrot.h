@@ -774,7 +774,8 @@ CONVROT_API size_t convrot_moe_workspace_bytes(int64_t T, const convrot_moe_weig
  *   Y            y_dtype CONVROT_BF16 or _F32.
  *   ids, weights device [T, top_k] int32 and F32: the choices, the first the largest, and
  *                their weights (outputs).  1 <= top_k <= min(E, CONVROT_MOE_MAX_TOP_K).
- * Outputs overlap neither inputs nor each other (EINVAL). */
+ * Outputs and ws overlap neither inputs (the experts' codes and scales among them) nor each
+ * other (EINVAL). */
 CONVROT_API int convrot_moe_forward(const void *X, int64_t T, const void *router, int router_dtype,
                                     const float *router_bias, const convrot_moe_weights *W,
                                     int top_k, int score, uint32_t flags, float scale, void *Y,

@@ -130,3 +130,33 @@ def test_binding_refusals(cr):
             lambda: f(x, r, W, 2)):                                  # on the host
         with pytest.raises(ValueError):
             call()
+
+
+def test_forward_overlaps(cr):
+    """Outputs and the workspace against every input's whole extent, the experts' codes and
+    scales among them, and against each other: the last 16 bytes, and the first ones behind."""
+    E, S, K, F, T, k = 16, 1, 512, 256, 4, 2
+    need = cr.library().convrot_moe_workspace_bytes(T, ctypes.byref(desc(cr)), k)
+    extents = {"gate_up": (E + S) * 2 * F * K, "gate_up_scale": (E + S) * 2 * F // 128 * K // 128 * 4,
+               "down": (E + S) * K * F, "down_scale": (E + S) * K // 128 * F // 128 * 4,
+               "X": T * K * 2, "r": E * K * 4, "bias": E * 4}
+    outs = {"Y": T * K * 2, "ids": T * k * 4, "w": T * k * 4, "ws": need}
+    base = {n: PTR[i] for i, n in enumerate((*extents, *outs))}
+
+    def f(**kw):
+        a = {**base, **kw}
+        d = desc(cr, **{n: a[n] for n in ("gate_up", "gate_up_scale", "down", "down_scale")})
+        # a workspace that is a byte short: nothing can be launched
+        return cr.library().convrot_moe_forward(
+            a["X"], T, a["r"], 0, a["bias"], ctypes.byref(d), k, 0, 1, 1.0, a["Y"], 1, a["ids"],
+            a["w"], a["ws"], need - 1, None)
+
+    assert f() == cr.EWORKSPACE
+    for o in outs:
+        for n, size in {**extents, **outs}.items():
+            if n == o:
+                continue
+            end = (size + 15) // 16 * 16
+            assert f(**{o: base[n] + end - 16}) == cr.EINVAL, (o, n)
+            assert f(**{o: base[n]}) == cr.EINVAL, (o, n)
+            assert f(**{o: base[n] + end}) == cr.EWORKSPACE, (o, n)

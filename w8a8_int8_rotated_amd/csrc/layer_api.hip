@@ -4,22 +4,43 @@
 #include "api_common.hpp"
 #include "moe.hpp"
 
+namespace {
+
+// Whether an output may stand where an input does: in its place, or apart from it.
+bool overlaps(const void *a, size_t na, const void *b, size_t nb)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && na > 0 && nb > 0 && x < y + nb && y < x + na;
+}
+bool in_place_or_apart(const void *a, size_t na, const void *b, size_t nb)
+{
+    return (a == b && na == nb) || !overlaps(a, na, b, nb);
+}
+
+// Whether everything a call writes is apart from all that it reads and from each other.
+struct Extent {
+    const void *p;
+    size_t n;
+};
+template <int O, int I>
+bool apart(const Extent (&out)[O], const Extent (&in)[I])
+{
+    for (int i = 0; i < O; ++i) {
+        for (const Extent &e : in)
+            if (overlaps(out[i].p, out[i].n, e.p, e.n)) return false;
+        for (int j = 0; j < i; ++j)
+            if (overlaps(out[i].p, out[i].n, out[j].p, out[j].n)) return false;
+    }
+    return true;
+}
+
+} // namespace
+
 extern "C" {
 
 // ---------------------------------------------------------------------------
 // The residual's addition and the RMS norm.
 // ---------------------------------------------------------------------------
-
-// Whether an output may stand where an input does: in its place, or apart from it.
-static bool overlaps(const void *a, size_t na, const void *b, size_t nb)
-{
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return a && b && na > 0 && nb > 0 && x < y + nb && y < x + na;
-}
-static bool in_place_or_apart(const void *a, size_t na, const void *b, size_t nb)
-{
-    return (a == b && na == nb) || !overlaps(a, na, b, nb);
-}
 
 static bool is_float_dtype(int t) { return t == CONVROT_F32 || t == CONVROT_BF16; }
 static size_t dtype_bytes(int t) { return t == CONVROT_F32 ? 4u : 2u; }
@@ -413,16 +434,18 @@ static int moe_forward_impl(const void *X, int64_t T, const void *router, int ro
     for (const void *p : all)
         if (!aligned16(p)) return CONVROT_EALIGN;
     const size_t n = (size_t)T * (size_t)W->K, nk = (size_t)T * (size_t)top_k * 4u;
-    const struct { const void *p; size_t n; } in[] = {
-        {X, n * 2u}, {router, (size_t)W->experts * (size_t)W->K * dtype_bytes(router_dtype)},
-        {router_bias, (size_t)W->experts * 4u}},
-        out[] = {{Y, n * dtype_bytes(y_dtype)}, {ids, nk}, {weights, nk}};
-    for (int i = 0; i < 3; ++i)
-        for (int j = 0; j < 3; ++j)
-            if (overlaps(out[i].p, out[i].n, in[j].p, in[j].n) ||
-                (j < i && overlaps(out[i].p, out[i].n, out[j].p, out[j].n)))
-                return CONVROT_EINVAL;
-    if (!ws || ws_bytes < convrot_moe_workspace_bytes(T, W, top_k)) return CONVROT_EWORKSPACE;
+    const size_t need = convrot_moe_workspace_bytes(T, W, top_k);
+    const int64_t experts = (int64_t)W->experts + W->shared;
+    const Extent out[] = {{Y, n * dtype_bytes(y_dtype)}, {ids, nk}, {weights, nk}, {ws, need}},
+                 in[] = {{X, n * 2u},
+                         {router, (size_t)W->experts * (size_t)W->K * dtype_bytes(router_dtype)},
+                         {router_bias, (size_t)W->experts * 4u},
+                         {W->gate_up, convrot_moe_packed_bytes(experts, 2 * W->F, W->K)},
+                         {W->gate_up_scale, convrot_moe_scale_bytes(experts, 2 * W->F, W->K)},
+                         {W->down, convrot_moe_packed_bytes(experts, W->K, W->F)},
+                         {W->down_scale, convrot_moe_scale_bytes(experts, W->K, W->F)}};
+    if (!apart(out, in)) return CONVROT_EINVAL;
+    if (!ws || ws_bytes < need) return CONVROT_EWORKSPACE;
 
     convrot::Moe m = {};
     m.router = router;
