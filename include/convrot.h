@@ -643,7 +643,8 @@ CONVROT_API int convrot_fp8_qkv_forward(const void *X, int64_t B, int64_t T,
  *   residual_out  h, of the residual's type; may be the residual, or x of that type.
  * K % 8 == 0, K <= 32768, M < 2^31 (EUNSUPPORTED otherwise).  An output may stand in
  * the place of an input of the same extent; otherwise outputs overlap neither inputs
- * nor each other (EINVAL).  A row with a NaN or an infinity has NaN outputs (where it
+ * nor each other, and ws overlaps none of them (EINVAL; of a linear, its bias and prepared
+ * weights are inputs too).  A row with a NaN or an infinity has NaN outputs (where it
  * is rounded to INT8, its scale is NaN) and leaves the other rows alone.  A w with a NaN or
  * an infinity reaches every row: its channel of n is not finite, and where n is rounded to
  * INT8 the row's scale is not. */
@@ -672,8 +673,9 @@ CONVROT_API int convrot_add_rms_norm_fp8_quantize(const void *x, int x_dtype,
 
 /* Y [M, W->N] = linear(n; W) + bias: the two calls above, then the product (two
  * launches; n itself is never written).  ws: convrot_linear_workspace_bytes(M, K, N, b)
- * or convrot_fp8_norm_linear_workspace_bytes(M, K, N) bytes.  Y may not overlap
- * residual_out.  Otherwise as convrot_linear_forward and convrot_fp8_linear_forward. */
+ * or convrot_fp8_norm_linear_workspace_bytes(M, K, N) bytes.  Y may stand
+ * in the place of x or of the residual, of the same extent.  Otherwise as
+ * convrot_linear_forward and convrot_fp8_linear_forward. */
 CONVROT_API size_t convrot_fp8_norm_linear_workspace_bytes(int64_t M, int64_t K, int64_t N);
 CONVROT_API int convrot_norm_linear_forward(const void *x, int x_dtype, const void *residual,
                                             int res_dtype, const float *w, float eps, int64_t M,

@@ -164,3 +164,55 @@ def test_binding_refusals(cr):
             lambda: cr.convrot_add_rms_norm_backward(x, r, w)):
         with bad:
             call()
+
+
+SPREAD = [A + (i << 40) for i in range(12)]
+
+
+def inside(base, size):
+    """The first and the last 16 bytes of an extent."""
+    return base, base + (size + 15) // 16 * 16 - 16
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["int8", "fp8"])
+def test_norm_linear_overlaps(cr, fp8):
+    """Y, residual_out and the workspace against every input, the bias and the prepared weights
+    among them, and against each other."""
+    lib, M, K, N = cr.library(), 4, 512, 256
+    need = lib.convrot_fp8_norm_linear_workspace_bytes(M, K, N) if fp8 else \
+        lib.convrot_linear_workspace_bytes(M, K, N, 128)
+    ins = {"w": K * 4, "bias": N * 4, "codes": N * K, "scale": N // 128 * K // 128 * 4 if fp8 else N * 4}
+    size = {"x": M * K * 2, "r": M * K * 4, "h": M * K * 4, "Y": M * N * 2, "ws": need, **ins}
+    base = dict(zip(size, SPREAD))
+
+    def f(**kw):
+        a = {**base, **kw}
+        d = cr.convrot_fp8_weights() if fp8 else cr.convrot_weights()
+        if fp8:
+            d.magic, d.version = cr.FP8_MAGIC, cr.FP8_VERSION
+        else:
+            d.magic, d.version, d.block = cr.WEIGHTS_MAGIC, cr.WEIGHTS_VERSION, 128
+        d.N, d.K, d.codes, d.scale = N, K, a["codes"], a["scale"]
+        fn = lib.convrot_fp8_norm_linear_forward if fp8 else lib.convrot_norm_linear_forward
+        return fn(a["x"], 1, a["r"], 0, a["w"], 1e-6, M, ctypes.byref(d), a["bias"], a["h"], a["Y"],
+                  1, a["ws"], need, None)
+
+    for o, others in (("Y", ("x", "r", "h", "ws", *ins)), ("h", ("ws", *ins)),
+                      ("ws", ("x", "r", *ins))):
+        for n in others:
+            for at in inside(base[n], size[n]):
+                assert f(**{o: at}) == cr.EINVAL, (o, n)
+
+
+def test_backward_workspace_overlaps(cr):
+    lib, M, K = cr.library(), 4, 512
+    need = lib.convrot_add_rms_norm_workspace_bytes(M, K)
+    size = {"g": M * K * 4, "h": M * K * 4, "gh": M * K * 4, "w": K * 4, "dh": M * K * 4,
+            "dx": M * K * 2, "dw": K * 4}
+    base = dict(zip(size, SPREAD))
+    for n in size:
+        for at in inside(base[n], size[n]):
+            b = base
+            assert lib.convrot_add_rms_norm_backward(
+                b["g"], 0, b["h"], 0, b["gh"], b["w"], 1e-6, M, K, b["dh"], b["dx"], b["dw"], at,
+                need, None) == cr.EINVAL, n

@@ -487,3 +487,20 @@ def test_non_finite_weights_reach_every_row(cr, block, rotation, K):
         for W in (W8, F):
             y, _ = cr.convrot_norm_linear_forward(x, wb, W)
             assert bool(y.isnan().all())
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_norm_linear_in_place(cr, kind, M):
+    """Y in the place of x, or of the residual, which the first launch has read by then."""
+    K = N = 640
+    x, r, w = rows(1, M, K, BF16), rows(2, M, K, F32, 3.0), weight(K)
+    W32 = rows(3, N, K, F32) * 0.02
+    W = cr.convrot_linear_prepare_weights(W32, 128) if kind == "int8" else \
+        cr.convrot_fp8_prepare_weights(W32)
+    for out_t in (BF16, F32):
+        y, h = cr.convrot_norm_linear_forward(x, w, W, r, out_dtype=out_t)
+        t = (x.clone(), r.clone())
+        at = t[0] if out_t == BF16 else t[1]
+        y1, h1 = cr.convrot_norm_linear_forward(t[0], w, W, t[1], out=at)
+        assert y1 is at and torch.equal(y1, y) and torch.equal(h1, h)

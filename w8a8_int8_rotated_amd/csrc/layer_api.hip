@@ -179,10 +179,11 @@ size_t convrot_fp8_norm_linear_workspace_bytes(int64_t M, int64_t K, int64_t N)
     return codes_bytes(M, K) + fp8_row_scales_bytes(M, K);
 }
 
-// What both paths check before anything is launched (W was checked).
-static int norm_linear_check(const convrot::AddNorm &a, int64_t N, const float *bias,
-                             const void *Y, int y_dtype, const void *ws, size_t ws_bytes,
-                             size_t need)
+// What both paths check before anything is launched (W was checked): its outputs N, codes and
+// scales.  Y may stand in the place of x or of the residual, which the first launch reads.
+static int norm_linear_check(const convrot::AddNorm &a, int64_t N, const Extent &codes,
+                             const Extent &scale, const float *bias, const void *Y, int y_dtype,
+                             const void *ws, size_t ws_bytes, size_t need)
 {
     int rc = check_rows(a.M, a.K);
     if (rc != CONVROT_OK) return rc;
@@ -191,9 +192,14 @@ static int norm_linear_check(const convrot::AddNorm &a, int64_t N, const float *
     if (!Y) return CONVROT_EINVAL;
     if (!aligned16(Y) || !aligned16(bias) || !aligned16(ws)) return CONVROT_EALIGN;
     if (!ws || ws_bytes < need) return CONVROT_EWORKSPACE;
-    const size_t ny = (size_t)a.M * (size_t)N * dtype_bytes(y_dtype);
-    return overlaps(Y, ny, a.h, (size_t)a.M * (size_t)a.K * (a.r_f32 ? 4u : 2u))
-               ? CONVROT_EINVAL : CONVROT_OK;
+    const size_t e = (size_t)a.M * (size_t)a.K, nx = e * (a.x_f32 ? 4u : 2u),
+                 nr = e * (a.r_f32 ? 4u : 2u),
+                 ny = (size_t)a.M * (size_t)N * dtype_bytes(y_dtype);
+    const Extent out[] = {{a.h, nr}, {Y, ny}, {ws, need}},
+                 in[] = {{a.w, (size_t)a.K * 4u}, {bias, (size_t)N * 4u}, codes, scale};
+    return apart(out, in) && in_place_or_apart(Y, ny, a.x, nx) && in_place_or_apart(Y, ny, a.r, nr) &&
+                   !overlaps(ws, need, a.x, nx) && !overlaps(ws, need, a.r, nr)
+               ? CONVROT_OK : CONVROT_EINVAL;
 }
 
 static int norm_linear_impl(const void *x, int x_dtype, const void *residual, int res_dtype,
@@ -206,7 +212,9 @@ static int norm_linear_impl(const void *x, int x_dtype, const void *residual, in
     convrot::AddNorm a;
     rc = add_norm_args(x, x_dtype, residual, res_dtype, w, eps, M, W->K, residual_out, &a);
     if (rc == CONVROT_OK)
-        rc = norm_linear_check(a, W->N, bias, Y, y_dtype, ws, ws_bytes,
+        rc = norm_linear_check(a, W->N,
+                               {W->codes, convrot_weights_packed_bytes(W->N, W->K, W->block)},
+                               {W->scale, (size_t)W->N * 4u}, bias, Y, y_dtype, ws, ws_bytes,
                                convrot_linear_workspace_bytes(M, W->K, W->N, W->block));
     if (rc != CONVROT_OK || M == 0) return rc;
     Carve c(ws);
@@ -244,7 +252,9 @@ static int fp8_norm_linear_impl(const void *x, int x_dtype, const void *residual
     convrot::AddNorm a;
     rc = add_norm_args(x, x_dtype, residual, res_dtype, w, eps, M, W->K, residual_out, &a);
     if (rc == CONVROT_OK)
-        rc = norm_linear_check(a, W->N, bias, Y, y_dtype, ws, ws_bytes,
+        rc = norm_linear_check(a, W->N, {W->codes, convrot_fp8_packed_bytes(W->N, W->K)},
+                               {W->scale, convrot_fp8_scale_bytes(W->N, W->K)}, bias, Y, y_dtype,
+                               ws, ws_bytes,
                                convrot_fp8_norm_linear_workspace_bytes(M, W->K, W->N));
     if (rc != CONVROT_OK || M == 0) return rc;
     Carve c(ws);
@@ -305,6 +315,9 @@ int convrot_add_rms_norm_backward(const void *g, int g_dtype, const void *h, int
         return CONVROT_EINVAL;
     const size_t need = dw ? convrot_add_rms_norm_workspace_bytes(M, K) : 0;
     if (need > 0 && (!ws || ws_bytes < need)) return CONVROT_EWORKSPACE;
+    const Extent scratch[] = {{ws, need}},
+                 rest[] = {{g, ng}, {h, nh}, {g_h, nh}, {w, nk}, {dh, nh}, {dx, 2 * n}, {dw, nk}};
+    if (!apart(scratch, rest)) return CONVROT_EINVAL;
     const convrot::AddNormGrad a = {g, h, g_h, w, dh, dx, dw, static_cast<float *>(ws), M, (int)K,
                                     eps, g_dtype == CONVROT_F32, h_dtype == CONVROT_F32};
     return hip_status(convrot::launch_add_norm_grad(a, static_cast<hipStream_t>(stream)));
