@@ -409,3 +409,23 @@ def test_values_past_bf16(cr, T):
     ref = x.double()[:, :1] ** 2 * ((2 - 2.0 ** -23) * 2.0 ** 7)
     assert bool(((y[:n].double() - ref[:n]).abs() <= ref[:n] * 2.0 ** -22).all())
     assert not bool(y[n:].isfinite().any())
+
+
+# one token, and three: the experts' own workgroups choose, with two, four and eight experts a
+# lane; or in more than a round of them (F / 16 (k + S) > 768) the kernel of its own
+FEW_TOKENS = [
+    dict(T=1, K=256, F=128, E=256, k=32, S=1, bias=True, score="sigmoid"),
+    dict(T=1, K=384, F=256, E=129, k=8, out="f32"),
+    dict(T=3, K=256, F=128, E=200, k=10, S=2, bias=True, router="f32"),
+    dict(T=1, K=256, F=128, E=512, k=32, S=2, score="sigmoid", renormalize=False),
+    dict(T=1, K=128, F=384, E=257, k=5, bias=True, out="f32", scale=2.5),
+    dict(T=1, K=128, F=512, E=128, k=32, S=16, out="f32"),
+    dict(T=1, K=256, F=512, E=200, k=32, bias=True, score="sigmoid"),
+    dict(T=1, K=128, F=512, E=300, k=31, S=1, renormalize=False),
+    dict(T=1, K=128, F=1024, E=14, k=14, S=1),
+]
+
+
+@pytest.mark.parametrize("case", FEW_TOKENS, ids=str)
+def test_few_tokens_of_many_experts(cr, case):
+    test_layer(cr, case)

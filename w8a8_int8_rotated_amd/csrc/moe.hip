@@ -1008,6 +1008,19 @@ int down_parts(const Moe &m)
 
 } // namespace
 
+// Up to kOwnChoice tokens the workgroups of gate_up choose for themselves while they are one
+// round of the CUs (three a CU), since each pays for it.  us a call with that and with the
+// kernel of its own, 256 CUs:
+//   1 token: 8 of 128 experts of 2048 x 768 (384 workgroups) 20.6, 23.4; of 2048 x 1536 (768)
+//     27.4, 29.9; of 2048 x 2048 (1024) 34.0, 34.1; 16 of 256 of 2048 x 1024 (1024) 40.9, 37.7;
+//     32 of 512 of 1024 x 512 (1024) 55.8, 42.3; of 512 x 2048 (4096) 135, 58.5
+//   2 tokens: 45 experts, 8 each, of 2944 x 1792 (1792) 62.2, 57.8;  3 tokens: 5 experts of
+//     256 x 896 21.7, 25.2
+bool moe_own_choice(int T, int64_t workgroups, int64_t cus)
+{
+    return T <= kOwnChoice && workgroups <= 3 * cus;
+}
+
 size_t moe_workspace_bytes(int T, int E, int S, int top_k, int K, int F)
 {
     return moe_layout(std::min(T, kMoeTokens), E, S, top_k, K, F).bytes;
@@ -1041,11 +1054,7 @@ hipError_t launch_moe(const Moe &m, hipStream_t stream)
                            buffers * kGateWaves * 2 * 1024, stream, m, units, rows, g,
                            logits, pieces, sets);
     };
-    // The experts' own workgroups choose while they are one round of the CUs (three a CU),
-    // since each pays for it: us a call with that and with the kernel of its own, 3 tokens of
-    // 5 experts of 256 x 896: 21.7, 25.2; 2 tokens of 45 experts, 8 each, of 2944 x 1792 (1792
-    // workgroups): 62.2, 57.8.
-    if (m.T == 1 || (m.T <= kOwnChoice && tiles * most <= 3 * device_cu_count())) {
+    if (moe_own_choice(m.T, tiles * most, device_cu_count())) {
         by_experts([&](auto ep) { gate_up(gate_up_kernel<8, decltype(ep)::value>, 1); });
     } else {
         by_experts([&](auto ep) {

@@ -26,6 +26,8 @@ struct Moe {
 };
 // For passes of up to T tokens.
 size_t moe_workspace_bytes(int T, int E, int S, int top_k, int K, int F);
+// Whether gate_up chooses the experts itself, in a launch of so many workgroups.
+bool moe_own_choice(int T, int64_t workgroups, int64_t cus);
 hipError_t launch_moe(const Moe &m, hipStream_t stream);
 
 } // namespace convrot
