@@ -64,3 +64,23 @@ def test_linear_few_rows(cr):
     for M in (1, 2, 15, 16, 17, 33, 64):
         assert torch.equal(cr.convrot_linear_forward(x[:M].contiguous(), W, bias=b), full[:M])
     assert padded_rows(16) == 16
+
+
+@pytest.mark.parametrize("N", [2 ** 20, 2 ** 20 + 16])
+def test_both_sides_of_the_widest_border(cr, N):
+    """17 and 32 rows of the widest outputs that this kernel takes, and of wider ones."""
+    K = 128
+    g = torch.Generator(device="cuda").manual_seed(N)
+    codes = torch.randint(-127, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    W = cr.convrot_linear_prepare_weights(codes, 64, src_scale=torch.rand(N, generator=g,
+                                                                          device="cuda") * 1e-3)
+    rng = np.random.default_rng(3)
+    for M in (16, 17, 32):
+        announce(f"few rows M={M} N={N} K={K}")
+        q = rng.integers(-127, 128, (M, K)).astype(np.int8)
+        s = to_dev(rng.random(M).astype(np.float32))
+        whole = torch.full((M + 2, N), 7.0, dtype=torch.bfloat16, device="cuda")
+        y = cr.convrot_gemm_dequant(to_dev(tile(q)), s, W, out=whole[:M])
+        assert bool((whole[M:] == 7).all())
+        acc = (to_dev(q).float().double() @ codes.double().t()).float()
+        assert torch.equal(y, (acc * s[:, None] * W.scale).to(torch.bfloat16))

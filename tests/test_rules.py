@@ -37,3 +37,12 @@ def test_own_choice(ask):
     """Experts' workgroups choose for themselves up to one round of three a CU, one token's too."""
     assert ask("own 1 384", "own 1 768", "own 4 768") == [1, 1, 1]
     assert ask("own 1 769", "own 1 4096", "own 2 1792", "own 4 769", "own 5 16") == [0] * 5
+
+
+def test_few_rows(ask):
+    """The INT8 product's kernel for few rows: any N up to 16 rows, to 2^20 up to 32, to 96 a CU up
+    to 64."""
+    assert ask("few 1 16", "few 16 4194304", "few 17 1048576", "few 32 1048576",
+               "few 33 24576", "few 64 24576") == [1] * 6
+    assert ask("few 17 1048592", "few 32 4194304", "few 33 24592", "few 64 32768",
+               "few 65 16") == [0] * 5

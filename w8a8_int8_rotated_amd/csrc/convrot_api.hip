@@ -65,7 +65,7 @@ int hip_status(hipError_t e)
 hipError_t product_i8(const int8_t *qx, const float *sx, int64_t M, const convrot_weights *W,
                       const float *bias, void *Y, int y_dtype, hipStream_t s)
 {
-    if (few_rows(M, W->N))
+    if (few_rows(M, W->N, device_cu_count()))
         return launch_gemm_i8_few(qx, W->codes, sx, W->scale, bias, Y, y_dtype == CONVROT_F32, M,
                                   W->N, W->K, s);
     return launch_gemm_i8(qx, W->codes, sx, W->scale, bias, Y, out_kind(y_dtype), M, W->N, W->K, s);

@@ -14,14 +14,19 @@
 
 namespace convrot {
 
-// Whether this kernel takes M rows of N outputs.  us a call here and in tiles, K = 5376, 32 and 64
-// rows: N = 5376: 10.4, 18.6 and 10.4, 19.7; 16128: 17.5, 33.4 and 24.3, 35.6; 32256: 32.2, 39.8
-// and 45.9, 42.7; 43008: 45.0, 49.5 and 64.8, 51.8 (four row tiles of X come from L2 for every
-// two of the weight, and a tile's 256 rows cost the tiled kernel nothing once all CUs have
-// one); K = 21504, N = 5376: 30.9, 109 and 40.9, 117.
-inline bool few_rows(int64_t M, int64_t N)
+// Whether this kernel takes M rows of N outputs.  Up to 16 rows it always leads: N = 2^22, K = 128
+// and 256: 173 us a call here, 254 in tiles, and 234, 324.  Up to 32 it does to about 2^20 outputs,
+// where both write more than they read (K = 128, bf16, 32 rows: N = 2^19 37.1, 38.0; 2^20 74.4,
+// 74.2; 2^21 156, 147; K = 512: 65.5, 68.8; 131, 133; 265, 255; K = 1024, 2^20: 215, 226), and up to
+// 64 while a CU has at most 96 outputs: us here and in tiles for 32 and 64 rows, K = 5376: N = 5376:
+// 10.4, 18.6 and 10.4, 19.7; 16128: 17.5, 33.4 and 24.3, 35.6; 32256: 32.2, 39.8 and 45.9, 42.7;
+// 43008: 45.0, 49.5 and 64.8, 51.8 (four row tiles of X come from L2 for every two of the weight,
+// and a tile's 256 rows cost the tiled kernel nothing once all CUs have one); 64 rows of
+// N = 24576: K = 1024 9.8, 11.8; 5376 35.3, 40.0; 16384 99, 111; K = 21504, N = 5376: 30.9, 109 for
+// 32 and 40.9, 117 for 64.
+bool few_rows(int64_t M, int64_t N, int64_t cus)
 {
-    return M <= 32 || (M <= 64 && N <= 96 * device_cu_count());
+    return M <= 16 || (M <= 32 && N <= 4096 * cus) || (M <= 64 && N <= 96 * cus);
 }
 
 namespace {
