@@ -160,3 +160,19 @@ def test_forward_overlaps(cr):
             assert f(**{o: base[n] + end - 16}) == cr.EINVAL, (o, n)
             assert f(**{o: base[n]}) == cr.EINVAL, (o, n)
             assert f(**{o: base[n] + end}) == cr.EWORKSPACE, (o, n)
+
+
+def test_workspace_sizes_kept_are_few(cr):
+    """A layer called with many batch sizes keeps one size for each up to a pass of 64 tokens, and
+    each is the library's."""
+    d = desc(cr)
+    W = cr.MoEWeights(d, None, None, torch.zeros(1), None)
+    r = torch.zeros(16, 512)
+    for T in (*range(1, 130), 1000, 38656):
+        need = cr.library().convrot_moe_workspace_bytes(T, ctypes.byref(d), 2)
+        x = torch.zeros(T, 512, dtype=torch.bfloat16)
+        with pytest.raises(ValueError, match=f"{need} needed"):
+            cr.convrot_moe_forward(x, r, W, 2, workspace=torch.empty(need - 1, dtype=torch.uint8))
+        with pytest.raises(ValueError, match="GPU"):                 # large enough: on the host
+            cr.convrot_moe_forward(x, r, W, 2, workspace=torch.empty(need, dtype=torch.uint8))
+    assert len(W._workspace) <= 64

@@ -42,6 +42,7 @@ ROPE_INVERSE = 1
 MOE_MAGIC, MOE_VERSION = 0x454F4D43, 1
 MOE_SCORES = {"softmax": 0, "sigmoid": 1}
 MOE_RENORMALIZE = 1
+MOE_PASS = 64                # tokens of one pass over the experts; the workspace holds one
 
 _c_i64 = ctypes.c_int64
 _c_int = ctypes.c_int
@@ -1395,7 +1396,7 @@ class MoEWeights:
         self.gate_up, self.gate_up_scale = gate_up, gate_up_scale
         self.down, self.down_scale = down, down_scale
         self._ref = ctypes.byref(desc)
-        self._workspace = {}              # bytes by (tokens, top_k)
+        self._workspace = {}              # bytes by (tokens of a pass, top_k)
 
     @property
     def experts(self):
@@ -1495,9 +1496,10 @@ def convrot_moe_forward(X: torch.Tensor, router: torch.Tensor, W: MoEWeights, to
     _opt(out, "out", _FLOATS, (T, K))
     _opt(ids, "ids", torch.int32, (T, top_k))
     _opt(weights, "weights", torch.float32, (T, top_k))
-    wsb = W._workspace.get((T, top_k))
+    key = min(T, MOE_PASS), top_k
+    wsb = W._workspace.get(key)
     if wsb is None:
-        wsb = W._workspace[T, top_k] = convrot_moe_workspace_bytes(T, W, top_k)
+        wsb = W._workspace[key] = convrot_moe_workspace_bytes(T, W, top_k)
     _check_workspace(wsb, workspace)
     dev = W.down.device
     _on_device(dev, X=X, router=router, router_bias=router_bias, out=out, ids=ids,
