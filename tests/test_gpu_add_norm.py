@@ -504,3 +504,98 @@ def test_norm_linear_in_place(cr, kind, M):
         at = t[0] if out_t == BF16 else t[1]
         y1, h1 = cr.convrot_norm_linear_forward(t[0], w, W, t[1], out=at)
         assert y1 is at and torch.equal(y1, y) and torch.equal(h1, h)
+
+
+def rows_past_caches(K, bytes_a_channel):
+    """The least odd number of rows whose call moves more than 2^28 bytes (such calls read and
+    write past the caches)."""
+    return (2 ** 28 // (K * bytes_a_channel) + 1) | 1
+
+
+@pytest.mark.parametrize("out_t", [BF16, F32], ids=str)
+@pytest.mark.parametrize("x_t,r_t", TYPES, ids=str)
+@pytest.mark.parametrize("K", [40, 520, 4104, 8192])
+def test_forward_past_the_caches(cr, K, x_t, r_t, out_t):
+    """Against the definition, and bit for bit against parts of the rows, whose calls go through
+    the caches; in place too."""
+    size = {"bf16": 2, "f32": 4, None: 0}
+    M = rows_past_caches(K, size[x_t] + 2 * size[r_t] + (4 if out_t == F32 else 2))
+    announce(f"norm past the caches M={M} K={K} x={x_t} r={r_t} {out_t}")
+    x = rows(1, M, K, DT[x_t])
+    r = None if r_t is None else rows(2, M, K, DT[r_t], 3.0)
+    w = weight(K)
+    whole, out = guarded(M, K, out_t)
+    hw, h = guarded(M, K, r.dtype) if r is not None else (None, None)
+    y, _ = cr.convrot_add_rms_norm_forward(x, w, r, eps=EPS, out=out, residual_out=h)
+    unharmed(whole, M)
+    if r is not None:
+        unharmed(hw, M)
+    step = M // 3 + 1
+    for at in range(0, M, step):
+        part = slice(at, min(at + step, M))
+        rp = None if r is None else r[part]
+        y1, h1 = cr.convrot_add_rms_norm_forward(x[part], w, rp, eps=EPS, out_dtype=out_t)
+        h_ref, n = reference(x[part], w, rp)
+        assert torch.equal(y[part], y1)
+        assert r is None or (torch.equal(h[part], h1) and torch.equal(h1, h_ref))
+        assert bool(((y[part].double() - n).abs()
+                     <= n.abs() * (2.0 ** -18 + HALF[out_t])).all())
+        del n, h_ref
+    if r is not None:
+        xi, ri = x.clone(), r.clone()
+        y2, h2 = cr.convrot_add_rms_norm_forward(xi, w, ri, eps=EPS, out_dtype=out_t,
+                                                 out=xi if x.dtype == out_t else None,
+                                                 residual_out=ri)
+        assert h2 is ri and torch.equal(y2, y) and torch.equal(h2, h)
+
+
+@pytest.mark.parametrize("g_t,h_t", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"),
+                                     ("f32", "f32")])
+@pytest.mark.parametrize("K", [40, 520, 4104, 8192, 16384, 16392])
+def test_backward_past_the_caches(cr, K, g_t, h_t):
+    """Against the definition, the rows of dh bit for bit against parts of them, whose calls go
+    through the caches; in place too."""
+    size = {"bf16": 2, "f32": 4}
+    want_dx = h_t == "f32"
+    M = rows_past_caches(K, size[g_t] + 3 * size[h_t] + (2 if want_dx else 0))
+    announce(f"norm backward past the caches M={M} K={K} g={g_t} h={h_t}")
+    g, h, gh = rows(1, M, K, DT[g_t], 0.01), rows(2, M, K, DT[h_t]), rows(3, M, K, DT[h_t], 0.01)
+    w = weight(K)
+    whole, out = guarded(M, K, h.dtype)
+    dh, dx, dw = cr.convrot_add_rms_norm_backward(g, h, w, g_h=gh, eps=EPS, dh=out,
+                                                  x_dtype=BF16 if want_dx else None)
+    unharmed(whole, M)
+    dx_ok = torch.equal(dx, dh.to(BF16)) if want_dx else dx is dh
+    assert dx_ok
+    ref_dw, dw_size = (torch.zeros(K, dtype=torch.float64, device="cuda") for _ in range(2))
+    step = M // 3 + 1
+    for at in range(0, M, step):
+        part = slice(at, min(at + step, M))
+        d1, _, _ = cr.convrot_add_rms_norm_backward(g[part], h[part], w, g_h=gh[part], eps=EPS)
+        assert torch.equal(dh[part], d1)
+        d, size_d, a, b = reference_backward(g[part], h[part], w, gh[part])
+        assert bool(((dh[part].double() - d).abs() <= size_d * 2.0 ** -15
+                     + d.abs() * HALF[h.dtype] + 2.0 ** -130).all())
+        ref_dw += a
+        dw_size += b
+        del d, size_d
+    assert bool(((dw.double() - ref_dw).abs()
+                 <= dw_size * ((M + 64) * 2.0 ** -24) + 2.0 ** -130).all())
+    t = gh.clone()
+    d2, _, dw2 = cr.convrot_add_rms_norm_backward(g, h, w, g_h=t, eps=EPS, dh=t)
+    assert d2 is t and torch.equal(d2, dh) and torch.equal(dw2, dw)
+
+
+def test_more_rows_than_a_grid_dimension_holds_in_small_parts(cr):
+    """The same rows against calls below the border of the caches, at the ends and in the middle."""
+    M, K = 2 ** 27 + 37, 8
+    x = torch.empty(M, K, dtype=BF16, device="cuda")
+    x.view(torch.int16).copy_(torch.arange(K, device="cuda", dtype=torch.int16) + 0x3f80)
+    x[:, 3] = (torch.arange(M, device="cuda") % 251).to(BF16)
+    y, _ = cr.convrot_add_rms_norm_forward(x, None)
+    n = 2 ** 22 + 8                                  # 2^27 bytes
+    for at in (0, 5 * n + 3, M // 2 - n // 2, 2 ** 26 - n + 5, M - n):
+        part, _ = cr.convrot_add_rms_norm_forward(x[at:at + n], None)
+        ref = reference(x[at:at + n], None, None)[1]
+        assert torch.equal(y[at:at + n], part)
+        assert bool(((part.double() - ref).abs() <= ref.abs() * (2.0 ** -18 + HALF[BF16])).all())
