@@ -15,7 +15,11 @@
 //
 // Measured (us; K = 5376, bf16 rows beside an fp32 residual stream): 38656 rows forward 414
 // (6.0 TB/s of 12 bytes a channel), to INT8 codes 411 (5.6 TB/s), backward with bf16
-// gradients and dx 582 (5.7 TB/s of 16 bytes); 5 rows 3.5, a launch's length.
+// gradients and dx 582 (5.7 TB/s of 16 bytes); 5 rows 3.5, a launch's length.  Rows of more
+// than 16384 channels take 8 (forward) or 4 (backward) steps a wave in the 128 registers that
+// 1024 threads leave a lane; fp32 rows forward and every backward keep 40 to 68 bytes of them in
+// scratch (8192 rows of 32768, fp32: forward 863, 5.0 TB/s of 16 bytes, backward 833, 5.2; of 16384,
+// without: 367 and 375, 5.8).
 #include "add_norm.hpp"
 
 #include "fp8_common.hpp"
@@ -359,7 +363,7 @@ template <int MODE> void launch_types(const AddNorm &a, hipStream_t stream)
 constexpr int kGradStep = 512;
 
 // LEAN (rows of many steps a wave): no loads ahead, gh and w read where they are
-// needed; the registers hold g, h and dw.
+// needed; the registers hold g, h and dw (with four steps 10 to 16 of them are spilled).
 template <bool GF, bool HF, int SPR, int AUX>
 __global__ __launch_bounds__(1024) void add_norm_grad_kernel(AddNormGrad a, int W)
 {

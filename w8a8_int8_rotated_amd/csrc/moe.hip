@@ -25,10 +25,11 @@
 //
 // Kernels: router (partial logits over pieces of K), choose (a wave a token; for a few
 // tokens gate_up's workgroups choose for themselves), gate_up, down, and where down was
-// split a join.  Measured, the kernels of a call and in brackets the chosen experts' codes
-// at the 5.1 TB/s of a large copy, us: 64 tokens, 6 of 64 experts of 5376 x 1408 each: 272
-// [283]; 5 tokens, 4 of 32 of them and a shared one: 85 [74]; one token, 8 of 128 experts of
-// 2048 x 768: 20.9 [7.5], three launches whose shortest takes 4.4.
+// split a join.  Measured, us a call and in brackets the chosen experts' codes at the
+// 5.1 TB/s of a large copy (reading alone is faster: gate_up reaches 6.0): 64 tokens, 6 of 64
+// experts of 5376 x 1408 each: 262 to 267 [283]; 5 tokens, 4 of 32 of them and a shared one: 78
+// to 85 [74]; one token, 8 of 128 experts of 2048 x 768: 21 [7.5], three launches whose shortest
+// takes 4.4.
 #include "moe.hpp"
 
 #include "fp8_common.hpp"
@@ -47,9 +48,9 @@ constexpr int kMaxUnits = kMoeMaxExperts + kMoeMaxShared;
 constexpr float kMaxBf16 = 0x1.fep127f;
 
 // A unit is an expert and the tokens that chose it: choose leaves a set of tokens for every
-// expert, gate_up finds its unit from them and leaves it here for down.  Rows of g: an expert's lie behind those of the experts
-// before it, in the order of its tokens; the shared experts' behind all of them.  In memory a
-// unit's n rows, in `planes` parts of bf16 each (one, or three for F32 outputs), are
+// expert, gate_up finds its unit from them and leaves it here for down.  Rows of g: an expert's
+// lie behind those of the experts before it, in the order of its tokens; the shared experts'
+// behind all of them.  In memory a unit's n rows, in `planes` parts of bf16 each (one, or three for F32 outputs), are
 // [F / 8][planes][n][8]: a block of 128 inputs is one run of memory, and 8 inputs of all rows
 // are neighbours in it.  (A load takes its time for the cache lines that it touches; row by
 // row each of 16 lanes touches one of its own.  down of 64 tokens so 94.5 us, 102 by rows.)
@@ -990,7 +991,11 @@ Layout moe_layout(int T, int E, int S, int top_k, int K, int F)
 // K = 5376, F = 1408 (336 workgroups a part), us with 1, 2, 3, 4, 6 parts and without the
 // join (5 us): 120, 101, 95, 103, 101; 23 tokens, 40 experts of K = 2560, F = 640, F32 (160
 // workgroups a part): 25.5, 25.9, 20.8, 23.2, 23.1.  The bytes are those of the experts that
-// the tokens are expected to choose.
+// the tokens are expected to choose.  More than one part is charged 8 us, the join and the
+// parts' way through memory: with the join's 5 alone, the calls whose estimates lie between are
+// mostly slower, us with 5 and with 8: 1 token, 4 of 16 experts of 4096 x 2048, 2 parts and 1: 30.1,
+// 28.1; 23 tokens, 4 of 32 of 5376 x 384 and a shared one, 3 and 1: 58.0, 55.2; 64 tokens, 4 of 16
+// of 5376 x 640, 3 and 1: bf16 59.9, 57.9, F32 71.9, 74.9; 4 tokens, 6 of 64 of 5376 x 640: 55.6, 57.0.
 int down_parts(const Moe &m)
 {
     const double units = m.E * (1.0 - std::pow(1.0 - (double)m.top_k / m.E, m.T)) + m.S;
